@@ -26,6 +26,11 @@ MOE_ERR_BAD_IDS = -5
 MOE_ERR_TIMEOUT = -6
 MOE_PROBE_LINEAR = 0
 MOE_PROBE_TILES = 1
+MOE_F32 = 0
+MOE_BF16 = 1
+MOE_NORM_MAX_D = 16384
+MOE_ADAMW_BLOCK = 256
+GATE_KINDS = {"none": 0, "token": 1, "channel": 2, "element": 3}
 
 EXPORTED = (
     "moe_router_topk", "moe_route_workspace_size", "moe_route",
@@ -34,6 +39,9 @@ EXPORTED = (
     "moe_last_error", "moe_abi_version", "moe_kernel_name", "moe_probe_arm", "moe_probe_count",
     "moe_route_noalloc", "moe_selftest_wait_timeout", "moe_probe_read_stream",
     "moe_route_kernel_count", "moe_ep_row_weights", "moe_ep_segment_ids", "moe_route_logits",
+    "moe_block_norm_fwd", "moe_block_norm_workspace_size", "moe_block_norm_bwd",
+    "moe_router_loss_workspace_size", "moe_router_loss_fwd", "moe_router_bwd",
+    "moe_adamw_workspace_size", "moe_adamw_step",
 )
 
 
@@ -62,7 +70,25 @@ _lib = None
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
+_F = ctypes.c_float
+_D = ctypes.c_double
 _SZ = ctypes.c_size_t
+
+
+class MoeNormDesc(ctypes.Structure):
+    _fields_ = [("T", _I), ("d", _I), ("x_type", _I), ("y_type", _I), ("gate", _I),
+                ("gate_sigmoid", _I), ("scale", _F), ("eps", _F), ("w_offset", _F)]
+
+
+class MoeAdamWTensor(ctypes.Structure):
+    _fields_ = [("param", _P), ("master", _P), ("grad", _P), ("m", _P), ("v", _P),
+                ("scales", _P), ("n", ctypes.c_int64), ("param_type", _I), ("grad_type", _I),
+                ("state_bits", _I), ("lr_mult", _F), ("weight_decay", _F)]
+
+
+class MoeAdamWHyper(ctypes.Structure):
+    _fields_ = [("lr", _D), ("beta1", _D), ("beta2", _D), ("eps", _D), ("step", ctypes.c_int64),
+                ("grad_scale", _F), ("max_norm", _F), ("skip_nonfinite", _I)]
 
 
 def load(path: str = LIB_PATH):
@@ -101,6 +127,17 @@ def load(path: str = LIB_PATH):
             "moe_route_logits": (ctypes.c_int, [_P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P,
                                                 _P, _SZ, _P]),
             "moe_ep_segment_ids": (ctypes.c_int, [_P, _I, _I, ctypes.c_int64, _P, _P]),
+            "moe_block_norm_fwd": (ctypes.c_int, [ctypes.POINTER(MoeNormDesc)] + [_P] * 10),
+            "moe_block_norm_workspace_size": (_SZ, [_I, _I]),
+            "moe_block_norm_bwd": (ctypes.c_int, [ctypes.POINTER(MoeNormDesc)] + [_P] * 15
+                                   + [_SZ, _P]),
+            "moe_router_loss_workspace_size": (_SZ, [_I, _I]),
+            "moe_router_loss_fwd": (ctypes.c_int, [_P, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+            "moe_router_bwd": (ctypes.c_int, [_P, _P, _I, _I, _I, _P, _P, _P, _P, _F, _F, _P,
+                                              _P]),
+            "moe_adamw_workspace_size": (_SZ, [ctypes.POINTER(MoeAdamWTensor), _I]),
+            "moe_adamw_step": (ctypes.c_int, [ctypes.POINTER(MoeAdamWTensor), _I,
+                                              ctypes.POINTER(MoeAdamWHyper), _P, _P, _SZ, _P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -276,6 +313,205 @@ def moe_ep_segment_ids(counts, ids, stream=None):
     _check(load().moe_ep_segment_ids(_i32(counts, "counts"), P, E_loc, ids.numel(),
                                      _i32(ids, "ids") if ids.numel() else None, _stream(stream)),
            "moe_ep_segment_ids")
+
+
+# ------------------------------------------------- norms, router losses, optimizer
+
+_TYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def _type(t, name):
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise ValueError("%s must be torch.float32 or torch.bfloat16, got %s" % (name, t.dtype))
+    return code
+
+
+def _shaped(t, shape, dtype, name):
+    """Pointer of a contiguous CUDA tensor of this shape and type (None stays None)."""
+    if t is None:
+        return None
+    p = _ptr(t, dtype, name)
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    return p
+
+
+def _norm_desc(x, y, gate, gate_kind, gate_sigmoid, scale, eps, w_offset):
+    """Descriptor, shape [T,d], types of the two sides, and the gate's shape and
+    type, from the residual-side tensor x and the block-side tensor y."""
+    have = x if x is not None else y
+    if have is None:
+        raise ValueError("pass the residual-side tensor, the block-side tensor or both")
+    if have.dim() != 2:
+        raise ValueError("rows must be [T, d], got %s" % (tuple(have.shape),))
+    if gate_kind not in GATE_KINDS:
+        raise ValueError("gate_kind must be one of %s" % ", ".join(GATE_KINDS))
+    xt = (x if x is not None else y).dtype
+    yt = (y if y is not None else x).dtype
+    T, d = have.shape
+    desc = MoeNormDesc(T, d, _type(x if x is not None else y, "x"),
+                       _type(y if y is not None else x, "y"),
+                       GATE_KINDS[gate_kind], 1 if gate_sigmoid else 0, scale, eps, w_offset)
+    gshape, gtype = {"none": ((0,), None), "token": ((T,), torch.float32),
+                     "channel": ((d,), torch.float32), "element": ((T, d), yt)}[gate_kind]
+    if (gate is None) != (gate_kind == "none"):
+        raise ValueError("gate and gate_kind go together")
+    return desc, have.shape, xt, yt, gshape, gtype
+
+
+def moe_block_norm_fwd(x, y, r=None, n=None, w_post=None, w_pre=None, rstd_y=None, rstd_r=None,
+                       gate=None, gate_kind="none", gate_sigmoid=False, scale=1.0, eps=1e-6,
+                       w_offset=0.0, stream=None):
+    """r = x + scale a(gate) norm(y; w_post), n = norm(r; w_pre).  x, r [T,d] of
+    one type, y, n [T,d] of one type (x alone and n: two types as well); weights
+    [d] fp32; rstd_y, rstd_r [T] fp32 (written).  gate: [T] ("token") or [d]
+    ("channel") fp32, or [T,d] of y's type ("element")."""
+    if y is None and n is not None:   # the norm of x alone: n has the block side's type
+        desc, sh, xt, yt, gs, gt = _norm_desc(x, n, gate, gate_kind, gate_sigmoid, scale, eps,
+                                              w_offset)
+    else:
+        # without a residual, r's own type is the residual side's
+        desc, sh, xt, yt, gs, gt = _norm_desc(x if x is not None else r, y, gate, gate_kind,
+                                              gate_sigmoid, scale, eps, w_offset)
+    T, d = sh
+    f32 = torch.float32
+    _check(load().moe_block_norm_fwd(
+        ctypes.byref(desc), _shaped(x, sh, xt, "x"), _shaped(y, sh, yt, "y"),
+        _shaped(gate, gs, gt, "gate"), _shaped(w_post, (d,), f32, "w_post"),
+        _shaped(w_pre, (d,), f32, "w_pre"), _shaped(r, sh, xt, "r"), _shaped(n, sh, yt, "n"),
+        _shaped(rstd_y, (T,), f32, "rstd_y"), _shaped(rstd_r, (T,), f32, "rstd_r"),
+        _stream(stream)), "moe_block_norm_fwd")
+
+
+def moe_block_norm_workspace_size(T, d) -> int:
+    return int(load().moe_block_norm_workspace_size(int(T), int(d)))
+
+
+def moe_block_norm_bwd(dr, dn, r, y, dx=None, dy=None, w_post=None, w_pre=None, rstd_y=None,
+                       rstd_r=None, gate=None, gate_kind="none", gate_sigmoid=False, dgate=None,
+                       dw_post=None, dw_pre=None, ws=None, scale=1.0, eps=1e-6, w_offset=0.0,
+                       stream=None):
+    """Gradients of moe_block_norm_fwd from dr (of r; None: zero) and dn (of n);
+    outputs left out are not computed.  dgate has the gate's shape and type,
+    dw_post and dw_pre are [d] fp32."""
+    x_side = next((t for t in (dr, r, dx) if t is not None), None)
+    y_side = next((t for t in (y, dn, dy) if t is not None), None)
+    desc, sh, xt, yt, gs, gt = _norm_desc(x_side, y_side, gate, gate_kind, gate_sigmoid, scale,
+                                          eps, w_offset)
+    T, d = sh
+    f32 = torch.float32
+    _check(load().moe_block_norm_bwd(
+        ctypes.byref(desc), _shaped(dr, sh, xt, "dr"), _shaped(dn, sh, yt, "dn"),
+        _shaped(r, sh, xt, "r"), _shaped(y, sh, yt, "y"), _shaped(gate, gs, gt, "gate"),
+        _shaped(w_post, (d,), f32, "w_post"), _shaped(w_pre, (d,), f32, "w_pre"),
+        _shaped(rstd_y, (T,), f32, "rstd_y"), _shaped(rstd_r, (T,), f32, "rstd_r"),
+        _shaped(dx, sh, xt, "dx"), _shaped(dy, sh, yt, "dy"), _shaped(dgate, gs, gt, "dgate"),
+        _shaped(dw_post, (d,), f32, "dw_post"), _shaped(dw_pre, (d,), f32, "dw_pre"),
+        _ptr(ws, name="ws"), 0 if ws is None else ws.numel() * ws.element_size(),
+        _stream(stream)), "moe_block_norm_bwd")
+
+
+def moe_router_loss_workspace_size(T, E) -> int:
+    return int(load().moe_router_loss_workspace_size(int(T), int(E)))
+
+
+def _counts(counts, E):
+    if counts is None:
+        return None
+    p = _i32(counts, "counts")
+    if counts.dim() != 1 or counts.numel() < E:
+        raise ValueError("counts must hold one count for each of the %d experts" % E)
+    return p
+
+
+def moe_router_loss_fwd(logits, counts, k, losses, lse, pmean, ws, stream=None):
+    """losses [2] = (load-balancing loss, z loss), lse [T], pmean [E] of logits
+    [T,E]; counts: moe_route's (its first E entries are read)."""
+    T, E = logits.shape
+    f32 = torch.float32
+    _check(load().moe_router_loss_fwd(
+        _f32(logits, "logits"), T, E, int(k), _counts(counts, E),
+        _shaped(losses, (2,), f32, "losses"), _shaped(lse, (T,), f32, "lse"),
+        _shaped(pmean, (E,), f32, "pmean"), _ptr(ws, name="ws"),
+        ws.numel() * ws.element_size(), _stream(stream)), "moe_router_loss_fwd")
+
+
+def moe_router_bwd(logits, lse, counts, ids, weights, dweights, dlogits, aux_coef=0.0,
+                   z_coef=0.0, k=None, stream=None):
+    """dlogits [T,E] through the top-k weights (dweights [T,k], or None) and
+    through aux_coef losses[0] + z_coef losses[1].  k: needed without ids."""
+    T, E = logits.shape
+    f32 = torch.float32
+    k = int(k) if k is not None else ids.shape[1]
+    _check(load().moe_router_bwd(
+        _f32(logits, "logits"), _shaped(lse, (T,), f32, "lse"), T, E, k, _counts(counts, E),
+        _shaped(ids, (T, k), torch.int32, "ids"), _shaped(weights, (T, k), f32, "weights"),
+        _shaped(dweights, (T, k), f32, "dweights"), aux_coef, z_coef,
+        _shaped(dlogits, (T, E), f32, "dlogits"), _stream(stream)), "moe_router_bwd")
+
+
+class AdamWTable:
+    """The tensors of an AdamW step, checked once and kept as the array that
+    moe_adamw_step reads.  rows: dicts with param, grad, m, v (same number of
+    values each) and optionally master, scales, lr_mult (1), weight_decay (0).
+    m and v in fp32, or in 8 bits (uint8 or torch.float8_e4m3fn) with scales
+    [ceil(n / 256), 2] uint8."""
+
+    def __init__(self, rows):
+        self.rows = [dict(r) for r in rows]
+        self.array = (MoeAdamWTensor * max(1, len(self.rows)))()
+        self.n = len(self.rows)
+        for i, r in enumerate(self.rows):
+            self.array[i] = self._entry(r)
+
+    @staticmethod
+    def _entry(r):
+        p, n = r["param"], r["param"].numel()
+        eight = r["m"].element_size() == 1
+        state = (torch.uint8, torch.float8_e4m3fn) if eight else (torch.float32,)
+        for name in ("grad", "m", "v", "master"):
+            if r.get(name) is not None and r[name].numel() != n:
+                raise ValueError("%s must have as many values as param" % name)
+        for name in ("m", "v"):
+            if r[name].dtype not in state:
+                raise ValueError("%s must be fp32, uint8 or float8_e4m3fn (both alike)" % name)
+        sc = r.get("scales")
+        if eight != (sc is not None):
+            raise ValueError("scales go with 8-bit states")
+        if eight and sc.shape != (-(-n // MOE_ADAMW_BLOCK), 2):
+            raise ValueError("scales must have shape %s" % ((-(-n // MOE_ADAMW_BLOCK), 2),))
+        return MoeAdamWTensor(
+            _ptr(p, name="param"), _f32(r.get("master"), "master"), _ptr(r["grad"], name="grad"),
+            _ptr(r["m"], name="m"), _ptr(r["v"], name="v"), _ptr(sc, torch.uint8, "scales"), n,
+            _type(p, "param"), _type(r["grad"], "grad"), 8 if eight else 32,
+            float(r.get("lr_mult", 1.0)), float(r.get("weight_decay", 0.0)))
+
+    def set_grads(self, grads):
+        """Other gradient tensors, in the order of the rows."""
+        grads = list(grads)
+        if len(grads) != self.n:
+            raise ValueError("%d gradients for %d tensors" % (len(grads), self.n))
+        for i, g in enumerate(grads):
+            r = dict(self.rows[i], grad=g)
+            self.array[i], self.rows[i] = self._entry(r), r
+
+
+def moe_adamw_workspace_size(table: AdamWTable) -> int:
+    return int(load().moe_adamw_workspace_size(table.array, table.n))
+
+
+def moe_adamw_step(table: AdamWTable, step, lr, betas=(0.9, 0.999), eps=1e-8, grad_scale=1.0,
+                   max_norm=0.0, skip_nonfinite=False, grad_norm=None, ws=None, stream=None):
+    """One AdamW step (step counts from 1) over the table's tensors, in place.
+    max_norm > 0 clips by the global gradient norm, which grad_norm [1] fp32
+    receives; ws is needed for the norm only."""
+    h = MoeAdamWHyper(lr, betas[0], betas[1], eps, step, grad_scale, max_norm,
+                      1 if skip_nonfinite else 0)
+    _check(load().moe_adamw_step(
+        table.array, table.n, ctypes.byref(h), _shaped(grad_norm, (1,), torch.float32, "grad_norm"),
+        _ptr(ws, name="ws"), 0 if ws is None else ws.numel() * ws.element_size(),
+        _stream(stream)), "moe_adamw_step")
 
 
 def moe_status(stream=None) -> int:

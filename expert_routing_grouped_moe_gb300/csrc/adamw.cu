@@ -1,0 +1,524 @@
+// One AdamW step over many tensors at once, moments in 32 bits or in 8, with
+// the clip by the global gradient norm.
+//   g = c grad,  c = grad_scale min(1, max_norm / (norm + 1e-6)),  norm = |grad_scale grad|_2
+//   m = b1 m + (1 - b1) g,  v = b2 v + ((1 - b2) g) g,  root = sqrt(v)
+//   p = p (1 - lr wd) - lr/(1 - b1^t) (m / (root / sqrt(1 - b2^t) + eps))
+// in fp32, each operation rounded by itself (no contraction), so that the
+// results do not depend on how a launch is cut.
+//
+// 8-bit moments: m and root are held as e4m3 values (1-4-3 bits, largest 448,
+// subnormals down to 2^-9) times a power-of-two scale shared by a block of 256
+// consecutive values, its exponent held as E8M0 byte: the block's largest
+// value lands in [128, 256).  root rather than v, since v's exponents span
+// twice as many bits.  Values are rounded down to the grid after adding
+// u 2^-20 of a grid step, u the top 20 bits of i I + t T mod 2^32 (i the
+// value's index in its tensor, t the step, T and I odd, the fractional parts
+// of the golden ratio and of the square root of 2): over the steps the
+// thresholds of a value are spread evenly, so an update far below a grid step
+// (v moves by 0.1 % a step, the grid is 6-12 % apart) passes in its due share
+// of the steps, where rounding to nearest would lose it every time.  A root
+// above zero is kept above zero (it divides).
+//
+// The sum of squares is kept as a pair of floats (the rounding errors of each
+// product and each sum in the second), about 46 significant bits: the norm,
+// rounded to fp32, does not depend on the order either, to all purposes.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cuda_fp8.h>
+
+#include "../../include/moe_gb300.h"
+#include "internal.h"
+#include "rowvec.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBlock = MOE_ADAMW_BLOCK;        // values per scale: 8 for each lane of a warp
+constexpr int kThreads = 256;
+constexpr int kChunk = kThreads * 8;           // values of one pass of a block of threads
+constexpr int kNormBlocks = 4 * kSMs;          // rows of partial sums per norm launch
+constexpr uint32_t kDitherT = 2654435769u, kDitherI = 1779033703u;
+
+struct Tensor {
+  void* p;
+  float* master;
+  const void* g;
+  void* m;
+  void* v;
+  uint8_t* sc;
+  int64_t n;
+  float keep, lr;  // 1 - lr wd; lr / (1 - b1^t)
+  int chunk0;      // first chunk of the tensor in this launch
+  int vec;         // all pointers allow 8-value vectors
+};
+struct Consts {
+  float b1, c1, b2, c2, correct, eps, grad_scale, max_norm;
+  uint32_t dither;       // t T
+  const double* part;    // partial sums of squares, NULL: not needed
+  int nparts, skip;
+  float* norm_out;
+};
+// Tables travel as kernel arguments (constant memory, no copy, no lifetime):
+// a small one for the usual few tensors, a large one within the 32 KB limit.
+constexpr int kFew = 24, kMany = 400;
+template <int MAX>
+struct Table {
+  Consts c;
+  int n, chunks;
+  Tensor t[MAX];
+};
+struct NormTensor {
+  const void* g;
+  int64_t n;
+  int chunk0, bf16;
+};
+constexpr int kNormFew = 64, kNormMany = 1200;
+template <int MAX>
+struct NormTable {
+  int n, chunks;
+  double* part;
+  NormTensor t[MAX];
+};
+
+// Eight values from index i on (those past n read as 0 / are not written).
+template <typename T>
+__device__ __forceinline__ void get8(const T* p, int64_t i, int64_t n, bool vec, float (&f)[8]) {
+  Raw8<T> r;
+  if (vec) {
+    load8<true>(p + i, 0, 8, r);
+    widen(r, f);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      f[e] = 0.f;
+      if (i + e < n) {
+        if constexpr (sizeof(T) == 2)
+          f[e] = __uint_as_float(static_cast<uint32_t>(p[i + e].bits) << 16);
+        else
+          f[e] = p[i + e];
+      }
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void set8(T* p, int64_t i, int64_t n, bool vec, const float (&f)[8]) {
+  Raw8<T> r;
+  narrow(f, r);
+  if (vec) {
+    store8<true>(p + i, 0, 8, r);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (i + e < n) {
+        if constexpr (sizeof(T) == 2) {
+          const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+          p[i + e].bits = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+        } else {
+          p[i + e] = f[e];
+        }
+      }
+  }
+}
+// Eight code bytes.
+__device__ __forceinline__ uint2 get_codes(const uint8_t* p, int64_t i, int64_t n, bool vec) {
+  if (vec) return *reinterpret_cast<const uint2*>(p + i);
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (i + e < n) w[e >> 2] |= static_cast<uint32_t>(p[i + e]) << (8 * (e & 3));
+  return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void set_codes(uint8_t* p, int64_t i, int64_t n, bool vec, uint2 q) {
+  if (vec) {
+    *reinterpret_cast<uint2*>(p + i) = q;
+    return;
+  }
+  const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (i + e < n) p[i + e] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
+}
+__device__ __forceinline__ void decode8(uint2 q, float scale, float (&f)[8]) {
+  const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
+        static_cast<__nv_fp8x2_storage_t>(w[h >> 1] >> (16 * (h & 1))), __NV_E4M3);
+    const float2 x = __half22float2(__half2(hr));
+    f[2 * h] = x.x * scale;
+    f[2 * h + 1] = x.y * scale;
+  }
+}
+// E8M0 byte of a block whose largest magnitude has the bits `top`.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
+  const int b = static_cast<int>(top >> 23) - 7;
+  return b < 8 ? 8u : static_cast<uint32_t>(b);
+}
+// e4m3 magnitude of x >= 0 under the scale byte b; d: 20 dither bits.  Normal
+// values: exponent and top three mantissa bits, rebased.  Below the smallest
+// normal value (2^-6 scale), adding that value makes the grid linear.
+__device__ __forceinline__ uint32_t encode(float x, uint32_t d, uint32_t b) {
+  const float low = __uint_as_float((b - 6u) << 23);
+  const bool below = x < low;
+  const uint32_t bits = __float_as_uint(below ? __fadd_rn(x, low) : x);
+  return ((bits + d) >> 20) - ((b - 7u) << 3) - (below ? 8u : 0u);
+}
+
+template <typename PT, typename GT, bool MASTER, bool EIGHT, int MAX>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<MAX> tab) {
+  const Consts& c = tab.c;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float coef = c.grad_scale;
+  pdl_wait();
+  if (c.part != nullptr) {  // the norm: every block adds the same partials in the same order
+    __shared__ double s_sum[kThreads / 32];
+    double s = 0.0;
+    for (int i = threadIdx.x; i < c.nparts; i += kThreads) s += c.part[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) s_sum[warp] = s;
+    __syncthreads();
+    s = 0.0;
+    for (int i = 0; i < kThreads / 32; ++i) s += s_sum[i];
+    const float norm = __fmul_rn(static_cast<float>(sqrt(s)), fabsf(c.grad_scale));
+    if (c.norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *c.norm_out = norm;
+    if (c.skip && !(norm <= 3.402823466e38f)) return;  // Inf or NaN: nothing changes
+    if (c.max_norm > 0.f) {
+      const float q = __fdiv_rn(c.max_norm, __fadd_rn(norm, 1e-6f));
+      coef = __fmul_rn(coef, q >= 1.f ? 1.f : q);  // a NaN norm stays NaN
+    }
+  }
+  int ti = 0;
+  for (int ch = blockIdx.x; ch < tab.chunks; ch += gridDim.x) {
+    while (ti + 1 < tab.n && ch >= tab.t[ti + 1].chunk0) ++ti;
+    const Tensor& t = tab.t[ti];
+    const int64_t n = t.n;
+    const int64_t i = static_cast<int64_t>(ch - t.chunk0) * kChunk + threadIdx.x * 8;
+    const bool vec = t.vec && i + 8 <= n;
+    float p[8], g[8], m[8], v[8], root[8];
+    get8(static_cast<const GT*>(t.g), i, n, vec, g);
+    if (MASTER) get8(t.master, i, n, vec, p);
+    else get8(static_cast<const PT*>(t.p), i, n, vec, p);
+    const int64_t blk = i / kBlock;  // the same for the whole warp
+    if constexpr (EIGHT) {
+      uint32_t bm = 0, bv = 0;
+      if (blk * kBlock < n) {
+        bm = t.sc[2 * blk];
+        bv = t.sc[2 * blk + 1];
+      }
+      const uint2 qm = get_codes(static_cast<const uint8_t*>(t.m), i, n, vec);
+      const uint2 qv = get_codes(static_cast<const uint8_t*>(t.v), i, n, vec);
+      decode8(qm, __uint_as_float(bm << 23), m);
+      decode8(qv, __uint_as_float(bv << 23), v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], v[e]);
+    } else {
+      get8(static_cast<const float*>(t.m), i, n, vec, m);
+      get8(static_cast<const float*>(t.v), i, n, vec, v);
+    }
+    uint32_t top_m = 0, top_r = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      g[e] = __fmul_rn(g[e], coef);
+      m[e] = __fadd_rn(__fmul_rn(c.b1, m[e]), __fmul_rn(c.c1, g[e]));
+      v[e] = __fadd_rn(__fmul_rn(c.b2, v[e]), __fmul_rn(__fmul_rn(c.c2, g[e]), g[e]));
+      root[e] = __fsqrt_rn(v[e]);
+      const float upd = __fdiv_rn(m[e], __fadd_rn(__fmul_rn(root[e], c.correct), c.eps));
+      p[e] = __fsub_rn(__fmul_rn(p[e], t.keep), __fmul_rn(t.lr, upd));
+      if (EIGHT && i + e < n) {
+        top_m = max(top_m, __float_as_uint(m[e]) & 0x7FFFFFFFu);
+        top_r = max(top_r, __float_as_uint(root[e]) & 0x7FFFFFFFu);
+      }
+    }
+    if constexpr (EIGHT) {
+      const uint32_t bm = scale_byte(__reduce_max_sync(0xffffffffu, top_m));
+      const uint32_t bv = scale_byte(__reduce_max_sync(0xffffffffu, top_r));
+      uint32_t u = static_cast<uint32_t>(i) * kDitherI + c.dither;
+      uint32_t wm[2] = {0, 0}, wr[2] = {0, 0};
+#pragma unroll
+      for (int e = 0; e < 8; ++e, u += kDitherI) {
+        uint32_t q = encode(fabsf(m[e]), u >> 12, bm);
+        q |= m[e] < 0.f ? 128u : 0u;
+        wm[e >> 2] |= q << (8 * (e & 3));
+        q = encode(fabsf(root[e]), ~u >> 12, bv);
+        if (q < 1u && root[e] > 0.f) q = 1u;
+        wr[e >> 2] |= q << (8 * (e & 3));
+      }
+      set_codes(static_cast<uint8_t*>(t.m), i, n, vec, make_uint2(wm[0], wm[1]));
+      set_codes(static_cast<uint8_t*>(t.v), i, n, vec, make_uint2(wr[0], wr[1]));
+      if (lane == 0 && i < n) {
+        t.sc[2 * blk] = static_cast<uint8_t>(bm);
+        t.sc[2 * blk + 1] = static_cast<uint8_t>(bv);
+      }
+    } else {
+      set8(static_cast<float*>(t.m), i, n, vec, m);
+      set8(static_cast<float*>(t.v), i, n, vec, v);
+    }
+    set8(static_cast<PT*>(t.p), i, n, vec, p);
+    if (MASTER) set8(t.master, i, n, vec, p);
+  }
+}
+
+__device__ __forceinline__ void add_square(float x, float& hi, float& lo) {
+  const float p = __fmul_rn(x, x);
+  const float e = __fmaf_rn(x, x, -p);
+  const float s = __fadd_rn(hi, p);
+  const float b = __fsub_rn(s, hi);
+  const float err = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(p, b));
+  hi = s;
+  lo = __fadd_rn(lo, __fadd_rn(err, e));
+}
+
+template <int MAX>
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ NormTable<MAX> tab) {
+  __shared__ double s_sum[kThreads / 32];
+  pdl_wait();
+  float hi = 0.f, lo = 0.f;
+  int ti = 0;
+  for (int ch = blockIdx.x; ch < tab.chunks; ch += gridDim.x) {
+    while (ti + 1 < tab.n && ch >= tab.t[ti + 1].chunk0) ++ti;
+    const NormTensor& t = tab.t[ti];
+    const int64_t i = static_cast<int64_t>(ch - t.chunk0) * kChunk + threadIdx.x * 8;
+    const bool vec = (reinterpret_cast<uintptr_t>(t.g) & 15u) == 0 && i + 8 <= t.n;
+    float g[8];
+    if (t.bf16) get8(static_cast<const bf16_t*>(t.g), i, t.n, vec, g);
+    else get8(static_cast<const float*>(t.g), i, t.n, vec, g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) add_square(g[e], hi, lo);
+  }
+  double s = static_cast<double>(hi) + static_cast<double>(lo);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < kThreads / 32; ++i) s += s_sum[i];
+    tab.part[blockIdx.x] = s;
+  }
+}
+
+int64_t chunks_of(int64_t n) { return (n + kChunk - 1) / kChunk; }
+
+template <typename PT, typename GT, bool MASTER, bool EIGHT, int MAX>
+cudaError_t launch(const Table<MAX>& tab, cudaStream_t s) {
+  static const int per = [] {
+    int b = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+        &b, adamw_kernel<PT, GT, MASTER, EIGHT, MAX>, kThreads, 0);
+    return e == cudaSuccess && b > 0 ? b : 1;
+  }();
+  const int blocks = std::min(tab.chunks, per * kSMs);
+  return launch_pdl(adamw_kernel<PT, GT, MASTER, EIGHT, MAX>, dim3(blocks), dim3(kThreads), 0, s, tab);
+}
+
+int kind_of(const moe_adamw_tensor& t) {
+  const int p = t.param_type == MOE_F32 ? 0 : t.master == nullptr ? 1 : 2;
+  return (p * 2 + (t.grad_type == MOE_BF16 ? 1 : 0)) * 2 + (t.state_bits == 8 ? 1 : 0);
+}
+constexpr int kKinds = 12;
+
+template <int MAX>
+cudaError_t launch_kind(int kind, const Table<MAX>& tab, cudaStream_t s) {
+  switch (kind) {
+    case 0: return launch<float, float, false, false>(tab, s);
+    case 1: return launch<float, float, false, true>(tab, s);
+    case 2: return launch<float, bf16_t, false, false>(tab, s);
+    case 3: return launch<float, bf16_t, false, true>(tab, s);
+    case 4: return launch<bf16_t, float, false, false>(tab, s);
+    case 5: return launch<bf16_t, float, false, true>(tab, s);
+    case 6: return launch<bf16_t, bf16_t, false, false>(tab, s);
+    case 7: return launch<bf16_t, bf16_t, false, true>(tab, s);
+    case 8: return launch<bf16_t, float, true, false>(tab, s);
+    case 9: return launch<bf16_t, float, true, true>(tab, s);
+    case 10: return launch<bf16_t, bf16_t, true, false>(tab, s);
+    default: return launch<bf16_t, bf16_t, true, true>(tab, s);
+  }
+}
+
+// All tensors of one kind, up to MAX in a launch.
+template <int MAX>
+cudaError_t step_kind(int kind, const moe_adamw_tensor* ts, int n, const moe_adamw_hyper* h,
+                      Consts& c, cudaStream_t s) {
+  Table<MAX> tab;
+  tab.c = c;
+  tab.n = tab.chunks = 0;
+  const double b1t = 1.0 - std::pow(h->beta1, static_cast<double>(h->step));
+  auto flush = [&]() -> cudaError_t {
+    if (tab.n == 0) return cudaSuccess;
+    tab.c = c;
+    const cudaError_t e = launch_kind<MAX>(kind, tab, s);
+    c.norm_out = nullptr;  // written once
+    tab.n = tab.chunks = 0;
+    return e;
+  };
+  for (int i = 0; i < n; ++i) {
+    const moe_adamw_tensor& q = ts[i];
+    if (q.n == 0 || kind_of(q) != kind) continue;
+    const int64_t ch = chunks_of(q.n);
+    if (tab.n == MAX || tab.chunks + ch > (int64_t(1) << 30)) {
+      const cudaError_t e = flush();
+      if (e != cudaSuccess) return e;
+    }
+    Tensor& t = tab.t[tab.n++];
+    t.p = q.param; t.master = q.master; t.g = q.grad; t.m = q.m; t.v = q.v; t.sc = q.scales;
+    t.n = q.n;
+    const double lr = h->lr * static_cast<double>(q.lr_mult);
+    t.keep = static_cast<float>(1.0 - lr * static_cast<double>(q.weight_decay));
+    t.lr = static_cast<float>(lr / b1t);
+    t.chunk0 = tab.chunks;
+    const uintptr_t wide = reinterpret_cast<uintptr_t>(q.param) | reinterpret_cast<uintptr_t>(q.master) |
+                           reinterpret_cast<uintptr_t>(q.grad);
+    const uintptr_t st = reinterpret_cast<uintptr_t>(q.m) | reinterpret_cast<uintptr_t>(q.v);
+    t.vec = (wide & 15u) == 0 && (st & (q.state_bits == 8 ? 7u : 15u)) == 0;
+    tab.chunks += static_cast<int>(ch);
+  }
+  return flush();
+}
+
+template <int MAX>
+cudaError_t norm_all(const moe_adamw_tensor* ts, int n, double* part, int* nparts, cudaStream_t s) {
+  NormTable<MAX> tab;
+  tab.n = tab.chunks = 0;
+  *nparts = 0;
+  auto flush = [&]() -> cudaError_t {
+    if (tab.n == 0) return cudaSuccess;
+    tab.part = part + *nparts;
+    const int blocks = std::min(tab.chunks, kNormBlocks);
+    *nparts += blocks;
+    const cudaError_t e = launch_pdl(grad_norm_kernel<MAX>, dim3(blocks), dim3(kThreads), 0, s, tab);
+    tab.n = tab.chunks = 0;
+    return e;
+  };
+  for (int i = 0; i < n; ++i) {
+    if (ts[i].n == 0) continue;
+    const int64_t ch = chunks_of(ts[i].n);
+    if (tab.n == MAX || tab.chunks + ch > (int64_t(1) << 30)) {
+      const cudaError_t e = flush();
+      if (e != cudaSuccess) return e;
+    }
+    tab.t[tab.n++] = NormTensor{ts[i].grad, ts[i].n, tab.chunks, ts[i].grad_type == MOE_BF16 ? 1 : 0};
+    tab.chunks += static_cast<int>(ch);
+  }
+  return flush();
+}
+
+int bad(const char* msg) { return record_error(MOE_ERR_INVALID_ARG, msg); }
+
+// Rows of partial sums: at most kNormBlocks for each norm launch.
+size_t norm_rows(const moe_adamw_tensor* ts, int n) {
+  int64_t launches = 1, in_launch = 0, chunks = 0;
+  for (int i = 0; i < n; ++i) {
+    if (ts[i].n <= 0) continue;
+    const int64_t ch = chunks_of(ts[i].n);
+    const int most = n <= kNormFew ? kNormFew : kNormMany;
+    if (in_launch == most || chunks + ch > (int64_t(1) << 30)) {
+      ++launches;
+      in_launch = chunks = 0;
+    }
+    ++in_launch;
+    chunks += ch;
+  }
+  return static_cast<size_t>(launches) * kNormBlocks;
+}
+
+int check_tensor(const moe_adamw_tensor& t) {
+  if (t.n < 0 || t.n > (int64_t(1) << 40)) return bad("a tensor's n is negative or above 2^40");
+  if (t.param_type != MOE_F32 && t.param_type != MOE_BF16) return bad("param_type must be MOE_F32 or MOE_BF16");
+  if (t.grad_type != MOE_F32 && t.grad_type != MOE_BF16) return bad("grad_type must be MOE_F32 or MOE_BF16");
+  if (t.state_bits != 8 && t.state_bits != 32) return bad("state_bits must be 8 or 32");
+  if (t.param_type == MOE_F32 && t.master != nullptr) return bad("an fp32 parameter has no master copy");
+  if (!std::isfinite(t.weight_decay) || !std::isfinite(t.lr_mult) || t.weight_decay < 0.f || t.lr_mult < 0.f)
+    return bad("weight_decay and lr_mult must be finite and not negative");
+  if (t.n == 0) return MOE_OK;
+  if (!t.param || !t.grad || !t.m || !t.v) return bad("NULL pointer in a tensor");
+  if ((t.state_bits == 8) != (t.scales != nullptr)) return bad("scales go with 8-bit states");
+  auto off = [](const void* p, unsigned size) { return (reinterpret_cast<uintptr_t>(p) & (size - 1)) != 0; };
+  const unsigned ss = t.state_bits == 8 ? 1 : 4;
+  if (off(t.param, t.param_type == MOE_BF16 ? 2 : 4) || off(t.grad, t.grad_type == MOE_BF16 ? 2 : 4) ||
+      off(t.master, 4) || off(t.m, ss) || off(t.v, ss))
+    return bad("misaligned pointer in a tensor");
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_adamw_workspace_size(const moe_adamw_tensor* tensors, int32_t n) {
+  if (n < 0 || (n > 0 && tensors == nullptr)) return 0;
+  return norm_rows(tensors, n) * sizeof(double);
+}
+
+int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n, const moe_adamw_hyper* hyper,
+                   float* grad_norm, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  NvtxScope nvtx("moe_adamw_step");
+  if (n < 0 || (n > 0 && tensors == nullptr)) return bad("tensors is NULL or n negative");
+  const moe_adamw_hyper* h = hyper;
+  if (h == nullptr) return bad("hyper is NULL");
+  if (!(h->lr >= 0.0) || !std::isfinite(h->lr)) return bad("lr must be finite and not negative");
+  if (!(h->beta1 >= 0.0 && h->beta1 < 1.0) || !(h->beta2 >= 0.0 && h->beta2 < 1.0))
+    return bad("betas must be in [0, 1)");
+  if (!(h->eps > 0.0) || !std::isfinite(h->eps)) return bad("eps must be positive");
+  if (!(h->max_norm >= 0.f) || !std::isfinite(h->max_norm)) return bad("max_norm must be finite and not negative");
+  if (!std::isfinite(h->grad_scale)) return bad("grad_scale must be finite");
+  if (h->step < 1) return bad("step counts from 1");
+  if (h->skip_nonfinite != 0 && h->skip_nonfinite != 1) return bad("skip_nonfinite must be 0 or 1");
+  bool work[kKinds] = {};
+  int count[kKinds] = {};
+  bool any = false;
+  for (int i = 0; i < n; ++i) {
+    const int rc = check_tensor(tensors[i]);
+    if (rc) return rc;
+    if (tensors[i].n == 0) continue;
+    const int k = kind_of(tensors[i]);
+    work[k] = any = true;
+    ++count[k];
+  }
+  const bool need_norm = h->max_norm > 0.f || grad_norm != nullptr || h->skip_nonfinite;
+  if (need_norm) {
+    if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 15u)) return bad("ws NULL or misaligned");
+    if (ws_bytes < moe_adamw_workspace_size(tensors, n))
+      return record_error(MOE_ERR_WORKSPACE, "AdamW workspace too small");
+    if (reinterpret_cast<uintptr_t>(grad_norm) & 3u) return bad("grad_norm misaligned");
+  }
+  if (!any) {
+    if (grad_norm != nullptr) {
+      const cudaError_t e = cudaMemsetAsync(grad_norm, 0, sizeof(float), stream);
+      if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
+    }
+    return record_error(MOE_OK, "");
+  }
+  Consts c = {};
+  c.b1 = static_cast<float>(h->beta1);
+  c.c1 = static_cast<float>(1.0 - h->beta1);
+  c.b2 = static_cast<float>(h->beta2);
+  c.c2 = static_cast<float>(1.0 - h->beta2);
+  c.correct = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(h->beta2, static_cast<double>(h->step))));
+  c.eps = static_cast<float>(h->eps);
+  c.grad_scale = h->grad_scale;
+  c.max_norm = h->max_norm;
+  c.dither = static_cast<uint32_t>(h->step) * kDitherT;
+  c.skip = h->skip_nonfinite;
+  c.norm_out = grad_norm;
+  cudaError_t e = cudaSuccess;
+  if (need_norm) {
+    c.part = static_cast<const double*>(ws);
+    ProbeScope probe("grad_norm", stream);
+    e = n <= kNormFew ? norm_all<kNormFew>(tensors, n, static_cast<double*>(ws), &c.nparts, stream)
+                      : norm_all<kNormMany>(tensors, n, static_cast<double*>(ws), &c.nparts, stream);
+  }
+  ProbeScope probe("adamw", stream);
+  for (int k = 0; k < kKinds && e == cudaSuccess; ++k) {
+    if (!work[k]) continue;
+    e = count[k] <= kFew ? step_kind<kFew>(k, tensors, n, h, c, stream)
+                         : step_kind<kMany>(k, tensors, n, h, c, stream);
+  }
+  if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
+  return record_error(MOE_OK, "");
+}
+
+}  // extern "C"

@@ -1,0 +1,171 @@
+// C ABI of the norms around a block: argument checks and launches.
+#include <cmath>
+
+#include "norm.cuh"
+
+namespace moe {
+namespace {
+
+// Blocks of the backward, which also bound the rows of partial column sums: two
+// for each SM (a block holds up to 512 threads, two fill an SM's registers).
+constexpr int kNormBwdBlocks = 2 * kSMs;
+
+int bwd_blocks(int64_t T, int d) {
+  const int64_t g = norm_groups(d), need = (T + g - 1) / g;
+  return static_cast<int>(need < kNormBwdBlocks ? need : kNormBwdBlocks);
+}
+
+int bad(const char* msg) { return record_error(MOE_ERR_INVALID_ARG, msg); }
+
+// Type-dependent alignment every pointer must have, and 16 bytes for the
+// vector path: vec is cleared where a pointer or d does not allow it.
+bool aligned(const void* p, size_t size, bool& vec) {
+  const uintptr_t u = reinterpret_cast<uintptr_t>(p);
+  if (u & 15u) vec = false;
+  return (u & (size - 1)) == 0;
+}
+
+int check_desc(const moe_norm_desc* q) {
+  if (q == nullptr) return bad("desc is NULL");
+  if (q->T < 0 || q->d <= 0) return bad("T must not be negative, d must be positive");
+  if (q->d > kNormMaxD) return record_error(MOE_ERR_UNSUPPORTED, "d > MOE_NORM_MAX_D");
+  if ((q->x_type != MOE_F32 && q->x_type != MOE_BF16) ||
+      (q->y_type != MOE_F32 && q->y_type != MOE_BF16))
+    return bad("x_type and y_type must be MOE_F32 or MOE_BF16");
+  if (q->x_type == MOE_BF16 && q->y_type == MOE_F32)
+    return record_error(MOE_ERR_UNSUPPORTED, "a bf16 residual stream needs a bf16 block output");
+  if (q->gate < MOE_GATE_NONE || q->gate > MOE_GATE_ELEMENT) return bad("bad gate kind");
+  if (q->gate_sigmoid != 0 && q->gate_sigmoid != 1) return bad("gate_sigmoid must be 0 or 1");
+  if (!(q->eps > 0.f) || !std::isfinite(q->eps)) return bad("eps must be positive");
+  if (!std::isfinite(q->scale) || !std::isfinite(q->w_offset))
+    return bad("scale and w_offset must be finite");
+  return MOE_OK;
+}
+
+size_t size_of(int type) { return type == MOE_BF16 ? 2 : 4; }
+
+// wide: cleared where p does not allow 16-byte vectors (values read one by one,
+// such as [T] vectors, have a flag of their own that nothing reads)
+#define NORM_PTR(p, size, wide)                                   \
+  do {                                                            \
+    if ((p) == nullptr) return bad(#p " is NULL");                \
+    if (!aligned(p, size, wide)) return bad(#p " is misaligned"); \
+  } while (0)
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_block_norm_fwd(const moe_norm_desc* desc, const void* x, const void* y, const void* gate,
+                       const float* w_post, const float* w_pre, void* r, void* n, float* rstd_y,
+                       float* rstd_r, moe_stream_t stream) {
+  NvtxScope nvtx("moe_block_norm_fwd");
+  int rc = check_desc(desc);
+  if (rc) return rc;
+  if (desc->T == 0) return record_error(MOE_OK, "");
+  const size_t xs = size_of(desc->x_type), ys = size_of(desc->y_type);
+  bool vec = desc->d % 8 == 0, per_row = true;
+  if (x == nullptr && y == nullptr) return bad("x and y are both NULL");
+  if (y == nullptr && (r != nullptr || w_post != nullptr || desc->gate != MOE_GATE_NONE))
+    return bad("r, w_post and a gate go with y");
+  if (y == nullptr && w_pre == nullptr) return bad("nothing to compute: no y and no w_pre");
+  if ((w_pre == nullptr) != (n == nullptr)) return bad("w_pre and n go together");
+  if ((gate == nullptr) != (desc->gate == MOE_GATE_NONE)) return bad("gate and its kind go together");
+  if (x) NORM_PTR(x, xs, vec);
+  if (y) { NORM_PTR(y, ys, vec); NORM_PTR(r, xs, vec); }
+  if (desc->gate == MOE_GATE_TOKEN) NORM_PTR(gate, 4, per_row);
+  else if (gate) NORM_PTR(gate, (desc->gate == MOE_GATE_ELEMENT ? ys : 4), vec);
+  if (w_post) { NORM_PTR(w_post, 4, vec); NORM_PTR(rstd_y, 4, per_row); }
+  if (w_pre) { NORM_PTR(w_pre, 4, vec); NORM_PTR(n, ys, vec); NORM_PTR(rstd_r, 4, per_row); }
+  NormArgs a = {};
+  a.x = x; a.y = y; a.gate = gate; a.w_post = w_post; a.w_pre = w_pre;
+  a.r = r; a.n = n; a.rstd_y = rstd_y; a.rstd_r = rstd_r;
+  a.T = desc->T; a.d = desc->d; a.W = norm_warps(desc->d);
+  a.gate_kind = desc->gate; a.sigmoid = desc->gate_sigmoid;
+  a.scale = desc->scale; a.eps = desc->eps; a.w_off = desc->w_offset;
+  ProbeScope probe("block_norm_fwd", stream);
+  const cudaError_t e = launch_norm_fwd(a, desc->x_type, desc->y_type, vec, stream);
+  if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
+  return record_error(MOE_OK, "");
+}
+
+size_t moe_block_norm_workspace_size(int32_t T, int32_t d) {
+  if (T < 0 || d <= 0 || d > kNormMaxD) return 0;
+  const size_t rows = static_cast<size_t>(bwd_blocks(T, d)) * norm_groups(d);
+  return rows * 3 * static_cast<size_t>(d) * 4;
+}
+
+int moe_block_norm_bwd(const moe_norm_desc* desc, const void* dr, const void* dn, const void* r,
+                       const void* y, const void* gate, const float* w_post, const float* w_pre,
+                       const float* rstd_y, const float* rstd_r, void* dx, void* dy, void* dgate,
+                       float* dw_post, float* dw_pre, void* ws, size_t ws_bytes,
+                       moe_stream_t stream) {
+  NvtxScope nvtx("moe_block_norm_bwd");
+  int rc = check_desc(desc);
+  if (rc) return rc;
+  // sums over the tokens, the only outputs that T = 0 has
+  float* sums[3] = {nullptr, nullptr, nullptr};
+  NormArgs a = {};
+  a.sum_post = a.sum_pre = a.sum_gate = -1;
+  if (dw_post) { a.sum_post = a.nsum; sums[a.nsum++] = dw_post; }
+  if (dw_pre) { a.sum_pre = a.nsum; sums[a.nsum++] = dw_pre; }
+  if (dgate && desc->gate == MOE_GATE_CHANNEL) {
+    a.sum_gate = a.nsum;
+    sums[a.nsum++] = static_cast<float*>(dgate);
+  }
+  for (int i = 0; i < a.nsum; ++i)
+    if (reinterpret_cast<uintptr_t>(sums[i]) & 3u) return bad("a sum over the tokens is misaligned");
+  a.T = desc->T; a.d = desc->d; a.W = norm_warps(desc->d);
+  const int blocks = bwd_blocks(desc->T, desc->d);
+  if (desc->T == 0) {
+    const cudaError_t e = launch_norm_bwd(a, desc->x_type, desc->y_type, false, 0, sums, stream);
+    if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
+    return record_error(MOE_OK, "");
+  }
+  const size_t xs = size_of(desc->x_type), ys = size_of(desc->y_type);
+  bool vec = desc->d % 8 == 0, per_row = true;
+  if (dr == nullptr && dn == nullptr) return bad("dr and dn are both NULL");
+  if ((w_pre == nullptr) != (dn == nullptr)) return bad("w_pre and dn go together");
+  if (y == nullptr && (w_post != nullptr || dy != nullptr || desc->gate != MOE_GATE_NONE))
+    return bad("w_post, dy and a gate go with y");
+  if ((gate == nullptr) != (desc->gate == MOE_GATE_NONE)) return bad("gate and its kind go together");
+  if ((dgate && !gate) || (dw_post && !w_post) || (dw_pre && !w_pre))
+    return bad("the gradient of an input that is not there");
+  if (dx == nullptr && dy == nullptr && dgate == nullptr && dw_post == nullptr && dw_pre == nullptr)
+    return bad("nothing to compute");
+  if (dr) NORM_PTR(dr, xs, vec);
+  if (dn) {
+    NORM_PTR(dn, ys, vec); NORM_PTR(r, xs, vec); NORM_PTR(w_pre, 4, vec);
+    NORM_PTR(rstd_r, 4, per_row);
+  }
+  if (y) NORM_PTR(y, ys, vec);
+  if (w_post) { NORM_PTR(w_post, 4, vec); NORM_PTR(rstd_y, 4, per_row); }
+  if (desc->gate == MOE_GATE_TOKEN) NORM_PTR(gate, 4, per_row);
+  else if (gate) NORM_PTR(gate, (desc->gate == MOE_GATE_ELEMENT ? ys : 4), vec);
+  if (dx) NORM_PTR(dx, xs, vec);
+  if (dy) NORM_PTR(dy, ys, vec);
+  if (dgate && desc->gate == MOE_GATE_TOKEN) NORM_PTR(dgate, 4, per_row);
+  if (dgate && desc->gate == MOE_GATE_ELEMENT) NORM_PTR(dgate, ys, vec);
+  if (a.nsum > 0) {
+    if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 15u)) return bad("ws NULL or misaligned");
+    if (ws_bytes < moe_block_norm_workspace_size(desc->T, desc->d))
+      return record_error(MOE_ERR_WORKSPACE, "norm workspace too small");
+  }
+  a.x = dr; a.y = y; a.gate = gate; a.w_post = w_post; a.w_pre = w_pre;
+  a.r = const_cast<void*>(r); a.n = const_cast<void*>(dn);
+  a.rstd_y = const_cast<float*>(rstd_y); a.rstd_r = const_cast<float*>(rstd_r);
+  a.dx = dx; a.dy = dy; a.dgate = dgate;
+  a.part = static_cast<float*>(ws);
+  a.gate_kind = desc->gate; a.sigmoid = desc->gate_sigmoid;
+  a.scale = desc->scale; a.eps = desc->eps; a.w_off = desc->w_offset;
+  ProbeScope probe("block_norm_bwd", stream);
+  const cudaError_t e =
+      launch_norm_bwd(a, desc->x_type, desc->y_type, vec, blocks, sums, stream);
+  if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
+  return record_error(MOE_OK, "");
+}
+
+}  // extern "C"

@@ -1,0 +1,397 @@
+// The router's two losses and the gradient of its logits.
+//   P = softmax(l),  lse = log sum_e exp l,  f_e = counts_e / (T k)
+//   aux = E sum_e f_e mean_t P_te            z = mean_t lse_t^2
+//   dl_te = c_aux E/T P_te (f_e - sum_e' f_e' P_te') + 2 c_z/T lse_t P_te
+//         + sum_{j: ids_tj = e} w_tj (dw_tj - sum_i w_ti dw_ti)
+// A row is held by LPR lanes (a power of two), NV vectors of 4 logits each.  A
+// row whose logits are all -inf has P = 0, adds nothing to either loss and
+// gets a zero gradient; its lse is -inf.
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/moe_gb300.h"
+#include "internal.h"
+#include "ptx.cuh"
+#include "rowvec.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kRouterThreads = 256;
+constexpr int kRouterWarps = kRouterThreads / 32;
+// Blocks of the forward, which also bound the rows of partial sums: four for
+// each SM.
+constexpr int kRouterBlocks = 4 * kSMs;
+
+template <bool VEC, int LPR>
+__device__ __forceinline__ int ecol(int sub, int i, int e) {
+  return VEC ? 4 * (sub + LPR * i) + e : sub + LPR * (4 * i + e);
+}
+template <bool VEC, int LPR, int NV>
+__device__ __forceinline__ void load_row(const float* row, int sub, int E, float fill,
+                                         float (&l)[NV][4]) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (VEC) {
+      float4 q = make_float4(fill, fill, fill, fill);
+      if (ecol<VEC, LPR>(sub, i, 0) < E) q = __ldg(reinterpret_cast<const float4*>(row) + sub + LPR * i);
+      l[i][0] = q.x; l[i][1] = q.y; l[i][2] = q.z; l[i][3] = q.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = ecol<VEC, LPR>(sub, i, e);
+        l[i][e] = c < E ? __ldg(row + c) : fill;
+      }
+    }
+  }
+}
+template <int LPR>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <int LPR>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// part: [gridDim.x][E + 1]: sums of P over the block's rows, then of lse^2.
+template <bool VEC, int LPR, int NV>
+__global__ void __launch_bounds__(kRouterThreads) router_loss_kernel(const float* __restrict__ logits,
+                                                                     int T, int E,
+                                                                     float* __restrict__ lse,
+                                                                     float* __restrict__ part) {
+  extern __shared__ float s_acc[];  // [kRouterWarps][E + 1]
+  constexpr int RPW = 32 / LPR;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = lane % LPR, r = lane / LPR;
+  float acc[NV][4], zacc = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+  pdl_wait();
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRouterWarps * RPW;
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kRouterWarps + warp) * RPW; t0 < T;
+       t0 += step) {
+    const int64_t t = t0 + r;
+    const bool ok = t < T;
+    float l[NV][4];
+    load_row<VEC, LPR, NV>(logits + (ok ? t * E : 0), sub, ok ? E : 0, -INFINITY, l);
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m = fmaxf(m, l[i][e]);
+    m = lanes_max<LPR>(m);
+    const float m0 = m == -INFINITY ? 0.f : m;  // an empty row: every term 0
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        l[i][e] = __expf(l[i][e] - m0);
+        s += l[i][e];
+      }
+    s = lanes_sum<LPR>(s);
+    const bool some = s != 0.f;  // also where s is NaN
+    const float inv = some ? 1.f / s : 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(l[i][e], inv, acc[i][e]);
+    const float ls = some ? m0 + logf(s) : -INFINITY;
+    if (ok && sub == 0) {
+      lse[t] = ls;
+      if (some) zacc = fmaf(ls, ls, zacc);
+    }
+  }
+  // over the row groups of a warp, then over the warps
+#pragma unroll
+  for (int o = LPR; o < 32; o <<= 1) {
+    zacc += __shfl_xor_sync(0xffffffffu, zacc, o);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] += __shfl_xor_sync(0xffffffffu, acc[i][e], o);
+  }
+  if (r == 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = ecol<VEC, LPR>(sub, i, e);
+        if (c < E) s_acc[warp * (E + 1) + c] = acc[i][e];
+      }
+    if (sub == 0) s_acc[warp * (E + 1) + E] = zacc;
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c <= E; c += kRouterThreads) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kRouterWarps; ++w) v += s_acc[w * (E + 1) + c];
+    part[static_cast<int64_t>(blockIdx.x) * (E + 1) + c] = v;
+  }
+}
+
+// One block: pmean, then losses[0] = aux, losses[1] = z.  P rows of partials.
+__global__ void __launch_bounds__(1024) router_loss_final_kernel(const float* __restrict__ part, int P,
+                                                                 const int32_t* __restrict__ counts,
+                                                                 int T, int E, int k,
+                                                                 float* __restrict__ losses,
+                                                                 float* __restrict__ pmean) {
+  __shared__ float s[32][33];
+  __shared__ float s_aux[32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const float inv_T = 1.f / static_cast<float>(T);
+  float aux = 0.f;
+  pdl_wait();
+  for (int c0 = 0; c0 <= E; c0 += 32) {
+    const int c = c0 + lane;
+    float v = 0.f;
+    if (c <= E) {
+#pragma unroll 4
+      for (int b = w; b < P; b += 32) v += part[static_cast<int64_t>(b) * (E + 1) + c];
+    }
+    s[w][lane] = v;
+    __syncthreads();
+    // warp w adds up column c0 + w
+    v = s[lane][w];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int cw = c0 + w;
+    if (lane == 0) {
+      v *= inv_T;
+      if (cw < E) {
+        pmean[cw] = v;
+        aux = fmaf(static_cast<float>(counts[cw]), v, aux);
+      } else if (cw == E) {
+        losses[1] = v;
+      }
+    }
+    __syncthreads();
+  }
+  if (lane == 0) s_aux[w] = aux;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float v = 0.f;
+    for (int i = 0; i < 32; ++i) v += s_aux[i];
+    losses[0] = v * (static_cast<float>(E) / (static_cast<float>(T) * static_cast<float>(k)));
+  }
+}
+
+template <bool VEC, int LPR, int NV>
+__global__ void __launch_bounds__(kRouterThreads) router_bwd_kernel(
+    const float* __restrict__ logits, const float* __restrict__ lse,
+    const int32_t* __restrict__ counts, const int32_t* __restrict__ ids,
+    const float* __restrict__ w, const float* __restrict__ dw, int T, int E, int k, float c_aux,
+    float c_z, float inv_Tk, float* __restrict__ dlogits, int* status) {
+  constexpr int RPW = 32 / LPR;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = lane % LPR, r = lane / LPR;
+  pdl_wait();
+  float f[NV][4];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int c = ecol<VEC, LPR>(sub, i, e);
+      f[i][e] = counts != nullptr && c < E ? static_cast<float>(__ldg(counts + c)) * inv_Tk : 0.f;
+    }
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRouterWarps * RPW;
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kRouterWarps + warp) * RPW; t0 < T;
+       t0 += step) {
+    const int64_t t = t0 + r;
+    const bool ok = t < T;
+    const int64_t tt = ok ? t : T - 1;
+    float l[NV][4];
+    load_row<VEC, LPR, NV>(logits + tt * E, sub, E, -INFINITY, l);
+    const float ls = __ldg(lse + tt);
+    const bool empty = ls == -INFINITY;
+    const float ls0 = empty ? 0.f : ls;
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        l[i][e] = __expf(l[i][e] - ls0);
+        dot = fmaf(f[i][e], l[i][e], dot);
+      }
+    dot = lanes_sum<LPR>(dot);
+    const float base = fmaf(c_z, ls0, -c_aux * dot);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) l[i][e] *= fmaf(c_aux, f[i][e], base);
+    if (dw != nullptr) {
+      float g = 0.f;
+      for (int j = sub; j < k; j += LPR) g = fmaf(__ldg(w + tt * k + j), __ldg(dw + tt * k + j), g);
+      g = lanes_sum<LPR>(g);
+      for (int j = 0; j < k; ++j) {
+        const int id = __ldg(ids + tt * k + j);
+        const float v = empty ? 0.f : __ldg(w + tt * k + j) * (__ldg(dw + tt * k + j) - g);
+        if (ok && sub == 0 && (id < 0 || id >= E)) atomicCAS(status, 0, kErrBadIds);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) l[i][e] += ecol<VEC, LPR>(sub, i, e) == id ? v : 0.f;
+      }
+    }
+    if (ok) {
+      float* row = dlogits + t * E;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (VEC) {
+          if (ecol<VEC, LPR>(sub, i, 0) < E)
+            *(reinterpret_cast<float4*>(row) + sub + LPR * i) =
+                make_float4(l[i][0], l[i][1], l[i][2], l[i][3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int c = ecol<VEC, LPR>(sub, i, e);
+            if (c < E) row[c] = l[i][e];
+          }
+        }
+      }
+    }
+  }
+}
+
+struct RouterLaunch {
+  const float* logits;
+  int T, E, k;
+  const int32_t *counts, *ids;
+  const float *w, *dw;
+  float* lse;
+  float *losses, *pmean, *part, *dlogits;
+  float aux_coef, z_coef;
+  int* status;
+  bool bwd;
+  cudaStream_t s;
+};
+
+int rows_per_block(int E) {
+  int lpr = 1;
+  while (lpr < 32 && lpr * 4 < E) lpr *= 2;
+  return kRouterWarps * (32 / lpr);
+}
+int fwd_blocks(int T, int E) {
+  const int per = rows_per_block(E);
+  return static_cast<int>(std::min<int64_t>((static_cast<int64_t>(T) + per - 1) / per, kRouterBlocks));
+}
+
+template <bool VEC, int LPR, int NV>
+cudaError_t go(const RouterLaunch& q) {
+  if (q.bwd) {
+    const int per = kRouterWarps * (32 / LPR);
+    const int blocks = static_cast<int>(
+        std::min<int64_t>((static_cast<int64_t>(q.T) + per - 1) / per, 8 * kSMs));
+    const float T = static_cast<float>(q.T);
+    return launch_pdl(router_bwd_kernel<VEC, LPR, NV>, dim3(blocks), dim3(kRouterThreads), 0, q.s,
+                      q.logits, static_cast<const float*>(q.lse), q.counts, q.ids, q.w, q.dw, q.T,
+                      q.E, q.k, q.aux_coef * static_cast<float>(q.E) / T, 2.f * q.z_coef / T,
+                      1.f / (T * static_cast<float>(q.k)), q.dlogits, q.status);
+  }
+  const int blocks = fwd_blocks(q.T, q.E);
+  const size_t smem = static_cast<size_t>(kRouterWarps) * (q.E + 1) * 4;
+  return launch_pdl(router_loss_kernel<VEC, LPR, NV>, dim3(blocks), dim3(kRouterThreads), smem, q.s,
+                    q.logits, q.T, q.E, q.lse, q.part);
+}
+
+// Lanes for a row: the fewest (a power of two) that hold it in one vector
+// each; above 128 experts a whole warp with several vectors.
+template <bool VEC>
+cudaError_t pick(const RouterLaunch& q) {
+  const int E = q.E;
+  if (E <= 4) return go<VEC, 1, 1>(q);
+  if (E <= 8) return go<VEC, 2, 1>(q);
+  if (E <= 16) return go<VEC, 4, 1>(q);
+  if (E <= 32) return go<VEC, 8, 1>(q);
+  if (E <= 64) return go<VEC, 16, 1>(q);
+  if (E <= 128) return go<VEC, 32, 1>(q);
+  if (E <= 256) return go<VEC, 32, 2>(q);
+  if (E <= 512) return go<VEC, 32, 4>(q);
+  return go<VEC, 32, 8>(q);
+}
+cudaError_t launch_router(const RouterLaunch& q, bool vec) {
+  return vec ? pick<true>(q) : pick<false>(q);
+}
+
+int bad(const char* msg) { return record_error(MOE_ERR_INVALID_ARG, msg); }
+bool misaligned(const void* p, unsigned size) { return (reinterpret_cast<uintptr_t>(p) & (size - 1)) != 0; }
+
+int check_sizes(int32_t T, int32_t E, int32_t k) {
+  if (T < 0 || E <= 0 || k <= 0 || k > E) return bad("bad T/E/k");
+  if (E > kMaxExperts || k > 32) return record_error(MOE_ERR_UNSUPPORTED, "E > 1024 or k > 32");
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_router_loss_workspace_size(int32_t T, int32_t E) {
+  if (T < 0 || E <= 0 || E > kMaxExperts) return 0;
+  return static_cast<size_t>(fwd_blocks(T, E)) * (static_cast<size_t>(E) + 1) * 4;
+}
+
+int moe_router_loss_fwd(const float* logits, int32_t T, int32_t E, int32_t k, const int32_t* counts,
+                        float* losses, float* lse, float* pmean, void* ws, size_t ws_bytes,
+                        moe_stream_t stream) {
+  NvtxScope nvtx("moe_router_loss_fwd");
+  int rc = check_sizes(T, E, k);
+  if (rc) return rc;
+  if (T == 0) return bad("the mean over no tokens: T must be positive");
+  if (!logits || !counts || !losses || !lse || !pmean || !ws) return bad("NULL pointer");
+  if (misaligned(logits, 4) || misaligned(counts, 4) || misaligned(losses, 4) || misaligned(lse, 4) ||
+      misaligned(pmean, 4) || misaligned(ws, 16))
+    return bad("misaligned pointer");
+  if (ws_bytes < moe_router_loss_workspace_size(T, E))
+    return record_error(MOE_ERR_WORKSPACE, "router loss workspace too small");
+  RouterLaunch q = {};
+  q.logits = logits; q.T = T; q.E = E; q.k = k; q.lse = lse; q.part = static_cast<float*>(ws);
+  q.s = stream;
+  ProbeScope probe("router_loss", stream);
+  cudaError_t e = launch_router(q, E % 4 == 0 && !misaligned(logits, 16));
+  if (e == cudaSuccess)
+    e = launch_pdl(router_loss_final_kernel, dim3(1), dim3(1024), 0, stream,
+                   static_cast<const float*>(q.part), fwd_blocks(T, E), counts, static_cast<int>(T),
+                   static_cast<int>(E), static_cast<int>(k), losses, pmean);
+  if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
+  return record_error(MOE_OK, "");
+}
+
+int moe_router_bwd(const float* logits, const float* lse, int32_t T, int32_t E, int32_t k,
+                   const int32_t* counts, const int32_t* ids, const float* weights,
+                   const float* dweights, float aux_coef, float z_coef, float* dlogits,
+                   moe_stream_t stream) {
+  NvtxScope nvtx("moe_router_bwd");
+  int rc = check_sizes(T, E, k);
+  if (rc) return rc;
+  if (T == 0) return record_error(MOE_OK, "");
+  if (!logits || !lse || !dlogits) return bad("NULL pointer");
+  if (dweights != nullptr && (!ids || !weights)) return bad("dweights needs ids and weights");
+  if (aux_coef != 0.f && !counts) return bad("the load-balancing loss needs counts");
+  if (misaligned(logits, 4) || misaligned(lse, 4) || misaligned(dlogits, 4) || misaligned(counts, 4) ||
+      misaligned(ids, 4) || misaligned(weights, 4) || misaligned(dweights, 4))
+    return bad("misaligned pointer");
+  RouterLaunch q = {};
+  rc = device_status_word(&q.status);
+  if (rc != MOE_OK) return rc;
+  q.logits = logits; q.T = T; q.E = E; q.k = k; q.counts = counts; q.ids = ids; q.w = weights;
+  q.dw = dweights; q.lse = const_cast<float*>(lse); q.dlogits = dlogits; q.aux_coef = aux_coef;
+  q.z_coef = z_coef; q.bwd = true; q.s = stream;
+  ProbeScope probe("router_bwd", stream);
+  const cudaError_t e =
+      launch_router(q, E % 4 == 0 && !misaligned(logits, 16) && !misaligned(dlogits, 16));
+  if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
+  return record_error(MOE_OK, "");
+}
+
+}  // extern "C"

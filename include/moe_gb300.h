@@ -333,6 +333,142 @@ MOE_API int moe_ep_segment_ids(const int32_t* counts, int32_t P, int32_t E_loc, 
                                int32_t* ids, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Around the layer in a training step: norms, router losses, optimizer       */
+/* ------------------------------------------------------------------------ */
+/* These calls share the conventions above, with two differences: rows may
+ * have any width (16-byte alignment and multiples of 8 are the fast path, not
+ * a condition; pointers need their element's alignment), and T = 0 is valid
+ * where it has a meaning. */
+
+/* Element types of buffers passed as void*. */
+enum { MOE_F32 = 0, MOE_BF16 = 1 };
+
+/* What a gate varies over: nothing, one value for each token ([T] fp32), for
+ * each channel ([d] fp32), or for each element ([T,d], the block's type). */
+enum { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_CHANNEL = 2, MOE_GATE_ELEMENT = 3 };
+
+#define MOE_NORM_MAX_D 16384
+
+typedef struct moe_norm_desc {
+  int32_t T, d;
+  int32_t x_type;        /* residual stream x, r, dr, dx: MOE_F32 or MOE_BF16 */
+  int32_t y_type;        /* block side y, n, dn, dy, element gate: likewise;
+                            (BF16, F32) is not supported */
+  int32_t gate;          /* MOE_GATE_* */
+  int32_t gate_sigmoid;  /* 1: the gate's factor is sigmoid(gate), 0: the gate */
+  float scale;           /* residual scale s */
+  float eps;             /* > 0 */
+  float w_offset;        /* added to the norm weights (1 for weights kept around 0) */
+} moe_norm_desc;
+
+/* The norm after a block, its gated and scaled residual sum, and the norm
+ * before the next block, in one pass; RMS norms, fp32 arithmetic:
+ *   p = y rstd_y (w_post + w_offset), or y when w_post is NULL
+ *   r = x + scale a(gate) p           (x NULL: without the residual)
+ *   n = r rstd_r (w_pre + w_offset)   when w_pre is not NULL
+ *   rstd(z) = 1 / sqrt(mean(z^2) + eps)
+ * With y NULL (then r, w_post NULL and no gate) it is the norm of x alone.
+ * n is the norm of r before r is rounded.  Outputs: r [T,d], n [T,d], rstd_y
+ * [T] fp32 (with w_post), rstd_r [T] fp32 (with w_pre); weights [d] fp32.  r
+ * may be x, and n may be y, for a step in place (y is then gone for the
+ * backward); other overlaps are not allowed.  T = 0 does nothing. */
+MOE_API int moe_block_norm_fwd(const moe_norm_desc* desc, const void* x, const void* y,
+                               const void* gate, const float* w_post, const float* w_pre, void* r,
+                               void* n, float* rstd_y, float* rstd_r, moe_stream_t stream);
+
+/* Bytes of scratch moe_block_norm_bwd needs when it sums over tokens. */
+MOE_API size_t moe_block_norm_workspace_size(int32_t T, int32_t d);
+
+/* Gradients, given dr (of r as the residual stream hands it back; NULL: 0) and
+ * dn (of n, when the forward had w_pre).  r, y, gate, rstd_y, rstd_r as given
+ * to or saved by the forward (r only with w_pre: x itself where y was NULL).
+ *   t = dr + the gradient through the norm of r;   dx = t
+ *   dy = the gradient of y;   dgate in the gate's own shape and type
+ *   dw_post, dw_pre [d] fp32 sums over the tokens
+ * Each output may be NULL when it is not wanted.  dx may be dr, dy may be dn.
+ * ws: moe_block_norm_workspace_size bytes, 16-byte aligned; needed for dw_post,
+ * dw_pre and a channel gate's dgate.  T = 0 writes zeros to those. */
+MOE_API int moe_block_norm_bwd(const moe_norm_desc* desc, const void* dr, const void* dn,
+                               const void* r, const void* y, const void* gate,
+                               const float* w_post, const float* w_pre, const float* rstd_y,
+                               const float* rstd_r, void* dx, void* dy, void* dgate,
+                               float* dw_post, float* dw_pre, void* ws, size_t ws_bytes,
+                               moe_stream_t stream);
+
+/* The router's losses over T >= 1 tokens.  With P = softmax(logits), lse the
+ * log of a row's sum of exponentials, f_e = counts_e / (T k):
+ *   losses[0] = E sum_e f_e mean_t P[t,e]      (load balancing; E/T/k-normed: 1
+ *                                               for an even load)
+ *   losses[1] = mean_t lse_t^2                 (z loss)
+ *   lse [T], pmean [E] = mean_t P[t,:]
+ * counts: the first E counts of moe_route (a shared expert is not counted).
+ * A logit of -inf is an expert that is switched off; a row of nothing else has
+ * P = 0, lse = -inf and adds nothing.  All fp32.  ws: at least
+ * moe_router_loss_workspace_size bytes, 16-byte aligned. */
+MOE_API size_t moe_router_loss_workspace_size(int32_t T, int32_t E);
+MOE_API int moe_router_loss_fwd(const float* logits, int32_t T, int32_t E, int32_t k,
+                                const int32_t* counts, float* losses, float* lse, float* pmean,
+                                void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Gradient of the logits, all paths in one call:
+ *   dlogits[t,e] = sum_{j: ids[t,j] = e} w_j (dw_j - sum_i w_i dw_i)
+ *                + aux_coef d losses[0] / d logits[t,e] + z_coef d losses[1] / d logits[t,e]
+ * ids, weights [T,k] from moe_router_topk, dweights [T,k] the gradient of the
+ * weights (NULL: no such path), lse from moe_router_loss_fwd, counts as there
+ * (may be NULL when aux_coef is 0).  An id outside [0,E) sets MOE_ERR_BAD_IDS
+ * in the status word and its slot is left out.  A row without a finite logit
+ * gets zeros.  dlogits [T,E] must not overlap the inputs.  T = 0 does nothing. */
+MOE_API int moe_router_bwd(const float* logits, const float* lse, int32_t T, int32_t E, int32_t k,
+                           const int32_t* counts, const int32_t* ids, const float* weights,
+                           const float* dweights, float aux_coef, float z_coef, float* dlogits,
+                           moe_stream_t stream);
+
+/* Values that share a scale in 8-bit optimizer states. */
+#define MOE_ADAMW_BLOCK 256
+
+typedef struct moe_adamw_tensor {
+  void* param;         /* [n], updated in place */
+  float* master;       /* [n] fp32 copy that is updated and rounded to param, or
+                          NULL; bf16 parameters only */
+  const void* grad;    /* [n] */
+  void* m;             /* [n] fp32, or e4m3 bytes */
+  void* v;             /* [n] fp32, or e4m3 bytes of sqrt(v) */
+  uint8_t* scales;     /* 8-bit states: [ceil(n / MOE_ADAMW_BLOCK), 2] exponent bytes
+                          (scale 2^(byte - 127)) of m and of sqrt(v); else NULL */
+  int64_t n;
+  int32_t param_type, grad_type;   /* MOE_F32 or MOE_BF16 */
+  int32_t state_bits;              /* 32 or 8 */
+  float lr_mult, weight_decay;
+} moe_adamw_tensor;
+
+typedef struct moe_adamw_hyper {
+  double lr, beta1, beta2, eps;
+  int64_t step;            /* t: 1 for the first step */
+  float grad_scale;        /* multiplies every gradient (1 / loss scale) */
+  float max_norm;          /* > 0: clip by the global norm; 0: no clip */
+  int32_t skip_nonfinite;  /* 1: leave everything as it is when the norm is not finite */
+} moe_adamw_hyper;
+
+/* One AdamW step over n tensors (HOST arrays of descriptors and settings, read
+ * during the call; they reach the GPU as kernel arguments):
+ *   g = c grad;  m = b1 m + (1-b1) g;  v = b2 v + (1-b2) g^2
+ *   p = p (1 - lr wd) - lr / (1-b1^t) m / (sqrt(v) / sqrt(1-b2^t) + eps)
+ *   c = grad_scale min(1, max_norm / (norm + 1e-6)),  norm = |grad_scale grad|_2
+ * with lr = hyper.lr * lr_mult, in fp32.  States start as zeros (codes and
+ * scale bytes too).  8-bit states hold m and sqrt(v) to 3 bits after the
+ * leading one, with a dithered rounding that depends on t and on a value's
+ * index only, so equal inputs give equal results.  grad_norm (device, [1]) gets
+ * norm when not NULL.  A gradient that is not finite spoils its values, and in
+ * 8 bits the states of its block of MOE_ADAMW_BLOCK; skip_nonfinite = 1
+ * prevents it.  Gradients above 1.8e19 count as not finite in the norm.
+ * ws: moe_adamw_workspace_size bytes, 16-byte aligned; needed only for the norm
+ * (max_norm > 0, grad_norm or skip_nonfinite).  Tensors must not overlap. */
+MOE_API size_t moe_adamw_workspace_size(const moe_adamw_tensor* tensors, int32_t n);
+MOE_API int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n,
+                           const moe_adamw_hyper* hyper, float* grad_norm, void* ws,
+                           size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Status                                                                    */
 /* ------------------------------------------------------------------------ */
 
@@ -379,8 +515,11 @@ MOE_API int moe_probe_read_stream(const void* src, size_t bytes, int32_t pattern
 /* Kernel names the probe knows, i = 0, 1, ...; NULL past the last one:
  * route, permute, combine, router_topk, the grouped GEMMs xa_gu, gate_up,
  * xa_dn, down, u, dgrad_dn, v, dgrad_gu, the weight-gradient GEMMs dB_dn,
- * dA_dn, dB_gu, dA_gu, dw_reduce, and the full weight-gradient GEMMs dW_dn
- * and dW_gu.  ("route" covers all of its kernels: moe_route_kernel_count.) */
+ * dA_dn, dB_gu, dA_gu, dw_reduce, the full weight-gradient GEMMs dW_dn and
+ * dW_gu, ep_row_weights, ep_segment_ids, block_norm_fwd, block_norm_bwd,
+ * router_loss, router_bwd, grad_norm and adamw.  (A name covers all kernels of
+ * its call: "route" moe_route_kernel_count, "router_loss" two, "block_norm_bwd"
+ * two with sums over tokens, "adamw" one for each kind of tensor.) */
 MOE_API const char* moe_kernel_name(int32_t i);
 
 /* Arms the probe of one kernel: its next n launches record start_events[i]
