@@ -8,6 +8,7 @@ the compiled library is missing the calls raise; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -94,6 +95,8 @@ class MoeAdamWHyper(ctypes.Structure):
 def load(path: str = LIB_PATH):
     """Load the compiled library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -179,9 +182,18 @@ def _f32(t, name):
     return _ptr(t, torch.float32, name)
 
 
+try:   # the current stream's handle without building a Stream object (3 us a call)
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream, _cuda_getDevice as _device
+except ImportError:
+    _raw_stream = None
+
+
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and torch.cuda.is_initialized():
+        return _raw_stream(_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def make_dims(T, d, f, E, k, r, lora_scale, shared_expert=False) -> MoeDims:
@@ -320,10 +332,10 @@ def moe_ep_segment_ids(counts, ids, stream=None):
 _TYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
-def _type(t, name):
-    code = _TYPES.get(t.dtype)
+def _type(dtype, name):
+    code = _TYPES.get(dtype)
     if code is None:
-        raise ValueError("%s must be torch.float32 or torch.bfloat16, got %s" % (name, t.dtype))
+        raise ValueError("%s must be torch.float32 or torch.bfloat16, got %s" % (name, dtype))
     return code
 
 
@@ -331,33 +343,45 @@ def _shaped(t, shape, dtype, name):
     """Pointer of a contiguous CUDA tensor of this shape and type (None stays None)."""
     if t is None:
         return None
-    p = _ptr(t, dtype, name)
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda
+            and t.is_contiguous()):
+        return t.data_ptr()
+    p = _ptr(t, dtype, name)   # says what is wrong
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     return p
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_setup(T, d, xt, yt, gate_kind, gate_sigmoid, scale, eps, w_offset):
+    """Descriptor of a call with these settings, the gate's shape and its type."""
+    if gate_kind not in GATE_KINDS:
+        raise ValueError("gate_kind must be one of %s" % ", ".join(GATE_KINDS))
+    desc = MoeNormDesc(T, d, _type(xt, "x"), _type(yt, "y"), GATE_KINDS[gate_kind],
+                       1 if gate_sigmoid else 0, scale, eps, w_offset)
+    gshape, gtype = {"none": ((0,), None), "token": ((T,), torch.float32),
+                     "channel": ((d,), torch.float32), "element": ((T, d), yt)}[gate_kind]
+    return ctypes.byref(desc), gshape, gtype
+
+
 def _norm_desc(x, y, gate, gate_kind, gate_sigmoid, scale, eps, w_offset):
     """Descriptor, shape [T,d], types of the two sides, and the gate's shape and
     type, from the residual-side tensor x and the block-side tensor y."""
-    have = x if x is not None else y
-    if have is None:
+    if x is None:
+        x = y
+    elif y is None:
+        y = x
+    if x is None:
         raise ValueError("pass the residual-side tensor, the block-side tensor or both")
-    if have.dim() != 2:
-        raise ValueError("rows must be [T, d], got %s" % (tuple(have.shape),))
-    if gate_kind not in GATE_KINDS:
-        raise ValueError("gate_kind must be one of %s" % ", ".join(GATE_KINDS))
-    xt = (x if x is not None else y).dtype
-    yt = (y if y is not None else x).dtype
-    T, d = have.shape
-    desc = MoeNormDesc(T, d, _type(x if x is not None else y, "x"),
-                       _type(y if y is not None else x, "y"),
-                       GATE_KINDS[gate_kind], 1 if gate_sigmoid else 0, scale, eps, w_offset)
-    gshape, gtype = {"none": ((0,), None), "token": ((T,), torch.float32),
-                     "channel": ((d,), torch.float32), "element": ((T, d), yt)}[gate_kind]
+    sh = x.shape
+    if len(sh) != 2:
+        raise ValueError("rows must be [T, d], got %s" % (tuple(sh),))
     if (gate is None) != (gate_kind == "none"):
         raise ValueError("gate and gate_kind go together")
-    return desc, have.shape, xt, yt, gshape, gtype
+    xt, yt = x.dtype, y.dtype
+    desc, gshape, gtype = _norm_setup(sh[0], sh[1], xt, yt, gate_kind, bool(gate_sigmoid),
+                                      float(scale), float(eps), float(w_offset))
+    return desc, sh, xt, yt, gshape, gtype
 
 
 def moe_block_norm_fwd(x, y, r=None, n=None, w_post=None, w_pre=None, rstd_y=None, rstd_r=None,
@@ -377,7 +401,7 @@ def moe_block_norm_fwd(x, y, r=None, n=None, w_post=None, w_pre=None, rstd_y=Non
     T, d = sh
     f32 = torch.float32
     _check(load().moe_block_norm_fwd(
-        ctypes.byref(desc), _shaped(x, sh, xt, "x"), _shaped(y, sh, yt, "y"),
+        desc, _shaped(x, sh, xt, "x"), _shaped(y, sh, yt, "y"),
         _shaped(gate, gs, gt, "gate"), _shaped(w_post, (d,), f32, "w_post"),
         _shaped(w_pre, (d,), f32, "w_pre"), _shaped(r, sh, xt, "r"), _shaped(n, sh, yt, "n"),
         _shaped(rstd_y, (T,), f32, "rstd_y"), _shaped(rstd_r, (T,), f32, "rstd_r"),
@@ -402,7 +426,7 @@ def moe_block_norm_bwd(dr, dn, r, y, dx=None, dy=None, w_post=None, w_pre=None, 
     T, d = sh
     f32 = torch.float32
     _check(load().moe_block_norm_bwd(
-        ctypes.byref(desc), _shaped(dr, sh, xt, "dr"), _shaped(dn, sh, yt, "dn"),
+        desc, _shaped(dr, sh, xt, "dr"), _shaped(dn, sh, yt, "dn"),
         _shaped(r, sh, xt, "r"), _shaped(y, sh, yt, "y"), _shaped(gate, gs, gt, "gate"),
         _shaped(w_post, (d,), f32, "w_post"), _shaped(w_pre, (d,), f32, "w_pre"),
         _shaped(rstd_y, (T,), f32, "rstd_y"), _shaped(rstd_r, (T,), f32, "rstd_r"),
@@ -484,7 +508,7 @@ class AdamWTable:
         return MoeAdamWTensor(
             _ptr(p, name="param"), _f32(r.get("master"), "master"), _ptr(r["grad"], name="grad"),
             _ptr(r["m"], name="m"), _ptr(r["v"], name="v"), _ptr(sc, torch.uint8, "scales"), n,
-            _type(p, "param"), _type(r["grad"], "grad"), 8 if eight else 32,
+            _type(p.dtype, "param"), _type(r["grad"].dtype, "grad"), 8 if eight else 32,
             float(r.get("lr_mult", 1.0)), float(r.get("weight_decay", 0.0)))
 
     def set_grads(self, grads):
