@@ -58,13 +58,13 @@ __device__ __forceinline__ float lanes_max(float v) {
   return v;
 }
 
-// part: [gridDim.x][E + 1]: sums of P over the block's rows, then of lse^2.
+// part: [gridDim.x][ld]: sums of P over the block's rows, then of lse^2, then zeros.
 template <bool VEC, int LPR, int NV>
 __global__ void __launch_bounds__(kRouterThreads) router_loss_kernel(const float* __restrict__ logits,
                                                                      int T, int E,
                                                                      float* __restrict__ lse,
-                                                                     float* __restrict__ part) {
-  extern __shared__ float s_acc[];  // [kRouterWarps][E + 1]
+                                                                     float* __restrict__ part, int ld) {
+  extern __shared__ float s_acc[];  // [kRouterWarps][ld]
   constexpr int RPW = 32 / LPR;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane % LPR, r = lane / LPR;
@@ -124,74 +124,88 @@ __global__ void __launch_bounds__(kRouterThreads) router_loss_kernel(const float
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int c = ecol<VEC, LPR>(sub, i, e);
-        if (c < E) s_acc[warp * (E + 1) + c] = acc[i][e];
+        if (c < E) s_acc[warp * ld + c] = acc[i][e];
       }
-    if (sub == 0) s_acc[warp * (E + 1) + E] = zacc;
+    if (sub == 0) s_acc[warp * ld + E] = zacc;
   }
   __syncthreads();
-  for (int c = threadIdx.x; c <= E; c += kRouterThreads) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kRouterWarps; ++w) v += s_acc[w * (E + 1) + c];
-    part[static_cast<int64_t>(blockIdx.x) * (E + 1) + c] = v;
-  }
-}
-
-// One block: pmean, then losses[0] = aux, losses[1] = z.  P rows of partials.
-__global__ void __launch_bounds__(1024) router_loss_final_kernel(const float* __restrict__ part, int P,
-                                                                 const int32_t* __restrict__ counts,
-                                                                 int T, int E, int k,
-                                                                 float* __restrict__ losses,
-                                                                 float* __restrict__ pmean) {
-  __shared__ float s[32][33];
-  __shared__ float s_aux[32];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const float inv_T = 1.f / static_cast<float>(T);
-  float aux = 0.f;
-  pdl_wait();
-  for (int c0 = 0; c0 <= E; c0 += 32) {
-    const int c = c0 + lane;
+  for (int c = threadIdx.x; c < ld; c += kRouterThreads) {
     float v = 0.f;
     if (c <= E) {
-#pragma unroll 4
-      for (int b = w; b < P; b += 32) v += part[static_cast<int64_t>(b) * (E + 1) + c];
-    }
-    s[w][lane] = v;
-    __syncthreads();
-    // warp w adds up column c0 + w
-    v = s[lane][w];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    const int cw = c0 + w;
-    if (lane == 0) {
-      v *= inv_T;
-      if (cw < E) {
-        pmean[cw] = v;
-        aux = fmaf(static_cast<float>(counts[cw]), v, aux);
-      } else if (cw == E) {
-        losses[1] = v;
-      }
+      for (int w = 0; w < kRouterWarps; ++w) v += s_acc[w * ld + c];
     }
-    __syncthreads();
-  }
-  if (lane == 0) s_aux[w] = aux;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float v = 0.f;
-    for (int i = 0; i < 32; ++i) v += s_aux[i];
-    losses[0] = v * (static_cast<float>(E) / (static_cast<float>(T) * static_cast<float>(k)));
+    part[static_cast<int64_t>(blockIdx.x) * ld + c] = v;
   }
 }
 
+// One block: pmean, then losses[0] = aux, losses[1] = z, from P rows of partials
+// of `ld` floats (E sums of P, the sum of lse^2, zeros up to a multiple of 4).
+// Each thread adds every G-th row of one vector of 4 columns, all loads
+// independent; then the G sums of a column are added in order.
+constexpr int kFinalThreads = 1024;
+__global__ void __launch_bounds__(kFinalThreads) router_loss_final_kernel(
+    const float* __restrict__ part, int P, int ld, const int32_t* __restrict__ counts, int T, int E,
+    int k, float* __restrict__ losses, float* __restrict__ pmean) {
+  __shared__ float4 s_col[kFinalThreads];
+  __shared__ float s_aux[32];
+  const int nv = ld / 4, G = kFinalThreads / nv;  // nv <= 257
+  const int g = threadIdx.x / nv, c = threadIdx.x - g * nv;
+  const float inv_T = 1.f / static_cast<float>(T);
+  pdl_wait();
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (g < G) {
+    const float4* col = reinterpret_cast<const float4*>(part) + c;
+#pragma unroll 8
+    for (int b = g; b < P; b += G) {
+      const float4 q = col[static_cast<int64_t>(b) * nv];
+      v.x += q.x; v.y += q.y; v.z += q.z; v.w += q.w;
+    }
+  }
+  s_col[threadIdx.x] = v;
+  __syncthreads();
+  float aux = 0.f;
+  for (int e = threadIdx.x; e <= E; e += kFinalThreads) {
+    const float* col = reinterpret_cast<const float*>(s_col) + e;
+    float t = 0.f;
+    for (int q = 0; q < G; ++q) t += col[q * ld];
+    t *= inv_T;
+    if (e < E) {
+      pmean[e] = t;
+      aux = fmaf(static_cast<float>(counts[e]), t, aux);
+    } else {
+      losses[1] = t;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) aux += __shfl_xor_sync(0xffffffffu, aux, o);
+  if ((threadIdx.x & 31) == 0) s_aux[threadIdx.x >> 5] = aux;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    aux = s_aux[threadIdx.x];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) aux += __shfl_xor_sync(0xffffffffu, aux, o);
+    if (threadIdx.x == 0)
+      losses[0] = aux * (static_cast<float>(E) / (static_cast<float>(T) * static_cast<float>(k)));
+  }
+}
+
+// The gradient rows of a warp pass through shared memory for the top-k terms:
+// lane `sub` of a row adds the terms of slots sub, sub + LPR, ...  Slots of one
+// row name different experts (then no two lanes meet); each slot first writes
+// its number where its term goes and reads it back, and where that shows an
+// expert named twice the terms are added slot by slot instead.
 template <bool VEC, int LPR, int NV>
 __global__ void __launch_bounds__(kRouterThreads) router_bwd_kernel(
     const float* __restrict__ logits, const float* __restrict__ lse,
     const int32_t* __restrict__ counts, const int32_t* __restrict__ ids,
     const float* __restrict__ w, const float* __restrict__ dw, int T, int E, int k, float c_aux,
     float c_z, float inv_Tk, float* __restrict__ dlogits, int* status) {
-  constexpr int RPW = 32 / LPR;
+  extern __shared__ float4 s_rows[];  // [kRouterWarps][RPW][4 LPR NV]
+  constexpr int RPW = 32 / LPR, LD = 4 * LPR * NV;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane % LPR, r = lane / LPR;
+  float* s_row = reinterpret_cast<float*>(s_rows) + (warp * RPW + r) * LD;
   pdl_wait();
   float f[NV][4];
 #pragma unroll
@@ -212,6 +226,24 @@ __global__ void __launch_bounds__(kRouterThreads) router_bwd_kernel(
     const float ls = __ldg(lse + tt);
     const bool empty = ls == -INFINITY;
     const float ls0 = empty ? 0.f : ls;
+    float g = 0.f;
+    bool twice = false;
+    if (dw != nullptr) {
+      for (int j = sub; j < k; j += LPR) {
+        const int id = __ldg(ids + tt * k + j);
+        const bool in = id >= 0 && id < E;
+        if (in) s_row[id] = __int_as_float(j);
+        else if (ok) atomicCAS(status, 0, kErrBadIds);
+        g = fmaf(__ldg(w + tt * k + j), __ldg(dw + tt * k + j), g);
+      }
+      g = lanes_sum<LPR>(g);
+      __syncwarp();
+      for (int j = sub; j < k; j += LPR) {
+        const int id = __ldg(ids + tt * k + j);
+        if (id >= 0 && id < E) twice |= __float_as_int(s_row[id]) != j;
+      }
+      twice = __any_sync(0xffffffffu, twice);  // also: every read before the rows are written
+    }
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -223,22 +255,38 @@ __global__ void __launch_bounds__(kRouterThreads) router_bwd_kernel(
     dot = lanes_sum<LPR>(dot);
     const float base = fmaf(c_z, ls0, -c_aux * dot);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) l[i][e] *= fmaf(c_aux, f[i][e], base);
-    if (dw != nullptr) {
-      float g = 0.f;
-      for (int j = sub; j < k; j += LPR) g = fmaf(__ldg(w + tt * k + j), __ldg(dw + tt * k + j), g);
-      g = lanes_sum<LPR>(g);
-      for (int j = 0; j < k; ++j) {
-        const int id = __ldg(ids + tt * k + j);
-        const float v = empty ? 0.f : __ldg(w + tt * k + j) * (__ldg(dw + tt * k + j) - g);
-        if (ok && sub == 0 && (id < 0 || id >= E)) atomicCAS(status, 0, kErrBadIds);
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) l[i][e] += ecol<VEC, LPR>(sub, i, e) == id ? v : 0.f;
+      for (int e = 0; e < 4; ++e) {
+        l[i][e] *= fmaf(c_aux, f[i][e], base);
+        if (!VEC && dw != nullptr) s_row[ecol<VEC, LPR>(sub, i, e)] = l[i][e];
       }
+      if (VEC && dw != nullptr)
+        *(reinterpret_cast<float4*>(s_row) + sub + LPR * i) =
+            make_float4(l[i][0], l[i][1], l[i][2], l[i][3]);
+    }
+    if (dw != nullptr) {
+      __syncwarp();
+      for (int q = 0; q < (twice ? LPR : 1); ++q) {  // one lane of a row after the other, or all
+        if (!empty && (!twice || sub == q))
+          for (int j = sub; j < k; j += LPR) {
+            const int id = __ldg(ids + tt * k + j);
+            if (id >= 0 && id < E)
+              s_row[id] += __ldg(w + tt * k + j) * (__ldg(dw + tt * k + j) - g);
+          }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (VEC) {
+          const float4 v = *(reinterpret_cast<const float4*>(s_row) + sub + LPR * i);
+          l[i][0] = v.x; l[i][1] = v.y; l[i][2] = v.z; l[i][3] = v.w;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) l[i][e] = s_row[ecol<VEC, LPR>(sub, i, e)];
+        }
+      }
+      __syncwarp();  // read before the next turn writes its slot numbers
     }
     if (ok) {
       float* row = dlogits + t * E;
@@ -273,48 +321,50 @@ struct RouterLaunch {
   cudaStream_t s;
 };
 
-int rows_per_block(int E) {
+// Lanes for a row: each holds up to 16 logits (few lanes mean few shuffles for a
+// sum, and several rows of a warp share them); more than 512 experts take a
+// warp with 32 each.
+int lanes_for(int E) {
   int lpr = 1;
-  while (lpr < 32 && lpr * 4 < E) lpr *= 2;
-  return kRouterWarps * (32 / lpr);
+  while (lpr < 32 && lpr * 16 < E) lpr *= 2;
+  return lpr;
 }
+int rows_per_block(int E) { return kRouterWarps * (32 / lanes_for(E)); }
 int fwd_blocks(int T, int E) {
   const int per = rows_per_block(E);
   return static_cast<int>(std::min<int64_t>((static_cast<int64_t>(T) + per - 1) / per, kRouterBlocks));
 }
+int part_ld(int E) { return (E + 1 + 3) / 4 * 4; }
 
 template <bool VEC, int LPR, int NV>
 cudaError_t go(const RouterLaunch& q) {
   if (q.bwd) {
     const int per = kRouterWarps * (32 / LPR);
     const int blocks = static_cast<int>(
-        std::min<int64_t>((static_cast<int64_t>(q.T) + per - 1) / per, 8 * kSMs));
+        std::min<int64_t>((static_cast<int64_t>(q.T) + per - 1) / per, kRouterBlocks));
     const float T = static_cast<float>(q.T);
-    return launch_pdl(router_bwd_kernel<VEC, LPR, NV>, dim3(blocks), dim3(kRouterThreads), 0, q.s,
+    const size_t smem = q.dw != nullptr ? static_cast<size_t>(kRouterWarps) * 128 * NV * 4 : 0;
+    return launch_pdl(router_bwd_kernel<VEC, LPR, NV>, dim3(blocks), dim3(kRouterThreads), smem, q.s,
                       q.logits, static_cast<const float*>(q.lse), q.counts, q.ids, q.w, q.dw, q.T,
                       q.E, q.k, q.aux_coef * static_cast<float>(q.E) / T, 2.f * q.z_coef / T,
                       1.f / (T * static_cast<float>(q.k)), q.dlogits, q.status);
   }
-  const int blocks = fwd_blocks(q.T, q.E);
-  const size_t smem = static_cast<size_t>(kRouterWarps) * (q.E + 1) * 4;
+  const int blocks = fwd_blocks(q.T, q.E), ld = part_ld(q.E);
+  const size_t smem = static_cast<size_t>(kRouterWarps) * ld * 4;
   return launch_pdl(router_loss_kernel<VEC, LPR, NV>, dim3(blocks), dim3(kRouterThreads), smem, q.s,
-                    q.logits, q.T, q.E, q.lse, q.part);
+                    q.logits, q.T, q.E, q.lse, q.part, ld);
 }
 
-// Lanes for a row: the fewest (a power of two) that hold it in one vector
-// each; above 128 experts a whole warp with several vectors.
 template <bool VEC>
 cudaError_t pick(const RouterLaunch& q) {
-  const int E = q.E;
-  if (E <= 4) return go<VEC, 1, 1>(q);
-  if (E <= 8) return go<VEC, 2, 1>(q);
-  if (E <= 16) return go<VEC, 4, 1>(q);
-  if (E <= 32) return go<VEC, 8, 1>(q);
-  if (E <= 64) return go<VEC, 16, 1>(q);
-  if (E <= 128) return go<VEC, 32, 1>(q);
-  if (E <= 256) return go<VEC, 32, 2>(q);
-  if (E <= 512) return go<VEC, 32, 4>(q);
-  return go<VEC, 32, 8>(q);
+  switch (lanes_for(q.E)) {
+    case 1: return q.E <= 4 ? go<VEC, 1, 1>(q) : q.E <= 8 ? go<VEC, 1, 2>(q) : go<VEC, 1, 4>(q);
+    case 2: return go<VEC, 2, 4>(q);
+    case 4: return go<VEC, 4, 4>(q);
+    case 8: return go<VEC, 8, 4>(q);
+    case 16: return go<VEC, 16, 4>(q);
+    default: return q.E <= 512 ? go<VEC, 32, 4>(q) : go<VEC, 32, 8>(q);
+  }
 }
 cudaError_t launch_router(const RouterLaunch& q, bool vec) {
   return vec ? pick<true>(q) : pick<false>(q);
@@ -338,7 +388,7 @@ extern "C" {
 
 size_t moe_router_loss_workspace_size(int32_t T, int32_t E) {
   if (T < 0 || E <= 0 || E > kMaxExperts) return 0;
-  return static_cast<size_t>(fwd_blocks(T, E)) * (static_cast<size_t>(E) + 1) * 4;
+  return static_cast<size_t>(fwd_blocks(T, E)) * static_cast<size_t>(part_ld(E)) * 4;
 }
 
 int moe_router_loss_fwd(const float* logits, int32_t T, int32_t E, int32_t k, const int32_t* counts,
@@ -360,8 +410,9 @@ int moe_router_loss_fwd(const float* logits, int32_t T, int32_t E, int32_t k, co
   ProbeScope probe("router_loss", stream);
   cudaError_t e = launch_router(q, E % 4 == 0 && !misaligned(logits, 16));
   if (e == cudaSuccess)
-    e = launch_pdl(router_loss_final_kernel, dim3(1), dim3(1024), 0, stream,
-                   static_cast<const float*>(q.part), fwd_blocks(T, E), counts, static_cast<int>(T),
+    e = launch_pdl(router_loss_final_kernel, dim3(1), dim3(kFinalThreads), 0, stream,
+                   static_cast<const float*>(q.part), fwd_blocks(T, E), part_ld(E), counts,
+                   static_cast<int>(T),
                    static_cast<int>(E), static_cast<int>(k), losses, pmean);
   if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
   return record_error(MOE_OK, "");
