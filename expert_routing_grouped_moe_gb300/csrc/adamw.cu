@@ -54,6 +54,7 @@ struct Tensor {
 };
 struct Consts {
   float b1, c1, b2, c2, correct, eps, grad_scale, max_norm;
+  float zero;            // -0
   uint32_t dither;       // t T
   const double* part;    // partial sums of squares, NULL: not needed
   int nparts, skip;
@@ -77,48 +78,62 @@ constexpr int kNormFew = 64, kNormMany = 1200;
 template <int MAX>
 struct NormTable {
   int n, chunks;
+  float zero;  // -0
   double* part;
   NormTensor t[MAX];
 };
 
+// Packed product that no later sum is contracted with: the assembler makes one
+// fma of a packed mul and add in spite of their rounding modifiers, so the
+// product is an fma itself, with a zero that it cannot know (-0, so that every
+// product comes through as it is).
+struct Product {
+  f2 zero;
+  __device__ __forceinline__ f2 operator()(f2 a, f2 b) const { return fma2(a, b, zero); }
+};
+
 // Eight values from index i on (those past n read as 0 / are not written).
 template <typename T>
-__device__ __forceinline__ void get8(const T* p, int64_t i, int64_t n, bool vec, float (&f)[8]) {
+__device__ __forceinline__ void take(const T* p, int64_t i, int64_t n, bool vec, f2 (&f)[4]) {
   Raw8<T> r;
   if (vec) {
     load8<true>(p + i, 0, 8, r);
     widen(r, f);
-  } else {
+    return;
+  }
+  float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      f[e] = 0.f;
-      if (i + e < n) {
-        if constexpr (sizeof(T) == 2)
-          f[e] = __uint_as_float(static_cast<uint32_t>(p[i + e].bits) << 16);
-        else
-          f[e] = p[i + e];
-      }
+  for (int e = 0; e < 8; ++e) {
+    x[e] = 0.f;
+    if (i + e < n) {
+      if constexpr (sizeof(T) == 2)
+        x[e] = __uint_as_float(static_cast<uint32_t>(p[i + e].bits) << 16);
+      else
+        x[e] = p[i + e];
     }
   }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f[e] = pk(x[2 * e], x[2 * e + 1]);
 }
 template <typename T>
-__device__ __forceinline__ void set8(T* p, int64_t i, int64_t n, bool vec, const float (&f)[8]) {
+__device__ __forceinline__ void give(T* p, int64_t i, int64_t n, bool vec, const f2 (&f)[4]) {
   Raw8<T> r;
   narrow(f, r);
   if (vec) {
     store8<true>(p + i, 0, 8, r);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (i + e < n) {
-        if constexpr (sizeof(T) == 2) {
-          const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
-          p[i + e].bits = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
-        } else {
-          p[i + e] = f[e];
-        }
-      }
+    return;
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (i + e < n) {
+      if constexpr (sizeof(T) == 2) {
+        const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+        p[i + e].bits = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+      } else {
+        const float2 x = unpk(f[e >> 1]);
+        p[i + e] = e & 1 ? x.y : x.x;
+      }
+    }
 }
 // Eight code bytes.
 __device__ __forceinline__ uint2 get_codes(const uint8_t* p, int64_t i, int64_t n, bool vec) {
@@ -139,15 +154,14 @@ __device__ __forceinline__ void set_codes(uint8_t* p, int64_t i, int64_t n, bool
   for (int e = 0; e < 8; ++e)
     if (i + e < n) p[i + e] = static_cast<uint8_t>(w[e >> 2] >> (8 * (e & 3)));
 }
-__device__ __forceinline__ void decode8(uint2 q, float scale, float (&f)[8]) {
+__device__ __forceinline__ void decode8(uint2 q, float scale, f2 (&f)[4]) {
   const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
     const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
         static_cast<__nv_fp8x2_storage_t>(w[h >> 1] >> (16 * (h & 1))), __NV_E4M3);
     const float2 x = __half22float2(__half2(hr));
-    f[2 * h] = x.x * scale;
-    f[2 * h + 1] = x.y * scale;
+    f[h] = mul2(pk(x.x, x.y), pk(scale));  // exact
   }
 }
 // E8M0 byte of a block whose largest magnitude has the bits `top`.
@@ -169,6 +183,7 @@ template <typename PT, typename GT, bool MASTER, bool EIGHT, int MAX>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<MAX> tab) {
   const Consts& c = tab.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Product mul{pk(c.zero)};
   float coef = c.grad_scale;
   pdl_wait();
   if (c.part != nullptr) {  // the norm: every block adds the same partials in the same order
@@ -196,10 +211,10 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     const int64_t n = t.n;
     const int64_t i = static_cast<int64_t>(ch - t.chunk0) * kChunk + threadIdx.x * 8;
     const bool vec = t.vec && i + 8 <= n;
-    float p[8], g[8], m[8], v[8], root[8];
-    get8(static_cast<const GT*>(t.g), i, n, vec, g);
-    if (MASTER) get8(t.master, i, n, vec, p);
-    else get8(static_cast<const PT*>(t.p), i, n, vec, p);
+    f2 p[4], g[4], m[4], v[4], root[4];
+    take(static_cast<const GT*>(t.g), i, n, vec, g);
+    if (MASTER) take(t.master, i, n, vec, p);
+    else take(static_cast<const PT*>(t.p), i, n, vec, p);
     const int64_t blk = i / kBlock;  // the same for the whole warp
     if constexpr (EIGHT) {
       uint32_t bm = 0, bv = 0;
@@ -212,23 +227,28 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       decode8(qm, __uint_as_float(bm << 23), m);
       decode8(qv, __uint_as_float(bv << 23), v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], v[e]);
+      for (int e = 0; e < 4; ++e) v[e] = mul(v[e], v[e]);
     } else {
-      get8(static_cast<const float*>(t.m), i, n, vec, m);
-      get8(static_cast<const float*>(t.v), i, n, vec, v);
+      take(static_cast<const float*>(t.m), i, n, vec, m);
+      take(static_cast<const float*>(t.v), i, n, vec, v);
     }
+    const f2 coef2 = pk(coef), b1 = pk(c.b1), c1 = pk(c.c1), b2 = pk(c.b2), c2 = pk(c.c2),
+             keep = pk(t.keep), nlr = pk(-t.lr);
     uint32_t top_m = 0, top_r = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      g[e] = __fmul_rn(g[e], coef);
-      m[e] = __fadd_rn(__fmul_rn(c.b1, m[e]), __fmul_rn(c.c1, g[e]));
-      v[e] = __fadd_rn(__fmul_rn(c.b2, v[e]), __fmul_rn(__fmul_rn(c.c2, g[e]), g[e]));
-      root[e] = __fsqrt_rn(v[e]);
-      const float upd = __fdiv_rn(m[e], __fadd_rn(__fmul_rn(root[e], c.correct), c.eps));
-      p[e] = __fsub_rn(__fmul_rn(p[e], t.keep), __fmul_rn(t.lr, upd));
-      if (EIGHT && i + e < n) {
-        top_m = max(top_m, __float_as_uint(m[e]) & 0x7FFFFFFFu);
-        top_r = max(top_r, __float_as_uint(root[e]) & 0x7FFFFFFFu);
+    for (int e = 0; e < 4; ++e) {
+      g[e] = mul(g[e], coef2);
+      m[e] = add2(mul(b1, m[e]), mul(c1, g[e]));
+      v[e] = add2(mul(b2, v[e]), mul(mul(c2, g[e]), g[e]));
+      const float2 vv = unpk(v[e]), mm = unpk(m[e]);
+      const float r0 = __fsqrt_rn(vv.x), r1 = __fsqrt_rn(vv.y);
+      root[e] = pk(r0, r1);
+      const float2 den = unpk(add2(mul(root[e], pk(c.correct)), pk(c.eps)));
+      const f2 upd = pk(__fdiv_rn(mm.x, den.x), __fdiv_rn(mm.y, den.y));
+      p[e] = add2(mul(p[e], keep), mul(nlr, upd));
+      if (EIGHT) {  // values past n are 0: they do not raise the maximum
+        top_m = max(top_m, max(__float_as_uint(mm.x) & 0x7FFFFFFFu, __float_as_uint(mm.y) & 0x7FFFFFFFu));
+        top_r = max(top_r, max(__float_as_uint(r0) & 0x7FFFFFFFu, __float_as_uint(r1) & 0x7FFFFFFFu));
       }
     }
     if constexpr (EIGHT) {
@@ -238,11 +258,13 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       uint32_t wm[2] = {0, 0}, wr[2] = {0, 0};
 #pragma unroll
       for (int e = 0; e < 8; ++e, u += kDitherI) {
-        uint32_t q = encode(fabsf(m[e]), u >> 12, bm);
-        q |= m[e] < 0.f ? 128u : 0u;
+        const float2 m2 = unpk(m[e >> 1]), r2 = unpk(root[e >> 1]);
+        const float x = e & 1 ? m2.y : m2.x, r = e & 1 ? r2.y : r2.x;
+        uint32_t q = encode(fabsf(x), u >> 12, bm);
+        q |= x < 0.f ? 128u : 0u;
         wm[e >> 2] |= q << (8 * (e & 3));
-        q = encode(fabsf(root[e]), ~u >> 12, bv);
-        if (q < 1u && root[e] > 0.f) q = 1u;
+        q = encode(fabsf(r), ~u >> 12, bv);
+        if (q < 1u && r > 0.f) q = 1u;
         wr[e >> 2] |= q << (8 * (e & 3));
       }
       set_codes(static_cast<uint8_t*>(t.m), i, n, vec, make_uint2(wm[0], wm[1]));
@@ -252,42 +274,48 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         t.sc[2 * blk + 1] = static_cast<uint8_t>(bv);
       }
     } else {
-      set8(static_cast<float*>(t.m), i, n, vec, m);
-      set8(static_cast<float*>(t.v), i, n, vec, v);
+      give(static_cast<float*>(t.m), i, n, vec, m);
+      give(static_cast<float*>(t.v), i, n, vec, v);
     }
-    set8(static_cast<PT*>(t.p), i, n, vec, p);
-    if (MASTER) set8(t.master, i, n, vec, p);
+    give(static_cast<PT*>(t.p), i, n, vec, p);
+    if (MASTER) give(t.master, i, n, vec, p);
   }
 }
 
-__device__ __forceinline__ void add_square(float x, float& hi, float& lo) {
-  const float p = __fmul_rn(x, x);
-  const float e = __fmaf_rn(x, x, -p);
-  const float s = __fadd_rn(hi, p);
-  const float b = __fsub_rn(s, hi);
-  const float err = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(p, b));
+// hi + lo += x^2, elementwise: the exact error of the product and of the sum
+// with hi go to lo.
+__device__ __forceinline__ void add_square(f2 x, f2& hi, f2& lo, const Product& mul) {
+  const f2 minus = pk(-1.f);
+  const f2 p = mul(x, x);
+  const f2 e = fma2(x, x, mul(p, minus));
+  const f2 s = add2(hi, p);
+  const f2 b = fma2(hi, minus, s);                                    // s - hi
+  const f2 err = add2(fma2(fma2(b, minus, s), minus, hi), fma2(b, minus, p));
   hi = s;
-  lo = __fadd_rn(lo, __fadd_rn(err, e));
+  lo = add2(lo, add2(err, e));
 }
 
 template <int MAX>
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ NormTable<MAX> tab) {
   __shared__ double s_sum[kThreads / 32];
   pdl_wait();
-  float hi = 0.f, lo = 0.f;
+  const Product mul{pk(tab.zero)};
+  f2 hi = pk(0.f), lo = pk(0.f);
   int ti = 0;
   for (int ch = blockIdx.x; ch < tab.chunks; ch += gridDim.x) {
     while (ti + 1 < tab.n && ch >= tab.t[ti + 1].chunk0) ++ti;
     const NormTensor& t = tab.t[ti];
     const int64_t i = static_cast<int64_t>(ch - t.chunk0) * kChunk + threadIdx.x * 8;
     const bool vec = (reinterpret_cast<uintptr_t>(t.g) & 15u) == 0 && i + 8 <= t.n;
-    float g[8];
-    if (t.bf16) get8(static_cast<const bf16_t*>(t.g), i, t.n, vec, g);
-    else get8(static_cast<const float*>(t.g), i, t.n, vec, g);
+    f2 g[4];
+    if (t.bf16) take(static_cast<const bf16_t*>(t.g), i, t.n, vec, g);
+    else take(static_cast<const float*>(t.g), i, t.n, vec, g);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) add_square(g[e], hi, lo);
+    for (int e = 0; e < 4; ++e) add_square(g[e], hi, lo, mul);
   }
-  double s = static_cast<double>(hi) + static_cast<double>(lo);
+  const float2 h2 = unpk(hi), l2 = unpk(lo);
+  double s = (static_cast<double>(h2.x) + static_cast<double>(h2.y)) +
+             (static_cast<double>(l2.x) + static_cast<double>(l2.y));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = s;
@@ -379,6 +407,7 @@ cudaError_t step_kind(int kind, const moe_adamw_tensor* ts, int n, const moe_ada
 template <int MAX>
 cudaError_t norm_all(const moe_adamw_tensor* ts, int n, double* part, int* nparts, cudaStream_t s) {
   NormTable<MAX> tab;
+  tab.zero = -0.f;
   tab.n = tab.chunks = 0;
   *nparts = 0;
   auto flush = [&]() -> cudaError_t {
@@ -493,6 +522,7 @@ int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n, const moe_adamw_h
     return record_error(MOE_OK, "");
   }
   Consts c = {};
+  c.zero = -0.f;
   c.b1 = static_cast<float>(h->beta1);
   c.c1 = static_cast<float>(1.0 - h->beta1);
   c.b2 = static_cast<float>(h->beta2);

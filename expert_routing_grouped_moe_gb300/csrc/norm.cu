@@ -86,6 +86,8 @@ int moe_block_norm_fwd(const moe_norm_desc* desc, const void* x, const void* y, 
   a.T = desc->T; a.d = desc->d; a.W = norm_warps(desc->d);
   a.gate_kind = desc->gate; a.sigmoid = desc->gate_sigmoid;
   a.scale = desc->scale; a.eps = desc->eps; a.w_off = desc->w_offset;
+  rc = device_status_word(&a.status);
+  if (rc != MOE_OK) return rc;
   ProbeScope probe("block_norm_fwd", stream);
   const cudaError_t e = launch_norm_fwd(a, desc->x_type, desc->y_type, vec, stream);
   if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
@@ -95,7 +97,7 @@ int moe_block_norm_fwd(const moe_norm_desc* desc, const void* x, const void* y, 
 size_t moe_block_norm_workspace_size(int32_t T, int32_t d) {
   if (T < 0 || d <= 0 || d > kNormMaxD) return 0;
   const size_t rows = static_cast<size_t>(bwd_blocks(T, d)) * norm_groups(d);
-  return rows * 3 * static_cast<size_t>(d) * 4;
+  return rows * 2 * static_cast<size_t>(d) * 4;
 }
 
 int moe_block_norm_bwd(const moe_norm_desc* desc, const void* dr, const void* dn, const void* r,
@@ -107,21 +109,23 @@ int moe_block_norm_bwd(const moe_norm_desc* desc, const void* dr, const void* dn
   int rc = check_desc(desc);
   if (rc) return rc;
   // sums over the tokens, the only outputs that T = 0 has
-  float* sums[3] = {nullptr, nullptr, nullptr};
   NormArgs a = {};
-  a.sum_post = a.sum_pre = a.sum_gate = -1;
-  if (dw_post) { a.sum_post = a.nsum; sums[a.nsum++] = dw_post; }
-  if (dw_pre) { a.sum_pre = a.nsum; sums[a.nsum++] = dw_pre; }
-  if (dgate && desc->gate == MOE_GATE_CHANNEL) {
-    a.sum_gate = a.nsum;
-    sums[a.nsum++] = static_cast<float*>(dgate);
-  }
-  for (int i = 0; i < a.nsum; ++i)
-    if (reinterpret_cast<uintptr_t>(sums[i]) & 3u) return bad("a sum over the tokens is misaligned");
+  const bool sum_gate = dgate != nullptr && desc->gate == MOE_GATE_CHANNEL;
+  a.sum_y = dw_post != nullptr || sum_gate ? a.nsum++ : -1;
+  a.sum_r = dw_pre != nullptr ? a.nsum++ : -1;
+  for (const void* p : {static_cast<const void*>(dw_post), static_cast<const void*>(dw_pre),
+                        static_cast<const void*>(sum_gate ? dgate : nullptr)})
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return bad("a sum over the tokens is misaligned");
+  if ((dgate && !gate) || (dw_post && !w_post) || (dw_pre && !w_pre))
+    return bad("the gradient of an input that is not there");
+  a.dw_post = dw_post; a.dw_pre = dw_pre; a.gate = gate; a.dgate = dgate;
+  a.w_post = w_post; a.w_pre = w_pre;
+  a.gate_kind = desc->gate; a.sigmoid = desc->gate_sigmoid;
+  a.scale = desc->scale; a.eps = desc->eps; a.w_off = desc->w_offset;
   a.T = desc->T; a.d = desc->d; a.W = norm_warps(desc->d);
   const int blocks = bwd_blocks(desc->T, desc->d);
   if (desc->T == 0) {
-    const cudaError_t e = launch_norm_bwd(a, desc->x_type, desc->y_type, false, 0, sums, stream);
+    const cudaError_t e = launch_norm_bwd(a, desc->x_type, desc->y_type, false, 0, stream);
     if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
     return record_error(MOE_OK, "");
   }
@@ -132,8 +136,6 @@ int moe_block_norm_bwd(const moe_norm_desc* desc, const void* dr, const void* dn
   if (y == nullptr && (w_post != nullptr || dy != nullptr || desc->gate != MOE_GATE_NONE))
     return bad("w_post, dy and a gate go with y");
   if ((gate == nullptr) != (desc->gate == MOE_GATE_NONE)) return bad("gate and its kind go together");
-  if ((dgate && !gate) || (dw_post && !w_post) || (dw_pre && !w_pre))
-    return bad("the gradient of an input that is not there");
   if (dx == nullptr && dy == nullptr && dgate == nullptr && dw_post == nullptr && dw_pre == nullptr)
     return bad("nothing to compute");
   if (dr) NORM_PTR(dr, xs, vec);
@@ -154,16 +156,16 @@ int moe_block_norm_bwd(const moe_norm_desc* desc, const void* dr, const void* dn
     if (ws_bytes < moe_block_norm_workspace_size(desc->T, desc->d))
       return record_error(MOE_ERR_WORKSPACE, "norm workspace too small");
   }
-  a.x = dr; a.y = y; a.gate = gate; a.w_post = w_post; a.w_pre = w_pre;
+  a.x = dr; a.y = y;
   a.r = const_cast<void*>(r); a.n = const_cast<void*>(dn);
   a.rstd_y = const_cast<float*>(rstd_y); a.rstd_r = const_cast<float*>(rstd_r);
-  a.dx = dx; a.dy = dy; a.dgate = dgate;
+  a.dx = dx; a.dy = dy;
   a.part = static_cast<float*>(ws);
-  a.gate_kind = desc->gate; a.sigmoid = desc->gate_sigmoid;
-  a.scale = desc->scale; a.eps = desc->eps; a.w_off = desc->w_offset;
+  rc = device_status_word(&a.status);
+  if (rc != MOE_OK) return rc;
   ProbeScope probe("block_norm_bwd", stream);
   const cudaError_t e =
-      launch_norm_bwd(a, desc->x_type, desc->y_type, vec, blocks, sums, stream);
+      launch_norm_bwd(a, desc->x_type, desc->y_type, vec, blocks, stream);
   if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
   return record_error(MOE_OK, "");
 }

@@ -24,12 +24,22 @@ struct NormArgs {
   void* dy;
   void* dgate;
   float* part;        // bwd: column partial sums [rows of partials][nsum][d]
-  int sum_post, sum_pre, sum_gate;  // index of each column sum in part, -1: not wanted
+  float *dw_post, *dw_pre;
+  int sum_y, sum_r;   // index of each column sum in part, -1: not wanted
   int nsum;
   int64_t T;
   int d, W;           // columns; warps that share a row
   int gate_kind, sigmoid;
   float scale, eps, w_off;
+  int stages, tile;   // ring: tiles held and bytes of one; 0: rows are read directly
+  int* status;
+};
+
+// The vectors [d] that a kernel applies to every row are kept in registers while
+// a thread has at most two shares of a row, else read again for each row.
+template <int NV>
+struct RowConst {
+  f2 f[NV <= 2 ? NV : 1][4];
 };
 
 // A row's shares: NV of 8 values for each thread of W warps, 32 W NV 8 >= d.
@@ -41,45 +51,147 @@ inline int norm_nv(int d) { return d <= 4096 ? 1 : d <= 8192 ? 2 : 4; }
 inline int norm_warps(int d) { const int per = 256 * norm_nv(d); return (d + per - 1) / per; }
 inline int norm_groups(int d) { const int w = norm_warps(d); return w >= 8 ? 1 : 8 / w; }
 
-// Sums v over the W warps of this thread's row group (all threads of the block
-// call it, same W).  buf: two arrays of 32 warps x 4; the caller alternates
-// them, so one barrier per call is enough: a warp writes an array again only
-// after the barrier of the call in between, which every reader has passed.
+// Sums v[0..K) (K = 1 or 3) over the W <= 16 warps of this thread's row group;
+// all threads of the block call it.  buf: 16 warps x 4 values, one of two
+// arrays that the caller alternates, so one barrier per call is enough: a warp
+// writes an array again only after the barrier of the call in between, which
+// every reader has passed.
+// Three sums: the first two exchanges halve what a lane carries (lanes 0-7 end
+// with v[0], 8-15 with v[1], 16-23 with v[2]): 6 shuffles instead of 15.
 template <int K>
-__device__ __forceinline__ void row_sum(float (&v)[K], float (*buf)[4], int W, int warp,
-                                        int first) {
+__device__ __forceinline__ void row_sum(float (&v)[K], float (*buf)[4], int W, int warp, int first) {
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  if (K == 1) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+    for (int o = 16; o > 0; o >>= 1) v[0] += __shfl_xor_sync(kAll, v[0], o);
+    if (W == 1) return;
+    if (lane == 0) buf[warp][0] = v[0];
+    __syncthreads();
+    float t = (lane & 15) < W ? buf[first + (lane & 15)][0] : 0.f;
 #pragma unroll
-    for (int i = 0; i < K; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (W == 1) return;
-  if ((threadIdx.x & 31) == 0)
+    for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(kAll, t, o);
+    v[0] = t;
+  } else {
+    const bool up = lane & 16, right = lane & 8;
+    const float s0 = __shfl_xor_sync(kAll, up ? v[0] : v[2], 16);
+    const float s1 = __shfl_xor_sync(kAll, up ? v[1] : 0.f, 16);
+    const float x = (up ? v[2] : v[0]) + s0, y = (up ? 0.f : v[1]) + s1;  // up: y unused
+    float t = (right ? y : x) + __shfl_xor_sync(kAll, right ? x : y, 8);
 #pragma unroll
-    for (int i = 0; i < K; ++i) buf[warp][i] = v[i];
-  __syncthreads();
+    for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(kAll, t, o);
+    if (W == 1) {
+      v[0] = __shfl_sync(kAll, t, 0);
+      v[1] = __shfl_sync(kAll, t, 8);
+      v[2] = __shfl_sync(kAll, t, 16);
+      return;
+    }
+    if ((lane & 7) == 0) buf[warp][lane >> 3] = t;
+    __syncthreads();
+    const int q = lane >> 2;
+    t = q < W ? buf[first + q][lane & 3] : 0.f;
+    if (q + 8 < W) t += buf[first + q + 8][lane & 3];
 #pragma unroll
-  for (int i = 0; i < K; ++i) v[i] = 0.f;
-  for (int w = 0; w < W; ++w) {
-    const float4 q = *reinterpret_cast<const float4*>(buf[first + w]);
-    v[0] += q.x;
-    if (K > 1) v[1] += q.y;
-    if (K > 2) v[2] += q.z;
+    for (int o = 16; o >= 4; o >>= 1) t += __shfl_xor_sync(kAll, t, o);
+    v[0] = __shfl_sync(kAll, t, 0);
+    v[1] = __shfl_sync(kAll, t, 1);
+    v[2] = __shfl_sync(kAll, t, 2);
   }
 }
 
-// a(gate) and its derivative.
+// a(gate) and its derivative; sigmoid from e^-|g|, so neither a nor 1 - a cancels.
 __device__ __forceinline__ void gate_value(float g, int sigmoid, float& a, float& da) {
   if (sigmoid) {
-    a = 1.f / (1.f + expf(-g));
-    da = a * (1.f / (1.f + expf(g)));  // 1 - a without its cancellation
+    const float e = expf(-fabsf(g));
+    const float big = __fdividef(1.f, 1.f + e), small = e * big;
+    a = g >= 0.f ? big : small;
+    da = big * small;
+    if (g != g) a = da = g;
   } else {
     a = g;
     da = 1.f;
   }
 }
 
+__device__ __forceinline__ f2 gate_pair(f2 g, int sigmoid) {
+  if (!sigmoid) return g;
+  const float2 x = unpk(g);
+  float a, b, unused;
+  gate_value(x.x, 1, a, unused);
+  gate_value(x.y, 1, b, unused);
+  return pk(a, b);
+}
+
+// How a kernel is told the gate's kind: fixed when it is compiled, or GATE_ANY.
+constexpr int kGateRow = 0, kGateChannel = 1, kGateElement = 2, kGateAny = 3;
+template <int GATE>
+__device__ __forceinline__ bool gate_is(int kind, int want) {
+  if (GATE == kGateRow) return false;
+  if (GATE == kGateChannel) return want == MOE_GATE_CHANNEL;
+  if (GATE == kGateElement) return want == MOE_GATE_ELEMENT;
+  return kind == want;
+}
+inline int gate_class(int kind) {
+  return kind == MOE_GATE_CHANNEL ? kGateChannel : kind == MOE_GATE_ELEMENT ? kGateElement : kGateRow;
+}
+
+// ---- rows staged through shared memory ---------------------------------------
+// A tile is the rows of a block's groups, consecutive in memory: one bulk copy
+// for each input.  A ring of `stages` tiles is filled ahead by thread 0; a
+// tile's place is filled again after the first block-wide barrier of the next
+// tile, which every thread reaches after its last read of this one.
+struct RingSrc {
+  const void* p;   // [T,d] input, NULL: none
+  int esize;       // bytes of an element
+};
+constexpr int kRingSrcs = 5, kRingMaxStages = 4;
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// The tile of rows [base, base + groups) into `stage`; inputs one after the other.
+__device__ __forceinline__ void ring_fill(const RingSrc (&src)[kRingSrcs], uint8_t* stage,
+                                          uint64_t* bar, int64_t base, int64_t T, int groups, int d) {
+  const int64_t left = T - base;
+  const int rows = left < groups ? static_cast<int>(left) : groups;
+  uint32_t total = 0;
+#pragma unroll
+  for (int i = 0; i < kRingSrcs; ++i)
+    if (src[i].p != nullptr) total += static_cast<uint32_t>(rows * d * src[i].esize);
+  mbar_expect_tx(bar, total);
+  int at = 0;
+#pragma unroll
+  for (int i = 0; i < kRingSrcs; ++i)
+    if (src[i].p != nullptr) {
+      bulk_load(stage + at, static_cast<const uint8_t*>(src[i].p) + base * d * src[i].esize,
+                static_cast<uint32_t>(rows * d * src[i].esize), bar);
+      at += groups * d * src[i].esize;
+    }
+}
+
+// After a wait that gave up: the copies still in flight, once more with a limit
+// (in a normal run every copy issued has been waited for).
+__device__ __forceinline__ void ring_drain(uint64_t* full, int stages, int stage, int phase) {
+  int never = 0;
+  for (int q = 0; q < stages; ++q) mbar_wait(&full[q], phase ^ (q < stage ? 0 : 1), &never, 1000000000ull);
+}
+
+// Stages of a ring of `tile` bytes each: as many, up to 4, as leave room for
+// `per` blocks on an SM; 0 when not even two fit one block.
+constexpr int kRingBytes = 208 * 1024;
+// Fewer tiles than this are read directly (a block would have one or two).
+constexpr int kNormRingTiles = 2 * kSMs;
+inline int ring_stages(size_t tile, int per) {
+  const int64_t room = kRingBytes / per, n = room / static_cast<int64_t>(tile);
+  return n >= kRingMaxStages ? kRingMaxStages : n >= 2 ? static_cast<int>(n) : per > 1 ? ring_stages(tile, per - 1) : 0;
+}
+
 cudaError_t launch_norm_fwd(const NormArgs& a, int x_type, int y_type, bool vec, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormArgs& a, int x_type, int y_type, bool vec, int blocks,
-                            float* const (&sums)[3], cudaStream_t s);
+                            cudaStream_t s);
 
 }  // namespace moe

@@ -1,0 +1,224 @@
+// Backward of norm_fwd.cu, in one pass over the rows.  With rh = r rstd_r,
+// yh = y rstd_y, u = w_pre + off, q = w_post + off:
+//   e = dr + rstd_r dn u,  c1 = mean(dn u rh),  t = e - rstd_r c1 rh        dx = t
+//   p = yh q (or y);  dp = s a t;  dy = rstd_y (dp q - yh mean(dp p))      (or dp)
+//   dgate = s a' t p, summed over what the gate is broadcast over
+//   dw_pre = sum_rows dn rh;  dw_post = sum_rows dp yh
+// t is linear in c1, so one reduction gives every row sum:
+//   S1 = sum dn u rh,  S2 = sum A p e,  S3 = sum A p rh,
+//   sum A p t = S2 - rstd_r c1 S3     (A = a(gate) where it varies along the row, else 1)
+// Column sums are kept in registers over the rows of a block, written once as
+// partials and added by a second kernel in a fixed order (no atomics).  Two
+// give all three gradients: sum dn rh = dw_pre, and with Y = yh (or y)
+//   no gate, token, element: S = sum a t Y,  dw_post = s S
+//   channel:                 S = sum t Y,    dw_post = s a S,  dgate = s a' q S
+#pragma once
+
+#include "norm.cuh"
+
+namespace moe {
+
+// The two families, compiled apart: rows read directly (any width, alignment
+// and gate; column sums always kept) and rows through the ring.
+cudaError_t launch_norm_bwd_direct(const NormArgs& a, int x_type, int y_type, bool vec, int blocks,
+                                   cudaStream_t s);
+cudaError_t launch_norm_bwd_ring(const NormArgs& a, int x_type, int y_type, int blocks, cudaStream_t s);
+
+template <typename XT, typename YT, bool VEC, int NV, int GATE, bool SUMS, bool RING>
+__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormArgs a) {
+  extern __shared__ __align__(128) uint8_t s_tiles[];
+  __shared__ float s_red[2][16][4];
+  __shared__ uint64_t s_full[kRingMaxStages];
+  __shared__ int s_abort;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int W = a.W, groups = (blockDim.x >> 5) / W;
+  const int grp = warp / W, first = grp * W;
+  const int v0 = (warp - first) * 32 + lane;
+  const int d = a.d;
+  const bool has_y = a.y != nullptr, post = a.w_post != nullptr, pre = a.w_pre != nullptr;
+  const bool channel = gate_is<GATE>(a.gate_kind, MOE_GATE_CHANNEL);
+  const bool element = gate_is<GATE>(a.gate_kind, MOE_GATE_ELEMENT);
+  const bool sum_gate_row = a.gate_kind == MOE_GATE_TOKEN && a.dgate != nullptr;
+  const float inv_d = 1.f / static_cast<float>(d);
+  const RingSrc src[kRingSrcs] = {{a.x, sizeof(XT)},
+                                  {pre ? a.r : nullptr, sizeof(XT)},
+                                  {pre ? a.n : nullptr, sizeof(YT)},
+                                  {a.y, sizeof(YT)},
+                                  {element ? a.gate : nullptr, sizeof(YT)}};
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  int64_t base = static_cast<int64_t>(blockIdx.x) * groups;
+  f2 acc_y[NV][4], acc_r[NV][4];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc_y[i][e] = acc_r[i][e] = pk(0.f);
+  if (RING) {
+    if (threadIdx.x == 0) {
+      s_abort = 0;
+      for (int q = 0; q < a.stages; ++q) mbar_init(&s_full[q], 1);
+      fence_mbar_init();
+    }
+    __syncthreads();
+  }
+  pdl_wait();
+  if (RING && threadIdx.x == 0)
+    for (int q = 0; q < a.stages && base + q * step < a.T; ++q)
+      ring_fill(src, s_tiles + q * a.tile, &s_full[q], base + q * step, a.T, groups, d);
+  // per column: k = (w_post + off) a(channel gate), u = w_pre + off
+  auto make_k = [&](int v, f2 (&k)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) k[e] = pk(1.f);
+    if (post) {
+      get8<float, VEC>(a.w_post, v, d, k);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) k[e] = add2(k[e], pk(a.w_off));
+    }
+    if (channel) {
+      f2 g[4];
+      get8<float, VEC>(static_cast<const float*>(a.gate), v, d, g);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) k[e] = mul2(k[e], gate_pair(g[e], a.sigmoid));
+    }
+  };
+  auto make_u = [&](int v, f2 (&u)[4]) {
+    get8<float, VEC>(a.w_pre, v, d, u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[e] = add2(u[e], pk(a.w_off));
+  };
+  RowConst<NV> ck, cu;
+  if (NV <= 2) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (has_y) make_k(v0 + i * 32 * W, ck.f[NV <= 2 ? i : 0]);
+      if (pre) make_u(v0 + i * 32 * W, cu.f[NV <= 2 ? i : 0]);
+    }
+  }
+  int turn = 0, stage = 0, phase = 0, before = 0;
+  for (; base < a.T; base += step, turn ^= 1) {
+    const int64_t row = base + grp;
+    const bool ok = row < a.T;
+    const int64_t off = ok ? row * d : 0;
+    const int dd = ok ? d : 0;
+    const XT* pdr = static_cast<const XT*>(a.x) + off;
+    const XT* pr = static_cast<const XT*>(a.r) + off;
+    const YT* pdn = static_cast<const YT*>(a.n) + off;
+    const YT* py = static_cast<const YT*>(a.y) + off;
+    const YT* pg = static_cast<const YT*>(a.gate) + off;
+    const float rs_r = pre && ok ? a.rstd_r[row] : 0.f;
+    const float rs_y = !post ? 1.f : ok ? a.rstd_y[row] : 0.f;
+    float a_row = 1.f, da_row = 0.f;
+    if (a.gate_kind == MOE_GATE_TOKEN)
+      gate_value(ok ? static_cast<const float*>(a.gate)[row] : 0.f, a.sigmoid, a_row, da_row);
+    if constexpr (RING) {
+      if (!mbar_wait(&s_full[stage], phase, &s_abort, kWaitTimeoutNs) && threadIdx.x == 0)
+        atomicCAS(a.status, 0, kErrTimeout);
+      const uint8_t* t = s_tiles + stage * a.tile;
+      pdr = reinterpret_cast<const XT*>(t) + grp * d;
+      if (a.x != nullptr) t += groups * d * sizeof(XT);
+      pr = reinterpret_cast<const XT*>(t) + grp * d;
+      if (pre) t += groups * d * sizeof(XT);
+      pdn = reinterpret_cast<const YT*>(t) + grp * d;
+      if (pre) t += groups * d * sizeof(YT);
+      py = reinterpret_cast<const YT*>(t) + grp * d;
+      if (has_y) t += groups * d * sizeof(YT);
+      pg = reinterpret_cast<const YT*>(t) + grp * d;
+    }
+    // pass 1: e in place of dr; the row sums, of r and y as they are (their rstd
+    // factors follow)
+    f2 ev[NV][4], r[NV][4], y[NV][4];
+    f2 sum_g = pk(0.f), sum_e = pk(0.f), sum_h = pk(0.f);
+    const f2 rs_r2 = pk(rs_r);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = v0 + i * 32 * W;
+      f2 k[4], dn[4];
+      get8<XT, VEC>(pdr, v, a.x != nullptr ? dd : 0, ev[i]);
+      get8<XT, VEC>(pr, v, pre ? dd : 0, r[i]);
+      get8<YT, VEC>(py, v, has_y ? dd : 0, y[i]);
+      if (pre) {
+        get8<YT, VEC>(pdn, v, dd, dn);
+        if (NV > 2) make_u(v, k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (SUMS) acc_r[i][e] = fma2(dn[e], mul2(r[i][e], rs_r2), acc_r[i][e]);
+          const f2 g = mul2(dn[e], NV > 2 ? k[e] : cu.f[NV <= 2 ? i : 0][e]);
+          ev[i][e] = fma2(rs_r2, g, ev[i][e]);
+          sum_g = fma2(g, r[i][e], sum_g);
+        }
+      }
+      if (post || sum_gate_row) {
+        if (NV > 2) make_k(v, k);
+        if (element) get8<YT, VEC>(pg, v, dd, dn);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          f2 ap = mul2(y[i][e], NV > 2 ? k[e] : ck.f[NV <= 2 ? i : 0][e]);
+          if (element) ap = mul2(ap, gate_pair(dn[e], a.sigmoid));
+          sum_e = fma2(ap, ev[i][e], sum_e);
+          sum_h = fma2(ap, r[i][e], sum_h);
+        }
+      }
+    }
+    float sum[3] = {sum2(sum_g), sum2(sum_e), sum2(sum_h)};
+    if (pre || post || sum_gate_row) row_sum<3>(sum, s_red[turn], W, warp, first);
+    if (RING && threadIdx.x == 0 && base >= step) {  // the previous tile's place is free
+      const int64_t next = base + (a.stages - 1) * step;
+      if (next < a.T) ring_fill(src, s_tiles + before * a.tile, &s_full[before], next, a.T, groups, d);
+    }
+    const float c1 = rs_r * (rs_r * (rs_r * (sum[0] * inv_d)));  // t = e - c1 r
+    const float apt = rs_y * fmaf(-c1, sum[2], sum[1]);     // sum A p t
+    if (sum_gate_row && ok && v0 == 0)
+      static_cast<float*>(a.dgate)[row] = a.scale * da_row * apt;
+    const float fac = a.scale * a_row;                      // dp = fac A t
+    const float c2 = post ? fac * apt * inv_d * rs_y * rs_y : 0.f;  // dy = rstd_y fac k t - c2 y
+    const f2 c1n = pk(-c1), c2n = pk(-c2), facy = pk(fac * rs_y), ry2 = pk(a_row * rs_y);
+    // pass 2: the outputs
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = v0 + i * 32 * W;
+      f2 k[4], o[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ev[i][e] = fma2(c1n, r[i][e], ev[i][e]);  // t
+      put8<XT, VEC>(static_cast<XT*>(a.dx) + off, v, a.dx != nullptr ? dd : 0, ev[i]);
+      if (!has_y) continue;
+      if (NV > 2) make_k(v, k);
+      f2 g[4], dg[4];
+      if (element) {
+        get8<YT, VEC>(pg, v, dd, g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 gv = unpk(g[e]);
+          float a0, a1, d0, d1;
+          gate_value(gv.x, a.sigmoid, a0, d0);
+          gate_value(gv.y, a.sigmoid, a1, d1);
+          g[e] = pk(a0, a1);
+          dg[e] = pk(d0, d1);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const f2 kk = NV > 2 ? k[e] : ck.f[NV <= 2 ? i : 0][e];
+        const f2 at = element ? mul2(g[e], ev[i][e]) : ev[i][e];
+        const f2 yh = mul2(y[i][e], ry2);  // a_row Y
+        if (SUMS) acc_y[i][e] = fma2(at, yh, acc_y[i][e]);
+        o[e] = mul2(mul2(at, kk), facy);
+        if (post) o[e] = fma2(y[i][e], c2n, o[e]);
+        if (element) dg[e] = mul2(mul2(dg[e], mul2(ev[i][e], pk(a.scale))), mul2(yh, kk));
+      }
+      put8<YT, VEC>(static_cast<YT*>(a.dy) + off, v, a.dy != nullptr ? dd : 0, o);
+      if (element && a.dgate != nullptr) put8<YT, VEC>(static_cast<YT*>(a.dgate) + off, v, dd, dg);
+    }
+    before = stage;
+    if (++stage == a.stages) { stage = 0; phase ^= 1; }
+  }
+  if (RING && s_abort) ring_drain(s_full, a.stages, stage, phase);
+  if (!SUMS) return;
+  float* part = a.part + (static_cast<int64_t>(blockIdx.x) * groups + grp) * a.nsum * d;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = v0 + i * 32 * W;
+    if (a.sum_y >= 0) put8<float, VEC>(part + static_cast<int64_t>(a.sum_y) * d, v, d, acc_y[i]);
+    if (a.sum_r >= 0) put8<float, VEC>(part + static_cast<int64_t>(a.sum_r) * d, v, d, acc_r[i]);
+  }
+}
+
+}  // namespace moe

@@ -1,0 +1,40 @@
+// Backward of the norms around a block, rows through the ring of bulk copies.
+#include "norm_bwd.cuh"
+
+namespace moe {
+namespace {
+
+template <typename XT, typename YT, int NV, int GATE, bool SUMS>
+cudaError_t go(const NormArgs& a, int blocks, cudaStream_t s) {
+  auto kern = norm_bwd_kernel<XT, YT, true, NV, GATE, SUMS, true>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(norm_groups(a.d) * a.W * 32),
+                    static_cast<size_t>(a.stages) * a.tile, s, a);
+}
+
+template <typename XT, typename YT, int NV, bool SUMS>
+cudaError_t pick_gate(const NormArgs& a, int blocks, cudaStream_t s) {
+  switch (gate_class(a.gate_kind)) {
+    case kGateRow: return go<XT, YT, NV, kGateRow, SUMS>(a, blocks, s);
+    case kGateChannel: return go<XT, YT, NV, kGateChannel, SUMS>(a, blocks, s);
+    default: return go<XT, YT, NV, kGateElement, SUMS>(a, blocks, s);
+  }
+}
+
+template <typename XT, typename YT>
+cudaError_t pick(const NormArgs& a, int blocks, cudaStream_t s) {
+  if (norm_nv(a.d) == 1)
+    return a.nsum > 0 ? pick_gate<XT, YT, 1, true>(a, blocks, s) : pick_gate<XT, YT, 1, false>(a, blocks, s);
+  return a.nsum > 0 ? pick_gate<XT, YT, 2, true>(a, blocks, s) : pick_gate<XT, YT, 2, false>(a, blocks, s);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_bwd_ring(const NormArgs& a, int x_type, int y_type, int blocks, cudaStream_t s) {
+  if (x_type == MOE_BF16) return pick<bf16_t, bf16_t>(a, blocks, s);
+  return y_type == MOE_BF16 ? pick<float, bf16_t>(a, blocks, s) : pick<float, float>(a, blocks, s);
+}
+
+}  // namespace moe

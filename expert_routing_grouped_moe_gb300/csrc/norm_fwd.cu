@@ -10,9 +10,14 @@
 namespace moe {
 namespace {
 
-template <typename XT, typename YT, bool VEC, int NV, bool PERCOL>
+// RING: rows come through the ring of bulk copies (vector path, at least one
+// norm, rows of several warps); else each thread loads its share from memory.
+template <typename XT, typename YT, bool VEC, int NV, int GATE, bool RING>
 __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs a) {
-  __shared__ alignas(16) float s_red[2][32][4];
+  extern __shared__ __align__(128) uint8_t s_tiles[];
+  __shared__ float s_red[2][16][4];
+  __shared__ uint64_t s_full[kRingMaxStages];
+  __shared__ int s_abort;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int W = a.W, groups = (blockDim.x >> 5) / W;
   const int grp = warp / W, first = grp * W;
@@ -20,35 +25,101 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs a) {
   const int d = a.d;
   const bool has_y = a.y != nullptr, post = a.w_post != nullptr, pre = a.w_pre != nullptr;
   const float inv_d = 1.f / static_cast<float>(d);
-  int turn = 0;  // which of the two arrays the next row sum uses
+  const RingSrc src[kRingSrcs] = {
+      {a.x, sizeof(XT)}, {a.y, sizeof(YT)},
+      {gate_is<GATE>(a.gate_kind, MOE_GATE_ELEMENT) ? a.gate : nullptr, sizeof(YT)}, {nullptr, 0},
+      {nullptr, 0}};
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  int64_t base = static_cast<int64_t>(blockIdx.x) * groups;
+  if (RING) {
+    if (threadIdx.x == 0) {
+      s_abort = 0;
+      for (int q = 0; q < a.stages; ++q) mbar_init(&s_full[q], 1);
+      fence_mbar_init();
+    }
+    __syncthreads();
+  }
   pdl_wait();
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * groups; base < a.T;
-       base += static_cast<int64_t>(gridDim.x) * groups) {
+  if (RING && threadIdx.x == 0)
+    for (int q = 0; q < a.stages && base + q * step < a.T; ++q)
+      ring_fill(src, s_tiles + q * a.tile, &s_full[q], base + q * step, a.T, groups, d);
+  const bool channel = gate_is<GATE>(a.gate_kind, MOE_GATE_CHANNEL);
+  const bool element = gate_is<GATE>(a.gate_kind, MOE_GATE_ELEMENT);
+  // per column: k = (w_post + off) a(channel gate), u = w_pre + off
+  auto make_k = [&](int v, f2 (&k)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) k[e] = pk(1.f);
+    if (post) {
+      get8<float, VEC>(a.w_post, v, d, k);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) k[e] = add2(k[e], pk(a.w_off));
+    }
+    if (channel) {
+      f2 g[4];
+      get8<float, VEC>(static_cast<const float*>(a.gate), v, d, g);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) k[e] = mul2(k[e], gate_pair(g[e], a.sigmoid));
+    }
+  };
+  auto make_u = [&](int v, f2 (&u)[4]) {
+    get8<float, VEC>(a.w_pre, v, d, u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[e] = add2(u[e], pk(a.w_off));
+  };
+  RowConst<NV> ck, cu;
+  if (NV <= 2) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (has_y) make_k(v0 + i * 32 * W, ck.f[NV <= 2 ? i : 0]);
+      if (pre) make_u(v0 + i * 32 * W, cu.f[NV <= 2 ? i : 0]);
+    }
+  }
+  int turn = 0;  // which of the two arrays the next row sum uses
+  int stage = 0, phase = 0, before = 0;
+  for (; base < a.T; base += step) {
     const int64_t row = base + grp;
     const bool ok = row < a.T;
     const int64_t off = ok ? row * d : 0;
     const int dd = ok ? d : 0;  // no column of a row past the end
-    float x[NV][8], y[NV][8];
+    const XT* px = static_cast<const XT*>(a.x) + off;
+    const YT* py = static_cast<const YT*>(a.y) + off;
+    const YT* pg = static_cast<const YT*>(a.gate) + off;
+    if constexpr (RING) {
+      if (!mbar_wait(&s_full[stage], phase, &s_abort, kWaitTimeoutNs) && threadIdx.x == 0)
+        atomicCAS(a.status, 0, kErrTimeout);
+      const uint8_t* t = s_tiles + stage * a.tile;
+      px = reinterpret_cast<const XT*>(t) + grp * d;
+      if (a.x != nullptr) t += groups * d * sizeof(XT);
+      py = reinterpret_cast<const YT*>(t) + grp * d;
+      if (has_y) t += groups * d * sizeof(YT);
+      pg = reinterpret_cast<const YT*>(t) + grp * d;
+    }
+    // after the first barrier of this tile: the previous tile's place is free
+    auto refill = [&]() {
+      if (RING && threadIdx.x == 0 && base >= step) {
+        const int64_t next = base + (a.stages - 1) * step;
+        if (next < a.T) ring_fill(src, s_tiles + before * a.tile, &s_full[before], next, a.T, groups, d);
+      }
+    };
+    f2 x[NV][4], y[NV][4];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = v0 + i * 32 * W;
-      Raw8<XT> rx;
-      Raw8<YT> ry;
-      load8<VEC>(static_cast<const XT*>(a.x) + off, v, a.x != nullptr ? dd : 0, rx);
-      load8<VEC>(static_cast<const YT*>(a.y) + off, v, has_y ? dd : 0, ry);
-      widen(rx, x[i]);
-      widen(ry, y[i]);
+      get8<XT, VEC>(px, v, a.x != nullptr ? dd : 0, x[i]);
+      get8<YT, VEC>(py, v, has_y ? dd : 0, y[i]);
     }
     if (has_y) {
       float rs = 1.f;
       if (post) {
-        float sum[1] = {0.f};
+        f2 ss = pk(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum[0] = fmaf(y[i][e], y[i][e], sum[0]);
+          for (int e = 0; e < 4; ++e) ss = fma2(y[i][e], y[i][e], ss);
+        float sum[1] = {sum2(ss)};
         row_sum<1>(sum, s_red[turn], W, warp, first);
         turn ^= 1;
+        refill();
         rs = rsqrtf(fmaf(sum[0], inv_d, a.eps));
         if (ok && v0 == 0) a.rstd_y[row] = rs;
       }
@@ -58,93 +129,104 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs a) {
         gate_value(ok ? static_cast<const float*>(a.gate)[row] : 0.f, a.sigmoid, g, dg);
         fac *= g;
       }
+      const f2 fac2 = pk(fac);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = v0 + i * 32 * W;
-        float w[8];
-        if (post) {
-          load8f<VEC>(a.w_post, v, d, w);
+        f2 k[4];
+        if (NV > 2) make_k(v, k);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[i][e] *= w[e] + a.w_off;
-        }
-        if (PERCOL && a.gate_kind >= MOE_GATE_CHANNEL) {
-          if (a.gate_kind == MOE_GATE_CHANNEL) {
-            load8f<VEC>(static_cast<const float*>(a.gate), v, d, w);
-          } else {
-            Raw8<YT> rg;
-            load8<VEC>(static_cast<const YT*>(a.gate) + off, v, dd, rg);
-            widen(rg, w);
-          }
+        for (int e = 0; e < 4; ++e) y[i][e] = mul2(y[i][e], NV > 2 ? k[e] : ck.f[NV <= 2 ? i : 0][e]);
+        if (element) {
+          get8<YT, VEC>(pg, v, dd, k);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float g, dg;
-            gate_value(w[e], a.sigmoid, g, dg);
-            y[i][e] *= g;
-          }
+          for (int e = 0; e < 4; ++e) y[i][e] = mul2(y[i][e], gate_pair(k[e], a.sigmoid));
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] = fmaf(fac, y[i][e], x[i][e]);
+        for (int e = 0; e < 4; ++e) x[i][e] = fma2(fac2, y[i][e], x[i][e]);
         put8<XT, VEC>(static_cast<XT*>(a.r) + off, v, dd, x[i]);
       }
     }
     if (pre) {
-      float sum[1] = {0.f};
+      f2 ss = pk(0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[0] = fmaf(x[i][e], x[i][e], sum[0]);
+        for (int e = 0; e < 4; ++e) ss = fma2(x[i][e], x[i][e], ss);
+      float sum[1] = {sum2(ss)};
       row_sum<1>(sum, s_red[turn], W, warp, first);
       turn ^= 1;
+      if (!post) refill();
       const float rs = rsqrtf(fmaf(sum[0], inv_d, a.eps));
       if (ok && v0 == 0) a.rstd_r[row] = rs;
+      const f2 rs2 = pk(rs);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int v = v0 + i * 32 * W;
-        float w[8];
-        load8f<VEC>(a.w_pre, v, d, w);
+        f2 u[4];
+        if (NV > 2) make_u(v, u);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] *= rs * (w[e] + a.w_off);
+        for (int e = 0; e < 4; ++e)
+          x[i][e] = mul2(mul2(x[i][e], rs2), NV > 2 ? u[e] : cu.f[NV <= 2 ? i : 0][e]);
         put8<YT, VEC>(static_cast<YT*>(a.n) + off, v, dd, x[i]);
       }
     }
+    before = stage;
+    if (++stage == a.stages) { stage = 0; phase ^= 1; }
   }
+  if (RING && s_abort) ring_drain(s_full, a.stages, stage, phase);
 }
 
-template <typename XT, typename YT, bool VEC, int NV, bool PERCOL>
+template <typename XT, typename YT, bool VEC, int NV, int GATE, bool RING>
 cudaError_t go(const NormArgs& a, cudaStream_t s) {
   const int groups = norm_groups(a.d), threads = groups * a.W * 32;
-  // blocks that fit an SM, found once for each block size
-  static std::atomic<int> fit[kNormMaxWarps + 1];
-  int per = fit[threads / 32].load(std::memory_order_relaxed);
+  const size_t smem = static_cast<size_t>(a.stages) * a.tile;
+  auto kern = norm_fwd_kernel<XT, YT, VEC, NV, GATE, RING>;
+  if (RING) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kRingBytes);
+    if (e != cudaSuccess) return e;
+  }
+  // blocks that fit an SM, found once for each block size and ring
+  static std::atomic<int> fit[kNormMaxWarps + 1][kRingMaxStages + 1];
+  int per = fit[threads / 32][a.stages].load(std::memory_order_relaxed);
   if (per == 0) {
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-        &per, norm_fwd_kernel<XT, YT, VEC, NV, PERCOL>, threads, 0);
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, threads, smem);
     if (e != cudaSuccess) return e;
     if (per < 1) per = 1;
-    fit[threads / 32].store(per, std::memory_order_relaxed);
+    fit[threads / 32][a.stages].store(per, std::memory_order_relaxed);
   }
   const int64_t need = (a.T + groups - 1) / groups;
   const int64_t most = static_cast<int64_t>(per) * kSMs;
-  return launch_pdl(norm_fwd_kernel<XT, YT, VEC, NV, PERCOL>,
-                    dim3(static_cast<unsigned>(need < most ? need : most)), dim3(threads), 0, s, a);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(need < most ? need : most)), dim3(threads), smem,
+                    s, a);
+}
+
+template <typename XT, typename YT, int NV>
+cudaError_t pick_nv(const NormArgs& a, bool vec, cudaStream_t s) {
+  if constexpr (NV <= 2)
+    if (vec && a.stages > 0) switch (gate_class(a.gate_kind)) {
+        case kGateRow: return go<XT, YT, true, NV, kGateRow, true>(a, s);
+        case kGateChannel: return go<XT, YT, true, NV, kGateChannel, true>(a, s);
+        default: return go<XT, YT, true, NV, kGateElement, true>(a, s);
+      }
+  return vec ? go<XT, YT, true, NV, kGateAny, false>(a, s)
+             : go<XT, YT, false, NV, kGateAny, false>(a, s);
 }
 
 template <typename XT, typename YT>
-cudaError_t pick(const NormArgs& a, bool vec, cudaStream_t s) {
-  const bool percol = a.gate_kind >= MOE_GATE_CHANNEL;
-  switch (norm_nv(a.d)) {
-    case 1:
-      return !vec     ? go<XT, YT, false, 1, true>(a, s)
-             : percol ? go<XT, YT, true, 1, true>(a, s)
-                      : go<XT, YT, true, 1, false>(a, s);
-    case 2:
-      return !vec     ? go<XT, YT, false, 2, true>(a, s)
-             : percol ? go<XT, YT, true, 2, true>(a, s)
-                      : go<XT, YT, true, 2, false>(a, s);
-    default:
-      return !vec     ? go<XT, YT, false, 4, true>(a, s)
-             : percol ? go<XT, YT, true, 4, true>(a, s)
-                      : go<XT, YT, true, 4, false>(a, s);
+cudaError_t pick(NormArgs a, bool vec, cudaStream_t s) {
+  const int groups = norm_groups(a.d), nv = norm_nv(a.d);
+  a.tile = groups * a.d * static_cast<int>((a.x ? sizeof(XT) : 0) + (a.y ? sizeof(YT) : 0) +
+                                           (a.gate_kind == MOE_GATE_ELEMENT ? sizeof(YT) : 0));
+  const bool ring = vec && nv <= 2 && a.W > 1 && (a.w_post || a.w_pre) &&
+                    a.T > static_cast<int64_t>(kNormRingTiles) * groups;
+  a.stages = ring ? ring_stages(a.tile, groups * a.W * 32 > 256 ? 3 : 4) : 0;
+  if (a.stages == 0) a.tile = 0;
+  switch (nv) {
+    case 1: return pick_nv<XT, YT, 1>(a, vec, s);
+    case 2: return pick_nv<XT, YT, 2>(a, vec, s);
+    default: return pick_nv<XT, YT, 4>(a, vec, s);
   }
 }
 

