@@ -43,11 +43,11 @@ struct RowConst {
 };
 
 // A row's shares: NV of 8 values for each thread of W warps, 32 W NV 8 >= d.
-// The fewest values per thread whose row fits 16 warps, so that a row's loads
-// are spread over as many threads as there are.
+// One share for each thread while a row fits 12 warps (two such blocks fit an SM
+// at 80 registers), then as few as fit 16 warps.
 constexpr int kNormMaxWarps = 16;
 constexpr int kNormMaxD = kNormMaxWarps * 32 * 8 * 4;
-inline int norm_nv(int d) { return d <= 4096 ? 1 : d <= 8192 ? 2 : 4; }
+inline int norm_nv(int d) { return d <= 3072 ? 1 : d <= 8192 ? 2 : 4; }
 inline int norm_warps(int d) { const int per = 256 * norm_nv(d); return (d + per - 1) / per; }
 inline int norm_groups(int d) { const int w = norm_warps(d); return w >= 8 ? 1 : 8 / w; }
 

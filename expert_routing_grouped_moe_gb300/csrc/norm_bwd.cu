@@ -43,8 +43,8 @@ __global__ void __launch_bounds__(kSumThreads) norm_colsum_kernel(const NormArgs
 template <typename XT, typename YT, int NV>
 cudaError_t go(const NormArgs& a, bool vec, int blocks, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(blocks)), threads(norm_groups(a.d) * a.W * 32);
-  return vec ? launch_pdl(norm_bwd_kernel<XT, YT, true, NV, kGateAny, true, false>, grid, threads, 0, s, a)
-             : launch_pdl(norm_bwd_kernel<XT, YT, false, NV, kGateAny, true, false>, grid, threads, 0,
+  return vec ? launch_pdl(norm_bwd_kernel<XT, YT, true, NV, kGateAny, true, false, 512, 1>, grid, threads, 0, s, a)
+             : launch_pdl(norm_bwd_kernel<XT, YT, false, NV, kGateAny, true, false, 512, 1>, grid, threads, 0,
                           s, a);
 }
 

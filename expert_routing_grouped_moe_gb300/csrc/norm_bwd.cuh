@@ -24,8 +24,9 @@ cudaError_t launch_norm_bwd_direct(const NormArgs& a, int x_type, int y_type, bo
                                    cudaStream_t s);
 cudaError_t launch_norm_bwd_ring(const NormArgs& a, int x_type, int y_type, int blocks, cudaStream_t s);
 
-template <typename XT, typename YT, bool VEC, int NV, int GATE, bool SUMS, bool RING>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormArgs a) {
+// MAXT, MINB: threads of a block at most, blocks an SM holds at least.
+template <typename XT, typename YT, bool VEC, int NV, int GATE, bool SUMS, bool RING, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) {
   extern __shared__ __align__(128) uint8_t s_tiles[];
   __shared__ float s_red[2][16][4];
   __shared__ uint64_t s_full[kRingMaxStages];
@@ -93,6 +94,15 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormArgs a) {
       if (pre) make_u(v0 + i * 32 * W, cu.f[NV <= 2 ? i : 0]);
     }
   }
+  // the scalars of a row are read one tile ahead
+  float next_r = 0.f, next_y = 0.f, next_g = 0.f;
+  auto read_ahead = [&](int64_t row) {
+    const bool in = row < a.T;
+    next_r = pre && in ? a.rstd_r[row] : 0.f;
+    next_y = !post ? 1.f : in ? a.rstd_y[row] : 0.f;
+    if (a.gate_kind == MOE_GATE_TOKEN) next_g = in ? static_cast<const float*>(a.gate)[row] : 0.f;
+  };
+  read_ahead(base + grp);
   int turn = 0, stage = 0, phase = 0, before = 0;
   for (; base < a.T; base += step, turn ^= 1) {
     const int64_t row = base + grp;
@@ -104,11 +114,10 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormArgs a) {
     const YT* pdn = static_cast<const YT*>(a.n) + off;
     const YT* py = static_cast<const YT*>(a.y) + off;
     const YT* pg = static_cast<const YT*>(a.gate) + off;
-    const float rs_r = pre && ok ? a.rstd_r[row] : 0.f;
-    const float rs_y = !post ? 1.f : ok ? a.rstd_y[row] : 0.f;
+    const float rs_r = next_r, rs_y = next_y;
     float a_row = 1.f, da_row = 0.f;
-    if (a.gate_kind == MOE_GATE_TOKEN)
-      gate_value(ok ? static_cast<const float*>(a.gate)[row] : 0.f, a.sigmoid, a_row, da_row);
+    if (a.gate_kind == MOE_GATE_TOKEN) gate_value(next_g, a.sigmoid, a_row, da_row);
+    read_ahead(row + step);
     if constexpr (RING) {
       if (!mbar_wait(&s_full[stage], phase, &s_abort, kWaitTimeoutNs) && threadIdx.x == 0)
         atomicCAS(a.status, 0, kErrTimeout);

@@ -4,9 +4,9 @@
 namespace moe {
 namespace {
 
-template <typename XT, typename YT, int NV, int GATE, bool SUMS>
+template <typename XT, typename YT, int NV, int GATE, bool SUMS, int MAXT, int MINB>
 cudaError_t go(const NormArgs& a, int blocks, cudaStream_t s) {
-  auto kern = norm_bwd_kernel<XT, YT, true, NV, GATE, SUMS, true>;
+  auto kern = norm_bwd_kernel<XT, YT, true, NV, GATE, SUMS, true, MAXT, MINB>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
   if (e != cudaSuccess) return e;
@@ -14,20 +14,24 @@ cudaError_t go(const NormArgs& a, int blocks, cudaStream_t s) {
                     static_cast<size_t>(a.stages) * a.tile, s, a);
 }
 
-template <typename XT, typename YT, int NV, bool SUMS>
+template <typename XT, typename YT, int NV, bool SUMS, int MAXT, int MINB>
 cudaError_t pick_gate(const NormArgs& a, int blocks, cudaStream_t s) {
   switch (gate_class(a.gate_kind)) {
-    case kGateRow: return go<XT, YT, NV, kGateRow, SUMS>(a, blocks, s);
-    case kGateChannel: return go<XT, YT, NV, kGateChannel, SUMS>(a, blocks, s);
-    default: return go<XT, YT, NV, kGateElement, SUMS>(a, blocks, s);
+    case kGateRow: return go<XT, YT, NV, kGateRow, SUMS, MAXT, MINB>(a, blocks, s);
+    case kGateChannel: return go<XT, YT, NV, kGateChannel, SUMS, MAXT, MINB>(a, blocks, s);
+    default: return go<XT, YT, NV, kGateElement, SUMS, MAXT, MINB>(a, blocks, s);
   }
 }
 
 template <typename XT, typename YT>
 cudaError_t pick(const NormArgs& a, int blocks, cudaStream_t s) {
-  if (norm_nv(a.d) == 1)
-    return a.nsum > 0 ? pick_gate<XT, YT, 1, true>(a, blocks, s) : pick_gate<XT, YT, 1, false>(a, blocks, s);
-  return a.nsum > 0 ? pick_gate<XT, YT, 2, true>(a, blocks, s) : pick_gate<XT, YT, 2, false>(a, blocks, s);
+  if (norm_nv(a.d) == 1) {
+    if (a.nsum == 0) return pick_gate<XT, YT, 1, false, 384, 2>(a, blocks, s);
+    return a.W <= 8 ? pick_gate<XT, YT, 1, true, 256, 2>(a, blocks, s)
+                    : pick_gate<XT, YT, 1, true, 384, 2>(a, blocks, s);
+  }
+  return a.nsum > 0 ? pick_gate<XT, YT, 2, true, 512, 1>(a, blocks, s)
+                    : pick_gate<XT, YT, 2, false, 512, 1>(a, blocks, s);
 }
 
 }  // namespace

@@ -13,7 +13,7 @@ namespace {
 // RING: rows come through the ring of bulk copies (vector path, at least one
 // norm, rows of several warps); else each thread loads its share from memory.
 template <typename XT, typename YT, bool VEC, int NV, int GATE, bool RING>
-__global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(RING && NV == 1 ? 384 : 512, RING && NV == 1 ? 2 : 1) norm_fwd_kernel(const NormArgs a) {
   extern __shared__ __align__(128) uint8_t s_tiles[];
   __shared__ float s_red[2][16][4];
   __shared__ uint64_t s_full[kRingMaxStages];
@@ -74,6 +74,9 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs a) {
       if (pre) make_u(v0 + i * 32 * W, cu.f[NV <= 2 ? i : 0]);
     }
   }
+  // a token's gate is read one tile ahead
+  const float* tokens = a.gate_kind == MOE_GATE_TOKEN ? static_cast<const float*>(a.gate) : nullptr;
+  float next_g = tokens && base + grp < a.T ? tokens[base + grp] : 0.f;
   int turn = 0;  // which of the two arrays the next row sum uses
   int stage = 0, phase = 0, before = 0;
   for (; base < a.T; base += step) {
@@ -124,10 +127,11 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormArgs a) {
         if (ok && v0 == 0) a.rstd_y[row] = rs;
       }
       float fac = a.scale * rs;
-      if (a.gate_kind == MOE_GATE_TOKEN) {
+      if (tokens) {
         float g, dg;
-        gate_value(ok ? static_cast<const float*>(a.gate)[row] : 0.f, a.sigmoid, g, dg);
+        gate_value(next_g, a.sigmoid, g, dg);
         fac *= g;
+        next_g = row + step < a.T ? tokens[row + step] : 0.f;
       }
       const f2 fac2 = pk(fac);
 #pragma unroll
