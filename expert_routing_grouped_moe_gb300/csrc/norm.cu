@@ -6,13 +6,12 @@
 namespace moe {
 namespace {
 
-// Blocks of the backward, which also bound the rows of partial column sums: two
-// for each SM (a block holds up to 512 threads, two fill an SM's registers).
-constexpr int kNormBwdBlocks = 2 * kSMs;
-
+// Blocks of the backward, which also bound the rows of partial column sums: as
+// many as fit the SMs' registers, three up to 256 threads, else two.
 int bwd_blocks(int64_t T, int d) {
-  const int64_t g = norm_groups(d), need = (T + g - 1) / g;
-  return static_cast<int>(need < kNormBwdBlocks ? need : kNormBwdBlocks);
+  const NormShape sh = norm_bwd_shape(d);
+  const int64_t need = (T + sh.groups - 1) / sh.groups, most = (sh.threads() <= 256 ? 3 : 2) * kSMs;
+  return static_cast<int>(need < most ? need : most);
 }
 
 int bad(const char* msg) { return record_error(MOE_ERR_INVALID_ARG, msg); }
@@ -83,7 +82,7 @@ int moe_block_norm_fwd(const moe_norm_desc* desc, const void* x, const void* y, 
   NormArgs a = {};
   a.x = x; a.y = y; a.gate = gate; a.w_post = w_post; a.w_pre = w_pre;
   a.r = r; a.n = n; a.rstd_y = rstd_y; a.rstd_r = rstd_r;
-  a.T = desc->T; a.d = desc->d; a.W = norm_warps(desc->d);
+  a.T = desc->T; a.d = desc->d;
   a.gate_kind = desc->gate; a.sigmoid = desc->gate_sigmoid;
   a.scale = desc->scale; a.eps = desc->eps; a.w_off = desc->w_offset;
   rc = device_status_word(&a.status);
@@ -96,7 +95,7 @@ int moe_block_norm_fwd(const moe_norm_desc* desc, const void* x, const void* y, 
 
 size_t moe_block_norm_workspace_size(int32_t T, int32_t d) {
   if (T < 0 || d <= 0 || d > kNormMaxD) return 0;
-  const size_t rows = static_cast<size_t>(bwd_blocks(T, d)) * norm_groups(d);
+  const size_t rows = static_cast<size_t>(bwd_blocks(T, d)) * norm_bwd_shape(d).groups;
   return rows * 2 * static_cast<size_t>(d) * 4;
 }
 
@@ -122,7 +121,7 @@ int moe_block_norm_bwd(const moe_norm_desc* desc, const void* dr, const void* dn
   a.w_post = w_post; a.w_pre = w_pre;
   a.gate_kind = desc->gate; a.sigmoid = desc->gate_sigmoid;
   a.scale = desc->scale; a.eps = desc->eps; a.w_off = desc->w_offset;
-  a.T = desc->T; a.d = desc->d; a.W = norm_warps(desc->d);
+  a.T = desc->T; a.d = desc->d;
   const int blocks = bwd_blocks(desc->T, desc->d);
   if (desc->T == 0) {
     const cudaError_t e = launch_norm_bwd(a, desc->x_type, desc->y_type, false, 0, stream);

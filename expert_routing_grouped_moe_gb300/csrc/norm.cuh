@@ -42,14 +42,27 @@ struct RowConst {
   f2 f[NV <= 2 ? NV : 1][4];
 };
 
-// A row's shares: NV of 8 values for each thread of W warps, 32 W NV 8 >= d.
-// One share for each thread while a row fits 12 warps (two such blocks fit an SM
-// at 80 registers), then as few as fit 16 warps.
+// A row's shares: NV of 8 values for each thread of W <= 16 warps, 32 W NV 8 >= d;
+// as many groups of W warps, a row each, as fill 8 warps.
 constexpr int kNormMaxWarps = 16;
 constexpr int kNormMaxD = kNormMaxWarps * 32 * 8 * 4;
-inline int norm_nv(int d) { return d <= 3072 ? 1 : d <= 8192 ? 2 : 4; }
-inline int norm_warps(int d) { const int per = 256 * norm_nv(d); return (d + per - 1) / per; }
-inline int norm_groups(int d) { const int w = norm_warps(d); return w >= 8 ? 1 : 8 / w; }
+struct NormShape {
+  int nv, W, groups;
+  int threads() const { return 32 * W * groups; }
+};
+inline NormShape norm_shape(int d, int nv) {
+  NormShape s;
+  s.nv = nv;
+  s.W = (d + 256 * nv - 1) / (256 * nv);
+  s.groups = s.W >= 8 ? 1 : 8 / s.W;
+  return s;
+}
+// Forward: two shares for each thread beyond 1024 columns (fewer warps to wait for
+// one another; 4096x2048 12.9 us, with one share 16.4).
+inline NormShape norm_fwd_shape(int d) { return norm_shape(d, d <= 1024 ? 1 : d <= 8192 ? 2 : 4); }
+// Backward: one share for each thread while a row fits 12 warps (two such blocks
+// fit an SM at 80 registers), then as few as fit 16 warps.
+inline NormShape norm_bwd_shape(int d) { return norm_shape(d, d <= 3072 ? 1 : d <= 8192 ? 2 : 4); }
 
 // Sums v[0..K) (K = 1 or 3) over the W <= 16 warps of this thread's row group;
 // all threads of the block call it.  buf: 16 warps x 4 values, one of two
@@ -181,8 +194,18 @@ __device__ __forceinline__ void ring_drain(uint64_t* full, int stages, int stage
 }
 
 // Stages of a ring of `tile` bytes each: as many, up to 4, as leave room for
-// `per` blocks on an SM; 0 when not even two fit one block.
+// `per` blocks on an SM (each with `extra` bytes besides); 0 when not even two
+// fit one block.
 constexpr int kRingBytes = 208 * 1024;
+inline int ring_stages(size_t tile, int per, size_t extra) {
+  const int64_t n = (kRingBytes / per - static_cast<int64_t>(extra)) / static_cast<int64_t>(tile);
+  return n >= kRingMaxStages ? kRingMaxStages
+         : n >= 2            ? static_cast<int>(n)
+         : per > 1           ? ring_stages(tile, per - 1, extra)
+                             : 0;
+}
+// The backward's two vectors of per-column factors.
+inline size_t norm_const_bytes(const NormShape& s) { return static_cast<size_t>(s.threads()) * s.nv * 64; }
 // Fewer tiles than this are read directly (a block would have one or two).
 constexpr int kNormRingTiles = 2 * kSMs;
 inline int ring_stages(size_t tile, int per) {

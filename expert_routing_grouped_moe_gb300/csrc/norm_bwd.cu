@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kSumThreads) norm_colsum_kernel(const NormArgs
 
 template <typename XT, typename YT, int NV>
 cudaError_t go(const NormArgs& a, bool vec, int blocks, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(blocks)), threads(norm_groups(a.d) * a.W * 32);
+  const dim3 grid(static_cast<unsigned>(blocks)), threads(norm_bwd_shape(a.d).threads());
   return vec ? launch_pdl(norm_bwd_kernel<XT, YT, true, NV, kGateAny, true, false, 512, 1>, grid, threads, 0, s, a)
              : launch_pdl(norm_bwd_kernel<XT, YT, false, NV, kGateAny, true, false, 512, 1>, grid, threads, 0,
                           s, a);
@@ -50,7 +50,7 @@ cudaError_t go(const NormArgs& a, bool vec, int blocks, cudaStream_t s) {
 
 template <typename XT, typename YT>
 cudaError_t pick(const NormArgs& a, bool vec, int blocks, cudaStream_t s) {
-  switch (norm_nv(a.d)) {
+  switch (norm_bwd_shape(a.d).nv) {
     case 1: return go<XT, YT, 1>(a, vec, blocks, s);
     case 2: return go<XT, YT, 2>(a, vec, blocks, s);
     default: return go<XT, YT, 4>(a, vec, blocks, s);
@@ -69,23 +69,25 @@ cudaError_t launch_norm_bwd_direct(const NormArgs& a, int x_type, int y_type, bo
 cudaError_t launch_norm_bwd(const NormArgs& args, int x_type, int y_type, bool vec, int blocks,
                             cudaStream_t s) {
   NormArgs a = args;
+  const NormShape sh = norm_bwd_shape(a.d);
+  a.W = sh.W;
   cudaError_t e = cudaSuccess;
   if (blocks > 0) {
-    const int groups = norm_groups(a.d), xs = x_type == MOE_BF16 ? 2 : 4, ys = y_type == MOE_BF16 ? 2 : 4;
+    const int groups = sh.groups, xs = x_type == MOE_BF16 ? 2 : 4, ys = y_type == MOE_BF16 ? 2 : 4;
     const bool pre = a.w_pre != nullptr;
     a.tile = groups * a.d * ((a.x ? xs : 0) + (pre ? xs + ys : 0) + (a.y ? ys : 0) +
                              (a.gate_kind == MOE_GATE_ELEMENT ? ys : 0));
     const bool barrier = pre || a.w_post || (a.gate_kind == MOE_GATE_TOKEN && a.dgate);
-    const bool ring = vec && norm_nv(a.d) <= 2 && a.W > 1 && barrier &&
+    const bool ring = vec && sh.nv <= 2 && a.W > 1 && barrier &&
                       a.T > static_cast<int64_t>(kNormRingTiles) * groups;
-    a.stages = ring ? ring_stages(a.tile, 2) : 0;
+    a.stages = ring ? ring_stages(a.tile, sh.threads() <= 256 ? 3 : 2, norm_const_bytes(sh)) : 0;
     e = a.stages > 0 ? launch_norm_bwd_ring(a, x_type, y_type, blocks, s)
                      : launch_norm_bwd_direct(a, x_type, y_type, vec, blocks, s);
   }
   if (e != cudaSuccess || a.nsum == 0) return e;
   const int64_t n = static_cast<int64_t>(a.nsum) * a.d;
   return launch_pdl(norm_colsum_kernel, dim3(static_cast<unsigned>((n + 31) / 32)), dim3(kSumThreads),
-                    0, s, a, blocks * norm_groups(a.d));
+                    0, s, a, blocks * sh.groups);
 }
 
 }  // namespace moe

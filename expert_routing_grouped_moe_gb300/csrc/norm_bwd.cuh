@@ -86,14 +86,54 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) 
 #pragma unroll
     for (int e = 0; e < 4; ++e) u[e] = add2(u[e], pk(a.w_off));
   };
+  // Kept for all rows: in shared memory behind the ring (registers are what
+  // limits the blocks on an SM), in registers without one, or made again.
   RowConst<NV> ck, cu;
-  if (NV <= 2) {
+  float4* s_const = reinterpret_cast<float4*>(s_tiles + a.stages * a.tile) + threadIdx.x;
+  const int nthr = blockDim.x;
+  if (RING || NV <= 2) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (has_y) make_k(v0 + i * 32 * W, ck.f[NV <= 2 ? i : 0]);
-      if (pre) make_u(v0 + i * 32 * W, cu.f[NV <= 2 ? i : 0]);
+      f2 k[4], u[4];
+      if (has_y) make_k(v0 + i * 32 * W, k);
+      if (pre) make_u(v0 + i * 32 * W, u);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (!has_y) k[e] = pk(0.f);
+        if (!pre) u[e] = pk(0.f);
+        if (!RING) ck.f[NV <= 2 ? i : 0][e] = k[e], cu.f[NV <= 2 ? i : 0][e] = u[e];
+      }
+      if (RING) {
+        Raw8<float> q;
+        narrow(k, q);
+        s_const[(4 * i) * nthr] = q.a;
+        s_const[(4 * i + 1) * nthr] = q.b;
+        narrow(u, q);
+        s_const[(4 * i + 2) * nthr] = q.a;
+        s_const[(4 * i + 3) * nthr] = q.b;
+      }
     }
   }
+  auto get_const = [&](int i, int which, f2 (&f)[4]) {  // which: 0 k, 1 u
+    if (RING) {
+      Raw8<float> q;
+      q.a = s_const[(4 * i + 2 * which) * nthr];
+      q.b = s_const[(4 * i + 2 * which + 1) * nthr];
+      widen(q, f);
+    } else if (NV <= 2) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = which ? cu.f[NV <= 2 ? i : 0][e] : ck.f[NV <= 2 ? i : 0][e];
+    } else if (which) {
+      make_u(v0 + i * 32 * W, f);
+    } else {
+      make_k(v0 + i * 32 * W, f);
+    }
+  };
+  // offsets of this thread's row of each input in a tile
+  const int rx = groups * d * static_cast<int>(sizeof(XT)), ry_ = groups * d * static_cast<int>(sizeof(YT));
+  const int at_r = a.x != nullptr ? rx : 0, at_n = at_r + (pre ? rx : 0), at_y = at_n + (pre ? ry_ : 0),
+            at_g = at_y + (has_y ? ry_ : 0);
+  const int in_x = grp * d * static_cast<int>(sizeof(XT)), in_y = grp * d * static_cast<int>(sizeof(YT));
   // the scalars of a row are read one tile ahead
   float next_r = 0.f, next_y = 0.f, next_g = 0.f;
   auto read_ahead = [&](int64_t row) {
@@ -122,48 +162,57 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) 
       if (!mbar_wait(&s_full[stage], phase, &s_abort, kWaitTimeoutNs) && threadIdx.x == 0)
         atomicCAS(a.status, 0, kErrTimeout);
       const uint8_t* t = s_tiles + stage * a.tile;
-      pdr = reinterpret_cast<const XT*>(t) + grp * d;
-      if (a.x != nullptr) t += groups * d * sizeof(XT);
-      pr = reinterpret_cast<const XT*>(t) + grp * d;
-      if (pre) t += groups * d * sizeof(XT);
-      pdn = reinterpret_cast<const YT*>(t) + grp * d;
-      if (pre) t += groups * d * sizeof(YT);
-      py = reinterpret_cast<const YT*>(t) + grp * d;
-      if (has_y) t += groups * d * sizeof(YT);
-      pg = reinterpret_cast<const YT*>(t) + grp * d;
+      pdr = reinterpret_cast<const XT*>(t + in_x);
+      pr = reinterpret_cast<const XT*>(t + (at_r + in_x));
+      pdn = reinterpret_cast<const YT*>(t + (at_n + in_y));
+      py = reinterpret_cast<const YT*>(t + (at_y + in_y));
+      pg = reinterpret_cast<const YT*>(t + (at_g + in_y));
     }
     // pass 1: e in place of dr; the row sums, of r and y as they are (their rstd
     // factors follow)
-    f2 ev[NV][4], r[NV][4], y[NV][4];
+    constexpr bool kAgain = RING && NV >= 2;  // pass 2 reads r and y again: registers
+    constexpr int NK = kAgain ? 1 : NV;
+    f2 ev[NV][4], r_[NK][4], y_[NK][4];
     f2 sum_g = pk(0.f), sum_e = pk(0.f), sum_h = pk(0.f);
     const f2 rs_r2 = pk(rs_r);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = v0 + i * 32 * W;
+      if (col_of<VEC>(v, 0) >= dd) continue;  // no column of this share
       f2 k[4], dn[4];
-      get8<XT, VEC>(pdr, v, a.x != nullptr ? dd : 0, ev[i]);
-      get8<XT, VEC>(pr, v, pre ? dd : 0, r[i]);
-      get8<YT, VEC>(py, v, has_y ? dd : 0, y[i]);
+      f2(&r)[4] = r_[kAgain ? 0 : i];
+      f2(&y)[4] = y_[kAgain ? 0 : i];
+      if (a.x != nullptr) {
+        get8<XT, VEC>(pdr, v, d, ev[i]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ev[i][e] = pk(0.f);
+      }
+      if (has_y) get8<YT, VEC>(py, v, d, y);
       if (pre) {
-        get8<YT, VEC>(pdn, v, dd, dn);
-        if (NV > 2) make_u(v, k);
+        get8<XT, VEC>(pr, v, d, r);
+        get8<YT, VEC>(pdn, v, d, dn);
+        get_const(i, 1, k);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if (SUMS) acc_r[i][e] = fma2(dn[e], mul2(r[i][e], rs_r2), acc_r[i][e]);
-          const f2 g = mul2(dn[e], NV > 2 ? k[e] : cu.f[NV <= 2 ? i : 0][e]);
+          if (SUMS) acc_r[i][e] = fma2(dn[e], mul2(r[e], rs_r2), acc_r[i][e]);
+          const f2 g = mul2(dn[e], k[e]);
           ev[i][e] = fma2(rs_r2, g, ev[i][e]);
-          sum_g = fma2(g, r[i][e], sum_g);
+          sum_g = fma2(g, r[e], sum_g);
         }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = pk(0.f);
       }
       if (post || sum_gate_row) {
-        if (NV > 2) make_k(v, k);
-        if (element) get8<YT, VEC>(pg, v, dd, dn);
+        get_const(i, 0, k);
+        if (element) get8<YT, VEC>(pg, v, d, dn);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          f2 ap = mul2(y[i][e], NV > 2 ? k[e] : ck.f[NV <= 2 ? i : 0][e]);
+          f2 ap = mul2(y[e], k[e]);
           if (element) ap = mul2(ap, gate_pair(dn[e], a.sigmoid));
           sum_e = fma2(ap, ev[i][e], sum_e);
-          sum_h = fma2(ap, r[i][e], sum_h);
+          sum_h = fma2(ap, r[e], sum_h);
         }
       }
     }
@@ -184,15 +233,22 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) 
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = v0 + i * 32 * W;
+      if (col_of<VEC>(v, 0) >= dd) continue;
       f2 k[4], o[4];
+      f2(&r)[4] = r_[kAgain ? 0 : i];
+      f2(&y)[4] = y_[kAgain ? 0 : i];
+      if (kAgain) {
+        if (pre) get8<XT, VEC>(pr, v, d, r);
+        if (has_y) get8<YT, VEC>(py, v, d, y);
+      }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) ev[i][e] = fma2(c1n, r[i][e], ev[i][e]);  // t
-      put8<XT, VEC>(static_cast<XT*>(a.dx) + off, v, a.dx != nullptr ? dd : 0, ev[i]);
+      for (int e = 0; e < 4; ++e) ev[i][e] = fma2(c1n, r[e], ev[i][e]);  // t
+      if (a.dx != nullptr) put8<XT, VEC>(static_cast<XT*>(a.dx) + off, v, d, ev[i]);
       if (!has_y) continue;
-      if (NV > 2) make_k(v, k);
+      get_const(i, 0, k);
       f2 g[4], dg[4];
       if (element) {
-        get8<YT, VEC>(pg, v, dd, g);
+        get8<YT, VEC>(pg, v, d, g);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 gv = unpk(g[e]);
@@ -205,16 +261,15 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) 
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const f2 kk = NV > 2 ? k[e] : ck.f[NV <= 2 ? i : 0][e];
         const f2 at = element ? mul2(g[e], ev[i][e]) : ev[i][e];
-        const f2 yh = mul2(y[i][e], ry2);  // a_row Y
+        const f2 yh = mul2(y[e], ry2);  // a_row Y
         if (SUMS) acc_y[i][e] = fma2(at, yh, acc_y[i][e]);
-        o[e] = mul2(mul2(at, kk), facy);
-        if (post) o[e] = fma2(y[i][e], c2n, o[e]);
-        if (element) dg[e] = mul2(mul2(dg[e], mul2(ev[i][e], pk(a.scale))), mul2(yh, kk));
+        o[e] = mul2(mul2(at, k[e]), facy);
+        if (post) o[e] = fma2(y[e], c2n, o[e]);
+        if (element) dg[e] = mul2(mul2(dg[e], mul2(ev[i][e], pk(a.scale))), mul2(yh, k[e]));
       }
-      put8<YT, VEC>(static_cast<YT*>(a.dy) + off, v, a.dy != nullptr ? dd : 0, o);
-      if (element && a.dgate != nullptr) put8<YT, VEC>(static_cast<YT*>(a.dgate) + off, v, dd, dg);
+      if (a.dy != nullptr) put8<YT, VEC>(static_cast<YT*>(a.dy) + off, v, d, o);
+      if (element && a.dgate != nullptr) put8<YT, VEC>(static_cast<YT*>(a.dgate) + off, v, d, dg);
     }
     before = stage;
     if (++stage == a.stages) { stage = 0; phase ^= 1; }

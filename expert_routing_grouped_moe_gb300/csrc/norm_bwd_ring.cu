@@ -10,8 +10,9 @@ cudaError_t go(const NormArgs& a, int blocks, cudaStream_t s) {
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(norm_groups(a.d) * a.W * 32),
-                    static_cast<size_t>(a.stages) * a.tile, s, a);
+  const NormShape sh = norm_bwd_shape(a.d);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(sh.threads()),
+                    static_cast<size_t>(a.stages) * a.tile + norm_const_bytes(sh), s, a);
 }
 
 template <typename XT, typename YT, int NV, bool SUMS, int MAXT, int MINB>
@@ -25,9 +26,9 @@ cudaError_t pick_gate(const NormArgs& a, int blocks, cudaStream_t s) {
 
 template <typename XT, typename YT>
 cudaError_t pick(const NormArgs& a, int blocks, cudaStream_t s) {
-  if (norm_nv(a.d) == 1) {
+  if (norm_bwd_shape(a.d).nv == 1) {
     if (a.nsum == 0) return pick_gate<XT, YT, 1, false, 384, 2>(a, blocks, s);
-    return a.W <= 8 ? pick_gate<XT, YT, 1, true, 256, 2>(a, blocks, s)
+    return a.W <= 8 ? pick_gate<XT, YT, 1, true, 256, 3>(a, blocks, s)
                     : pick_gate<XT, YT, 1, true, 384, 2>(a, blocks, s);
   }
   return a.nsum > 0 ? pick_gate<XT, YT, 2, true, 512, 1>(a, blocks, s)

@@ -183,7 +183,8 @@ __global__ void __launch_bounds__(RING && NV == 1 ? 384 : 512, RING && NV == 1 ?
 
 template <typename XT, typename YT, bool VEC, int NV, int GATE, bool RING>
 cudaError_t go(const NormArgs& a, cudaStream_t s) {
-  const int groups = norm_groups(a.d), threads = groups * a.W * 32;
+  const NormShape sh = norm_fwd_shape(a.d);
+  const int groups = sh.groups, threads = sh.threads();
   const size_t smem = static_cast<size_t>(a.stages) * a.tile;
   auto kern = norm_fwd_kernel<XT, YT, VEC, NV, GATE, RING>;
   if (RING) {
@@ -220,12 +221,14 @@ cudaError_t pick_nv(const NormArgs& a, bool vec, cudaStream_t s) {
 
 template <typename XT, typename YT>
 cudaError_t pick(NormArgs a, bool vec, cudaStream_t s) {
-  const int groups = norm_groups(a.d), nv = norm_nv(a.d);
+  const NormShape sh = norm_fwd_shape(a.d);
+  const int groups = sh.groups, nv = sh.nv;
+  a.W = sh.W;
   a.tile = groups * a.d * static_cast<int>((a.x ? sizeof(XT) : 0) + (a.y ? sizeof(YT) : 0) +
                                            (a.gate_kind == MOE_GATE_ELEMENT ? sizeof(YT) : 0));
   const bool ring = vec && nv <= 2 && a.W > 1 && (a.w_post || a.w_pre) &&
                     a.T > static_cast<int64_t>(kNormRingTiles) * groups;
-  a.stages = ring ? ring_stages(a.tile, groups * a.W * 32 > 256 ? 3 : 4) : 0;
+  a.stages = ring ? ring_stages(a.tile, sh.threads() > 256 ? 3 : 4, 0) : 0;
   if (a.stages == 0) a.tile = 0;
   switch (nv) {
     case 1: return pick_nv<XT, YT, 1>(a, vec, s);
