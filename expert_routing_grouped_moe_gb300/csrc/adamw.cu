@@ -37,7 +37,7 @@ namespace {
 constexpr int kBlock = MOE_ADAMW_BLOCK;        // values per scale: 8 for each lane of a warp
 constexpr int kThreads = 256;
 constexpr int kChunk = kThreads * 8;           // values of one pass of a block of threads
-constexpr int kNormBlocks = 4 * kSMs;          // rows of partial sums per norm launch
+constexpr int kNormBlocks = 8 * kSMs;          // rows of partial sums per norm launch
 constexpr uint32_t kDitherT = 2654435769u, kDitherI = 1779033703u;
 
 struct Tensor {
@@ -167,7 +167,7 @@ __device__ __forceinline__ void decode8(uint2 q, float scale, f2 (&f)[4]) {
 // E8M0 byte of a block whose largest magnitude has the bits `top`.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
   const int b = static_cast<int>(top >> 23) - 7;
-  return b < 8 ? 8u : static_cast<uint32_t>(b);
+  return b < 8 ? 8u : b > 248 ? 248u : static_cast<uint32_t>(b);
 }
 // e4m3 magnitude of x >= 0 under the scale byte b; d: 20 dither bits.  Normal
 // values: exponent and top three mantissa bits, rebased.  Below the smallest
@@ -177,6 +177,76 @@ __device__ __forceinline__ uint32_t encode(float x, uint32_t d, uint32_t b) {
   const bool below = x < low;
   const uint32_t bits = __float_as_uint(below ? __fadd_rn(x, low) : x);
   return ((bits + d) >> 20) - ((b - 7u) << 3) - (below ? 8u : 0u);
+}
+// Top bytes of four words.
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+// The eight codes of this lane: m with its sign, root not below 1 where positive.
+__device__ __forceinline__ void encode8(const float (&m)[8], const float (&root)[8], uint32_t u,
+                                        uint32_t bm, uint32_t bv, uint2& qm, uint2& qr) {
+  // Where every value is normal (m and root within 2^-14 of their block's
+  // largest, nearly always) the code is in place after one addition: bits 20-26
+  // of the rebased, dithered word.
+  const uint32_t sub_m = (bm - 7u) << 23, sub_r = (bv - 7u) << 23;
+  uint32_t least_m = 0xFFFFFFFFu, least_r = 0xFFFFFFFFu;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    least_m = min(least_m, __float_as_uint(m[e]) & 0x7FFFFFFFu);
+    least_r = min(least_r, __float_as_uint(root[e]));
+  }
+  uint32_t wm[8], wr[8];
+  if (least_m >= ((bm - 6u) << 23) && least_r >= ((bv - 6u) << 23)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e, u += kDitherI) {
+      const uint32_t d = u >> 12;
+      const uint32_t x = __float_as_uint(m[e]) + d - sub_m;
+      wm[e] = ((x << 4) & 0x7FFFFFFFu) | (x & 0x80000000u);
+      wr[e] = (__float_as_uint(root[e]) + (0xFFFFFu - d) - sub_r) << 4;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e, u += kDitherI) {
+      const uint32_t d = u >> 12;
+      wm[e] = (encode(fabsf(m[e]), d, bm) << 24) | (m[e] < 0.f ? 0x80000000u : 0u);
+      uint32_t q = encode(fabsf(root[e]), 0xFFFFFu - d, bv);
+      if (q < 1u && root[e] > 0.f) q = 1u;
+      wr[e] = q << 24;
+    }
+  }
+  qm = make_uint2(top_bytes(wm[0], wm[1], wm[2], wm[3]), top_bytes(wm[4], wm[5], wm[6], wm[7]));
+  qr = make_uint2(top_bytes(wr[0], wr[1], wr[2], wr[3]), top_bytes(wr[4], wr[5], wr[6], wr[7]));
+}
+
+// Square root and quotient, rounded to nearest: an approximate reciprocal
+// (square root), one Newton step, and a last correction by the exact residual
+// (Markstein, IBM J. Res. Dev. 34, 1990).  x >= 0; d from 2^-100 to 2^120.
+__device__ __forceinline__ float approx_rsqrt(float x) {
+  float r;
+  asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float approx_rcp(float x) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ f2 root2(f2 x, const Product& mul) {
+  const float2 v = unpk(x);
+  const f2 y = pk(approx_rsqrt(v.x), approx_rsqrt(v.y));
+  const f2 s = mul(x, y), h = mul(y, pk(0.5f)), minus = pk(-1.f);
+  const f2 e = fma2(mul(s, minus), h, pk(0.5f));
+  const f2 h1 = fma2(h, e, h), s1 = fma2(s, e, s);
+  const float2 r = unpk(fma2(fma2(mul(s1, minus), s1, x), h1, s1));
+  return pk(v.x > 0.f ? (v.x < INFINITY ? r.x : v.x) : v.x, v.y > 0.f ? (v.y < INFINITY ? r.y : v.y) : v.y);
+}
+__device__ __forceinline__ f2 ratio2(f2 n, f2 d, const Product& mul) {
+  const float2 v = unpk(d);  // an infinite d counts as 2^120
+  const float x = fminf(v.x, 0x1p120f), y = fminf(v.y, 0x1p120f);
+  const f2 r = pk(approx_rcp(x), approx_rcp(y)), nd = pk(-x, -y);
+  const f2 r1 = fma2(r, fma2(nd, r, pk(1.f)), r);
+  const f2 q = mul(n, r1);
+  return fma2(fma2(nd, q, n), r1, q);
 }
 
 template <typename PT, typename GT, bool MASTER, bool EIGHT, int MAX>
@@ -234,41 +304,32 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     }
     const f2 coef2 = pk(coef), b1 = pk(c.b1), c1 = pk(c.c1), b2 = pk(c.b2), c2 = pk(c.c2),
              keep = pk(t.keep), nlr = pk(-t.lr);
-    uint32_t top_m = 0, top_r = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       g[e] = mul(g[e], coef2);
       m[e] = add2(mul(b1, m[e]), mul(c1, g[e]));
       v[e] = add2(mul(b2, v[e]), mul(mul(c2, g[e]), g[e]));
-      const float2 vv = unpk(v[e]), mm = unpk(m[e]);
-      const float r0 = __fsqrt_rn(vv.x), r1 = __fsqrt_rn(vv.y);
-      root[e] = pk(r0, r1);
-      const float2 den = unpk(add2(mul(root[e], pk(c.correct)), pk(c.eps)));
-      const f2 upd = pk(__fdiv_rn(mm.x, den.x), __fdiv_rn(mm.y, den.y));
+      root[e] = root2(v[e], mul);
+      const f2 upd = ratio2(m[e], add2(mul(root[e], pk(c.correct)), pk(c.eps)), mul);
       p[e] = add2(mul(p[e], keep), mul(nlr, upd));
-      if (EIGHT) {  // values past n are 0: they do not raise the maximum
-        top_m = max(top_m, max(__float_as_uint(mm.x) & 0x7FFFFFFFu, __float_as_uint(mm.y) & 0x7FFFFFFFu));
-        top_r = max(top_r, max(__float_as_uint(r0) & 0x7FFFFFFFu, __float_as_uint(r1) & 0x7FFFFFFFu));
-      }
     }
     if constexpr (EIGHT) {
+      float mm[8], rr[8];
+      uint32_t top_m = 0, top_r = 0;   // values past n are 0: they do not raise the maximum
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = unpk(m[e]), y = unpk(root[e]);
+        mm[2 * e] = x.x; mm[2 * e + 1] = x.y;
+        rr[2 * e] = y.x; rr[2 * e + 1] = y.y;
+        top_m = max(top_m, max(__float_as_uint(x.x) & 0x7FFFFFFFu, __float_as_uint(x.y) & 0x7FFFFFFFu));
+        top_r = max(top_r, max(__float_as_uint(y.x), __float_as_uint(y.y)));
+      }
       const uint32_t bm = scale_byte(__reduce_max_sync(0xffffffffu, top_m));
       const uint32_t bv = scale_byte(__reduce_max_sync(0xffffffffu, top_r));
-      uint32_t u = static_cast<uint32_t>(i) * kDitherI + c.dither;
-      uint32_t wm[2] = {0, 0}, wr[2] = {0, 0};
-#pragma unroll
-      for (int e = 0; e < 8; ++e, u += kDitherI) {
-        const float2 m2 = unpk(m[e >> 1]), r2 = unpk(root[e >> 1]);
-        const float x = e & 1 ? m2.y : m2.x, r = e & 1 ? r2.y : r2.x;
-        uint32_t q = encode(fabsf(x), u >> 12, bm);
-        q |= x < 0.f ? 128u : 0u;
-        wm[e >> 2] |= q << (8 * (e & 3));
-        q = encode(fabsf(r), ~u >> 12, bv);
-        if (q < 1u && r > 0.f) q = 1u;
-        wr[e >> 2] |= q << (8 * (e & 3));
-      }
-      set_codes(static_cast<uint8_t*>(t.m), i, n, vec, make_uint2(wm[0], wm[1]));
-      set_codes(static_cast<uint8_t*>(t.v), i, n, vec, make_uint2(wr[0], wr[1]));
+      uint2 qm, qr;
+      encode8(mm, rr, static_cast<uint32_t>(i) * kDitherI + c.dither, bm, bv, qm, qr);
+      set_codes(static_cast<uint8_t*>(t.m), i, n, vec, qm);
+      set_codes(static_cast<uint8_t*>(t.v), i, n, vec, qr);
       if (lane == 0 && i < n) {
         t.sc[2 * blk] = static_cast<uint8_t>(bm);
         t.sc[2 * blk + 1] = static_cast<uint8_t>(bv);
@@ -491,7 +552,7 @@ int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n, const moe_adamw_h
   if (!(h->lr >= 0.0) || !std::isfinite(h->lr)) return bad("lr must be finite and not negative");
   if (!(h->beta1 >= 0.0 && h->beta1 < 1.0) || !(h->beta2 >= 0.0 && h->beta2 < 1.0))
     return bad("betas must be in [0, 1)");
-  if (!(h->eps > 0.0) || !std::isfinite(h->eps)) return bad("eps must be positive");
+  if (!(h->eps >= 1e-30) || !(h->eps <= 1e30)) return bad("eps must be from 1e-30 to 1e30");
   if (!(h->max_norm >= 0.f) || !std::isfinite(h->max_norm)) return bad("max_norm must be finite and not negative");
   if (!std::isfinite(h->grad_scale)) return bad("grad_scale must be finite");
   if (h->step < 1) return bad("step counts from 1");

@@ -442,7 +442,8 @@ typedef struct moe_adamw_tensor {
 } moe_adamw_tensor;
 
 typedef struct moe_adamw_hyper {
-  double lr, beta1, beta2, eps;
+  double lr, beta1, beta2;
+  double eps;              /* 1e-30 .. 1e30 */
   int64_t step;            /* t: 1 for the first step */
   float grad_scale;        /* multiplies every gradient (1 / loss scale) */
   float max_norm;          /* > 0: clip by the global norm; 0: no clip */
