@@ -56,7 +56,7 @@ struct Consts {
   float b1, c1, b2, c2, correct, eps, grad_scale, max_norm;
   float zero;            // -0
   uint32_t dither;       // t T
-  const double* part;    // partial sums of squares, NULL: not needed
+  const float2* part;    // partial sums of squares (value, rest), NULL: not needed
   int nparts, skip;
   float* norm_out;
 };
@@ -79,7 +79,7 @@ template <int MAX>
 struct NormTable {
   int n, chunks;
   float zero;  // -0
-  double* part;
+  float2* part;
   NormTensor t[MAX];
 };
 
@@ -218,6 +218,38 @@ __device__ __forceinline__ void encode8(const float (&m)[8], const float (&root)
   qr = make_uint2(top_bytes(wr[0], wr[1], wr[2], wr[3]), top_bytes(wr[4], wr[5], wr[6], wr[7]));
 }
 
+// Sums held as a pair of floats (value, rest), since 64-bit adds are some 60
+// times slower here: the exact error of each fp32 addition goes to the rest.
+__device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
+  const float s = __fadd_rn(a.x, b.x), t = __fsub_rn(s, a.x);
+  const float err = __fadd_rn(__fsub_rn(a.x, __fsub_rn(s, t)), __fsub_rn(b.x, t));
+  const float rest = __fadd_rn(err, __fadd_rn(a.y, b.y));
+  const float v = __fadd_rn(s, rest);
+  return make_float2(v, __fsub_rn(rest, __fsub_rn(v, s)));
+}
+__device__ __forceinline__ float2 warp_pair(float2 a) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    a = add_pair(a, make_float2(__shfl_xor_sync(0xffffffffu, a.x, o), __shfl_xor_sync(0xffffffffu, a.y, o)));
+  return a;
+}
+// The sum over the block, in every thread.
+__device__ __forceinline__ float2 block_pair(float2 a, float2* s_warp) {
+  a = warp_pair(a);
+  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = a;
+  __syncthreads();
+  a = s_warp[0];
+#pragma unroll
+  for (int i = 1; i < kThreads / 32; ++i) a = add_pair(a, s_warp[i]);
+  return a;
+}
+__device__ __forceinline__ float root_of_pair(float2 a) {
+  const float s = __fsqrt_rn(a.x);
+  if (!(s > 0.f && s < INFINITY)) return s;
+  const float r = __fadd_rn(__fmaf_rn(-s, s, a.x), a.y);
+  return __fmaf_rn(r, __fdiv_rn(0.5f, s), s);
+}
+
 // Square root and quotient, rounded to nearest: an approximate reciprocal
 // (square root), one Newton step, and a last correction by the exact residual
 // (Markstein, IBM J. Res. Dev. 34, 1990).  x >= 0; d from 2^-100 to 2^120.
@@ -252,21 +284,15 @@ __device__ __forceinline__ f2 ratio2(f2 n, f2 d, const Product& mul) {
 template <typename PT, typename GT, bool MASTER, bool EIGHT, int MAX>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<MAX> tab) {
   const Consts& c = tab.c;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
   const Product mul{pk(c.zero)};
   float coef = c.grad_scale;
   pdl_wait();
   if (c.part != nullptr) {  // the norm: every block adds the same partials in the same order
-    __shared__ double s_sum[kThreads / 32];
-    double s = 0.0;
-    for (int i = threadIdx.x; i < c.nparts; i += kThreads) s += c.part[i];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) s_sum[warp] = s;
-    __syncthreads();
-    s = 0.0;
-    for (int i = 0; i < kThreads / 32; ++i) s += s_sum[i];
-    const float norm = __fmul_rn(static_cast<float>(sqrt(s)), fabsf(c.grad_scale));
+    __shared__ float2 s_sum[kThreads / 32];
+    float2 s = make_float2(0.f, 0.f);
+    for (int i = threadIdx.x; i < c.nparts; i += kThreads) s = add_pair(s, c.part[i]);
+    const float norm = __fmul_rn(root_of_pair(block_pair(s, s_sum)), fabsf(c.grad_scale));
     if (c.norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *c.norm_out = norm;
     if (c.skip && !(norm <= 3.402823466e38f)) return;  // Inf or NaN: nothing changes
     if (c.max_norm > 0.f) {
@@ -274,9 +300,10 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       coef = __fmul_rn(coef, q >= 1.f ? 1.f : q);  // a NaN norm stays NaN
     }
   }
-  int ti = 0;
-  for (int ch = blockIdx.x; ch < tab.chunks; ch += gridDim.x) {
-    while (ti + 1 < tab.n && ch >= tab.t[ti + 1].chunk0) ++ti;
+  // Backwards: after a norm the gradients' end is what is left of them in the L2.
+  int ti = tab.n - 1;
+  for (int ch = tab.chunks - 1 - static_cast<int>(blockIdx.x); ch >= 0; ch -= gridDim.x) {
+    while (ch < tab.t[ti].chunk0) --ti;
     const Tensor& t = tab.t[ti];
     const int64_t n = t.n;
     const int64_t i = static_cast<int64_t>(ch - t.chunk0) * kChunk + threadIdx.x * 8;
@@ -358,7 +385,7 @@ __device__ __forceinline__ void add_square(f2 x, f2& hi, f2& lo, const Product& 
 
 template <int MAX>
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ NormTable<MAX> tab) {
-  __shared__ double s_sum[kThreads / 32];
+  __shared__ float2 s_sum[kThreads / 32];
   pdl_wait();
   const Product mul{pk(tab.zero)};
   f2 hi = pk(0.f), lo = pk(0.f);
@@ -375,16 +402,8 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
     for (int e = 0; e < 4; ++e) add_square(g[e], hi, lo, mul);
   }
   const float2 h2 = unpk(hi), l2 = unpk(lo);
-  double s = (static_cast<double>(h2.x) + static_cast<double>(h2.y)) +
-             (static_cast<double>(l2.x) + static_cast<double>(l2.y));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = s;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < kThreads / 32; ++i) s += s_sum[i];
-    tab.part[blockIdx.x] = s;
-  }
+  const float2 s = block_pair(add_pair(make_float2(h2.x, l2.x), make_float2(h2.y, l2.y)), s_sum);
+  if (threadIdx.x == 0) tab.part[blockIdx.x] = s;
 }
 
 int64_t chunks_of(int64_t n) { return (n + kChunk - 1) / kChunk; }
@@ -466,7 +485,7 @@ cudaError_t step_kind(int kind, const moe_adamw_tensor* ts, int n, const moe_ada
 }
 
 template <int MAX>
-cudaError_t norm_all(const moe_adamw_tensor* ts, int n, double* part, int* nparts, cudaStream_t s) {
+cudaError_t norm_all(const moe_adamw_tensor* ts, int n, float2* part, int* nparts, cudaStream_t s) {
   NormTable<MAX> tab;
   tab.zero = -0.f;
   tab.n = tab.chunks = 0;
@@ -540,7 +559,7 @@ extern "C" {
 
 size_t moe_adamw_workspace_size(const moe_adamw_tensor* tensors, int32_t n) {
   if (n < 0 || (n > 0 && tensors == nullptr)) return 0;
-  return norm_rows(tensors, n) * sizeof(double);
+  return norm_rows(tensors, n) * sizeof(float2);
 }
 
 int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n, const moe_adamw_hyper* hyper,
@@ -597,10 +616,10 @@ int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n, const moe_adamw_h
   c.norm_out = grad_norm;
   cudaError_t e = cudaSuccess;
   if (need_norm) {
-    c.part = static_cast<const double*>(ws);
+    c.part = static_cast<const float2*>(ws);
     ProbeScope probe("grad_norm", stream);
-    e = n <= kNormFew ? norm_all<kNormFew>(tensors, n, static_cast<double*>(ws), &c.nparts, stream)
-                      : norm_all<kNormMany>(tensors, n, static_cast<double*>(ws), &c.nparts, stream);
+    e = n <= kNormFew ? norm_all<kNormFew>(tensors, n, static_cast<float2*>(ws), &c.nparts, stream)
+                      : norm_all<kNormMany>(tensors, n, static_cast<float2*>(ws), &c.nparts, stream);
   }
   ProbeScope probe("adamw", stream);
   for (int k = 0; k < kKinds && e == cudaSuccess; ++k) {
