@@ -264,13 +264,12 @@ __device__ __forceinline__ float approx_rcp(float x) {
   return r;
 }
 __device__ __forceinline__ f2 root2(f2 x, const Product& mul) {
-  const float2 v = unpk(x);
-  const f2 y = pk(approx_rsqrt(v.x), approx_rsqrt(v.y));
-  const f2 s = mul(x, y), h = mul(y, pk(0.5f)), minus = pk(-1.f);
-  const f2 e = fma2(mul(s, minus), h, pk(0.5f));
-  const f2 h1 = fma2(h, e, h), s1 = fma2(s, e, s);
-  const float2 r = unpk(fma2(fma2(mul(s1, minus), s1, x), h1, s1));
-  return pk(v.x > 0.f ? (v.x < INFINITY ? r.x : v.x) : v.x, v.y > 0.f ? (v.y < INFINITY ? r.y : v.y) : v.y);
+  const float2 v = unpk(x);  // 0: a finite factor, so that 0 comes out
+  const f2 y = pk(approx_rsqrt(fmaxf(v.x, 1e-45f)), approx_rsqrt(fmaxf(v.y, 1e-45f)));
+  const f2 s = mul(x, y), nh = mul(y, pk(-0.5f));
+  const f2 e = fma2(s, nh, pk(0.5f));
+  const f2 nh1 = fma2(nh, e, nh), s1 = fma2(s, e, s);
+  return fma2(fma2(s1, s1, mul(x, pk(-1.f))), nh1, s1);
 }
 __device__ __forceinline__ f2 ratio2(f2 n, f2 d, const Product& mul) {
   const float2 v = unpk(d);  // an infinite d counts as 2^120
@@ -282,7 +281,7 @@ __device__ __forceinline__ f2 ratio2(f2 n, f2 d, const Product& mul) {
 }
 
 template <typename PT, typename GT, bool MASTER, bool EIGHT, int MAX>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<MAX> tab) {
+__global__ void __launch_bounds__(kThreads, EIGHT ? 5 : 4) adamw_kernel(const __grid_constant__ Table<MAX> tab) {
   const Consts& c = tab.c;
   const int lane = threadIdx.x & 31;
   const Product mul{pk(c.zero)};
