@@ -213,6 +213,13 @@ inline int ring_stages(size_t tile, int per) {
   return n >= kRingMaxStages ? kRingMaxStages : n >= 2 ? static_cast<int>(n) : per > 1 ? ring_stages(tile, per - 1) : 0;
 }
 
+// Blocks of the backward that an SM's registers hold: at 128 a thread where they
+// keep column sums or two shares, at 80 otherwise.
+inline int norm_bwd_per_sm(const NormShape& s, bool sums) {
+  if (s.nv > 1) return s.threads() <= 256 ? 2 : 1;
+  return !sums && s.threads() <= 256 ? 3 : 2;
+}
+
 cudaError_t launch_norm_fwd(const NormArgs& a, int x_type, int y_type, bool vec, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormArgs& a, int x_type, int y_type, bool vec, int blocks,
                             cudaStream_t s);

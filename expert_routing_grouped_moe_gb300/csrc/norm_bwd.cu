@@ -80,7 +80,7 @@ cudaError_t launch_norm_bwd(const NormArgs& args, int x_type, int y_type, bool v
     const bool barrier = pre || a.w_post || (a.gate_kind == MOE_GATE_TOKEN && a.dgate);
     const bool ring = vec && sh.nv <= 2 && a.W > 1 && barrier &&
                       a.T > static_cast<int64_t>(kNormRingTiles) * groups;
-    a.stages = ring ? ring_stages(a.tile, sh.threads() <= 256 ? 3 : 2, norm_const_bytes(sh)) : 0;
+    a.stages = ring ? ring_stages(a.tile, norm_bwd_per_sm(sh, a.nsum > 0), norm_const_bytes(sh)) : 0;
     e = a.stages > 0 ? launch_norm_bwd_ring(a, x_type, y_type, blocks, s)
                      : launch_norm_bwd_direct(a, x_type, y_type, vec, blocks, s);
   }

@@ -28,7 +28,7 @@ template <typename XT, typename YT>
 cudaError_t pick(const NormArgs& a, int blocks, cudaStream_t s) {
   if (norm_bwd_shape(a.d).nv == 1) {
     if (a.nsum == 0) return pick_gate<XT, YT, 1, false, 384, 2>(a, blocks, s);
-    return a.W <= 8 ? pick_gate<XT, YT, 1, true, 256, 3>(a, blocks, s)
+    return a.W <= 8 ? pick_gate<XT, YT, 1, true, 256, 2>(a, blocks, s)
                     : pick_gate<XT, YT, 1, true, 384, 2>(a, blocks, s);
   }
   return a.nsum > 0 ? pick_gate<XT, YT, 2, true, 512, 1>(a, blocks, s)
