@@ -6,14 +6,6 @@
 namespace moe {
 namespace {
 
-// Blocks of the backward; those that keep column sums write a row of partial
-// sums for each of their groups.
-int bwd_blocks(int64_t T, int d, bool sums) {
-  const NormShape sh = norm_bwd_shape(d);
-  const int64_t need = (T + sh.groups - 1) / sh.groups, most = norm_bwd_per_sm(sh, sums) * kSMs;
-  return static_cast<int>(need < most ? need : most);
-}
-
 int bad(const char* msg) { return record_error(MOE_ERR_INVALID_ARG, msg); }
 
 // Type-dependent alignment every pointer must have, and 16 bytes for the
@@ -95,7 +87,12 @@ int moe_block_norm_fwd(const moe_norm_desc* desc, const void* x, const void* y, 
 
 size_t moe_block_norm_workspace_size(int32_t T, int32_t d) {
   if (T < 0 || d <= 0 || d > kNormMaxD) return 0;
-  const size_t rows = static_cast<size_t>(bwd_blocks(T, d, true)) * norm_bwd_shape(d).groups;
+  size_t rows = 0;  // the larger of the two ways to read rows
+  for (const bool ring : {false, true}) {
+    const NormShape sh = norm_bwd_shape(d, ring);
+    const size_t r = static_cast<size_t>(norm_bwd_blocks(sh, T, true)) * sh.groups;
+    rows = r > rows ? r : rows;
+  }
   return rows * 2 * static_cast<size_t>(d) * 4;
 }
 
@@ -122,9 +119,8 @@ int moe_block_norm_bwd(const moe_norm_desc* desc, const void* dr, const void* dn
   a.gate_kind = desc->gate; a.sigmoid = desc->gate_sigmoid;
   a.scale = desc->scale; a.eps = desc->eps; a.w_off = desc->w_offset;
   a.T = desc->T; a.d = desc->d;
-  const int blocks = bwd_blocks(desc->T, desc->d, a.nsum > 0);
   if (desc->T == 0) {
-    const cudaError_t e = launch_norm_bwd(a, desc->x_type, desc->y_type, false, 0, stream);
+    const cudaError_t e = launch_norm_bwd(a, desc->x_type, desc->y_type, false, stream);
     if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
     return record_error(MOE_OK, "");
   }
@@ -164,7 +160,7 @@ int moe_block_norm_bwd(const moe_norm_desc* desc, const void* dr, const void* dn
   if (rc != MOE_OK) return rc;
   ProbeScope probe("block_norm_bwd", stream);
   const cudaError_t e =
-      launch_norm_bwd(a, desc->x_type, desc->y_type, vec, blocks, stream);
+      launch_norm_bwd(a, desc->x_type, desc->y_type, vec, stream);
   if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
   return record_error(MOE_OK, "");
 }

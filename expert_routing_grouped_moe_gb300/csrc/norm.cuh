@@ -60,9 +60,13 @@ inline NormShape norm_shape(int d, int nv) {
 // Forward: two shares for each thread beyond 1024 columns (fewer warps to wait for
 // one another; 4096x2048 12.9 us, with one share 16.4).
 inline NormShape norm_fwd_shape(int d) { return norm_shape(d, d <= 1024 ? 1 : d <= 8192 ? 2 : 4); }
-// Backward: one share for each thread while a row fits 12 warps (two such blocks
-// fit an SM at 80 registers), then as few as fit 16 warps.
-inline NormShape norm_bwd_shape(int d) { return norm_shape(d, d <= 3072 ? 1 : d <= 8192 ? 2 : 4); }
+// Backward, rows read directly: one share for each thread while that takes 16
+// warps at most.  Through the ring: one up to 2048 columns, where two save
+// nothing (16384x2048 83 us and 85), two above (frozen weights, 16384x2880: 96 us,
+// with one 110; 4096 columns: 142, with one share no second block fits).
+inline NormShape norm_bwd_shape(int d, bool ring) {
+  return norm_shape(d, d <= (ring ? 2048 : 4096) ? 1 : d <= 8192 ? 2 : 4);
+}
 
 // Sums v[0..K) (K = 1 or 3) over the W <= 16 warps of this thread's row group;
 // all threads of the block call it.  buf: 16 warps x 4 values, one of two
@@ -213,15 +217,18 @@ inline int ring_stages(size_t tile, int per) {
   return n >= kRingMaxStages ? kRingMaxStages : n >= 2 ? static_cast<int>(n) : per > 1 ? ring_stages(tile, per - 1) : 0;
 }
 
-// Blocks of the backward that an SM's registers hold: at 128 a thread where they
-// keep column sums or two shares, at 80 otherwise.
+// Blocks of the backward: what the SMs' registers hold, at 128 a thread where
+// they keep column sums or two shares, at 80 otherwise.  Those that keep column
+// sums write a row of partial sums for each of their groups.
 inline int norm_bwd_per_sm(const NormShape& s, bool sums) {
-  if (s.nv > 1) return s.threads() <= 256 ? 2 : 1;
-  return !sums && s.threads() <= 256 ? 3 : 2;
+  return !sums && s.nv == 1 && s.threads() <= 256 ? 3 : s.threads() <= 256 ? 2 : 1;
+}
+inline int norm_bwd_blocks(const NormShape& s, int64_t T, bool sums) {
+  const int64_t need = (T + s.groups - 1) / s.groups, most = norm_bwd_per_sm(s, sums) * kSMs;
+  return static_cast<int>(need < most ? need : most);
 }
 
 cudaError_t launch_norm_fwd(const NormArgs& a, int x_type, int y_type, bool vec, cudaStream_t s);
-cudaError_t launch_norm_bwd(const NormArgs& a, int x_type, int y_type, bool vec, int blocks,
-                            cudaStream_t s);
+cudaError_t launch_norm_bwd(const NormArgs& a, int x_type, int y_type, bool vec, cudaStream_t s);
 
 }  // namespace moe

@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kSumThreads) norm_colsum_kernel(const NormArgs
 
 template <typename XT, typename YT, int NV>
 cudaError_t go(const NormArgs& a, bool vec, int blocks, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(blocks)), threads(norm_bwd_shape(a.d).threads());
+  const dim3 grid(static_cast<unsigned>(blocks)), threads(norm_bwd_shape(a.d, false).threads());
   return vec ? launch_pdl(norm_bwd_kernel<XT, YT, true, NV, kGateAny, true, false, 512, 1>, grid, threads, 0, s, a)
              : launch_pdl(norm_bwd_kernel<XT, YT, false, NV, kGateAny, true, false, 512, 1>, grid, threads, 0,
                           s, a);
@@ -50,7 +50,7 @@ cudaError_t go(const NormArgs& a, bool vec, int blocks, cudaStream_t s) {
 
 template <typename XT, typename YT>
 cudaError_t pick(const NormArgs& a, bool vec, int blocks, cudaStream_t s) {
-  switch (norm_bwd_shape(a.d).nv) {
+  switch (norm_bwd_shape(a.d, false).nv) {
     case 1: return go<XT, YT, 1>(a, vec, blocks, s);
     case 2: return go<XT, YT, 2>(a, vec, blocks, s);
     default: return go<XT, YT, 4>(a, vec, blocks, s);
@@ -66,28 +66,31 @@ cudaError_t launch_norm_bwd_direct(const NormArgs& a, int x_type, int y_type, bo
                             : pick<float, float>(a, vec, blocks, s);
 }
 
-cudaError_t launch_norm_bwd(const NormArgs& args, int x_type, int y_type, bool vec, int blocks,
-                            cudaStream_t s) {
+cudaError_t launch_norm_bwd(const NormArgs& args, int x_type, int y_type, bool vec, cudaStream_t s) {
   NormArgs a = args;
-  const NormShape sh = norm_bwd_shape(a.d);
-  a.W = sh.W;
   cudaError_t e = cudaSuccess;
-  if (blocks > 0) {
-    const int groups = sh.groups, xs = x_type == MOE_BF16 ? 2 : 4, ys = y_type == MOE_BF16 ? 2 : 4;
+  int rows = 0;  // of partial column sums
+  if (a.T > 0) {
+    const int xs = x_type == MOE_BF16 ? 2 : 4, ys = y_type == MOE_BF16 ? 2 : 4;
     const bool pre = a.w_pre != nullptr;
-    a.tile = groups * a.d * ((a.x ? xs : 0) + (pre ? xs + ys : 0) + (a.y ? ys : 0) +
-                             (a.gate_kind == MOE_GATE_ELEMENT ? ys : 0));
+    NormShape sh = norm_bwd_shape(a.d, true);
+    a.tile = sh.groups * a.d * ((a.x ? xs : 0) + (pre ? xs + ys : 0) + (a.y ? ys : 0) +
+                                (a.gate_kind == MOE_GATE_ELEMENT ? ys : 0));
     const bool barrier = pre || a.w_post || (a.gate_kind == MOE_GATE_TOKEN && a.dgate);
-    const bool ring = vec && sh.nv <= 2 && a.W > 1 && barrier &&
-                      a.T > static_cast<int64_t>(kNormRingTiles) * groups;
+    const bool ring = vec && sh.nv <= 2 && sh.W > 1 && barrier &&
+                      a.T > static_cast<int64_t>(kNormRingTiles) * sh.groups;
     a.stages = ring ? ring_stages(a.tile, norm_bwd_per_sm(sh, a.nsum > 0), norm_const_bytes(sh)) : 0;
+    if (a.stages == 0) sh = norm_bwd_shape(a.d, false);
+    a.W = sh.W;
+    const int blocks = norm_bwd_blocks(sh, a.T, a.nsum > 0);
+    rows = blocks * sh.groups;
     e = a.stages > 0 ? launch_norm_bwd_ring(a, x_type, y_type, blocks, s)
                      : launch_norm_bwd_direct(a, x_type, y_type, vec, blocks, s);
   }
   if (e != cudaSuccess || a.nsum == 0) return e;
   const int64_t n = static_cast<int64_t>(a.nsum) * a.d;
   return launch_pdl(norm_colsum_kernel, dim3(static_cast<unsigned>((n + 31) / 32)), dim3(kSumThreads),
-                    0, s, a, blocks * sh.groups);
+                    0, s, a, rows);
 }
 
 }  // namespace moe

@@ -10,7 +10,7 @@ cudaError_t go(const NormArgs& a, int blocks, cudaStream_t s) {
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
   if (e != cudaSuccess) return e;
-  const NormShape sh = norm_bwd_shape(a.d);
+  const NormShape sh = norm_bwd_shape(a.d, true);
   return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(sh.threads()),
                     static_cast<size_t>(a.stages) * a.tile + norm_const_bytes(sh), s, a);
 }
@@ -26,11 +26,9 @@ cudaError_t pick_gate(const NormArgs& a, int blocks, cudaStream_t s) {
 
 template <typename XT, typename YT>
 cudaError_t pick(const NormArgs& a, int blocks, cudaStream_t s) {
-  if (norm_bwd_shape(a.d).nv == 1) {
-    if (a.nsum == 0) return pick_gate<XT, YT, 1, false, 384, 2>(a, blocks, s);
-    return a.W <= 8 ? pick_gate<XT, YT, 1, true, 256, 2>(a, blocks, s)
-                    : pick_gate<XT, YT, 1, true, 384, 2>(a, blocks, s);
-  }
+  if (norm_bwd_shape(a.d, true).nv == 1)  // 256 threads
+    return a.nsum > 0 ? pick_gate<XT, YT, 1, true, 256, 2>(a, blocks, s)
+                      : pick_gate<XT, YT, 1, false, 256, 3>(a, blocks, s);
   return a.nsum > 0 ? pick_gate<XT, YT, 2, true, 512, 1>(a, blocks, s)
                     : pick_gate<XT, YT, 2, false, 512, 1>(a, blocks, s);
 }
