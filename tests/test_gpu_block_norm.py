@@ -146,6 +146,37 @@ def test_many_rows_for_each_block_and_ragged_groups():
         check(b, "channel", True)
 
 
+@pytest.mark.parametrize("xt,yt", [(BF, BF), (F32, BF), (F32, F32)])
+@pytest.mark.parametrize("T,d", [(1300, 264), (701, 1000), (641, 2048), (613, 2880), (311, 4104),
+                                 (333, 8192)])
+def test_rows_through_the_ring(T, d, xt, yt):
+    """Enough rows that they come by bulk copies, with a last tile that is not
+    full; every gate with every choice of norms."""
+    for i, (kind, sigmoid) in enumerate(GATES):
+        for post, pre in NORMS[:3]:
+            b = make(T, d, xt, yt, kind, post, pre, seed=i)
+            forward(b, kind, sigmoid, scale=0.5)
+            if i % 2:     # frozen weights and gate
+                b["dw_post"] = b["dw_pre"] = None
+                b["dgate"] = b["dgate"] if kind in ("token", "element") else None
+            backward(b, kind, sigmoid, scale=0.5)
+            check(b, kind, sigmoid, scale=0.5)
+    # without a residual's gradient, without some outputs
+    b = make(T, d, xt, yt, "channel", True, True)
+    forward(b, "channel", True)
+    b["dr"] = None
+    L.moe_block_norm_bwd(None, b["dn"], b["r"], b["y"], None, b["dy"], w_post=b["w_post"],
+                         w_pre=b["w_pre"], rstd_y=b["rstd_y"], rstd_r=b["rstd_r"], gate=b["gate"],
+                         gate_kind="channel", gate_sigmoid=True, dgate=b["dgate"], ws=b["ws"])
+    b["dx"] = b["dw_post"] = b["dw_pre"] = None
+    check(b, "channel", True, fwd=False)
+    # the norm of x alone
+    L.moe_block_norm_fwd(b["x"], None, None, b["n"], w_pre=b["w_pre"], rstd_r=b["rstd_r"])
+    o = bo.block_norm_forward(n64(b["x"]), None, w_pre=n64(b["w_pre"]))
+    close(b["n"], o["n"], o["mag_n"], "n")
+    assert L.moe_status() == L.MOE_OK
+
+
 def test_norm_alone_and_gate_alone():
     # the norm of x alone (fp32 residual stream, bf16 block input), and its gradient
     b = make(50, 384, F32, BF, "none", False, True)
@@ -178,8 +209,8 @@ def test_norm_alone_and_gate_alone():
 
 
 def test_in_place_equals_out_of_place():
-    for d in (2048, 1001):
-        b = make(77, d, BF, BF, "element", True, True)
+    for T, d in ((77, 2048), (77, 1001), (650, 2048), (330, 4096)):
+        b = make(T, d, BF, BF, "element", True, True)
         forward(b, "element", False)
         backward(b, "element", False)
         torch.cuda.synchronize()
@@ -207,16 +238,18 @@ def test_rows_of_zeros_and_extreme_gates():
     check(b, "channel", True)
 
 
-def test_a_row_with_nan_spoils_no_other_row():
-    b = make(40, 512, BF, BF, "token", True, True)
+@pytest.mark.parametrize("d", [512, 1001, 2048])
+def test_a_row_with_nan_spoils_no_other_row(d):
+    T = 40 if d < 2048 else 640
+    b = make(T, d, BF, BF, "token", True, True)
     forward(b, "token", False)
     backward(b, "token", False)
     ref = {k: b[k].clone() for k in ("r", "n", "dx", "dy", "dgate")}
     b["y"][7, 3] = float("nan")
-    b["x"][9, 500] = float("inf")
+    b["x"][9, 300] = float("inf")
     forward(b, "token", False)
     backward(b, "token", False)
-    keep = [t for t in range(40) if t not in (7, 9)]
+    keep = [t for t in range(T) if t not in (7, 9)]
     for k in ref:
         assert torch.equal(b[k][keep], ref[k][keep]), k
     assert torch.isnan(b["n"][7].float()).all()
@@ -315,7 +348,7 @@ def test_nothing_is_written_past_a_buffer():
         raw = torch.full((n + 512,), 0xA5, dtype=torch.uint8, device=DEV)
         bands.append((raw, n))
         return raw[256:256 + n].view(dtype).view(shape)
-    for T, d in ((9, 96), (311, 1001), (17, 2880), (5, 4104)):
+    for T, d in ((9, 96), (311, 1001), (17, 2880), (5, 4104), (650, 2048), (320, 4104)):
         for kind in ("token", "channel", "element"):
             b = make(T, d, BF, BF, kind, True, True, place=place)
             raw = torch.full((b["ws"].numel() + 512,), 0xA5, dtype=torch.uint8, device=DEV)
