@@ -98,6 +98,28 @@ def test_every_kind_bit_for_bit(pt, gt, master, bits):
             check(r, e)
 
 
+@pytest.mark.parametrize("seed", range(4))
+def test_roots_and_quotients_over_the_exponents(seed):
+    """Moments and gradients over some hundred binades: the step's own square root
+    and division are the nearest fp32 values, as numpy's are."""
+    n, g = 500_000, torch.Generator(DEV).manual_seed(seed)
+    lo, hi, vlo, vhi = [(-40, 20, -80, 40), (-10, 10, -20, 20), (-60, -30, -126, -60),
+                        (-45, 10, -126, 20)][seed]
+
+    def mag(a, b):
+        return torch.exp2(a + (b - a) * torch.rand(n, generator=g, device=DEV))
+    sign = torch.where(torch.rand(n, generator=g, device=DEV) < 0.5, -1.0, 1.0)
+    row = dict(param=torch.zeros(n, device=DEV), grad=mag(lo, hi) * sign, m=mag(lo, hi) * sign.flip(0),
+               v=mag(vlo, vhi), master=None, scales=None, weight_decay=0.0, lr_mult=1.0)
+    if seed == 3:
+        row["v"].zero_()
+        row["grad"][::3] = 0
+    h = dict(HYPER, lr=1.0)
+    exp = expect(row, 3, **h)
+    L.moe_adamw_step(L.AdamWTable([row]), 3, **h)
+    check(row, exp)
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_mixed_kinds_and_pointers_that_no_vector_fits(bits):
     rows = [tensor(300 + 11 * i, *KINDS[i % 6], 8 if (i % 5 == 0) else bits, seed=i, off=i % 4)
