@@ -154,14 +154,30 @@ inline int gate_class(int kind) {
 
 // ---- rows staged through shared memory ---------------------------------------
 // A tile is the rows of a block's groups, consecutive in memory: one bulk copy
-// for each input.  A ring of `stages` tiles is filled ahead by thread 0; a
+// for each input.  A ring of `stages` tiles is filled ahead by one thread; a
 // tile's place is filled again after the first block-wide barrier of the next
 // tile, which every thread reaches after its last read of this one.
+// Bulk copies move 16-byte words.  Where rows do not begin and end on them
+// (VEC false) the words around a tile's first and last value come along, and
+// its values lie as far into their place as they lie into the first word; what
+// would reach past either end of the tensor is copied value by value instead.
 struct RingSrc {
   const void* p;   // [T,d] input, NULL: none
   int esize;       // bytes of an element
 };
 constexpr int kRingSrcs = 5, kRingMaxStages = 4;
+
+// Bytes of a tile's place for `bytes` of rows.
+template <bool VEC>
+__host__ __device__ __forceinline__ int ring_place(int bytes) {
+  return VEC ? bytes : (bytes + 30) & ~15;
+}
+// The first row of the tile at row `base` within its place.
+template <bool VEC, typename T>
+__device__ __forceinline__ const T* ring_row(const uint8_t* place, const T* src, int64_t base, int d) {
+  return reinterpret_cast<const T*>(
+      place + (VEC ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(src + base * d) & 15u)));
+}
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -170,24 +186,64 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// The words of one input's tile: [from, to) of memory, the rest of [begin, end)
+// outside them at most 15 bytes on either side.
+struct RingSpan {
+  uintptr_t begin, end, from, to;
+};
+template <bool VEC>
+__device__ __forceinline__ RingSpan ring_span(const RingSrc& q, int64_t base, int rows, int64_t T, int d) {
+  RingSpan s;
+  s.begin = reinterpret_cast<uintptr_t>(q.p) + static_cast<uintptr_t>(base * d * q.esize);
+  s.end = s.begin + static_cast<uintptr_t>(rows) * d * q.esize;
+  s.from = s.begin;
+  s.to = s.end;
+  if (!VEC) {
+    s.from = base == 0 ? (s.begin + 15) & ~uintptr_t(15) : s.begin & ~uintptr_t(15);
+    s.to = base + rows == T ? s.end & ~uintptr_t(15) : (s.end + 15) & ~uintptr_t(15);
+    if (s.to < s.from) s.to = s.from = s.begin & ~uintptr_t(15);  // within one word: value by value
+  }
+  return s;
+}
 // The tile of rows [base, base + groups) into `stage`; inputs one after the other.
+template <bool VEC>
 __device__ __forceinline__ void ring_fill(const RingSrc (&src)[kRingSrcs], uint8_t* stage,
                                           uint64_t* bar, int64_t base, int64_t T, int groups, int d) {
   const int64_t left = T - base;
   const int rows = left < groups ? static_cast<int>(left) : groups;
   uint32_t total = 0;
-#pragma unroll
-  for (int i = 0; i < kRingSrcs; ++i)
-    if (src[i].p != nullptr) total += static_cast<uint32_t>(rows * d * src[i].esize);
-  mbar_expect_tx(bar, total);
   int at = 0;
 #pragma unroll
-  for (int i = 0; i < kRingSrcs; ++i)
-    if (src[i].p != nullptr) {
-      bulk_load(stage + at, static_cast<const uint8_t*>(src[i].p) + base * d * src[i].esize,
-                static_cast<uint32_t>(rows * d * src[i].esize), bar);
-      at += groups * d * src[i].esize;
+  for (int i = 0; i < kRingSrcs; ++i) {
+    if (src[i].p == nullptr) continue;
+    const RingSpan s = ring_span<VEC>(src[i], base, rows, T, d);
+    total += static_cast<uint32_t>(s.to - s.from);
+    if (!VEC) {  // before the barrier's arrival, which makes them visible
+      const int es = src[i].esize;
+      const uintptr_t word = s.begin & ~uintptr_t(15);
+      auto one_by_one = [&](uintptr_t p, uintptr_t end) {
+        for (; p < end; p += es) {
+          uint8_t* to = stage + at + static_cast<int>(p - word);
+          if (es == 2) *reinterpret_cast<uint16_t*>(to) = *reinterpret_cast<const uint16_t*>(p);
+          else *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(p);
+        }
+      };
+      one_by_one(s.begin, s.from < s.end ? s.from : s.end);
+      one_by_one(s.to > s.begin ? s.to : s.begin, s.end);
+      at += ring_place<VEC>(groups * d * es);
     }
+  }
+  mbar_expect_tx(bar, total);
+  at = 0;
+#pragma unroll
+  for (int i = 0; i < kRingSrcs; ++i) {
+    if (src[i].p == nullptr) continue;
+    const RingSpan s = ring_span<VEC>(src[i], base, rows, T, d);
+    if (VEC || s.to > s.from)
+      bulk_load(stage + at + (VEC ? 0 : static_cast<int>(s.from - (s.begin & ~uintptr_t(15)))),
+                reinterpret_cast<const void*>(s.from), static_cast<uint32_t>(s.to - s.from), bar);
+    at += ring_place<VEC>(groups * d * src[i].esize);
+  }
 }
 
 // After a wait that gave up: the copies still in flight, once more with a limit

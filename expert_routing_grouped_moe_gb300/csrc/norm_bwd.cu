@@ -74,17 +74,22 @@ cudaError_t launch_norm_bwd(const NormArgs& args, int x_type, int y_type, bool v
     const int xs = x_type == MOE_BF16 ? 2 : 4, ys = y_type == MOE_BF16 ? 2 : 4;
     const bool pre = a.w_pre != nullptr;
     NormShape sh = norm_bwd_shape(a.d, true);
-    a.tile = sh.groups * a.d * ((a.x ? xs : 0) + (pre ? xs + ys : 0) + (a.y ? ys : 0) +
-                                (a.gate_kind == MOE_GATE_ELEMENT ? ys : 0));
+    auto place = [&](int size) {
+      const int bytes = sh.groups * a.d * size;
+      return vec ? ring_place<true>(bytes) : ring_place<false>(bytes);
+    };
+    a.tile = (a.x ? place(xs) : 0) + (pre ? place(xs) + place(ys) : 0) + (a.y ? place(ys) : 0) +
+             (a.gate_kind == MOE_GATE_ELEMENT ? place(ys) : 0);
     const bool barrier = pre || a.w_post || (a.gate_kind == MOE_GATE_TOKEN && a.dgate);
-    const bool ring = vec && sh.nv <= 2 && sh.W > 1 && barrier &&
+    const bool ring = sh.nv <= 2 && sh.W > 1 && barrier &&
                       a.T > static_cast<int64_t>(kNormRingTiles) * sh.groups;
-    a.stages = ring ? ring_stages(a.tile, norm_bwd_per_sm(sh, a.nsum > 0), norm_const_bytes(sh)) : 0;
+    const bool sums = a.nsum > 0 || !vec;  // the kernels for any alignment always keep them
+    a.stages = ring ? ring_stages(a.tile, norm_bwd_per_sm(sh, sums), norm_const_bytes(sh)) : 0;
     if (a.stages == 0) sh = norm_bwd_shape(a.d, false);
     a.W = sh.W;
-    const int blocks = norm_bwd_blocks(sh, a.T, a.nsum > 0);
+    const int blocks = norm_bwd_blocks(sh, a.T, sums);
     rows = blocks * sh.groups;
-    e = a.stages > 0 ? launch_norm_bwd_ring(a, x_type, y_type, blocks, s)
+    e = a.stages > 0 ? launch_norm_bwd_ring(a, x_type, y_type, vec, blocks, s)
                      : launch_norm_bwd_direct(a, x_type, y_type, vec, blocks, s);
   }
   if (e != cudaSuccess || a.nsum == 0) return e;

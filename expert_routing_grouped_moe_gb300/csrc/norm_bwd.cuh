@@ -22,7 +22,8 @@ namespace moe {
 // and gate; column sums always kept) and rows through the ring.
 cudaError_t launch_norm_bwd_direct(const NormArgs& a, int x_type, int y_type, bool vec, int blocks,
                                    cudaStream_t s);
-cudaError_t launch_norm_bwd_ring(const NormArgs& a, int x_type, int y_type, int blocks, cudaStream_t s);
+cudaError_t launch_norm_bwd_ring(const NormArgs& a, int x_type, int y_type, bool vec, int blocks,
+                                 cudaStream_t s);
 
 // MAXT, MINB: threads of a block at most, blocks an SM holds at least.
 template <typename XT, typename YT, bool VEC, int NV, int GATE, bool SUMS, bool RING, int MAXT, int MINB>
@@ -64,7 +65,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) 
   pdl_wait();
   if (RING && threadIdx.x == 0)
     for (int q = 0; q < a.stages && base + q * step < a.T; ++q)
-      ring_fill(src, s_tiles + q * a.tile, &s_full[q], base + q * step, a.T, groups, d);
+      ring_fill<VEC>(src, s_tiles + q * a.tile, &s_full[q], base + q * step, a.T, groups, d);
   // per column: k = (w_post + off) a(channel gate), u = w_pre + off
   auto make_k = [&](int v, f2 (&k)[4]) {
 #pragma unroll
@@ -129,11 +130,11 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) 
       make_k(v0 + i * 32 * W, f);
     }
   };
-  // offsets of this thread's row of each input in a tile
-  const int rx = groups * d * static_cast<int>(sizeof(XT)), ry_ = groups * d * static_cast<int>(sizeof(YT));
-  const int at_r = a.x != nullptr ? rx : 0, at_n = at_r + (pre ? rx : 0), at_y = at_n + (pre ? ry_ : 0),
-            at_g = at_y + (has_y ? ry_ : 0);
-  const int in_x = grp * d * static_cast<int>(sizeof(XT)), in_y = grp * d * static_cast<int>(sizeof(YT));
+  // offsets of each input's rows in a tile
+  const int place_x = ring_place<VEC>(groups * d * static_cast<int>(sizeof(XT))),
+            place_y = ring_place<VEC>(groups * d * static_cast<int>(sizeof(YT)));
+  const int at_r = a.x != nullptr ? place_x : 0, at_n = at_r + (pre ? place_x : 0),
+            at_y = at_n + (pre ? place_y : 0), at_g = at_y + (has_y ? place_y : 0);
   // the scalars of a row are read one tile ahead
   float next_r = 0.f, next_y = 0.f, next_g = 0.f;
   auto read_ahead = [&](int64_t row) {
@@ -162,11 +163,11 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) 
       if (!mbar_wait(&s_full[stage], phase, &s_abort, kWaitTimeoutNs) && threadIdx.x == 0)
         atomicCAS(a.status, 0, kErrTimeout);
       const uint8_t* t = s_tiles + stage * a.tile;
-      pdr = reinterpret_cast<const XT*>(t + in_x);
-      pr = reinterpret_cast<const XT*>(t + (at_r + in_x));
-      pdn = reinterpret_cast<const YT*>(t + (at_n + in_y));
-      py = reinterpret_cast<const YT*>(t + (at_y + in_y));
-      pg = reinterpret_cast<const YT*>(t + (at_g + in_y));
+      pdr = ring_row<VEC>(t, static_cast<const XT*>(a.x), base, d) + grp * d;
+      pr = ring_row<VEC>(t + at_r, static_cast<const XT*>(a.r), base, d) + grp * d;
+      pdn = ring_row<VEC>(t + at_n, static_cast<const YT*>(a.n), base, d) + grp * d;
+      py = ring_row<VEC>(t + at_y, static_cast<const YT*>(a.y), base, d) + grp * d;
+      pg = ring_row<VEC>(t + at_g, static_cast<const YT*>(a.gate), base, d) + grp * d;
     }
     // pass 1: e in place of dr; the row sums, of r and y as they are (their rstd
     // factors follow)
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) 
     if (pre || post || sum_gate_row) row_sum<3>(sum, s_red[turn], W, warp, first);
     if (RING && threadIdx.x == 0 && base >= step) {  // the previous tile's place is free
       const int64_t next = base + (a.stages - 1) * step;
-      if (next < a.T) ring_fill(src, s_tiles + before * a.tile, &s_full[before], next, a.T, groups, d);
+      if (next < a.T) ring_fill<VEC>(src, s_tiles + before * a.tile, &s_full[before], next, a.T, groups, d);
     }
     const float c1 = rs_r * (rs_r * (rs_r * (sum[0] * inv_d)));  // t = e - c1 r
     const float apt = rs_y * fmaf(-c1, sum[2], sum[1]);     // sum A p t

@@ -4,9 +4,9 @@
 namespace moe {
 namespace {
 
-template <typename XT, typename YT, int NV, int GATE, bool SUMS, int MAXT, int MINB>
+template <typename XT, typename YT, bool VEC, int NV, int GATE, bool SUMS, int MAXT, int MINB>
 cudaError_t go(const NormArgs& a, int blocks, cudaStream_t s) {
-  auto kern = norm_bwd_kernel<XT, YT, true, NV, GATE, SUMS, true, MAXT, MINB>;
+  auto kern = norm_bwd_kernel<XT, YT, VEC, NV, GATE, SUMS, true, MAXT, MINB>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
   if (e != cudaSuccess) return e;
@@ -18,15 +18,19 @@ cudaError_t go(const NormArgs& a, int blocks, cudaStream_t s) {
 template <typename XT, typename YT, int NV, bool SUMS, int MAXT, int MINB>
 cudaError_t pick_gate(const NormArgs& a, int blocks, cudaStream_t s) {
   switch (gate_class(a.gate_kind)) {
-    case kGateRow: return go<XT, YT, NV, kGateRow, SUMS, MAXT, MINB>(a, blocks, s);
-    case kGateChannel: return go<XT, YT, NV, kGateChannel, SUMS, MAXT, MINB>(a, blocks, s);
-    default: return go<XT, YT, NV, kGateElement, SUMS, MAXT, MINB>(a, blocks, s);
+    case kGateRow: return go<XT, YT, true, NV, kGateRow, SUMS, MAXT, MINB>(a, blocks, s);
+    case kGateChannel: return go<XT, YT, true, NV, kGateChannel, SUMS, MAXT, MINB>(a, blocks, s);
+    default: return go<XT, YT, true, NV, kGateElement, SUMS, MAXT, MINB>(a, blocks, s);
   }
 }
 
 template <typename XT, typename YT>
-cudaError_t pick(const NormArgs& a, int blocks, cudaStream_t s) {
-  if (norm_bwd_shape(a.d, true).nv == 1)  // 256 threads
+cudaError_t pick(const NormArgs& a, bool vec, int blocks, cudaStream_t s) {
+  const bool one = norm_bwd_shape(a.d, true).nv == 1;  // 256 threads, else up to 512
+  if (!vec)
+    return one ? go<XT, YT, false, 1, kGateAny, true, 256, 2>(a, blocks, s)
+               : go<XT, YT, false, 2, kGateAny, true, 512, 1>(a, blocks, s);
+  if (one)
     return a.nsum > 0 ? pick_gate<XT, YT, 1, true, 256, 2>(a, blocks, s)
                       : pick_gate<XT, YT, 1, false, 256, 3>(a, blocks, s);
   return a.nsum > 0 ? pick_gate<XT, YT, 2, true, 512, 1>(a, blocks, s)
@@ -35,9 +39,11 @@ cudaError_t pick(const NormArgs& a, int blocks, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_norm_bwd_ring(const NormArgs& a, int x_type, int y_type, int blocks, cudaStream_t s) {
-  if (x_type == MOE_BF16) return pick<bf16_t, bf16_t>(a, blocks, s);
-  return y_type == MOE_BF16 ? pick<float, bf16_t>(a, blocks, s) : pick<float, float>(a, blocks, s);
+cudaError_t launch_norm_bwd_ring(const NormArgs& a, int x_type, int y_type, bool vec, int blocks,
+                                 cudaStream_t s) {
+  if (x_type == MOE_BF16) return pick<bf16_t, bf16_t>(a, vec, blocks, s);
+  return y_type == MOE_BF16 ? pick<float, bf16_t>(a, vec, blocks, s)
+                            : pick<float, float>(a, vec, blocks, s);
 }
 
 }  // namespace moe

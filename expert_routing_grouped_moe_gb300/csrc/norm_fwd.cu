@@ -10,8 +10,8 @@
 namespace moe {
 namespace {
 
-// RING: rows come through the ring of bulk copies (vector path, at least one
-// norm, rows of several warps); else each thread loads its share from memory.
+// RING: rows come through the ring of bulk copies (at least one norm, rows of
+// several warps); else each thread loads its share from memory.
 template <typename XT, typename YT, bool VEC, int NV, int GATE, bool RING>
 __global__ void __launch_bounds__(RING && NV == 1 ? 384 : 512, RING && NV == 1 ? 2 : 1) norm_fwd_kernel(const NormArgs a) {
   extern __shared__ __align__(128) uint8_t s_tiles[];
@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(RING && NV == 1 ? 384 : 512, RING && NV == 1 ?
   pdl_wait();
   if (RING && threadIdx.x == 0)
     for (int q = 0; q < a.stages && base + q * step < a.T; ++q)
-      ring_fill(src, s_tiles + q * a.tile, &s_full[q], base + q * step, a.T, groups, d);
+      ring_fill<VEC>(src, s_tiles + q * a.tile, &s_full[q], base + q * step, a.T, groups, d);
   const bool channel = gate_is<GATE>(a.gate_kind, MOE_GATE_CHANNEL);
   const bool element = gate_is<GATE>(a.gate_kind, MOE_GATE_ELEMENT);
   // per column: k = (w_post + off) a(channel gate), u = w_pre + off
@@ -91,17 +91,17 @@ __global__ void __launch_bounds__(RING && NV == 1 ? 384 : 512, RING && NV == 1 ?
       if (!mbar_wait(&s_full[stage], phase, &s_abort, kWaitTimeoutNs) && threadIdx.x == 0)
         atomicCAS(a.status, 0, kErrTimeout);
       const uint8_t* t = s_tiles + stage * a.tile;
-      px = reinterpret_cast<const XT*>(t) + grp * d;
-      if (a.x != nullptr) t += groups * d * sizeof(XT);
-      py = reinterpret_cast<const YT*>(t) + grp * d;
-      if (has_y) t += groups * d * sizeof(YT);
-      pg = reinterpret_cast<const YT*>(t) + grp * d;
+      px = ring_row<VEC>(t, static_cast<const XT*>(a.x), base, d) + grp * d;
+      if (a.x != nullptr) t += ring_place<VEC>(groups * d * sizeof(XT));
+      py = ring_row<VEC>(t, static_cast<const YT*>(a.y), base, d) + grp * d;
+      if (has_y) t += ring_place<VEC>(groups * d * sizeof(YT));
+      pg = ring_row<VEC>(t, static_cast<const YT*>(a.gate), base, d) + grp * d;
     }
     // after the first barrier of this tile: the previous tile's place is free
     auto refill = [&]() {
       if (RING && threadIdx.x == 0 && base >= step) {
         const int64_t next = base + (a.stages - 1) * step;
-        if (next < a.T) ring_fill(src, s_tiles + before * a.tile, &s_full[before], next, a.T, groups, d);
+        if (next < a.T) ring_fill<VEC>(src, s_tiles + before * a.tile, &s_full[before], next, a.T, groups, d);
       }
     };
     f2 x[NV][4], y[NV][4];
@@ -215,6 +215,8 @@ cudaError_t pick_nv(const NormArgs& a, bool vec, cudaStream_t s) {
         case kGateChannel: return go<XT, YT, true, NV, kGateChannel, true>(a, s);
         default: return go<XT, YT, true, NV, kGateElement, true>(a, s);
       }
+  if constexpr (NV <= 2)
+    if (!vec && a.stages > 0) return go<XT, YT, false, NV, kGateAny, true>(a, s);
   return vec ? go<XT, YT, true, NV, kGateAny, false>(a, s)
              : go<XT, YT, false, NV, kGateAny, false>(a, s);
 }
@@ -224,9 +226,13 @@ cudaError_t pick(NormArgs a, bool vec, cudaStream_t s) {
   const NormShape sh = norm_fwd_shape(a.d);
   const int groups = sh.groups, nv = sh.nv;
   a.W = sh.W;
-  a.tile = groups * a.d * static_cast<int>((a.x ? sizeof(XT) : 0) + (a.y ? sizeof(YT) : 0) +
-                                           (a.gate_kind == MOE_GATE_ELEMENT ? sizeof(YT) : 0));
-  const bool ring = vec && nv <= 2 && a.W > 1 && (a.w_post || a.w_pre) &&
+  auto place = [&](size_t size) {
+    const int bytes = groups * a.d * static_cast<int>(size);
+    return vec ? ring_place<true>(bytes) : ring_place<false>(bytes);
+  };
+  a.tile = (a.x ? place(sizeof(XT)) : 0) + (a.y ? place(sizeof(YT)) : 0) +
+           (a.gate_kind == MOE_GATE_ELEMENT ? place(sizeof(YT)) : 0);
+  const bool ring = nv <= 2 && a.W > 1 && (a.w_post || a.w_pre) &&
                     a.T > static_cast<int64_t>(kNormRingTiles) * groups;
   a.stages = ring ? ring_stages(a.tile, sh.threads() > 256 ? 3 : 4, 0) : 0;
   if (a.stages == 0) a.tile = 0;

@@ -147,14 +147,22 @@ def test_many_rows_for_each_block_and_ragged_groups():
 
 
 @pytest.mark.parametrize("xt,yt", [(BF, BF), (F32, BF), (F32, F32)])
-@pytest.mark.parametrize("T,d", [(1300, 264), (701, 1000), (641, 2048), (613, 2880), (311, 4104),
-                                 (333, 8192)])
-def test_rows_through_the_ring(T, d, xt, yt):
+@pytest.mark.parametrize("T,d,off", [
+    (1300, 264, 0), (701, 1000, 0), (641, 2048, 0), (613, 2880, 0), (311, 4104, 0), (333, 8192, 0),
+    (1301, 263, 0), (703, 1001, 0), (701, 1002, 0), (640, 2047, 0), (612, 2881, 0), (311, 4103, 0),
+    (310, 8191, 0), (641, 2048, 1), (640, 1000, 3), (1217, 261, 5)])
+def test_rows_through_the_ring(T, d, off, xt, yt):
     """Enough rows that they come by bulk copies, with a last tile that is not
-    full; every gate with every choice of norms."""
+    full; every gate with every choice of norms; widths and buffers (off values
+    past an aligned address) that the copies' 16-byte words do not fit."""
+    def place(shape, dtype):
+        n = int(np.prod(shape))
+        # NaN around each buffer: the words that come along must not matter
+        raw = torch.full((n + 2 * off,), float("nan"), dtype=dtype, device=DEV)
+        return raw[off:off + n].view(shape)
     for i, (kind, sigmoid) in enumerate(GATES):
         for post, pre in NORMS[:3]:
-            b = make(T, d, xt, yt, kind, post, pre, seed=i)
+            b = make(T, d, xt, yt, kind, post, pre, seed=i, place=place)
             forward(b, kind, sigmoid, scale=0.5)
             if i % 2:     # frozen weights and gate
                 b["dw_post"] = b["dw_pre"] = None
@@ -162,7 +170,7 @@ def test_rows_through_the_ring(T, d, xt, yt):
             backward(b, kind, sigmoid, scale=0.5)
             check(b, kind, sigmoid, scale=0.5)
     # without a residual's gradient, without some outputs
-    b = make(T, d, xt, yt, "channel", True, True)
+    b = make(T, d, xt, yt, "channel", True, True, place=place)
     forward(b, "channel", True)
     b["dr"] = None
     L.moe_block_norm_bwd(None, b["dn"], b["r"], b["y"], None, b["dy"], w_post=b["w_post"],
@@ -209,7 +217,7 @@ def test_norm_alone_and_gate_alone():
 
 
 def test_in_place_equals_out_of_place():
-    for T, d in ((77, 2048), (77, 1001), (650, 2048), (330, 4096)):
+    for T, d in ((77, 2048), (77, 1001), (650, 2048), (330, 4096), (700, 1001)):
         b = make(T, d, BF, BF, "element", True, True)
         forward(b, "element", False)
         backward(b, "element", False)
@@ -240,7 +248,7 @@ def test_rows_of_zeros_and_extreme_gates():
 
 @pytest.mark.parametrize("d", [512, 1001, 2048])
 def test_a_row_with_nan_spoils_no_other_row(d):
-    T = 40 if d < 2048 else 640
+    T = 40 if d < 1000 else 640
     b = make(T, d, BF, BF, "token", True, True)
     forward(b, "token", False)
     backward(b, "token", False)
@@ -348,7 +356,7 @@ def test_nothing_is_written_past_a_buffer():
         raw = torch.full((n + 512,), 0xA5, dtype=torch.uint8, device=DEV)
         bands.append((raw, n))
         return raw[256:256 + n].view(dtype).view(shape)
-    for T, d in ((9, 96), (311, 1001), (17, 2880), (5, 4104), (650, 2048), (320, 4104)):
+    for T, d in ((9, 96), (311, 1001), (17, 2880), (5, 4104), (650, 2048), (320, 4104), (701, 1001), (311, 4103)):
         for kind in ("token", "channel", "element"):
             b = make(T, d, BF, BF, kind, True, True, place=place)
             raw = torch.full((b["ws"].numel() + 512,), 0xA5, dtype=torch.uint8, device=DEV)
