@@ -343,9 +343,11 @@ def _shaped(t, shape, dtype, name):
     """Pointer of a contiguous CUDA tensor of this shape and type (None stays None)."""
     if t is None:
         return None
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda
-            and t.is_contiguous()):
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     p = _ptr(t, dtype, name)   # says what is wrong
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
@@ -419,8 +421,8 @@ def moe_block_norm_bwd(dr, dn, r, y, dx=None, dy=None, w_post=None, w_pre=None, 
     """Gradients of moe_block_norm_fwd from dr (of r; None: zero) and dn (of n);
     outputs left out are not computed.  dgate has the gate's shape and type,
     dw_post and dw_pre are [d] fp32."""
-    x_side = next((t for t in (dr, r, dx) if t is not None), None)
-    y_side = next((t for t in (y, dn, dy) if t is not None), None)
+    x_side = dr if dr is not None else r if r is not None else dx
+    y_side = y if y is not None else dn if dn is not None else dy
     desc, sh, xt, yt, gs, gt = _norm_desc(x_side, y_side, gate, gate_kind, gate_sigmoid, scale,
                                           eps, w_offset)
     T, d = sh

@@ -2,6 +2,7 @@
 // norm_bwd.cu): what the two share.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/moe_gb300.h"
@@ -166,6 +167,7 @@ struct RingSrc {
   int esize;       // bytes of an element
 };
 constexpr int kRingSrcs = 5, kRingMaxStages = 4;
+constexpr int kRingBytes = 208 * 1024;  // of an SM's shared memory
 
 // Bytes of a tile's place for `bytes` of rows.
 template <bool VEC>
@@ -246,6 +248,19 @@ __device__ __forceinline__ void ring_fill(const RingSrc (&src)[kRingSrcs], uint8
   }
 }
 
+// Lets a kernel use the ring's shared memory, once on each device.
+template <typename Kernel>
+cudaError_t allow_ring(Kernel kern, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 // After a wait that gave up: the copies still in flight, once more with a limit
 // (in a normal run every copy issued has been waited for).
 __device__ __forceinline__ void ring_drain(uint64_t* full, int stages, int stage, int phase) {
@@ -256,7 +271,6 @@ __device__ __forceinline__ void ring_drain(uint64_t* full, int stages, int stage
 // Stages of a ring of `tile` bytes each: as many, up to 4, as leave room for
 // `per` blocks on an SM (each with `extra` bytes besides); 0 when not even two
 // fit one block.
-constexpr int kRingBytes = 208 * 1024;
 inline int ring_stages(size_t tile, int per, size_t extra) {
   const int64_t n = (kRingBytes / per - static_cast<int64_t>(extra)) / static_cast<int64_t>(tile);
   return n >= kRingMaxStages ? kRingMaxStages

@@ -7,8 +7,8 @@ namespace {
 template <typename XT, typename YT, bool VEC, int NV, int GATE, bool SUMS, int MAXT, int MINB>
 cudaError_t go(const NormArgs& a, int blocks, cudaStream_t s) {
   auto kern = norm_bwd_kernel<XT, YT, VEC, NV, GATE, SUMS, true, MAXT, MINB>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_ring(kern, done);
   if (e != cudaSuccess) return e;
   const NormShape sh = norm_bwd_shape(a.d, true);
   return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(sh.threads()),

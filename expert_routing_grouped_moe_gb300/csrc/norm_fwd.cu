@@ -3,8 +3,6 @@
 //   p = y rstd(y) (w_post + off) or y;  r = x + s a(gate) p;  n = r rstd(r) (w_pre + off)
 // with rstd(z) = 1/sqrt(mean z^2 + eps).  Everything between the loads and the
 // stores is fp32; n is the norm of the unrounded r.
-#include <atomic>
-
 #include "norm.cuh"
 
 namespace moe {
@@ -188,8 +186,8 @@ cudaError_t go(const NormArgs& a, cudaStream_t s) {
   const size_t smem = static_cast<size_t>(a.stages) * a.tile;
   auto kern = norm_fwd_kernel<XT, YT, VEC, NV, GATE, RING>;
   if (RING) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kRingBytes);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_ring(kern, done);
     if (e != cudaSuccess) return e;
   }
   // blocks that fit an SM, found once for each block size and ring
