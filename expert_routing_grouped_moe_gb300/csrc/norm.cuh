@@ -268,15 +268,21 @@ __device__ __forceinline__ void ring_drain(uint64_t* full, int stages, int stage
   for (int q = 0; q < stages; ++q) mbar_wait(&full[q], phase ^ (q < stage ? 0 : 1), &never, 1000000000ull);
 }
 
-// Stages of a ring of `tile` bytes each: as many, up to 4, as leave room for
-// `per` blocks on an SM (each with `extra` bytes besides); 0 when not even two
-// fit one block.
-inline int ring_stages(size_t tile, int per, size_t extra) {
-  const int64_t n = (kRingBytes / per - static_cast<int64_t>(extra)) / static_cast<int64_t>(tile);
-  return n >= kRingMaxStages ? kRingMaxStages
-         : n >= 2            ? static_cast<int>(n)
-         : per > 1           ? ring_stages(tile, per - 1, extra)
-                             : 0;
+// Stages of a ring of `tile` bytes each for up to *per blocks on an SM (each with
+// `extra` bytes besides): as many, from 2 to 4, as keep at most `flight` bytes on
+// their way to an SM; fewer blocks where two stages each do not fit, 0 when they
+// do not fit one.  The forward does best with about 100 KB in flight (16384x2880
+// 62 us; 67.6 with 138 KB, 85 with 46), the backward, which computes longer on a
+// tile, with all that fits (16384x2048 70 us, 83 with 98 KB).
+constexpr int kFwdFlight = 104 * 1024, kBwdFlight = kRingBytes;
+inline int ring_stages(size_t tile, int* per, size_t extra, int64_t flight) {
+  for (; *per > 0; --*per) {
+    const int64_t room = kRingBytes / *per - static_cast<int64_t>(extra), t = static_cast<int64_t>(tile);
+    if (room < 2 * t) continue;
+    const int64_t fit = room / t, want = flight / (*per * t), n = want < fit ? want : fit;
+    return n < 2 ? 2 : n < kRingMaxStages ? static_cast<int>(n) : kRingMaxStages;
+  }
+  return 0;
 }
 // The backward's two vectors of per-column factors.
 inline size_t norm_const_bytes(const NormShape& s) { return static_cast<size_t>(s.threads()) * s.nv * 64; }

@@ -84,7 +84,8 @@ cudaError_t launch_norm_bwd(const NormArgs& args, int x_type, int y_type, bool v
     const bool ring = sh.nv <= 2 && sh.W > 1 && barrier &&
                       a.T > static_cast<int64_t>(kNormRingTiles) * sh.groups;
     const bool sums = a.nsum > 0 || !vec;  // the kernels for any alignment always keep them
-    a.stages = ring ? ring_stages(a.tile, norm_bwd_per_sm(sh, sums), norm_const_bytes(sh)) : 0;
+    int per = norm_bwd_per_sm(sh, sums);
+    a.stages = ring ? ring_stages(a.tile, &per, norm_const_bytes(sh), kBwdFlight) : 0;
     if (a.stages == 0) sh = norm_bwd_shape(a.d, false);
     a.W = sh.W;
     const int blocks = norm_bwd_blocks(sh, a.T, sums);

@@ -180,41 +180,41 @@ __global__ void __launch_bounds__(RING && NV == 1 ? 384 : 512, RING && NV == 1 ?
 }
 
 template <typename XT, typename YT, bool VEC, int NV, int GATE, bool RING>
-cudaError_t go(const NormArgs& a, cudaStream_t s) {
+cudaError_t go(const NormArgs& args, cudaStream_t s) {
+  NormArgs a = args;
   const NormShape sh = norm_fwd_shape(a.d);
-  const int groups = sh.groups, threads = sh.threads();
-  const size_t smem = static_cast<size_t>(a.stages) * a.tile;
   auto kern = norm_fwd_kernel<XT, YT, VEC, NV, GATE, RING>;
   if (RING) {
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_ring(kern, done);
     if (e != cudaSuccess) return e;
   }
-  // blocks that fit an SM, found once for each block size and ring
-  static std::atomic<int> fit[kNormMaxWarps + 1][kRingMaxStages + 1];
-  int per = fit[threads / 32][a.stages].load(std::memory_order_relaxed);
+  // blocks whose registers fit an SM, found once for each block size
+  static std::atomic<int> fit[kNormMaxWarps + 1];
+  int per = fit[sh.threads() / 32].load(std::memory_order_relaxed);
   if (per == 0) {
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, threads, smem);
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, sh.threads(), 0);
     if (e != cudaSuccess) return e;
     if (per < 1) per = 1;
-    fit[threads / 32][a.stages].store(per, std::memory_order_relaxed);
+    fit[sh.threads() / 32].store(per, std::memory_order_relaxed);
   }
-  const int64_t need = (a.T + groups - 1) / groups;
+  if (RING) a.stages = ring_stages(a.tile, &per, 0, kFwdFlight);
+  const int64_t need = (a.T + sh.groups - 1) / sh.groups;
   const int64_t most = static_cast<int64_t>(per) * kSMs;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(need < most ? need : most)), dim3(threads), smem,
-                    s, a);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(need < most ? need : most)), dim3(sh.threads()),
+                    static_cast<size_t>(a.stages) * a.tile, s, a);
 }
 
 template <typename XT, typename YT, int NV>
 cudaError_t pick_nv(const NormArgs& a, bool vec, cudaStream_t s) {
   if constexpr (NV <= 2)
-    if (vec && a.stages > 0) switch (gate_class(a.gate_kind)) {
+    if (vec && a.tile > 0) switch (gate_class(a.gate_kind)) {
         case kGateRow: return go<XT, YT, true, NV, kGateRow, true>(a, s);
         case kGateChannel: return go<XT, YT, true, NV, kGateChannel, true>(a, s);
         default: return go<XT, YT, true, NV, kGateElement, true>(a, s);
       }
   if constexpr (NV <= 2)
-    if (!vec && a.stages > 0) return go<XT, YT, false, NV, kGateAny, true>(a, s);
+    if (!vec && a.tile > 0) return go<XT, YT, false, NV, kGateAny, true>(a, s);
   return vec ? go<XT, YT, true, NV, kGateAny, false>(a, s)
              : go<XT, YT, false, NV, kGateAny, false>(a, s);
 }
@@ -232,8 +232,8 @@ cudaError_t pick(NormArgs a, bool vec, cudaStream_t s) {
            (a.gate_kind == MOE_GATE_ELEMENT ? place(sizeof(YT)) : 0);
   const bool ring = nv <= 2 && a.W > 1 && (a.w_post || a.w_pre) &&
                     a.T > static_cast<int64_t>(kNormRingTiles) * groups;
-  a.stages = ring ? ring_stages(a.tile, sh.threads() > 256 ? 3 : 4, 0) : 0;
-  if (a.stages == 0) a.tile = 0;
+  a.stages = 0;
+  if (!ring || 2 * a.tile > kRingBytes) a.tile = 0;  // rows are read directly
   switch (nv) {
     case 1: return pick_nv<XT, YT, 1>(a, vec, s);
     case 2: return pick_nv<XT, YT, 2>(a, vec, s);
