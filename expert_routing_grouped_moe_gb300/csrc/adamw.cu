@@ -49,7 +49,6 @@ struct Tensor {
   uint8_t* sc;
   int64_t n;
   float keep, lr;  // 1 - lr wd; lr / (1 - b1^t)
-  int chunk0;      // first chunk of the tensor in this launch
   int vec;         // all pointers allow 8-value vectors
 };
 struct Consts {
@@ -68,12 +67,12 @@ template <int MAX>
 struct Table {
   Consts c;
   int n, chunks;
+  int start[MAX];  // first chunk of each tensor in this launch
   Tensor t[MAX];
 };
 struct NormTensor {
   const void* g;
-  int64_t n;
-  int chunk0, bf16;
+  int64_t n2;      // 2 n, + 1 for bf16
 };
 constexpr int kNormFew = 64, kNormSome = 256, kNormMany = 1200;
 template <int MAX>
@@ -81,8 +80,19 @@ struct NormTable {
   int n, chunks;
   float zero;  // -0
   float2* part;
+  int start[MAX];
   NormTensor t[MAX];
 };
+// The tensor that chunk ch belongs to: the last that starts at or before it.
+__device__ __forceinline__ int tensor_of(const int* start, int n, int ch) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= ch) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
 
 // Packed product that no later sum is contracted with: the assembler makes one
 // fma of a packed mul and add in spite of their rounding modifiers, so the
@@ -301,12 +311,11 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? 5 : 4) adamw_kernel(const __
     }
   }
   // Backwards: after a norm the gradients' end is what is left of them in the L2.
-  int ti = tab.n - 1;
   for (int ch = tab.chunks - 1 - static_cast<int>(blockIdx.x); ch >= 0; ch -= gridDim.x) {
-    while (ch < tab.t[ti].chunk0) --ti;
+    const int ti = tensor_of(tab.start, tab.n, ch);
     const Tensor& t = tab.t[ti];
     const int64_t n = t.n;
-    const int64_t i = static_cast<int64_t>(ch - t.chunk0) * kChunk + threadIdx.x * 8;
+    const int64_t i = static_cast<int64_t>(ch - tab.start[ti]) * kChunk + threadIdx.x * 8;
     const bool vec = t.vec && i + 8 <= n;
     f2 p[4], g[4], m[4], v[4], root[4];
     take(static_cast<const GT*>(t.g), i, n, vec, g);
@@ -389,15 +398,14 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
   pdl_wait();
   const Product mul{pk(tab.zero)};
   f2 hi = pk(0.f), lo = pk(0.f);
-  int ti = 0;
   for (int ch = blockIdx.x; ch < tab.chunks; ch += gridDim.x) {
-    while (ti + 1 < tab.n && ch >= tab.t[ti + 1].chunk0) ++ti;
+    const int ti = tensor_of(tab.start, tab.n, ch);
     const NormTensor& t = tab.t[ti];
-    const int64_t i = static_cast<int64_t>(ch - t.chunk0) * kChunk + threadIdx.x * 8;
-    const bool vec = (reinterpret_cast<uintptr_t>(t.g) & 15u) == 0 && i + 8 <= t.n;
+    const int64_t i = static_cast<int64_t>(ch - tab.start[ti]) * kChunk + threadIdx.x * 8, n = t.n2 >> 1;
+    const bool vec = (reinterpret_cast<uintptr_t>(t.g) & 15u) == 0 && i + 8 <= n;
     f2 g[4];
-    if (t.bf16) take(static_cast<const bf16_t*>(t.g), i, t.n, vec, g);
-    else take(static_cast<const float*>(t.g), i, t.n, vec, g);
+    if (t.n2 & 1) take(static_cast<const bf16_t*>(t.g), i, n, vec, g);
+    else take(static_cast<const float*>(t.g), i, n, vec, g);
 #pragma unroll
     for (int e = 0; e < 4; ++e) add_square(g[e], hi, lo, mul);
   }
@@ -468,13 +476,13 @@ cudaError_t step_kind(int kind, const moe_adamw_tensor* ts, int n, const moe_ada
       const cudaError_t e = flush();
       if (e != cudaSuccess) return e;
     }
+    tab.start[tab.n] = tab.chunks;
     Tensor& t = tab.t[tab.n++];
     t.p = q.param; t.master = q.master; t.g = q.grad; t.m = q.m; t.v = q.v; t.sc = q.scales;
     t.n = q.n;
     const double lr = h->lr * static_cast<double>(q.lr_mult);
     t.keep = static_cast<float>(1.0 - lr * static_cast<double>(q.weight_decay));
     t.lr = static_cast<float>(lr / b1t);
-    t.chunk0 = tab.chunks;
     const uintptr_t wide = reinterpret_cast<uintptr_t>(q.param) | reinterpret_cast<uintptr_t>(q.master) |
                            reinterpret_cast<uintptr_t>(q.grad);
     const uintptr_t st = reinterpret_cast<uintptr_t>(q.m) | reinterpret_cast<uintptr_t>(q.v);
@@ -506,7 +514,8 @@ cudaError_t norm_all(const moe_adamw_tensor* ts, int n, float2* part, int* npart
       const cudaError_t e = flush();
       if (e != cudaSuccess) return e;
     }
-    tab.t[tab.n++] = NormTensor{ts[i].grad, ts[i].n, tab.chunks, ts[i].grad_type == MOE_BF16 ? 1 : 0};
+    tab.start[tab.n] = tab.chunks;
+    tab.t[tab.n++] = NormTensor{ts[i].grad, 2 * ts[i].n + (ts[i].grad_type == MOE_BF16 ? 1 : 0)};
     tab.chunks += static_cast<int>(ch);
   }
   return flush();

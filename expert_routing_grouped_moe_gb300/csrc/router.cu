@@ -82,8 +82,11 @@ __device__ __forceinline__ float end_column(const LossEnd& o, int e, int E, floa
   o.pmean[e] = t;
   return static_cast<float>(o.counts[e]) * t;
 }
-// losses[0] from the threads' shares; s_aux: 32 floats.
-__device__ __forceinline__ void end_aux(const LossEnd& o, float aux, int T, int E, float* s_aux) {
+__device__ __forceinline__ void end_aux(const LossEnd& o, float aux, int T, int E) {
+  o.losses[0] = aux * (static_cast<float>(E) / (static_cast<float>(T) * static_cast<float>(o.k)));
+}
+// Sum over a block of 1024 threads, in thread 0 (all of warp 0); s_aux: 32 floats.
+__device__ __forceinline__ float block_aux(float aux, float* s_aux) {
 #pragma unroll
   for (int i = 16; i > 0; i >>= 1) aux += __shfl_xor_sync(0xffffffffu, aux, i);
   if ((threadIdx.x & 31) == 0) s_aux[threadIdx.x >> 5] = aux;
@@ -92,9 +95,14 @@ __device__ __forceinline__ void end_aux(const LossEnd& o, float aux, int T, int 
     aux = s_aux[threadIdx.x];
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) aux += __shfl_xor_sync(0xffffffffu, aux, i);
-    if (threadIdx.x == 0)
-      o.losses[0] = aux * (static_cast<float>(E) / (static_cast<float>(T) * static_cast<float>(o.k)));
   }
+  return aux;
+}
+// A shared variable of the cluster's block q.
+__device__ __forceinline__ float cluster_float(const float* p, unsigned q) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(p), q)) : "memory");
+  return v;
 }
 
 // part: [gridDim.x][ld]: sums of P over the block's rows, then of lse^2, then zeros.
@@ -192,35 +200,34 @@ __global__ void __launch_bounds__(ONE ? kOneThreads : kRouterThreads) router_los
   if (cluster_ctarank() == 0) {
     float aux = 0.f;
     if (threadIdx.x <= E) {
-      const uint32_t mine = smem_u32(&s_sum[threadIdx.x]);
       float t = 0.f;
-      for (unsigned q = 0; q < gridDim.x; ++q) {
-        float v;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(mine, q)) : "memory");
-        t += v;
-      }
+      for (unsigned q = 0; q < gridDim.x; ++q) t += cluster_float(&s_sum[threadIdx.x], q);
       aux = end_column(end, threadIdx.x, E, t, 1.f / static_cast<float>(T));
     }
-    end_aux(end, aux, T, E, s_aux);
+    aux = block_aux(aux, s_aux);
+    if (threadIdx.x == 0) end_aux(end, aux, T, E);
   }
   cluster_sync();  // no block leaves while its sums are read
 }
 
-// One block: pmean, then losses[0] = aux, losses[1] = z, from P rows of partials
+// One cluster: pmean, then losses[0] = aux, losses[1] = z, from P rows of partials
 // of `ld` floats (E sums of P, the sum of lse^2, zeros up to a multiple of 4).
-// Each thread adds every G-th row of one vector of 4 columns, all loads
-// independent; then the G sums of a column are added in order.
-constexpr int kFinalThreads = 1024;
+// Each block takes a share of the columns; each of its threads adds every G-th
+// row of one vector of 4 columns, all loads independent; then the G sums of a
+// column are added in order, and the blocks' shares of aux by the first block.
+constexpr int kFinalThreads = 1024, kFinalBlocks = 8;
 __global__ void __launch_bounds__(kFinalThreads) router_loss_final_kernel(
     const float* __restrict__ part, int P, int ld, int T, int E, const LossEnd end) {
   __shared__ float4 s_col[kFinalThreads];
-  __shared__ float s_aux[32];
-  const int nv = ld / 4, G = kFinalThreads / nv;  // nv <= 257
-  const int g = threadIdx.x / nv, c = threadIdx.x - g * nv;
+  __shared__ float s_aux[32], s_share;
+  const int nv = ld / 4, per = (nv + gridDim.x - 1) / gridDim.x;  // vectors in all; of this block
+  const int v0 = blockIdx.x * per, mine = nv - v0 < per ? nv - v0 : per;
+  const int G = kFinalThreads / per;
+  const int g = threadIdx.x / per, c = threadIdx.x - g * per;
   pdl_wait();
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (g < G) {
-    const float4* col = reinterpret_cast<const float4*>(part) + c;
+  if (g < G && c < mine) {
+    const float4* col = reinterpret_cast<const float4*>(part) + v0 + c;
 #pragma unroll 8
     for (int b = g; b < P; b += G) {
       const float4 q = col[static_cast<int64_t>(b) * nv];
@@ -229,14 +236,26 @@ __global__ void __launch_bounds__(kFinalThreads) router_loss_final_kernel(
   }
   s_col[threadIdx.x] = v;
   __syncthreads();
+  // a warp adds up a column: lanes every 32nd of the G sums, then the lanes
   float aux = 0.f;
-  for (int e = threadIdx.x; e <= E; e += kFinalThreads) {
-    const float* col = reinterpret_cast<const float*>(s_col) + e;
+  for (int q = threadIdx.x >> 5; q < 4 * mine; q += kFinalThreads / 32) {
+    const int e = 4 * v0 + q;
     float t = 0.f;
-    for (int q = 0; q < G; ++q) t += col[q * ld];
-    aux += end_column(end, e, E, t, 1.f / static_cast<float>(T));
+    for (int r = threadIdx.x & 31; r < G; r += 32)
+      t += reinterpret_cast<const float*>(s_col)[r * 4 * per + q];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if ((threadIdx.x & 31) == 0 && e <= E) aux += end_column(end, e, E, t, 1.f / static_cast<float>(T));
   }
-  end_aux(end, aux, T, E, s_aux);
+  aux = block_aux(aux, s_aux);
+  if (threadIdx.x == 0) s_share = aux;
+  cluster_sync();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    aux = 0.f;
+    for (unsigned q = 0; q < gridDim.x; ++q) aux += cluster_float(&s_share, q);
+    end_aux(end, aux, T, E);
+  }
+  cluster_sync();  // no block leaves while its share is read
 }
 
 // The gradient rows of a warp pass through shared memory for the top-k terms:
@@ -416,8 +435,8 @@ cudaError_t go(const RouterLaunch& q) {
                                    dim3(kRouterThreads), static_cast<size_t>(kRouterWarps) * ld * 4,
                                    q.s, q.logits, q.T, q.E, q.lse, q.part, ld, end);
   if (e != cudaSuccess) return e;
-  return launch_pdl(router_loss_final_kernel, dim3(1), dim3(kFinalThreads), 0, q.s,
-                    static_cast<const float*>(q.part), blocks, ld, q.T, q.E, end);
+  return launch_pdl_cluster(router_loss_final_kernel, dim3(kFinalBlocks), dim3(kFinalThreads), 0, q.s,
+                            kFinalBlocks, static_cast<const float*>(q.part), blocks, ld, q.T, q.E, end);
 }
 
 template <bool VEC>
