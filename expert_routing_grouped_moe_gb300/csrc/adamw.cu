@@ -63,11 +63,48 @@ struct Consts {
 // three sizes up to the 32 KB limit, as a launch copies all of it (40 tensors:
 // 13.6 us of host time with the largest, 12.0 with the middle one).
 constexpr int kFew = 24, kSome = 96, kMany = 400;
+// The tensors' first chunks, and for every 2^shift chunks the tensor of the first
+// of them, which leaves little of the table to search.
+template <int MAX>
+struct Starts {
+  static constexpr int kHints = MAX <= 64 ? 64 : MAX <= 256 ? 256 : 1024;
+  int n, chunks, shift;
+  int start[MAX];
+  uint16_t hint[kHints + 1];
+
+  void clear() { n = chunks = 0; }
+  bool full(int64_t ch) const { return n == MAX || chunks + ch > (int64_t(1) << 30); }
+  int add(int64_t ch) {  // a tensor of ch chunks; its number
+    start[n] = chunks;
+    chunks += static_cast<int>(ch);
+    return n++;
+  }
+  void close() {
+    shift = 0;
+    while (((chunks - 1) >> shift) >= kHints) ++shift;
+    const int used = ((chunks - 1) >> shift) + 1;
+    for (int b = 0, t = 0; b < used; ++b) {
+      while (t + 1 < n && start[t + 1] <= b << shift) ++t;
+      hint[b] = static_cast<uint16_t>(t);
+    }
+    hint[used] = static_cast<uint16_t>(n - 1);
+  }
+  // The tensor that chunk ch belongs to: the last that starts at or before it.
+  __device__ __forceinline__ int of(int ch) const {
+    const int b = ch >> shift;
+    int lo = hint[b], hi = hint[b + 1] + 1;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (start[mid] <= ch) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  }
+};
 template <int MAX>
 struct Table {
   Consts c;
-  int n, chunks;
-  int start[MAX];  // first chunk of each tensor in this launch
+  Starts<MAX> s;
   Tensor t[MAX];
 };
 struct NormTensor {
@@ -77,22 +114,11 @@ struct NormTensor {
 constexpr int kNormFew = 64, kNormSome = 256, kNormMany = 1200;
 template <int MAX>
 struct NormTable {
-  int n, chunks;
   float zero;  // -0
   float2* part;
-  int start[MAX];
+  Starts<MAX> s;
   NormTensor t[MAX];
 };
-// The tensor that chunk ch belongs to: the last that starts at or before it.
-__device__ __forceinline__ int tensor_of(const int* start, int n, int ch) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (start[mid] <= ch) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
 
 // Packed product that no later sum is contracted with: the assembler makes one
 // fma of a packed mul and add in spite of their rounding modifiers, so the
@@ -311,11 +337,11 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? 5 : 4) adamw_kernel(const __
     }
   }
   // Backwards: after a norm the gradients' end is what is left of them in the L2.
-  for (int ch = tab.chunks - 1 - static_cast<int>(blockIdx.x); ch >= 0; ch -= gridDim.x) {
-    const int ti = tensor_of(tab.start, tab.n, ch);
+  for (int ch = tab.s.chunks - 1 - static_cast<int>(blockIdx.x); ch >= 0; ch -= gridDim.x) {
+    const int ti = tab.s.of(ch);
     const Tensor& t = tab.t[ti];
     const int64_t n = t.n;
-    const int64_t i = static_cast<int64_t>(ch - tab.start[ti]) * kChunk + threadIdx.x * 8;
+    const int64_t i = static_cast<int64_t>(ch - tab.s.start[ti]) * kChunk + threadIdx.x * 8;
     const bool vec = t.vec && i + 8 <= n;
     f2 p[4], g[4], m[4], v[4], root[4];
     take(static_cast<const GT*>(t.g), i, n, vec, g);
@@ -398,10 +424,10 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
   pdl_wait();
   const Product mul{pk(tab.zero)};
   f2 hi = pk(0.f), lo = pk(0.f);
-  for (int ch = blockIdx.x; ch < tab.chunks; ch += gridDim.x) {
-    const int ti = tensor_of(tab.start, tab.n, ch);
+  for (int ch = blockIdx.x; ch < tab.s.chunks; ch += gridDim.x) {
+    const int ti = tab.s.of(ch);
     const NormTensor& t = tab.t[ti];
-    const int64_t i = static_cast<int64_t>(ch - tab.start[ti]) * kChunk + threadIdx.x * 8, n = t.n2 >> 1;
+    const int64_t i = static_cast<int64_t>(ch - tab.s.start[ti]) * kChunk + threadIdx.x * 8, n = t.n2 >> 1;
     const bool vec = (reinterpret_cast<uintptr_t>(t.g) & 15u) == 0 && i + 8 <= n;
     f2 g[4];
     if (t.n2 & 1) take(static_cast<const bf16_t*>(t.g), i, n, vec, g);
@@ -424,7 +450,7 @@ cudaError_t launch(const Table<MAX>& tab, cudaStream_t s) {
         &b, adamw_kernel<PT, GT, MASTER, EIGHT, MAX>, kThreads, 0);
     return e == cudaSuccess && b > 0 ? b : 1;
   }();
-  const int blocks = std::min(tab.chunks, per * kSMs);
+  const int blocks = std::min(tab.s.chunks, per * kSMs);
   return launch_pdl(adamw_kernel<PT, GT, MASTER, EIGHT, MAX>, dim3(blocks), dim3(kThreads), 0, s, tab);
 }
 
@@ -458,26 +484,26 @@ cudaError_t step_kind(int kind, const moe_adamw_tensor* ts, int n, const moe_ada
                       Consts& c, cudaStream_t s) {
   Table<MAX> tab;
   tab.c = c;
-  tab.n = tab.chunks = 0;
+  tab.s.clear();
   const double b1t = 1.0 - std::pow(h->beta1, static_cast<double>(h->step));
   auto flush = [&]() -> cudaError_t {
-    if (tab.n == 0) return cudaSuccess;
+    if (tab.s.n == 0) return cudaSuccess;
+    tab.s.close();
     tab.c = c;
     const cudaError_t e = launch_kind<MAX>(kind, tab, s);
     c.norm_out = nullptr;  // written once
-    tab.n = tab.chunks = 0;
+    tab.s.clear();
     return e;
   };
   for (int i = 0; i < n; ++i) {
     const moe_adamw_tensor& q = ts[i];
     if (q.n == 0 || kind_of(q) != kind) continue;
     const int64_t ch = chunks_of(q.n);
-    if (tab.n == MAX || tab.chunks + ch > (int64_t(1) << 30)) {
+    if (tab.s.full(ch)) {
       const cudaError_t e = flush();
       if (e != cudaSuccess) return e;
     }
-    tab.start[tab.n] = tab.chunks;
-    Tensor& t = tab.t[tab.n++];
+    Tensor& t = tab.t[tab.s.add(ch)];
     t.p = q.param; t.master = q.master; t.g = q.grad; t.m = q.m; t.v = q.v; t.sc = q.scales;
     t.n = q.n;
     const double lr = h->lr * static_cast<double>(q.lr_mult);
@@ -487,7 +513,6 @@ cudaError_t step_kind(int kind, const moe_adamw_tensor* ts, int n, const moe_ada
                            reinterpret_cast<uintptr_t>(q.grad);
     const uintptr_t st = reinterpret_cast<uintptr_t>(q.m) | reinterpret_cast<uintptr_t>(q.v);
     t.vec = (wide & 15u) == 0 && (st & (q.state_bits == 8 ? 7u : 15u)) == 0;
-    tab.chunks += static_cast<int>(ch);
   }
   return flush();
 }
@@ -496,27 +521,26 @@ template <int MAX>
 cudaError_t norm_all(const moe_adamw_tensor* ts, int n, float2* part, int* nparts, cudaStream_t s) {
   NormTable<MAX> tab;
   tab.zero = -0.f;
-  tab.n = tab.chunks = 0;
+  tab.s.clear();
   *nparts = 0;
   auto flush = [&]() -> cudaError_t {
-    if (tab.n == 0) return cudaSuccess;
+    if (tab.s.n == 0) return cudaSuccess;
+    tab.s.close();
     tab.part = part + *nparts;
-    const int blocks = std::min(tab.chunks, kNormBlocks);
+    const int blocks = std::min(tab.s.chunks, kNormBlocks);
     *nparts += blocks;
     const cudaError_t e = launch_pdl(grad_norm_kernel<MAX>, dim3(blocks), dim3(kThreads), 0, s, tab);
-    tab.n = tab.chunks = 0;
+    tab.s.clear();
     return e;
   };
   for (int i = 0; i < n; ++i) {
     if (ts[i].n == 0) continue;
     const int64_t ch = chunks_of(ts[i].n);
-    if (tab.n == MAX || tab.chunks + ch > (int64_t(1) << 30)) {
+    if (tab.s.full(ch)) {
       const cudaError_t e = flush();
       if (e != cudaSuccess) return e;
     }
-    tab.start[tab.n] = tab.chunks;
-    tab.t[tab.n++] = NormTensor{ts[i].grad, 2 * ts[i].n + (ts[i].grad_type == MOE_BF16 ? 1 : 0)};
-    tab.chunks += static_cast<int>(ch);
+    tab.t[tab.s.add(ch)] = NormTensor{ts[i].grad, 2 * ts[i].n + (ts[i].grad_type == MOE_BF16 ? 1 : 0)};
   }
   return flush();
 }
