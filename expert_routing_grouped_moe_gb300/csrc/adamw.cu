@@ -206,49 +206,67 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
   const int b = static_cast<int>(top >> 23) - 7;
   return b < 8 ? 8u : b > 248 ? 248u : static_cast<uint32_t>(b);
 }
-// e4m3 magnitude of x >= 0 under the scale byte b; d: 20 dither bits.  Normal
-// values: exponent and top three mantissa bits, rebased.  Below the smallest
-// normal value (2^-6 scale), adding that value makes the grid linear.
-__device__ __forceinline__ uint32_t encode(float x, uint32_t d, uint32_t b) {
-  const float low = __uint_as_float((b - 6u) << 23);
-  const bool below = x < low;
-  const uint32_t bits = __float_as_uint(below ? __fadd_rn(x, low) : x);
-  return ((bits + d) >> 20) - ((b - 7u) << 3) - (below ? 8u : 0u);
-}
 // Top bytes of four words.
 __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
+// Largest (a NaN is the largest) and least (a NaN counts only among NaNs)
+// magnitude of eight values, three at a time.
+__device__ __forceinline__ float most3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float least3(float a, float b, float c) {
+  float r;
+  asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t most8(const float (&x)[8]) {
+  return __float_as_uint(most3(most3(x[0], x[1], x[2]), most3(x[3], x[4], x[5]), most3(x[6], x[7], x[7])));
+}
+__device__ __forceinline__ float least8(const float (&x)[8]) {
+  return least3(least3(x[0], x[1], x[2]), least3(x[3], x[4], x[5]), least3(x[6], x[7], x[7]));
+}
 // The eight codes of this lane: m with its sign, root not below 1 where positive.
-__device__ __forceinline__ void encode8(const float (&m)[8], const float (&root)[8], uint32_t u,
-                                        uint32_t bm, uint32_t bv, uint2& qm, uint2& qr) {
-  // Where every value is normal (m and root within 2^-14 of their block's
-  // largest, nearly always) the code is in place after one addition: bits 20-26
-  // of the rebased, dithered word.
+// least_v: the least of the roots' squares.
+__device__ __forceinline__ void encode8(const float (&m)[8], const float (&root)[8], float least_v,
+                                        uint32_t u, uint32_t bm, uint32_t bv, uint2& qm, uint2& qr) {
+  // A normal value's code is in place after one addition: bits 20-26 of the
+  // rebased, dithered word.  Below the smallest normal value (2^-6 scale), adding
+  // that value first makes the grid linear; its exponent comes off again.  A warp
+  // looks after such values where it has one: m or root below 2^-14 of their
+  // block's largest.
   const uint32_t sub_m = (bm - 7u) << 23, sub_r = (bv - 7u) << 23;
-  uint32_t least_m = 0xFFFFFFFFu, least_r = 0xFFFFFFFFu;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    least_m = min(least_m, __float_as_uint(m[e]) & 0x7FFFFFFFu);
-    least_r = min(least_r, __float_as_uint(root[e]));
-  }
+  const float low_m = __uint_as_float((bm - 6u) << 23), low_r = __uint_as_float((bv - 6u) << 23);
+  const float low_v = fmaxf(1.0001f * low_r * low_r, 0x1p-126f);  // the square may vanish
   uint32_t wm[8], wr[8];
-  if (least_m >= ((bm - 6u) << 23) && least_r >= ((bv - 6u) << 23)) {
+  if (__all_sync(0xffffffffu, least8(m) >= low_m)) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e, u += kDitherI) {
-      const uint32_t d = u >> 12;
-      const uint32_t x = __float_as_uint(m[e]) + d - sub_m;
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t x = __float_as_uint(m[e]) + ((u + e * kDitherI) >> 12) - sub_m;
       wm[e] = ((x << 4) & 0x7FFFFFFFu) | (x & 0x80000000u);
-      wr[e] = (__float_as_uint(root[e]) + (0xFFFFFu - d) - sub_r) << 4;
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e, u += kDitherI) {
-      const uint32_t d = u >> 12;
-      wm[e] = (encode(fabsf(m[e]), d, bm) << 24) | (m[e] < 0.f ? 0x80000000u : 0u);
-      uint32_t q = encode(fabsf(root[e]), 0xFFFFFu - d, bv);
-      if (q < 1u && root[e] > 0.f) q = 1u;
-      wr[e] = q << 24;
+    for (int e = 0; e < 8; ++e) {
+      const bool below = fabsf(m[e]) < low_m;
+      const uint32_t x = __float_as_uint(below ? __fadd_rn(m[e], m[e] < 0.f ? -low_m : low_m) : m[e]) +
+                         ((u + e * kDitherI) >> 12) - (below ? sub_m + (1u << 23) : sub_m);
+      wm[e] = ((x << 4) & 0x7FFFFFFFu) | (x & 0x80000000u);
+    }
+  }
+  if (__all_sync(0xffffffffu, least_v >= low_v)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      wr[e] = (__float_as_uint(root[e]) + (0xFFFFFu - ((u + e * kDitherI) >> 12)) - sub_r) << 4;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const bool below = root[e] < low_r;
+      wr[e] = (__float_as_uint(below ? __fadd_rn(root[e], low_r) : root[e]) +
+               (0xFFFFFu - ((u + e * kDitherI) >> 12)) - (below ? sub_r + (1u << 23) : sub_r)) << 4;
+      if (root[e] > 0.f) wr[e] = max(wr[e], 1u << 24);
     }
   }
   qm = make_uint2(top_bytes(wm[0], wm[1], wm[2], wm[3]), top_bytes(wm[4], wm[5], wm[6], wm[7]));
@@ -290,23 +308,40 @@ __device__ __forceinline__ float root_of_pair(float2 a) {
 // Square root and quotient, rounded to nearest: an approximate reciprocal
 // (square root), one Newton step, and a last correction by the exact residual
 // (Markstein, IBM J. Res. Dev. 34, 1990).  x >= 0; d from 2^-100 to 2^120.
+template <bool NORMAL>
 __device__ __forceinline__ float approx_rsqrt(float x) {
   float r;
-  asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  if (NORMAL) asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  else asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ float approx_rcp(float x) {
   float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ f2 root2(f2 x, const Product& mul) {
-  const float2 v = unpk(x);  // 0: a finite factor, so that 0 comes out
-  const f2 y = pk(approx_rsqrt(fmaxf(v.x, 1e-45f)), approx_rsqrt(fmaxf(v.y, 1e-45f)));
+__device__ __forceinline__ f2 root2(f2 x, f2 y, const Product& mul) {  // y: about 1 / sqrt(x)
   const f2 s = mul(x, y), nh = mul(y, pk(-0.5f));
   const f2 e = fma2(s, nh, pk(0.5f));
   const f2 nh1 = fma2(nh, e, nh), s1 = fma2(s, e, s);
   return fma2(fma2(s1, s1, mul(x, pk(-1.f))), nh1, s1);
+}
+// The roots of eight values, whose least is `least`: where it is a normal number
+// nothing below one need be looked after, nor zeros.
+__device__ __forceinline__ void roots8(const f2 (&x)[4], float least, const Product& mul, f2 (&root)[4]) {
+  if (least >= 0x1p-126f) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 v = unpk(x[e]);
+      root[e] = root2(x[e], pk(approx_rsqrt<true>(v.x), approx_rsqrt<true>(v.y)), mul);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 v = unpk(x[e]);  // 0: a finite factor, so that 0 comes out
+      root[e] = root2(x[e], pk(approx_rsqrt<false>(fmaxf(v.x, 1e-45f)), approx_rsqrt<false>(fmaxf(v.y, 1e-45f))), mul);
+    }
+  }
 }
 __device__ __forceinline__ f2 ratio2(f2 n, f2 d, const Product& mul) {
   const float2 v = unpk(d);  // an infinite d counts as 2^120
@@ -371,25 +406,33 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? 5 : 4) adamw_kernel(const __
       g[e] = mul(g[e], coef2);
       m[e] = add2(mul(b1, m[e]), mul(c1, g[e]));
       v[e] = add2(mul(b2, v[e]), mul(mul(c2, g[e]), g[e]));
-      root[e] = root2(v[e], mul);
+    }
+    float vv[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 x = unpk(v[e]);
+      vv[2 * e] = x.x; vv[2 * e + 1] = x.y;
+    }
+    const float least_v = least8(vv);
+    roots8(v, least_v, mul, root);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
       const f2 upd = ratio2(m[e], add2(mul(root[e], pk(c.correct)), pk(c.eps)), mul);
       p[e] = add2(mul(p[e], keep), mul(nlr, upd));
     }
     if constexpr (EIGHT) {
       float mm[8], rr[8];
-      uint32_t top_m = 0, top_r = 0;   // values past n are 0: they do not raise the maximum
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 x = unpk(m[e]), y = unpk(root[e]);
         mm[2 * e] = x.x; mm[2 * e + 1] = x.y;
         rr[2 * e] = y.x; rr[2 * e + 1] = y.y;
-        top_m = max(top_m, max(__float_as_uint(x.x) & 0x7FFFFFFFu, __float_as_uint(x.y) & 0x7FFFFFFFu));
-        top_r = max(top_r, max(__float_as_uint(y.x), __float_as_uint(y.y)));
       }
-      const uint32_t bm = scale_byte(__reduce_max_sync(0xffffffffu, top_m));
-      const uint32_t bv = scale_byte(__reduce_max_sync(0xffffffffu, top_r));
+      // values past n are 0: they do not raise the maximum
+      const uint32_t bm = scale_byte(__reduce_max_sync(0xffffffffu, most8(mm)));
+      const uint32_t bv = scale_byte(__reduce_max_sync(0xffffffffu, most8(rr)));
       uint2 qm, qr;
-      encode8(mm, rr, static_cast<uint32_t>(i) * kDitherI + c.dither, bm, bv, qm, qr);
+      encode8(mm, rr, least_v, static_cast<uint32_t>(i) * kDitherI + c.dither, bm, bv, qm, qr);
       set_codes(static_cast<uint8_t*>(t.m), i, n, vec, qm);
       set_codes(static_cast<uint8_t*>(t.v), i, n, vec, qr);
       if (lane == 0 && i < n) {

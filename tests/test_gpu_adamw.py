@@ -120,6 +120,23 @@ def test_roots_and_quotients_over_the_exponents(seed):
     check(row, exp)
 
 
+@pytest.mark.parametrize("lo,hi", [(-90, -60), (-72, -40), (-75, 10), (-3, -3)])
+def test_eight_bits_of_gradients_whose_squares_vanish(lo, hi):
+    """Blocks whose values lie many binades apart, m above zero where v is not, and
+    squares below the normal numbers: the codes are still the oracle's."""
+    n, g = 100_003, torch.Generator(DEV).manual_seed(hi)
+    grad = torch.exp2(lo + (hi - lo) * torch.rand(n, generator=g, device=DEV))
+    grad = torch.where(torch.rand(n, generator=g, device=DEV) < 0.5, -grad, grad)
+    grad[::7] = 0
+    grad[5::256] *= 2.0 ** 20
+    row = tensor(n, F32, F32, False, 8, seed=1, fresh=True)
+    row["grad"] = grad
+    for step in (1, 2, 3):
+        exp = expect(row, step, **HYPER)
+        L.moe_adamw_step(L.AdamWTable([row]), step, **HYPER)
+        check(row, exp)
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_mixed_kinds_and_pointers_that_no_vector_fits(bits):
     rows = [tensor(300 + 11 * i, *KINDS[i % 6], 8 if (i % 5 == 0) else bits, seed=i, off=i % 4)
