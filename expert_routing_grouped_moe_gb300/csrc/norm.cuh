@@ -288,10 +288,6 @@ inline int ring_stages(size_t tile, int* per, size_t extra, int64_t flight) {
 inline size_t norm_const_bytes(const NormShape& s) { return static_cast<size_t>(s.threads()) * s.nv * 64; }
 // Fewer tiles than this are read directly (a block would have one or two).
 constexpr int kNormRingTiles = 2 * kSMs;
-inline int ring_stages(size_t tile, int per) {
-  const int64_t room = kRingBytes / per, n = room / static_cast<int64_t>(tile);
-  return n >= kRingMaxStages ? kRingMaxStages : n >= 2 ? static_cast<int>(n) : per > 1 ? ring_stages(tile, per - 1) : 0;
-}
 
 // Blocks of the backward: what the SMs' registers hold, at 128 a thread where
 // they keep column sums or two shares, at 80 otherwise.  Those that keep column

@@ -7,7 +7,8 @@ namespace {
 
 // The column sums: P rows of partials [nsum][d], each thread adding every 32nd
 // row of one column, the 32 sums of a column then added in order; and the
-// gradients they give.
+// gradients they give.  Latency bounds it: ten loads a thread in flight, 304 rows
+// of 4096 sums (5 MB, in the L2) in 4 us.
 constexpr int kSumThreads = 1024;
 __global__ void __launch_bounds__(kSumThreads) norm_colsum_kernel(const NormArgs a, int P) {
   __shared__ float s[32][33];

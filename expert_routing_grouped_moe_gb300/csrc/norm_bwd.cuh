@@ -12,6 +12,13 @@
 // give all three gradients: sum dn rh = dw_pre, and with Y = yh (or y)
 //   no gate, token, element: S = sum a t Y,  dw_post = s S
 //   channel:                 S = sum t Y,    dw_post = s a S,  dgate = s a' q S
+// A row costs some 40 instructions for 8 columns and two waits for its sums, so
+// rows overlap: several blocks on an SM, and a ring that loads ahead.  Bound by
+// memory where the weights are frozen (32768x2880, fp32 stream, element gate:
+// 325 us with 6.3 TB/s); with column sums by what an SM issues between a row's two
+// barriers: 16384x2048, channel gate, 70 us (0.85 of a plain copy's rate).
+// 4096x2048 takes 24.7 us, and 4 for the second kernel: loading the factors, filling
+// the ring and writing the partial sums are about 7 us of it.
 #pragma once
 
 #include "norm.cuh"

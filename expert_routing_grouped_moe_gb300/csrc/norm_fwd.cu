@@ -3,6 +3,10 @@
 //   p = y rstd(y) (w_post + off) or y;  r = x + s a(gate) p;  n = r rstd(r) (w_pre + off)
 // with rstd(z) = 1/sqrt(mean z^2 + eps).  Everything between the loads and the
 // stores is fp32; n is the norm of the unrounded r.
+// Bound by memory: x and y are read once, r and n written once, a row waits in
+// registers for its two sums.  16384x2048 in bf16: 42 us, 6.4 TB/s (0.94 of a plain
+// copy's rate); 4096x2048: 12.5 us, 0.79 (27 rows an SM: filling the ring and the
+// last rows are 3 us of it); one row of 2048: 2.4 us, a launch.
 #include "norm.cuh"
 
 namespace moe {

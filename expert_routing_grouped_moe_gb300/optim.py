@@ -18,8 +18,9 @@ class MoEAdamW:
     tensor for each, bf16 or fp32, read at every step (the layer's gradient
     buffers, say); another list may be passed to step().
 
-    state_bits 8: the moments take 2 bytes and 1/128 a value instead of 8.  master: keep an fp32 copy of bf16 parameters, which
-    receives the update and is rounded to the parameter.  max_norm > 0 clips by
+    state_bits 8: the moments take 2 bytes and 1/128 a value instead of 8.
+    master: keep an fp32 copy of bf16 parameters, which receives the update and
+    is rounded to the parameter.  max_norm > 0 clips by
     the global norm of all gradients; grad_norm holds it after each step (also
     with track_norm).  skip_nonfinite: a step whose norm is not finite changes
     nothing; step_count advances all the same."""

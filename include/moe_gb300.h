@@ -519,7 +519,7 @@ MOE_API int moe_probe_read_stream(const void* src, size_t bytes, int32_t pattern
  * dA_dn, dB_gu, dA_gu, dw_reduce, the full weight-gradient GEMMs dW_dn and
  * dW_gu, ep_row_weights, ep_segment_ids, block_norm_fwd, block_norm_bwd,
  * router_loss, router_bwd, grad_norm and adamw.  (A name covers all kernels of
- * its call: "route" moe_route_kernel_count, "router_loss" two, "block_norm_bwd"
+ * its call: "route" moe_route_kernel_count, "router_loss" one or two, "block_norm_bwd"
  * two with sums over tokens, "adamw" one for each kind of tensor.) */
 MOE_API const char* moe_kernel_name(int32_t i);
 

@@ -20,6 +20,11 @@ Pins (checked by ``tests/test_oracle_*.py`` on the CPU):
                           linearity in the routing weights.
 * ``layer_backward``   -- pinned: central finite differences of
                           L = sum(Y * dY) in fp64 for every gradient.
+
+``oracle.block_oracle`` restates what stands around the layer in a training
+step: the block norms and the router's losses in fp64 (pinned in
+``tests/test_oracle_block.py`` by central differences and limits), AdamW in
+fp64 and, rounded operation by operation, in fp32 with the 8-bit states.
 """
 from .moe_oracle import (  # noqa: F401
     router_topk,
