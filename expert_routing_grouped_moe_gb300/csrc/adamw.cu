@@ -25,10 +25,11 @@
 //
 // One pass; a block of threads takes chunks of 2048 values, 8 for each thread.
 // 32-bit moments are bound by memory: 52 M bf16 parameters with fp32 gradients and
-// master copies take 264 us, 6.0 TB/s, and 35 us for the norm.  8-bit moments are
-// bound by what an SM issues as much as by memory: the same 160 us, 5.9 TB/s (0.87
-// of a plain copy's rate); 16 M bf16 values with bf16 gradients and no master copies
-// 41.7 us, 3.9 TB/s.
+// master copies take 274 us with the clip (0.96 of the rate of a plain copy on what
+// both passes read and write, some of it in the L2; 300 us with 16-byte accesses,
+// which touch every line of fp32 values by halves).  8-bit moments are bound by what
+// an SM issues as much as by memory: the same 161 us, 5.9 TB/s; 16 M bf16 values with
+// bf16 gradients and no master copies 41 us, 4 TB/s.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -56,7 +57,7 @@ struct Tensor {
   uint8_t* sc;
   int64_t n;
   float keep, lr;  // 1 - lr wd; lr / (1 - b1^t)
-  int vec;         // all pointers allow 8-value vectors
+  int vec;         // 1: all pointers allow 16-byte accesses, 2: fp32 ones 32-byte accesses
 };
 struct Consts {
   float b1, c1, b2, c2, correct, eps, grad_scale, max_norm;
@@ -137,11 +138,13 @@ struct Product {
 };
 
 // Eight values from index i on (those past n read as 0 / are not written).
-template <typename T>
+// vec: all eight are there and 16-byte accesses will do; WIDE: 32-byte ones.
+template <bool WIDE, typename T>
 __device__ __forceinline__ void take(const T* p, int64_t i, int64_t n, bool vec, f2 (&f)[4]) {
   Raw8<T> r;
   if (vec) {
-    load8<true>(p + i, 0, 8, r);
+    if constexpr (WIDE && sizeof(T) == 4) load8_wide(p + i, r);
+    else load8<true>(p + i, 0, 8, r);
     widen(r, f);
     return;
   }
@@ -159,12 +162,13 @@ __device__ __forceinline__ void take(const T* p, int64_t i, int64_t n, bool vec,
 #pragma unroll
   for (int e = 0; e < 4; ++e) f[e] = pk(x[2 * e], x[2 * e + 1]);
 }
-template <typename T>
+template <bool WIDE, typename T>
 __device__ __forceinline__ void give(T* p, int64_t i, int64_t n, bool vec, const f2 (&f)[4]) {
   Raw8<T> r;
   narrow(f, r);
   if (vec) {
-    store8<true>(p + i, 0, 8, r);
+    if constexpr (WIDE && sizeof(T) == 4) store8_wide(p + i, r);
+    else store8<true>(p + i, 0, 8, r);
     return;
   }
 #pragma unroll
@@ -359,10 +363,83 @@ __device__ __forceinline__ f2 ratio2(f2 n, f2 d, const Product& mul) {
   return fma2(fma2(nd, q, n), r1, q);
 }
 
+// Eight values of each thread, from index i of the tensor t on.
+template <typename PT, typename GT, bool MASTER, bool EIGHT, bool WIDE>
+__device__ __forceinline__ void update8(const Consts& c, const Tensor& t, int64_t i, bool vec, float coef,
+                                        const Product& mul) {
+  const int64_t n = t.n;
+  f2 p[4], g[4], m[4], v[4], root[4];
+  take<WIDE>(static_cast<const GT*>(t.g), i, n, vec, g);
+  if (MASTER) take<WIDE>(t.master, i, n, vec, p);
+  else take<WIDE>(static_cast<const PT*>(t.p), i, n, vec, p);
+  const int64_t blk = i / kBlock;  // the same for the whole warp
+  if constexpr (EIGHT) {
+    uint32_t bm = 0, bv = 0;
+    if (blk * kBlock < n) {
+      bm = t.sc[2 * blk];
+      bv = t.sc[2 * blk + 1];
+    }
+    const uint2 qm = get_codes(static_cast<const uint8_t*>(t.m), i, n, vec);
+    const uint2 qv = get_codes(static_cast<const uint8_t*>(t.v), i, n, vec);
+    decode8(qm, __uint_as_float(bm << 23), m);
+    decode8(qv, __uint_as_float(bv << 23), v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = mul(v[e], v[e]);
+  } else {
+    take<WIDE>(static_cast<const float*>(t.m), i, n, vec, m);
+    take<WIDE>(static_cast<const float*>(t.v), i, n, vec, v);
+  }
+  const f2 coef2 = pk(coef), b1 = pk(c.b1), c1 = pk(c.c1), b2 = pk(c.b2), c2 = pk(c.c2),
+           keep = pk(t.keep), nlr = pk(-t.lr);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    g[e] = mul(g[e], coef2);
+    m[e] = add2(mul(b1, m[e]), mul(c1, g[e]));
+    v[e] = add2(mul(b2, v[e]), mul(mul(c2, g[e]), g[e]));
+  }
+  float vv[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 x = unpk(v[e]);
+    vv[2 * e] = x.x; vv[2 * e + 1] = x.y;
+  }
+  const float least_v = least8(vv);
+  roots8(v, least_v, mul, root);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const f2 upd = ratio2(m[e], add2(mul(root[e], pk(c.correct)), pk(c.eps)), mul);
+    p[e] = add2(mul(p[e], keep), mul(nlr, upd));
+  }
+  if constexpr (EIGHT) {
+    float mm[8], rr[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 x = unpk(m[e]), y = unpk(root[e]);
+      mm[2 * e] = x.x; mm[2 * e + 1] = x.y;
+      rr[2 * e] = y.x; rr[2 * e + 1] = y.y;
+    }
+    // values past n are 0: they do not raise the maximum
+    const uint32_t bm = scale_byte(__reduce_max_sync(0xffffffffu, most8(mm)));
+    const uint32_t bv = scale_byte(__reduce_max_sync(0xffffffffu, most8(rr)));
+    uint2 qm, qr;
+    encode8(mm, rr, least_v, static_cast<uint32_t>(i) * kDitherI + c.dither, bm, bv, qm, qr);
+    set_codes(static_cast<uint8_t*>(t.m), i, n, vec, qm);
+    set_codes(static_cast<uint8_t*>(t.v), i, n, vec, qr);
+    if ((threadIdx.x & 31) == 0 && i < n) {
+      t.sc[2 * blk] = static_cast<uint8_t>(bm);
+      t.sc[2 * blk + 1] = static_cast<uint8_t>(bv);
+    }
+  } else {
+    give<WIDE>(static_cast<float*>(t.m), i, n, vec, m);
+    give<WIDE>(static_cast<float*>(t.v), i, n, vec, v);
+  }
+  give<WIDE>(static_cast<PT*>(t.p), i, n, vec, p);
+  if (MASTER) give<WIDE>(t.master, i, n, vec, p);
+}
+
 template <typename PT, typename GT, bool MASTER, bool EIGHT, int MAX>
 __global__ void __launch_bounds__(kThreads, EIGHT ? 5 : 4) adamw_kernel(const __grid_constant__ Table<MAX> tab) {
   const Consts& c = tab.c;
-  const int lane = threadIdx.x & 31;
   const Product mul{pk(c.zero)};
   float coef = c.grad_scale;
   pdl_wait();
@@ -382,76 +459,11 @@ __global__ void __launch_bounds__(kThreads, EIGHT ? 5 : 4) adamw_kernel(const __
   for (int ch = tab.s.chunks - 1 - static_cast<int>(blockIdx.x); ch >= 0; ch -= gridDim.x) {
     const int ti = tab.s.of(ch);
     const Tensor& t = tab.t[ti];
-    const int64_t n = t.n;
-    const int64_t i = static_cast<int64_t>(ch - tab.s.start[ti]) * kChunk + threadIdx.x * 8;
-    const bool vec = t.vec && i + 8 <= n;
-    f2 p[4], g[4], m[4], v[4], root[4];
-    take(static_cast<const GT*>(t.g), i, n, vec, g);
-    if (MASTER) take(t.master, i, n, vec, p);
-    else take(static_cast<const PT*>(t.p), i, n, vec, p);
-    const int64_t blk = i / kBlock;  // the same for the whole warp
-    if constexpr (EIGHT) {
-      uint32_t bm = 0, bv = 0;
-      if (blk * kBlock < n) {
-        bm = t.sc[2 * blk];
-        bv = t.sc[2 * blk + 1];
-      }
-      const uint2 qm = get_codes(static_cast<const uint8_t*>(t.m), i, n, vec);
-      const uint2 qv = get_codes(static_cast<const uint8_t*>(t.v), i, n, vec);
-      decode8(qm, __uint_as_float(bm << 23), m);
-      decode8(qv, __uint_as_float(bv << 23), v);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = mul(v[e], v[e]);
-    } else {
-      take(static_cast<const float*>(t.m), i, n, vec, m);
-      take(static_cast<const float*>(t.v), i, n, vec, v);
-    }
-    const f2 coef2 = pk(coef), b1 = pk(c.b1), c1 = pk(c.c1), b2 = pk(c.b2), c2 = pk(c.c2),
-             keep = pk(t.keep), nlr = pk(-t.lr);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      g[e] = mul(g[e], coef2);
-      m[e] = add2(mul(b1, m[e]), mul(c1, g[e]));
-      v[e] = add2(mul(b2, v[e]), mul(mul(c2, g[e]), g[e]));
-    }
-    float vv[8];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 x = unpk(v[e]);
-      vv[2 * e] = x.x; vv[2 * e + 1] = x.y;
-    }
-    const float least_v = least8(vv);
-    roots8(v, least_v, mul, root);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const f2 upd = ratio2(m[e], add2(mul(root[e], pk(c.correct)), pk(c.eps)), mul);
-      p[e] = add2(mul(p[e], keep), mul(nlr, upd));
-    }
-    if constexpr (EIGHT) {
-      float mm[8], rr[8];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 x = unpk(m[e]), y = unpk(root[e]);
-        mm[2 * e] = x.x; mm[2 * e + 1] = x.y;
-        rr[2 * e] = y.x; rr[2 * e + 1] = y.y;
-      }
-      // values past n are 0: they do not raise the maximum
-      const uint32_t bm = scale_byte(__reduce_max_sync(0xffffffffu, most8(mm)));
-      const uint32_t bv = scale_byte(__reduce_max_sync(0xffffffffu, most8(rr)));
-      uint2 qm, qr;
-      encode8(mm, rr, least_v, static_cast<uint32_t>(i) * kDitherI + c.dither, bm, bv, qm, qr);
-      set_codes(static_cast<uint8_t*>(t.m), i, n, vec, qm);
-      set_codes(static_cast<uint8_t*>(t.v), i, n, vec, qr);
-      if (lane == 0 && i < n) {
-        t.sc[2 * blk] = static_cast<uint8_t>(bm);
-        t.sc[2 * blk + 1] = static_cast<uint8_t>(bv);
-      }
-    } else {
-      give(static_cast<float*>(t.m), i, n, vec, m);
-      give(static_cast<float*>(t.v), i, n, vec, v);
-    }
-    give(static_cast<PT*>(t.p), i, n, vec, p);
-    if (MASTER) give(t.master, i, n, vec, p);
+    const int64_t first = static_cast<int64_t>(ch - tab.s.start[ti]) * kChunk, i = first + threadIdx.x * 8;
+    if (t.vec == 2 && first + kChunk <= t.n)  // the same for all threads: they vote
+      update8<PT, GT, MASTER, EIGHT, true>(c, t, i, true, coef, mul);
+    else
+      update8<PT, GT, MASTER, EIGHT, false>(c, t, i, t.vec != 0 && i + 8 <= t.n, coef, mul);
   }
 }
 
@@ -478,10 +490,12 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
     const int ti = tab.s.of(ch);
     const NormTensor& t = tab.t[ti];
     const int64_t i = static_cast<int64_t>(ch - tab.s.start[ti]) * kChunk + threadIdx.x * 8, n = t.n2 >> 1;
-    const bool vec = (reinterpret_cast<uintptr_t>(t.g) & 15u) == 0 && i + 8 <= n;
+    const unsigned low = static_cast<unsigned>(reinterpret_cast<uintptr_t>(t.g)) & 31u;
+    const int vec = i + 8 > n ? 0 : low == 0 ? 2 : low == 16 ? 1 : 0;
     f2 g[4];
-    if (t.n2 & 1) take(static_cast<const bf16_t*>(t.g), i, n, vec, g);
-    else take(static_cast<const float*>(t.g), i, n, vec, g);
+    if (t.n2 & 1) take<false>(static_cast<const bf16_t*>(t.g), i, n, vec != 0, g);
+    else if (vec == 2) take<true>(static_cast<const float*>(t.g), i, n, true, g);
+    else take<false>(static_cast<const float*>(t.g), i, n, vec != 0, g);
 #pragma unroll
     for (int e = 0; e < 4; ++e) add_square(g[e], hi, lo, mul);
   }
@@ -492,6 +506,10 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
 
 int64_t chunks_of(int64_t n) { return (n + kChunk - 1) / kChunk; }
 
+// Blocks on an SM with 32-bit moments: two, though four fit (adapters of 52 M values
+// with master copies and the clip 273 us against 276, 16 M bf16 values 55.7 against
+// 58.4: fewer streams at once).  8-bit moments take what fits, five.
+constexpr int kWideBlocks = 2;
 template <typename PT, typename GT, bool MASTER, bool EIGHT, int MAX>
 cudaError_t launch(const Table<MAX>& tab, cudaStream_t s) {
   static const int per = [] {
@@ -500,7 +518,7 @@ cudaError_t launch(const Table<MAX>& tab, cudaStream_t s) {
         &b, adamw_kernel<PT, GT, MASTER, EIGHT, MAX>, kThreads, 0);
     return e == cudaSuccess && b > 0 ? b : 1;
   }();
-  const int blocks = std::min(tab.s.chunks, per * kSMs);
+  const int blocks = std::min(tab.s.chunks, (EIGHT ? per : std::min(per, kWideBlocks)) * kSMs);
   return launch_pdl(adamw_kernel<PT, GT, MASTER, EIGHT, MAX>, dim3(blocks), dim3(kThreads), 0, s, tab);
 }
 
@@ -562,7 +580,9 @@ cudaError_t step_kind(int kind, const moe_adamw_tensor* ts, int n, const moe_ada
     const uintptr_t wide = reinterpret_cast<uintptr_t>(q.param) | reinterpret_cast<uintptr_t>(q.master) |
                            reinterpret_cast<uintptr_t>(q.grad);
     const uintptr_t st = reinterpret_cast<uintptr_t>(q.m) | reinterpret_cast<uintptr_t>(q.v);
-    t.vec = (wide & 15u) == 0 && (st & (q.state_bits == 8 ? 7u : 15u)) == 0;
+    t.vec = (wide & 15u) != 0 || (st & (q.state_bits == 8 ? 7u : 15u)) != 0      ? 0
+            : (wide & 31u) != 0 || (q.state_bits == 32 && (st & 31u) != 0) ? 1
+                                                                             : 2;
   }
   return flush();
 }

@@ -134,6 +134,20 @@ __device__ __forceinline__ void load8(const float* row, int v, int d, Raw8<float
     r.b = make_float4(f[4], f[5], f[6], f[7]);
   }
 }
+// Eight floats at a 32-byte aligned address as one access: a warp's shares are
+// then whole lines, where two 16-byte accesses each touch every line by half.
+__device__ __forceinline__ void load8_wide(const float* p, Raw8<float>& r) {
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(r.a.x), "=f"(r.a.y), "=f"(r.a.z), "=f"(r.a.w), "=f"(r.b.x), "=f"(r.b.y),
+                 "=f"(r.b.z), "=f"(r.b.w)
+               : "l"(p));
+}
+__device__ __forceinline__ void store8_wide(float* p, const Raw8<float>& r) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(r.a.x),
+               "f"(r.a.y), "f"(r.a.z), "f"(r.a.w), "f"(r.b.x), "f"(r.b.y), "f"(r.b.z), "f"(r.b.w)
+               : "memory");
+}
+
 template <bool VEC>
 __device__ __forceinline__ void store8(bf16_t* row, int v, int d, const Raw8<bf16_t>& r) {
   if (VEC) {
