@@ -16,9 +16,11 @@
 // rows overlap: several blocks on an SM, and a ring that loads ahead.  Bound by
 // memory where the weights are frozen (32768x2880, fp32 stream, element gate:
 // 325 us with 6.3 TB/s); with column sums by what an SM issues between a row's two
-// barriers: 16384x2048, channel gate, 70 us (0.85 of a plain copy's rate).
-// 4096x2048 takes 24.7 us, and 4 for the second kernel: loading the factors, filling
-// the ring and writing the partial sums are about 7 us of it.
+// barriers: channel gate, 4096x2048 29 us, 16384x2048 83 us, 4.3 ns a further row
+// (0.84 of a plain copy's rate; with frozen weights 4.0).  Of the 29 us the second
+// kernel takes 4, and loading the factors, filling the ring and writing the partial
+// sums about 7.  Rows read directly, above 8192 columns: 0.4 to 0.5, latency and
+// registers (4096x12000 in bf16: 371 us).
 #pragma once
 
 #include "norm.cuh"
@@ -54,6 +56,12 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) 
                                   {pre ? a.n : nullptr, sizeof(YT)},
                                   {a.y, sizeof(YT)},
                                   {element ? a.gate : nullptr, sizeof(YT)}};
+  bool ahead = false;
+  if (!RING && NV >= 2) {
+    int size = 0;
+    for (int i = 0; i < kRingSrcs; ++i) size += src[i].p != nullptr ? src[i].esize : 0;
+    ahead = size * d <= kPrefetchBytes;
+  }
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   int64_t base = static_cast<int64_t>(blockIdx.x) * groups;
   f2 acc_y[NV][4], acc_r[NV][4];
@@ -96,10 +104,11 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) 
   };
   // Kept for all rows: in shared memory behind the ring (registers are what
   // limits the blocks on an SM), in registers without one, or made again.
-  RowConst<NV> ck, cu;
+  constexpr bool kKeep = !RING && NV == 1;
+  f2 ck[kKeep ? 4 : 1], cu[kKeep ? 4 : 1];
   float4* s_const = reinterpret_cast<float4*>(s_tiles + a.stages * a.tile) + threadIdx.x;
   const int nthr = blockDim.x;
-  if (RING || NV <= 2) {
+  if (RING || kKeep) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       f2 k[4], u[4];
@@ -109,7 +118,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) 
       for (int e = 0; e < 4; ++e) {
         if (!has_y) k[e] = pk(0.f);
         if (!pre) u[e] = pk(0.f);
-        if (!RING) ck.f[NV <= 2 ? i : 0][e] = k[e], cu.f[NV <= 2 ? i : 0][e] = u[e];
+        if (kKeep) ck[kKeep ? e : 0] = k[e], cu[kKeep ? e : 0] = u[e];
       }
       if (RING) {
         Raw8<float> q;
@@ -128,9 +137,9 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) 
       q.a = s_const[(4 * i + 2 * which) * nthr];
       q.b = s_const[(4 * i + 2 * which + 1) * nthr];
       widen(q, f);
-    } else if (NV <= 2) {
+    } else if (kKeep) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) f[e] = which ? cu.f[NV <= 2 ? i : 0][e] : ck.f[NV <= 2 ? i : 0][e];
+      for (int e = 0; e < 4; ++e) f[e] = which ? cu[kKeep ? e : 0] : ck[kKeep ? e : 0];
     } else if (which) {
       make_u(v0 + i * 32 * W, f);
     } else {
@@ -157,6 +166,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) 
     const bool ok = row < a.T;
     const int64_t off = ok ? row * d : 0;
     const int dd = ok ? d : 0;
+    if (ahead && v0 == 0 && row + step < a.T) prefetch_row(src, row + step, d);
     const XT* pdr = static_cast<const XT*>(a.x) + off;
     const XT* pr = static_cast<const XT*>(a.r) + off;
     const YT* pdn = static_cast<const YT*>(a.n) + off;
@@ -178,7 +188,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) 
     }
     // pass 1: e in place of dr; the row sums, of r and y as they are (their rstd
     // factors follow)
-    constexpr bool kAgain = RING && NV >= 2;  // pass 2 reads r and y again: registers
+    constexpr bool kAgain = NV >= 2;  // pass 2 reads r and y again: registers
     constexpr int NK = kAgain ? 1 : NV;
     f2 ev[NV][4], r_[NK][4], y_[NK][4];
     f2 sum_g = pk(0.f), sum_e = pk(0.f), sum_h = pk(0.f);
