@@ -28,7 +28,7 @@
 // master copies take 274 us with the clip (0.96 of the rate of a plain copy on what
 // both passes read and write, some of it in the L2; 300 us with 16-byte accesses,
 // which touch every line of fp32 values by halves).  8-bit moments are bound by what
-// an SM issues as much as by memory: the same 161 us, 5.9 TB/s; 16 M bf16 values with
+// an SM issues as much as by memory: the same 164 us, 5.8 TB/s; 16 M bf16 values with
 // bf16 gradients and no master copies 41 us, 4 TB/s.
 #include <algorithm>
 #include <cmath>

@@ -292,7 +292,7 @@ __device__ __forceinline__ void ring_drain(uint64_t* full, int stages, int stage
 // their way to an SM; fewer blocks where two stages each do not fit, 0 when they
 // do not fit one.  The forward does best with about 100 KB in flight (16384x2880
 // 62 us; 67.6 with 138 KB, 85 with 46), the backward, which computes longer on a
-// tile, with all that fits (16384x2048 70 us, 83 with 98 KB).
+// tile, with all that fits (frozen weights, 16384x2048: 70 us, 83 with 98 KB).
 constexpr int kFwdFlight = 104 * 1024, kBwdFlight = kRingBytes;
 inline int ring_stages(size_t tile, int* per, size_t extra, int64_t flight) {
   for (; *per > 0; --*per) {
