@@ -147,6 +147,22 @@ def test_mixed_kinds_and_pointers_that_no_vector_fits(bits):
         check(r, e)
 
 
+@pytest.mark.parametrize("off", [4, 8, 16])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_pointers_on_16_and_32_byte_boundaries(bits, off):
+    """Whole chunks and ragged ends, with the norm, whatever widths the pointers allow."""
+    rows = [tensor(n, pt, gt, master, bits, seed=i, off=off)
+            for i, ((pt, gt, master), n) in enumerate(zip(KINDS, [2048, 6144, 5000, 4097, 8192, 2056]))]
+    norm = math.sqrt(sum(float(np.square(to64(r["grad"])).sum()) for r in rows))
+    out, table = torch.zeros(1, device=DEV), L.AdamWTable(rows)
+    ws = torch.empty(L.moe_adamw_workspace_size(table), dtype=torch.uint8, device=DEV)
+    exp = [expect(r, 4, **HYPER) for r in rows]
+    L.moe_adamw_step(table, 4, grad_norm=out, ws=ws, **HYPER)
+    assert abs(out.item() - norm) <= 2 ** -23 * norm
+    for r, e in zip(rows, exp):
+        check(r, e)
+
+
 def test_more_tensors_than_a_launch_takes():
     rows = [tensor(1 + (i * 37) % 600, *KINDS[4 * (i % 2)], 8 if i % 3 else 32, seed=i)
             for i in range(1700)]
