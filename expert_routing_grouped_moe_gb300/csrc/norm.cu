@@ -114,6 +114,12 @@ int moe_block_norm_bwd(const moe_norm_desc* desc, const void* dr, const void* dn
     if (reinterpret_cast<uintptr_t>(p) & 3u) return bad("a sum over the tokens is misaligned");
   if ((dgate && !gate) || (dw_post && !w_post) || (dw_pre && !w_pre))
     return bad("the gradient of an input that is not there");
+  // without tokens, a gate for each token or element has nothing to point to
+  const bool no_gate_values = desc->T == 0 && (desc->gate == MOE_GATE_TOKEN || desc->gate == MOE_GATE_ELEMENT);
+  if (!no_gate_values && (gate == nullptr) != (desc->gate == MOE_GATE_NONE))
+    return bad("gate and its kind go together");
+  for (const void* p : {desc->gate == MOE_GATE_CHANNEL ? gate : nullptr, static_cast<const void*>(w_post)})
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return bad("a vector of d values is misaligned");
   a.dw_post = dw_post; a.dw_pre = dw_pre; a.gate = gate; a.dgate = dgate;
   a.w_post = w_post; a.w_pre = w_pre;
   a.gate_kind = desc->gate; a.sigmoid = desc->gate_sigmoid;
@@ -130,7 +136,6 @@ int moe_block_norm_bwd(const moe_norm_desc* desc, const void* dr, const void* dn
   if ((w_pre == nullptr) != (dn == nullptr)) return bad("w_pre and dn go together");
   if (y == nullptr && (w_post != nullptr || dy != nullptr || desc->gate != MOE_GATE_NONE))
     return bad("w_post, dy and a gate go with y");
-  if ((gate == nullptr) != (desc->gate == MOE_GATE_NONE)) return bad("gate and its kind go together");
   if (dx == nullptr && dy == nullptr && dgate == nullptr && dw_post == nullptr && dw_pre == nullptr)
     return bad("nothing to compute");
   if (dr) NORM_PTR(dr, xs, vec);

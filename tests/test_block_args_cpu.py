@@ -64,6 +64,22 @@ def test_norm_backward_pointers(L, kw):
     assert bwd(L, desc(L), **kw) == L.MOE_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("kw", [
+    dict(gate=None), dict(gate=P((1 << 20) + 2)), dict(w_post=P((1 << 20) + 2)), dict(dgate=ODD)])
+def test_norm_backward_without_tokens_checks_the_vectors_of_d_values(L, kw):
+    """T = 0 leaves the gate of a channel kind and the weights as they are for T > 0."""
+    kw = dict(dict(gate=A), **kw)
+    assert bwd(L, desc(L, T=0, gate=2), **kw) == L.MOE_ERR_INVALID_ARG
+    assert bwd(L, desc(L, gate=2), **kw) == L.MOE_ERR_INVALID_ARG
+
+
+def test_norm_backward_without_tokens_and_a_gate_without_a_kind(L):
+    assert bwd(L, desc(L, T=0, gate=0), gate=A) == L.MOE_ERR_INVALID_ARG
+    # nothing is launched where no sum over the tokens is wanted
+    for kind in (1, 3):
+        assert bwd(L, desc(L, T=0, gate=kind), dw_post=None, dw_pre=None) == L.MOE_OK
+
+
 def test_norm_workspace(L):
     lib = L.load()
     assert bwd(L, desc(L), ws_bytes=8) == L.MOE_ERR_WORKSPACE
