@@ -125,9 +125,12 @@ int moe_block_norm_bwd(const moe_norm_desc* desc, const void* dr, const void* dn
   a.gate_kind = desc->gate; a.sigmoid = desc->gate_sigmoid;
   a.scale = desc->scale; a.eps = desc->eps; a.w_off = desc->w_offset;
   a.T = desc->T; a.d = desc->d;
-  if (desc->T == 0) {
-    const cudaError_t e = launch_norm_bwd(a, desc->x_type, desc->y_type, false, stream);
-    if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
+  if (desc->T == 0) {  // zeros, whatever the gate and the weights hold
+    for (void* p : {static_cast<void*>(dw_post), static_cast<void*>(dw_pre), sum_gate ? dgate : nullptr}) {
+      if (p == nullptr) continue;
+      const cudaError_t e = cudaMemsetAsync(p, 0, static_cast<size_t>(desc->d) * 4, stream);
+      if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
+    }
     return record_error(MOE_OK, "");
   }
   const size_t xs = size_of(desc->x_type), ys = size_of(desc->y_type);

@@ -69,35 +69,30 @@ cudaError_t launch_norm_bwd_direct(const NormArgs& a, int x_type, int y_type, bo
 
 cudaError_t launch_norm_bwd(const NormArgs& args, int x_type, int y_type, bool vec, cudaStream_t s) {
   NormArgs a = args;
-  cudaError_t e = cudaSuccess;
-  int rows = 0;  // of partial column sums
-  if (a.T > 0) {
-    const int xs = x_type == MOE_BF16 ? 2 : 4, ys = y_type == MOE_BF16 ? 2 : 4;
-    const bool pre = a.w_pre != nullptr;
-    NormShape sh = norm_bwd_shape(a.d, true);
-    auto place = [&](int size) {
-      const int bytes = sh.groups * a.d * size;
-      return vec ? ring_place<true>(bytes) : ring_place<false>(bytes);
-    };
-    a.tile = (a.x ? place(xs) : 0) + (pre ? place(xs) + place(ys) : 0) + (a.y ? place(ys) : 0) +
-             (a.gate_kind == MOE_GATE_ELEMENT ? place(ys) : 0);
-    const bool barrier = pre || a.w_post || (a.gate_kind == MOE_GATE_TOKEN && a.dgate);
-    const bool ring = sh.nv <= 2 && sh.W > 1 && barrier &&
-                      a.T > static_cast<int64_t>(kNormRingTiles) * sh.groups;
-    const bool sums = a.nsum > 0 || !vec;  // the kernels for any alignment always keep them
-    int per = norm_bwd_per_sm(sh, sums);
-    a.stages = ring ? ring_stages(a.tile, &per, norm_const_bytes(sh), kBwdFlight) : 0;
-    if (a.stages == 0) sh = norm_bwd_shape(a.d, false);
-    a.W = sh.W;
-    const int blocks = norm_bwd_blocks(sh, a.T, sums);
-    rows = blocks * sh.groups;
-    e = a.stages > 0 ? launch_norm_bwd_ring(a, x_type, y_type, vec, blocks, s)
-                     : launch_norm_bwd_direct(a, x_type, y_type, vec, blocks, s);
-  }
+  const int xs = x_type == MOE_BF16 ? 2 : 4, ys = y_type == MOE_BF16 ? 2 : 4;
+  const bool pre = a.w_pre != nullptr;
+  NormShape sh = norm_bwd_shape(a.d, true);
+  auto place = [&](int size) {
+    const int bytes = sh.groups * a.d * size;
+    return vec ? ring_place<true>(bytes) : ring_place<false>(bytes);
+  };
+  a.tile = (a.x ? place(xs) : 0) + (pre ? place(xs) + place(ys) : 0) + (a.y ? place(ys) : 0) +
+           (a.gate_kind == MOE_GATE_ELEMENT ? place(ys) : 0);
+  const bool barrier = pre || a.w_post || (a.gate_kind == MOE_GATE_TOKEN && a.dgate);
+  const bool ring = sh.nv <= 2 && sh.W > 1 && barrier &&
+                    a.T > static_cast<int64_t>(kNormRingTiles) * sh.groups;
+  const bool sums = a.nsum > 0 || !vec;  // the kernels for any alignment always keep them
+  int per = norm_bwd_per_sm(sh, sums);
+  a.stages = ring ? ring_stages(a.tile, &per, norm_const_bytes(sh), kBwdFlight) : 0;
+  if (a.stages == 0) sh = norm_bwd_shape(a.d, false);
+  a.W = sh.W;
+  const int blocks = norm_bwd_blocks(sh, a.T, sums);
+  const cudaError_t e = a.stages > 0 ? launch_norm_bwd_ring(a, x_type, y_type, vec, blocks, s)
+                                     : launch_norm_bwd_direct(a, x_type, y_type, vec, blocks, s);
   if (e != cudaSuccess || a.nsum == 0) return e;
   const int64_t n = static_cast<int64_t>(a.nsum) * a.d;
   return launch_pdl(norm_colsum_kernel, dim3(static_cast<unsigned>((n + 31) / 32)), dim3(kSumThreads),
-                    0, s, a, rows);
+                    0, s, a, blocks * sh.groups);
 }
 
 }  // namespace moe

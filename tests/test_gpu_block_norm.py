@@ -273,6 +273,20 @@ def test_no_tokens():
         assert torch.all(b[k] == 0), k
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_no_tokens_beside_gates_and_weights_that_are_not_finite(value):
+    """The sums over no tokens are zeros whatever they would be multiplied with."""
+    for sigmoid in (False, True):
+        b = make(0, 64, BF, BF, "channel", True, True)
+        b["gate"].fill_(value)
+        b["w_post"].fill_(value)
+        for k in ("dgate", "dw_post", "dw_pre"):
+            b[k].fill_(7.0)
+        backward(b, "channel", sigmoid)
+        for k in ("dgate", "dw_post", "dw_pre"):
+            assert torch.all(b[k] == 0), k
+
+
 def test_equal_inputs_give_equal_bits_on_another_stream_and_in_a_graph():
     b = make(1500, 1024, BF, BF, "channel", True, True)
     forward(b, "channel", True)
