@@ -42,7 +42,7 @@ EXPORTED = (
     "moe_route_kernel_count", "moe_ep_row_weights", "moe_ep_segment_ids", "moe_route_logits",
     "moe_block_norm_fwd", "moe_block_norm_workspace_size", "moe_block_norm_bwd",
     "moe_router_loss_workspace_size", "moe_router_loss_fwd", "moe_router_bwd",
-    "moe_adamw_workspace_size", "moe_adamw_step",
+    "moe_adamw_workspace_size", "moe_adamw_step", "moe_selftest_ring_timeout",
 )
 
 
@@ -124,6 +124,7 @@ def load(path: str = LIB_PATH):
                                              ctypes.POINTER(_P), _I]),
             "moe_probe_count": (_I, [ctypes.c_char_p]),
             "moe_route_noalloc": (ctypes.c_int, [_P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+            "moe_selftest_ring_timeout": (ctypes.c_int, [ctypes.c_uint32, _I, _P, _P]),
             "moe_probe_read_stream": (ctypes.c_int, [_P, _SZ, _I, _P]),
             "moe_route_kernel_count": (_I, [_I, _I, _I]),
             "moe_ep_row_weights": (ctypes.c_int, [_P, _P, _I, _I, _I, _P, _P]),
@@ -551,6 +552,14 @@ def moe_selftest_wait_timeout(timeout_us: int, stream=None):
     (read it with moe_status)."""
     _check(load().moe_selftest_wait_timeout(int(timeout_us), _stream(stream)),
            "moe_selftest_wait_timeout")
+
+
+def moe_selftest_ring_timeout(timeout_us: int, late: int, tiles, stream=None):
+    """Enqueue the self-test of the norms' ring: warp `late` (0: the filling
+    one, 1, or -1: none) misses a tile and gives up after timeout_us; tiles [1]
+    int32 receives how many tiles were filled (-1: one was left in flight)."""
+    _check(load().moe_selftest_ring_timeout(int(timeout_us), int(late), _i32(tiles, "tiles"),
+                                            _stream(stream)), "moe_selftest_ring_timeout")
 
 
 # ------------------------------------------------------------------ tracing

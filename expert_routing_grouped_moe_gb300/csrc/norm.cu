@@ -43,6 +43,51 @@ size_t size_of(int type) { return type == MOE_BF16 ? 2 : 4; }
     if (!aligned(p, size, wide)) return bad(#p " is misaligned"); \
   } while (0)
 
+// Self-test of the ring's failure path: one block of two warps passes its rows
+// through the norms' own ring.  Warp `late` (0: the one that fills the ring, at the
+// third tile; 1: the other, at the last; -1: none) waits there for a barrier that
+// nothing arrives on, and gives up after the limit.  *tiles: how many tiles were
+// filled, or -1 where one of them was still in flight at the end.
+constexpr int kSelfRows = 8, kSelfStages = 2, kSelfD = 64;
+__device__ __align__(16) float g_selftest_rows[kSelfRows * kSelfD];
+__global__ void __launch_bounds__(64) ring_selftest_kernel(int late, uint64_t limit_ns, int32_t* tiles,
+                                                           int* status) {
+  __shared__ __align__(128) uint8_t s_tiles[kSelfStages * kSelfD * 4];
+  __shared__ RingState s_ring;
+  __shared__ uint64_t s_never;
+  const RingSrc src[kRingSrcs] = {{g_selftest_rows, 4}, {nullptr, 0}, {nullptr, 0}, {nullptr, 0}, {nullptr, 0}};
+  const int place = kSelfD * 4;
+  int filled = 0;
+  auto fill = [&](int stage, int64_t row) {
+    ring_fill<true>(src, s_tiles + stage * place, &s_ring.full[stage], row, kSelfRows, 1, kSelfD);
+    ++filled;
+  };
+  if (threadIdx.x == 0) {
+    mbar_init(&s_never, 1);
+    ring_init(s_ring, kSelfStages);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0)
+    for (int q = 0; q < kSelfStages; ++q) fill(q, q);
+  int stage = 0, phase = 0, before = 0;
+  bool filling = true;
+  for (int64_t base = 0; base < kSelfRows; ++base) {
+    const bool miss = base == (late == 0 ? 2 : kSelfRows - 1) && static_cast<int>(threadIdx.x >> 5) == late;
+    filling &= ring_wait(s_ring, miss ? &s_never : &s_ring.full[stage], stage, miss ? 0 : phase, base, status, limit_ns);
+    __syncthreads();
+    if (threadIdx.x == 0 && filling && base >= 1 && base + kSelfStages - 1 < kSelfRows)
+      fill(before, base + kSelfStages - 1);
+    before = stage;
+    if (++stage == kSelfStages) { stage = 0; phase ^= 1; }
+  }
+  ring_drain(s_ring, kSelfStages, 1, kSelfRows);
+  if (threadIdx.x == 0) {
+    for (int t = filled - kSelfStages; t < filled; ++t)  // each place's last tile has landed
+      if (!mbar_try_wait(&s_ring.full[t % kSelfStages], (t / kSelfStages) & 1)) filled = -1;
+    *tiles = filled;
+  }
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -169,6 +214,19 @@ int moe_block_norm_bwd(const moe_norm_desc* desc, const void* dr, const void* dn
   ProbeScope probe("block_norm_bwd", stream);
   const cudaError_t e =
       launch_norm_bwd(a, desc->x_type, desc->y_type, vec, stream);
+  if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
+  return record_error(MOE_OK, "");
+}
+
+int moe_selftest_ring_timeout(uint32_t timeout_us, int32_t late, int32_t* tiles, moe_stream_t stream) {
+  if (timeout_us == 0 || timeout_us > 2000000u) return bad("timeout_us must be in (0, 2000000]");
+  if (late < -1 || late > 1) return bad("late must be -1, 0 or 1");
+  if (tiles == nullptr || (reinterpret_cast<uintptr_t>(tiles) & 3u)) return bad("tiles NULL or misaligned");
+  int* status = nullptr;
+  const int rc = device_status_word(&status);
+  if (rc != MOE_OK) return rc;
+  ring_selftest_kernel<<<1, 64, 0, stream>>>(late, static_cast<uint64_t>(timeout_us) * 1000u, tiles, status);
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
   return record_error(MOE_OK, "");
 }

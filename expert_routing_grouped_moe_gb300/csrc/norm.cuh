@@ -168,6 +168,44 @@ struct RingSrc {
 };
 constexpr int kRingSrcs = 5, kRingMaxStages = 4;
 constexpr int kRingBytes = 208 * 1024;  // of an SM's shared memory
+// A ring's barriers, and where the thread that fills it (thread 0) gave up waiting.
+struct RingState {
+  uint64_t full[kRingMaxStages];
+  int64_t lost_base;  // first row of that tile
+  int abort, lost_stage, lost_phase;
+};
+__device__ __forceinline__ void ring_init(RingState& r, int stages) {  // thread 0
+  r.abort = 0;
+  r.lost_base = -1;
+  for (int q = 0; q < stages; ++q) mbar_init(&r.full[q], 1);
+  fence_mbar_init();
+}
+// Waits for a tile.  Every thread waits by its own clock, so any of them may be the
+// only one that gives up (false), and each that does raises the status word.  Thread 0
+// fills no more from there on: a place it has not seen filled may still be written.
+__device__ __forceinline__ bool ring_wait(RingState& r, uint64_t* bar, int stage, int phase, int64_t base,
+                                          int* status, uint64_t limit_ns) {
+  if (mbar_wait(bar, phase, &r.abort, limit_ns)) return true;
+  atomicCAS(status, 0, kErrTimeout);
+  if (threadIdx.x == 0 && r.lost_base < 0) {
+    r.lost_base = base;
+    r.lost_stage = stage;
+    r.lost_phase = phase;
+  }
+  return false;
+}
+// Before thread 0 leaves the kernel: the copies still in flight where it gave up,
+// once more with a limit.  Those are the tiles from that one on that were filled:
+// all of the first `stages`, and one fewer once tiles follow them.
+__device__ __forceinline__ void ring_drain(RingState& r, int stages, int64_t step, int64_t T) {
+  if (threadIdx.x != 0 || r.lost_base < 0) return;
+  int never = 0, stage = r.lost_stage, phase = r.lost_phase;
+  const int filled = stages - (r.lost_base >= step ? 1 : 0);
+  for (int q = 0; q < filled && r.lost_base + q * step < T; ++q) {
+    mbar_wait(&r.full[stage], phase, &never, 1000000000ull);
+    if (++stage == stages) { stage = 0; phase ^= 1; }
+  }
+}
 
 // Bytes of a tile's place for `bytes` of rows.
 template <bool VEC>
@@ -278,13 +316,6 @@ cudaError_t allow_ring(Kernel kern, std::atomic<uint64_t>& done) {
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
-}
-
-// After a wait that gave up: the copies still in flight, once more with a limit
-// (in a normal run every copy issued has been waited for).
-__device__ __forceinline__ void ring_drain(uint64_t* full, int stages, int stage, int phase) {
-  int never = 0;
-  for (int q = 0; q < stages; ++q) mbar_wait(&full[q], phase ^ (q < stage ? 0 : 1), &never, 1000000000ull);
 }
 
 // Stages of a ring of `tile` bytes each for up to *per blocks on an SM (each with

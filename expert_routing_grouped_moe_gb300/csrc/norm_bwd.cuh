@@ -39,8 +39,7 @@ template <typename XT, typename YT, bool VEC, int NV, int GATE, bool SUMS, bool 
 __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) {
   extern __shared__ __align__(128) uint8_t s_tiles[];
   __shared__ float s_red[2][16][4];
-  __shared__ uint64_t s_full[kRingMaxStages];
-  __shared__ int s_abort;
+  __shared__ RingState s_ring;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int W = a.W, groups = (blockDim.x >> 5) / W;
   const int grp = warp / W, first = grp * W;
@@ -70,17 +69,13 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) 
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc_y[i][e] = acc_r[i][e] = pk(0.f);
   if (RING) {
-    if (threadIdx.x == 0) {
-      s_abort = 0;
-      for (int q = 0; q < a.stages; ++q) mbar_init(&s_full[q], 1);
-      fence_mbar_init();
-    }
+    if (threadIdx.x == 0) ring_init(s_ring, a.stages);
     __syncthreads();
   }
   pdl_wait();
   if (RING && threadIdx.x == 0)
     for (int q = 0; q < a.stages && base + q * step < a.T; ++q)
-      ring_fill<VEC>(src, s_tiles + q * a.tile, &s_full[q], base + q * step, a.T, groups, d);
+      ring_fill<VEC>(src, s_tiles + q * a.tile, &s_ring.full[q], base + q * step, a.T, groups, d);
   // per column: k = (w_post + off) a(channel gate), u = w_pre + off
   auto make_k = [&](int v, f2 (&k)[4]) {
 #pragma unroll
@@ -161,6 +156,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) 
   };
   read_ahead(base + grp);
   int turn = 0, stage = 0, phase = 0, before = 0;
+  bool filling = true;
   for (; base < a.T; base += step, turn ^= 1) {
     const int64_t row = base + grp;
     const bool ok = row < a.T;
@@ -177,8 +173,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) 
     if (a.gate_kind == MOE_GATE_TOKEN) gate_value(next_g, a.sigmoid, a_row, da_row);
     read_ahead(row + step);
     if constexpr (RING) {
-      if (!mbar_wait(&s_full[stage], phase, &s_abort, kWaitTimeoutNs) && threadIdx.x == 0)
-        atomicCAS(a.status, 0, kErrTimeout);
+      if (!ring_wait(s_ring, &s_ring.full[stage], stage, phase, base, a.status, kWaitTimeoutNs)) filling = false;
       const uint8_t* t = s_tiles + stage * a.tile;
       pdr = ring_row<VEC>(t, static_cast<const XT*>(a.x), base, d) + grp * d;
       pr = ring_row<VEC>(t + at_r, static_cast<const XT*>(a.r), base, d) + grp * d;
@@ -236,9 +231,9 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) 
     }
     float sum[3] = {sum2(sum_g), sum2(sum_e), sum2(sum_h)};
     if (pre || post || sum_gate_row) row_sum<3>(sum, s_red[turn], W, warp, first);
-    if (RING && threadIdx.x == 0 && base >= step) {  // the previous tile's place is free
+    if (RING && threadIdx.x == 0 && filling && base >= step) {  // the previous tile's place is free
       const int64_t next = base + (a.stages - 1) * step;
-      if (next < a.T) ring_fill<VEC>(src, s_tiles + before * a.tile, &s_full[before], next, a.T, groups, d);
+      if (next < a.T) ring_fill<VEC>(src, s_tiles + before * a.tile, &s_ring.full[before], next, a.T, groups, d);
     }
     const float c1 = rs_r * (rs_r * (rs_r * (sum[0] * inv_d)));  // t = e - c1 r
     const float apt = rs_y * fmaf(-c1, sum[2], sum[1]);     // sum A p t
@@ -292,7 +287,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a) 
     before = stage;
     if (++stage == a.stages) { stage = 0; phase ^= 1; }
   }
-  if (RING && s_abort) ring_drain(s_full, a.stages, stage, phase);
+  if (RING) ring_drain(s_ring, a.stages, step, a.T);
   if (!SUMS) return;
   float* part = a.part + (static_cast<int64_t>(blockIdx.x) * groups + grp) * a.nsum * d;
 #pragma unroll

@@ -18,8 +18,7 @@ template <typename XT, typename YT, bool VEC, int NV, int GATE, bool RING>
 __global__ void __launch_bounds__(RING && NV == 1 ? 384 : 512, RING && NV == 1 ? 2 : 1) norm_fwd_kernel(const NormArgs a) {
   extern __shared__ __align__(128) uint8_t s_tiles[];
   __shared__ float s_red[2][16][4];
-  __shared__ uint64_t s_full[kRingMaxStages];
-  __shared__ int s_abort;
+  __shared__ RingState s_ring;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int W = a.W, groups = (blockDim.x >> 5) / W;
   const int grp = warp / W, first = grp * W;
@@ -34,17 +33,13 @@ __global__ void __launch_bounds__(RING && NV == 1 ? 384 : 512, RING && NV == 1 ?
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   int64_t base = static_cast<int64_t>(blockIdx.x) * groups;
   if (RING) {
-    if (threadIdx.x == 0) {
-      s_abort = 0;
-      for (int q = 0; q < a.stages; ++q) mbar_init(&s_full[q], 1);
-      fence_mbar_init();
-    }
+    if (threadIdx.x == 0) ring_init(s_ring, a.stages);
     __syncthreads();
   }
   pdl_wait();
   if (RING && threadIdx.x == 0)
     for (int q = 0; q < a.stages && base + q * step < a.T; ++q)
-      ring_fill<VEC>(src, s_tiles + q * a.tile, &s_full[q], base + q * step, a.T, groups, d);
+      ring_fill<VEC>(src, s_tiles + q * a.tile, &s_ring.full[q], base + q * step, a.T, groups, d);
   const bool channel = gate_is<GATE>(a.gate_kind, MOE_GATE_CHANNEL);
   const bool element = gate_is<GATE>(a.gate_kind, MOE_GATE_ELEMENT);
   // per column: k = (w_post + off) a(channel gate), u = w_pre + off
@@ -81,6 +76,7 @@ __global__ void __launch_bounds__(RING && NV == 1 ? 384 : 512, RING && NV == 1 ?
   float next_g = tokens && base + grp < a.T ? tokens[base + grp] : 0.f;
   int turn = 0;  // which of the two arrays the next row sum uses
   int stage = 0, phase = 0, before = 0;
+  bool filling = true;
   for (; base < a.T; base += step) {
     const int64_t row = base + grp;
     const bool ok = row < a.T;
@@ -90,8 +86,7 @@ __global__ void __launch_bounds__(RING && NV == 1 ? 384 : 512, RING && NV == 1 ?
     const YT* py = static_cast<const YT*>(a.y) + off;
     const YT* pg = static_cast<const YT*>(a.gate) + off;
     if constexpr (RING) {
-      if (!mbar_wait(&s_full[stage], phase, &s_abort, kWaitTimeoutNs) && threadIdx.x == 0)
-        atomicCAS(a.status, 0, kErrTimeout);
+      if (!ring_wait(s_ring, &s_ring.full[stage], stage, phase, base, a.status, kWaitTimeoutNs)) filling = false;
       const uint8_t* t = s_tiles + stage * a.tile;
       px = ring_row<VEC>(t, static_cast<const XT*>(a.x), base, d) + grp * d;
       if (a.x != nullptr) t += ring_place<VEC>(groups * d * sizeof(XT));
@@ -101,9 +96,9 @@ __global__ void __launch_bounds__(RING && NV == 1 ? 384 : 512, RING && NV == 1 ?
     }
     // after the first barrier of this tile: the previous tile's place is free
     auto refill = [&]() {
-      if (RING && threadIdx.x == 0 && base >= step) {
+      if (RING && threadIdx.x == 0 && filling && base >= step) {
         const int64_t next = base + (a.stages - 1) * step;
-        if (next < a.T) ring_fill<VEC>(src, s_tiles + before * a.tile, &s_full[before], next, a.T, groups, d);
+        if (next < a.T) ring_fill<VEC>(src, s_tiles + before * a.tile, &s_ring.full[before], next, a.T, groups, d);
       }
     };
     f2 x[NV][4], y[NV][4];
@@ -180,7 +175,7 @@ __global__ void __launch_bounds__(RING && NV == 1 ? 384 : 512, RING && NV == 1 ?
     before = stage;
     if (++stage == a.stages) { stage = 0; phase ^= 1; }
   }
-  if (RING && s_abort) ring_drain(s_full, a.stages, stage, phase);
+  if (RING) ring_drain(s_ring, a.stages, step, a.T);
 }
 
 template <typename XT, typename YT, bool VEC, int NV, int GATE, bool RING>

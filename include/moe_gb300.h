@@ -490,6 +490,17 @@ MOE_API const char* moe_last_error(void);
  * MOE_ERR_INVALID_ARG for a timeout out of range. */
 MOE_API int moe_selftest_wait_timeout(uint32_t timeout_us, moe_stream_t stream);
 
+/* Self-test of the failure path of the norms' ring of tiles, in which every
+ * thread of a block waits for a tile by itself: enqueues one block of two
+ * warps that passes eight tiles through a ring of two.  Warp `late` (0: the one
+ * that fills the ring, at the third tile; 1: the other, at the last one; -1:
+ * none) misses its tile: it waits, bounded by timeout_us (1 .. 2,000,000), for
+ * a barrier that nothing arrives on, records MOE_ERR_TIMEOUT and goes on.  tiles
+ * (device, [1]): the tiles filled -- all 8, or 3 where the filling warp gave up
+ * and so filled no more -- or -1 if a copy was still in flight at the end. */
+MOE_API int moe_selftest_ring_timeout(uint32_t timeout_us, int32_t late, int32_t* tiles,
+                                      moe_stream_t stream);
+
 /* Read-stream probe (measurement): reads `bytes` of device memory at `src`
  * into shared memory with the asynchronous copies the grouped GEMMs load
  * their operands with, one CTA per SM, computes nothing and discards them.

@@ -163,3 +163,10 @@ def test_adamw_workspace_and_counts(L):
     assert lib.moe_adamw_step(None, 2, ctypes.byref(h), None, None, 0, None) == \
         L.MOE_ERR_INVALID_ARG
     assert lib.moe_adamw_workspace_size(None, 3) == 0
+
+
+def test_ring_selftest_arguments(L):
+    f, bad = L.load().moe_selftest_ring_timeout, L.MOE_ERR_INVALID_ARG
+    assert f(0, 0, A, None) == bad and f(2000001, 0, A, None) == bad
+    assert f(1000, 2, A, None) == bad and f(1000, -2, A, None) == bad
+    assert f(1000, 0, None, None) == bad and f(1000, 0, ODD, None) == bad

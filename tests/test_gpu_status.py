@@ -49,3 +49,17 @@ def test_read_stream_probe_runs_and_reports_ok():
     L.moe_probe_read_stream(tiles, L.MOE_PROBE_TILES)
     torch.cuda.synchronize()
     assert L.moe_status() == L.MOE_OK
+
+
+@pytest.mark.parametrize("late,status,filled", [(-1, L.MOE_OK, 8), (1, L.MOE_ERR_TIMEOUT, 8),
+                                                (0, L.MOE_ERR_TIMEOUT, 3)])
+def test_a_tile_that_one_warp_misses_is_reported(late, status, filled):
+    """In the norms' ring every thread waits for itself: a tile that only a warp
+    other than the filling one misses raises the status word too, and where the
+    filling one gives up it fills no more and sees its copies land."""
+    tiles = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert L.moe_status() == L.MOE_OK
+    L.moe_selftest_ring_timeout(20000, late, tiles)
+    assert L.moe_status() == status
+    assert int(tiles) == filled
+    assert L.moe_status() == L.MOE_OK
