@@ -273,6 +273,8 @@ __device__ __forceinline__ void ring_fill(const RingSrc (&src)[kRingSrcs], uint8
       at += ring_place<VEC>(groups * d * es);
     }
   }
+  // values stored by this thread come before the copies that fill the place again
+  if (!VEC && (base == 0 || base + rows == T)) fence_proxy_async_smem();
   mbar_expect_tx(bar, total);
   at = 0;
 #pragma unroll

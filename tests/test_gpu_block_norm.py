@@ -185,6 +185,23 @@ def test_rows_through_the_ring(T, d, off, xt, yt):
     assert L.moe_status() == L.MOE_OK
 
 
+@pytest.mark.parametrize("T,d,off", [(2500, 1001, 1), (3001, 520, 3), (2441, 2047, 0), (1601, 2881, 5)])
+def test_the_place_of_the_first_rows_is_filled_again(T, d, off):
+    """Rows that 16-byte words do not fit, and more tiles for a block than its ring
+    holds: the first tile's first values are stored one by one where later tiles are
+    copied to."""
+    def place(shape, dtype):
+        n = int(np.prod(shape))
+        raw = torch.full((n + 2 * off + 8,), float("nan"), dtype=dtype, device=DEV)
+        return raw[off:off + n].view(shape)
+    for xt, yt in ((BF, BF), (F32, BF), (F32, F32)):
+        b = make(T, d, xt, yt, "element", True, True, place=place)
+        forward(b, "element", True)
+        backward(b, "element", True)
+        check(b, "element", True)
+    assert L.moe_status() == L.MOE_OK
+
+
 def test_norm_alone_and_gate_alone():
     # the norm of x alone (fp32 residual stream, bf16 block input), and its gradient
     b = make(50, 384, F32, BF, "none", False, True)
