@@ -63,6 +63,22 @@ __device__ __forceinline__ float lanes_sum(float v) {
   for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+// Two sums at once: after the first exchange each half of the lanes carries one.
+template <int LPR>
+__device__ __forceinline__ void lanes_sums(float& a, float& b) {
+  if (LPR < 4) {
+    a = lanes_sum<LPR>(a);
+    b = lanes_sum<LPR>(b);
+    return;
+  }
+  const bool up = threadIdx.x & (LPR / 2);
+  float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, LPR / 2);
+#pragma unroll
+  for (int o = LPR / 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const float w = __shfl_xor_sync(0xffffffffu, v, LPR / 2);
+  a = up ? w : v;
+  b = up ? v : w;
+}
 template <int LPR>
 __device__ __forceinline__ float lanes_max(float v) {
 #pragma unroll
@@ -331,21 +347,25 @@ __global__ void __launch_bounds__(kRouterThreads) router_bwd_kernel(
         }
         twice = __any_sync(0xffffffffu, twice);  // also: every read before the rows are written
       }
-      float dot = 0.f;
+      float dot = 0.f, sum = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           l[i][e] = __expf(l[i][e] - ls0);
+          sum += l[i][e];
           dot = fmaf(f[i][e], l[i][e], dot);
         }
-      dot = lanes_sum<LPR>(dot);
-      const float base = fmaf(c_z, ls0, -c_aux * dot);
+      lanes_sums<LPR>(dot, sum);
+      // P = exp(l - lse) over its own sum: the rounding of lse, |lse| 2^-24 of every P,
+      // is common to the row and drops out
+      const float inv = empty ? 0.f : __fdividef(1.f, sum);
+      const float base = inv * fmaf(c_z, ls0, -c_aux * (dot * inv)), ca = c_aux * inv;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          l[i][e] *= fmaf(c_aux, f[i][e], base);
+          l[i][e] *= fmaf(ca, f[i][e], base);
           if (!VEC && dw != nullptr) s_row[ecol<VEC, LPR>(sub, i, e)] = l[i][e];
         }
         if (VEC && dw != nullptr)

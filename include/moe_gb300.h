@@ -417,7 +417,8 @@ MOE_API int moe_router_loss_fwd(const float* logits, int32_t T, int32_t E, int32
  * weights (NULL: no such path), lse from moe_router_loss_fwd, counts as there
  * (may be NULL when aux_coef is 0).  An id outside [0,E) sets MOE_ERR_BAD_IDS
  * in the status word and its slot is left out.  A row without a finite logit
- * gets zeros.  dlogits [T,E] must not overlap the inputs.  T = 0 does nothing. */
+ * gets zeros.  The probabilities are exp(logits - lse) divided by their own sum,
+ * so that the rounding of a large lse does not show in them.  dlogits [T,E] must not overlap the inputs.  T = 0 does nothing. */
 MOE_API int moe_router_bwd(const float* logits, const float* lse, int32_t T, int32_t E, int32_t k,
                            const int32_t* counts, const int32_t* ids, const float* weights,
                            const float* dweights, float aux_coef, float z_coef, float* dlogits,

@@ -138,6 +138,49 @@ def test_rows_without_an_expert_and_lowest_values(E):
     check(b)
 
 
+def check_gradient(b, aux, z):
+    """dlogits to 256 u of its terms whatever lse is.  Before any run: exp of an
+    argument down to -45 is off by (2 + 1.2 * 45) 2 u, its subtraction by 45 u, the
+    row's sum and the products by some 20 u: below 192 u of a P; the z term reads lse,
+    4 u of |max| + log E off."""
+    l, c = to64(b["logits"]), b["counts"].cpu().numpy()
+    aux, z = float(np.float32(aux)), float(np.float32(z))
+    d, mag = bo.router_backward(l, c, b["ids"].cpu().numpy(), to64(b["w"]), to64(b["dw"]), aux, z,
+                                b["k"])
+    size = np.abs(l.max(1, keepdims=True)) + np.log(l.shape[1])
+    e = np.exp(l - l.max(1, keepdims=True))
+    P = e / e.sum(1, keepdims=True)
+    bound = 256 * U * mag + 4 * U * size * P * 2 * z / l.shape[0] + 2.0 ** -60
+    err = np.abs(to64(b["dlogits"]) - d)
+    assert np.all(err <= bound), float(np.max(err / bound))
+
+
+@pytest.mark.parametrize("E", [7, 60, 64, 128, 300])
+@pytest.mark.parametrize("mean", [0.0, 30.0, -1000.0, 1e4, 1e6])
+def test_gradient_of_logits_that_are_not_centred(mean, E):
+    """The rounding of lse, |lse| 2^-24, must not show in the probabilities."""
+    b = make(500, E, 4)
+    b["logits"].mul_(2.0).add_(mean)
+    run(b, aux=0.7, z=0.0)
+    check_gradient(b, 0.7, 0.0)
+    b["dw"].zero_()                 # the balancing term alone
+    run(b, aux=0.7, z=0.2)
+    check_gradient(b, 0.7, 0.2)
+
+
+@pytest.mark.parametrize("E", [7, 8, 128, 300])
+def test_gradient_of_rows_of_the_lowest_value(E):
+    """A row masked by the lowest value instead of -inf is an even row, 1/E each."""
+    b = make(20, E, 2)
+    low = torch.finfo(torch.float32).min
+    b["logits"][5] = low
+    b["logits"][6, 1:] = low
+    b["w"][5] = 0.5
+    for z in (0.0, 0.2):
+        run(b, aux=0.3, z=z)
+        check_gradient(b, 0.3, z)
+
+
 def test_bad_ids_are_left_out_and_reported():
     b = make(16, 8, 2)
     run(b)
