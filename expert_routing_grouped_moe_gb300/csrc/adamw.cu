@@ -285,9 +285,12 @@ __device__ __forceinline__ void encode8(const float (&m)[8], const float (&root)
 }
 
 // Sums held as a pair of floats (value, rest), since 64-bit adds are some 60
-// times slower here: the exact error of each fp32 addition goes to the rest.
+// times slower here: the exact error of each fp32 addition goes to the rest.  A value
+// that is not finite has no rest (its error would be Inf - Inf), so that an infinite
+// sum stays infinite.
 __device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
   const float s = __fadd_rn(a.x, b.x), t = __fsub_rn(s, a.x);
+  if (!(fabsf(s) < INFINITY)) return make_float2(s, 0.f);
   const float err = __fadd_rn(__fsub_rn(a.x, __fsub_rn(s, t)), __fsub_rn(b.x, t));
   const float rest = __fadd_rn(err, __fadd_rn(a.y, b.y));
   const float v = __fadd_rn(s, rest);

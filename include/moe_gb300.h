@@ -418,7 +418,8 @@ MOE_API int moe_router_loss_fwd(const float* logits, int32_t T, int32_t E, int32
  * (may be NULL when aux_coef is 0).  An id outside [0,E) sets MOE_ERR_BAD_IDS
  * in the status word and its slot is left out.  A row without a finite logit
  * gets zeros.  The probabilities are exp(logits - lse) divided by their own sum,
- * so that the rounding of a large lse does not show in them.  dlogits [T,E] must not overlap the inputs.  T = 0 does nothing. */
+ * so that the rounding of a large lse does not show in them.  dlogits [T,E] must
+ * not overlap the inputs.  T = 0 does nothing. */
 MOE_API int moe_router_bwd(const float* logits, const float* lse, int32_t T, int32_t E, int32_t k,
                            const int32_t* counts, const int32_t* ids, const float* weights,
                            const float* dweights, float aux_coef, float z_coef, float* dlogits,
@@ -462,7 +463,10 @@ typedef struct moe_adamw_hyper {
  * index only, so equal inputs give equal results.  grad_norm (device, [1]) gets
  * norm when not NULL.  A gradient that is not finite spoils its values, and in
  * 8 bits the states of its block of MOE_ADAMW_BLOCK; skip_nonfinite = 1
- * prevents it.  Gradients above 1.8e19 count as not finite in the norm.
+ * prevents it.  With the clip an infinite norm gives c = 0 (every other gradient
+ * counts as zero in that step) and a NaN norm spoils all tensors.  The norm is
+ * summed from fp32 squares: a gradient above 1.8e19 makes it infinite, one below
+ * 3e-23 adds nothing.
  * ws: moe_adamw_workspace_size bytes, 16-byte aligned; needed only for the norm
  * (max_norm > 0, grad_norm or skip_nonfinite).  Tensors must not overlap. */
 MOE_API size_t moe_adamw_workspace_size(const moe_adamw_tensor* tensors, int32_t n);

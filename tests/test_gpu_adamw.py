@@ -234,6 +234,47 @@ def test_a_step_that_is_skipped_changes_nothing(value):
     assert not torch.isfinite(rows[0]["master"][600])
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("at", [0, 699, 250_000])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), 2e19, 1e20, 3e38])
+def test_a_norm_that_overflows_clips_to_nothing(value, at, bits):
+    """norm = inf gives a factor of 0: every gradient counts as zero, and only those
+    that are themselves infinite spoil their values (0 inf)."""
+    rows = [tensor(300_000, F32, F32, False, bits, seed=1), tensor(700, BF, F32, True, bits, seed=2),
+            tensor(5000, BF, BF, False, 32, seed=3)]
+    rows[0]["grad"][at] = value
+    table = L.AdamWTable(rows)
+    ws = torch.empty(L.moe_adamw_workspace_size(table), dtype=torch.uint8, device=DEV)
+    norm = torch.empty(1, device=DEV)
+    spoilt = not math.isfinite(value)
+    rows[0]["grad"][at] = 0.0 if spoilt else value
+    exp = [expect(r, 4, coef=0.0, **HYPER) for r in rows]
+    rows[0]["grad"][at] = value
+    L.moe_adamw_step(table, 4, max_norm=1.0, grad_norm=norm, ws=ws, **HYPER)
+    assert float(norm) == float("inf")
+    for r, e in zip(rows[1:], exp[1:]):
+        check(r, e)
+    if not spoilt:
+        check(rows[0], exp[0])
+        return
+    keep = torch.ones(300_000, dtype=torch.bool, device=DEV)
+    first = at // 256 * 256
+    keep[first:first + 256] = False
+    assert torch.equal(rows[0]["param"][keep], torch.from_numpy(exp[0][0]).to(DEV)[keep])
+    assert not torch.isfinite(rows[0]["param"][at])
+
+
+def test_a_norm_that_is_nan_stays_nan():
+    rows = [tensor(300_000, F32, F32, False, 32, seed=1), tensor(700, BF, F32, True, 32, seed=2)]
+    rows[0]["grad"][5] = float("inf")
+    rows[0]["grad"][200_000] = float("nan")
+    table = L.AdamWTable(rows)
+    ws = torch.empty(L.moe_adamw_workspace_size(table), dtype=torch.uint8, device=DEV)
+    norm = torch.empty(1, device=DEV)
+    L.moe_adamw_step(table, 4, max_norm=1.0, grad_norm=norm, ws=ws, **HYPER)
+    assert torch.isnan(norm).all() and torch.isnan(rows[1]["param"].float()).all()
+
+
 def test_no_tensors_and_empty_tensors():
     norm = torch.full((1,), 3.0, device=DEV)
     ws = torch.empty(1 << 14, dtype=torch.uint8, device=DEV)
