@@ -185,6 +185,26 @@ def test_rows_through_the_ring(T, d, off, xt, yt):
     assert L.moe_status() == L.MOE_OK
 
 
+@pytest.mark.parametrize("xt,yt", [(BF, BF), (F32, BF), (F32, F32)])
+@pytest.mark.parametrize("T,d,off", [(331, 8200, 0), (330, 12000, 0), (470, 12000, 1), (329, 16383, 0),
+                                     (331, 16384, 0)])
+def test_wide_rows_over_several_turns(T, d, off, xt, yt):
+    """Above 8192 columns (four shares a thread, rows read directly): more rows than
+    blocks, so that a block's loop turns, the next row is fetched ahead (or, with too
+    many bytes a row, is not) and the column sums gather several rows."""
+    def place(shape, dtype):
+        n = int(np.prod(shape))
+        raw = torch.full((n + 2 * off,), float("nan"), dtype=dtype, device=DEV)
+        return raw[off:off + n].view(shape)
+    for kind, sigmoid, (post, pre) in (("channel", True, (True, True)), ("element", False, (True, True)),
+                                       ("token", True, (True, False)), ("none", False, (False, True))):
+        b = make(T, d, xt, yt, kind, post, pre, seed=3, place=place)
+        forward(b, kind, sigmoid, scale=0.5)
+        backward(b, kind, sigmoid, scale=0.5)
+        check(b, kind, sigmoid, scale=0.5)
+    assert L.moe_status() == L.MOE_OK
+
+
 @pytest.mark.parametrize("T,d,off", [(2500, 1001, 1), (3001, 520, 3), (2441, 2047, 0), (1601, 2881, 5)])
 def test_the_place_of_the_first_rows_is_filled_again(T, d, off):
     """Rows that 16-byte words do not fit, and more tiles for a block than its ring
