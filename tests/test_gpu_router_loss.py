@@ -107,6 +107,30 @@ def test_pointers_that_no_vector_fits(E):
     check(b)
 
 
+@pytest.mark.parametrize("T,E,k,off", [
+    (160_000, 5, 2, 0), (330_000, 8, 2, 0), (160_001, 13, 2, 0), (160_000, 16, 2, 0),
+    (160_003, 19, 2, 0), (160_000, 30, 2, 0), (90_000, 32, 2, 0), (160_000, 32, 2, 1),
+    (80_001, 60, 2, 0), (80_000, 61, 2, 0), (80_000, 64, 2, 1), (40_000, 100, 2, 0),
+    (20_003, 130, 2, 0), (11_000, 260, 2, 0), (10_001, 515, 2, 0)])
+def test_two_launches_and_two_turns_of_rows(T, E, k, off):
+    """Every layout of a row, by vectors and by single logits, with more rows than the
+    blocks take at once (608 blocks of 8 warps, 1 to 32 rows a warp), the last turn not
+    full: the losses' two launches and the gradient."""
+    b = make(T, E, k, off=off, skew=0.02)
+    run(b)
+    check(b)
+    assert L.moe_status() == L.MOE_OK
+
+
+@pytest.mark.parametrize("E", [17, 19, 29, 30, 31, 32])
+@pytest.mark.parametrize("off", [0, 1])
+def test_rows_of_17_to_32_experts(E, off):
+    for T in (1, 7, 64, 1000):
+        b = make(T, E, 4, blocked=E // 16, off=off)
+        run(b)
+        check(b)
+
+
 def test_the_skewed_workload():
     cfg = synth.scaled(synth.CONFIGS["skewed_shared"], T=3000)
     act = synth.layer_activations(cfg, 1, device=DEV)
