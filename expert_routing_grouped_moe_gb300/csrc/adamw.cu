@@ -358,7 +358,8 @@ __device__ __forceinline__ void roots8(const f2 (&x)[4], float least, const Prod
   }
 }
 __device__ __forceinline__ f2 ratio2(f2 n, f2 d, const Product& mul) {
-  const float2 v = unpk(d);  // an infinite d counts as 2^120
+  // 2^120 where v overflowed: root2 makes NaN of an infinite v, and fminf drops it
+  const float2 v = unpk(d);
   const float x = fminf(v.x, 0x1p120f), y = fminf(v.y, 0x1p120f);
   const f2 r = pk(approx_rcp(x), approx_rcp(y)), nd = pk(-x, -y);
   const f2 r1 = fma2(r, fma2(nd, r, pk(1.f)), r);

@@ -275,6 +275,27 @@ def test_a_norm_that_is_nan_stays_nan():
     assert torch.isnan(norm).all() and torch.isnan(rows[1]["param"].float()).all()
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("value", [5e19, 1e21, -1e24])
+def test_a_finite_gradient_whose_square_overflows(value, bits):
+    """v = inf divides the update away, as the formula has it in fp32 (the kernel's
+    largest denominator is 2^120: 1e24 / 2^120 is far below an ulp of the parameters),
+    and spoils nothing."""
+    row = tensor(3000, F32, F32, False, bits, seed=5, fresh=bits == 8)
+    row["grad"][1000] = value
+    row["grad"][2999] = value
+    with np.errstate(all="ignore"):
+        exp = expect(row, 4, **HYPER)
+    assert np.isfinite(exp[0]).all()
+    L.moe_adamw_step(L.AdamWTable([row]), 4, **HYPER)
+    if bits == 32:
+        check(row, exp)
+    assert torch.equal(row["param"], torch.from_numpy(exp[0]).to(DEV))
+    row["grad"].fill_(1.0)
+    L.moe_adamw_step(L.AdamWTable([row]), 5, **HYPER)
+    assert torch.isfinite(row["param"]).all()
+
+
 def test_no_tensors_and_empty_tensors():
     norm = torch.full((1,), 3.0, device=DEV)
     ws = torch.empty(1 << 14, dtype=torch.uint8, device=DEV)
