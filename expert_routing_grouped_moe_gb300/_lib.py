@@ -515,13 +515,24 @@ class AdamWTable:
             float(r.get("lr_mult", 1.0)), float(r.get("weight_decay", 0.0)))
 
     def set_grads(self, grads):
-        """Other gradient tensors, in the order of the rows."""
+        """Other gradient tensors, in the order of the rows.  All are checked
+        before the first is taken: a refusal leaves the table as it was."""
         grads = list(grads)
         if len(grads) != self.n:
             raise ValueError("%d gradients for %d tensors" % (len(grads), self.n))
-        for i, g in enumerate(grads):
-            r = dict(self.rows[i], grad=g)
-            self.array[i], self.rows[i] = self._entry(r), r
+        new = [self._grad(g, e.n) for g, e in zip(grads, self.array)]
+        for r, e, g, (e_ptr, e_type) in zip(self.rows, self.array, grads, new):
+            r["grad"], e.grad, e.grad_type = g, e_ptr, e_type
+
+    @staticmethod
+    def _grad(g, n):
+        """Pointer and type of a gradient of n values."""
+        if g is None:
+            raise TypeError("grad must be a torch.Tensor")
+        p = _ptr(g, name="grad")
+        if g.numel() != n:
+            raise ValueError("grad must have as many values as param")
+        return p, _type(g.dtype, "grad")
 
 
 def moe_adamw_workspace_size(table: AdamWTable) -> int:

@@ -444,3 +444,30 @@ def test_refusals_of_tensors():
         with pytest.raises(L.MoeError, match=match):
             L.moe_adamw_step(table, args.pop("step"), **args)
     assert float(row["m"].abs().sum()) > 0
+
+
+def test_refused_gradients_leave_the_table_as_it_was():
+    rows = [tensor(n, BF, F32, False, 32, seed=i) for i, n in enumerate((64, 300, 1000))]
+    table = L.AdamWTable(rows)
+    new = [torch.randn_like(r["grad"]) for r in rows]
+    bad = [(new[:2] + [new[2][:999]], ValueError, "as many values"),
+           (new[:2] + [new[2].half()], ValueError, "float32 or"),
+           ([new[0], new[1].cpu(), new[2]], ValueError, "CUDA"),
+           ([new[0], new[1], torch.zeros(2000, device=DEV)[::2]], ValueError, "contiguous"),
+           ([new[0], None, new[2]], TypeError, "Tensor"), (new[:2], ValueError, "gradients for")]
+    for grads, error, match in bad:
+        with pytest.raises(error, match=match):
+            table.set_grads(grads)
+    exp = [expect(r, 2, **HYPER) for r in rows]
+    L.moe_adamw_step(table, 2, **HYPER)
+    for r, e in zip(rows, exp):
+        check(r, e)
+    # and all of them where none is refused, of another type too
+    new[1] = new[1].to(BF)
+    table.set_grads(new)
+    for r, g in zip(rows, new):
+        r["grad"] = g
+    exp = [expect(r, 3, **HYPER) for r in rows]
+    L.moe_adamw_step(table, 3, **HYPER)
+    for r, e in zip(rows, exp):
+        check(r, e)
