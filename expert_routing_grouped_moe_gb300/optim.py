@@ -58,13 +58,14 @@ class MoEAdamW:
                                device=dev) if needs_norm else None)
 
     def step(self, grads=None, lr=None, grad_scale=1.0, stream=None):
-        """One step; lr overrides the constructor's for this step (a schedule)."""
+        """One step; lr overrides the constructor's for this step (a schedule).  A
+        step that is refused does not count."""
         if grads is not None:
             self.table.set_grads(grads)
-        self.step_count += 1
-        L.moe_adamw_step(self.table, self.step_count, self.lr if lr is None else lr, self.betas,
+        L.moe_adamw_step(self.table, self.step_count + 1, self.lr if lr is None else lr, self.betas,
                          self.eps, grad_scale, self.max_norm, self.skip_nonfinite, self.grad_norm,
                          self.ws, stream)
+        self.step_count += 1
 
     def state_dict(self):
         """Step count and, for each tensor, its moments, scales and master copy."""

@@ -107,3 +107,19 @@ def test_optimizer_state_saves_and_loads():
         b.load_state_dict({"step": 1, "tensors": [{}, {}]})
     with pytest.raises(ValueError, match="gradients for"):
         b.step(grads[:1])
+
+
+def test_a_refused_step_does_not_count():
+    p, g = torch.randn(500, device=DEV), torch.randn(500, device=DEV)
+    q = p.clone()
+    a, b = MoEAdamW([p], [g], lr=1e-2), MoEAdamW([q], [g], lr=1e-2)
+    for bad in (dict(lr=float("nan")), dict(lr=-1.0), dict(grad_scale=float("inf"))):
+        with pytest.raises(L.MoeError):
+            a.step(**bad)
+    with pytest.raises(ValueError, match="as many values"):
+        a.step(grads=[g[:100]])
+    assert a.step_count == 0
+    for _ in range(2):
+        a.step()
+        b.step()
+    assert a.step_count == b.step_count == 2 and torch.equal(p, q)
