@@ -483,14 +483,50 @@ class AdamWTable:
     moe_adamw_step reads.  rows: dicts with param, grad, m, v (same number of
     values each) and optionally master, scales, lr_mult (1), weight_decay (0).
     m and v in fp32, or in 8 bits (uint8 or torch.float8_e4m3fn) with scales
-    [ceil(n / 256), 2] uint8."""
+    [ceil(n / 256), 2] uint8.
+
+    The array points to the memory that the tensors had when they were entered,
+    which the table keeps alive.  A tensor that was given other memory since
+    (t.data = ..., set_, resize_) is taken up by refresh()."""
+
+    _NAMES = ("param", "grad", "m", "v", "master", "scales")
 
     def __init__(self, rows):
         self.rows = [dict(r) for r in rows]
         self.array = (MoeAdamWTensor * max(1, len(self.rows)))()
         self.n = len(self.rows)
+        self._held = {}   # name -> rows that have one, the tensors, their pointers and storages
         for i, r in enumerate(self.rows):
             self.array[i] = self._entry(r)
+        self._enter(self._NAMES)
+
+    def _enter(self, names):
+        """Notes where the tensors of these names are, and keeps that memory alive."""
+        for name in names:
+            at = [i for i, r in enumerate(self.rows) if r.get(name) is not None]
+            ts = [self.rows[i][name] for i in at]
+            self._held[name] = (at, ts, list(map(torch.Tensor.data_ptr, ts)),
+                                [t.untyped_storage() for t in ts])
+
+    def refresh(self, names=_NAMES):
+        """Takes up the memory that the tensors of these names have now.  All that
+        moved are checked before the first is taken."""
+        moved = {}
+        for name in names:
+            at, ts, ptrs, _ = self._held[name]
+            now = list(map(torch.Tensor.data_ptr, ts))
+            if now != ptrs:
+                moved.update((i, None) for i, a, b in zip(at, now, ptrs) if a != b)
+        if not moved:
+            return
+        for i in moved:
+            moved[i] = self._entry(self.rows[i])
+            if moved[i].n != self.array[i].n:
+                raise ValueError("tensor %d has %d values now, not %d" % (i, moved[i].n,
+                                                                          self.array[i].n))
+        for i, e in moved.items():
+            self.array[i] = e
+        self._enter(self._NAMES)
 
     @staticmethod
     def _entry(r):
@@ -523,6 +559,7 @@ class AdamWTable:
         new = [self._grad(g, e.n) for g, e in zip(grads, self.array)]
         for r, e, g, (e_ptr, e_type) in zip(self.rows, self.array, grads, new):
             r["grad"], e.grad, e.grad_type = g, e_ptr, e_type
+        self._enter(("grad",))
 
     @staticmethod
     def _grad(g, n):

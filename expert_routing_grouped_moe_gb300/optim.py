@@ -62,6 +62,8 @@ class MoEAdamW:
         step that is refused does not count."""
         if grads is not None:
             self.table.set_grads(grads)
+        # a parameter or a gradient may have been given other memory (3 us for 24 tensors)
+        self.table.refresh(("param",) if grads is not None else ("param", "grad"))
         L.moe_adamw_step(self.table, self.step_count + 1, self.lr if lr is None else lr, self.betas,
                          self.eps, grad_scale, self.max_norm, self.skip_nonfinite, self.grad_norm,
                          self.ws, stream)

@@ -123,3 +123,47 @@ def test_a_refused_step_does_not_count():
         a.step()
         b.step()
     assert a.step_count == b.step_count == 2 and torch.equal(p, q)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_parameters_and_gradients_that_were_given_other_memory(bits):
+    """p.data = ... between two steps: the step goes to the new memory, and the old
+    one, kept by whoever still has it, stays as it is."""
+    g = torch.Generator(DEV).manual_seed(7)
+    mk = lambda: [torch.randn(n, generator=g, device=DEV) for n in (700, 33)]  # noqa: E731
+    p, grads, later, later_grads = mk(), mk(), mk(), mk()
+    q = [t.clone() for t in p]
+    a = MoEAdamW(p, grads, lr=1e-2, state_bits=bits, max_norm=1.0)
+    b = MoEAdamW(q, [t.clone() for t in grads], lr=1e-2, state_bits=bits, max_norm=1.0)
+    a.step()
+    b.step()
+    old, before = p[0].detach(), p[0].clone()
+    p[0].data = later[0].clone()
+    grads[1].data = later_grads[1].clone()
+    q[0].copy_(later[0])
+    b.table.rows[1]["grad"].copy_(later_grads[1])
+    a.step()
+    b.step()
+    assert torch.equal(old, before)
+    assert all(torch.equal(s, t) for s, t in zip(p, q))
+    # a size that does not fit is refused and changes nothing
+    p[1].data = torch.zeros(34, device=DEV)
+    with pytest.raises(ValueError):
+        a.step()
+    assert a.step_count == 2 and torch.equal(p[0], q[0])
+
+
+def test_the_optimizers_table_keeps_its_memory():
+    """The memory that the table points to is not handed out again while it does."""
+    ts = [torch.zeros(1 << 20, device=DEV) for _ in range(4)]
+    row = dict(zip(("param", "grad", "m", "v"), ts))
+    table = L.AdamWTable([row])
+    ptrs = {t.data_ptr() for t in ts}
+    for t in ts:
+        t.data = torch.empty(0, device=DEV)
+    again = [torch.ones(1 << 20, device=DEV) for _ in range(8)]
+    assert not ptrs & {t.data_ptr() for t in again}
+    with pytest.raises(ValueError):   # nothing of the row fits any more
+        table.refresh()
+    L.moe_adamw_step(table, 1, lr=0.1)
+    assert all(bool((t == 1).all()) for t in again)
