@@ -40,6 +40,8 @@ class MoEAdamW:
         for p, g in zip(params, grads):
             q = dict(p) if isinstance(p, dict) else {"param": p}
             t, bits = q["param"], q.pop("state_bits", state_bits)
+            if bits not in (8, 32):
+                raise ValueError("state_bits must be 8 or 32")
             keep = q.pop("master", master) and t.dtype == torch.bfloat16
             n, dev = t.numel(), t.device
             sdtype = torch.float32 if bits == 32 else torch.float8_e4m3fn

@@ -170,3 +170,12 @@ def test_ring_selftest_arguments(L):
     assert f(0, 0, A, None) == bad and f(2000001, 0, A, None) == bad
     assert f(1000, 2, A, None) == bad and f(1000, -2, A, None) == bad
     assert f(1000, 0, None, None) == bad and f(1000, 0, ODD, None) == bad
+
+
+@pytest.mark.parametrize("bits", [16, 0, 4])
+def test_state_bits_of_a_parameter(L, bits):
+    """Refused before anything is made of them (the tensors' device is checked later)."""
+    import torch
+    from expert_routing_grouped_moe_gb300 import MoEAdamW
+    with pytest.raises(ValueError, match="state_bits"):
+        MoEAdamW([dict(param=torch.zeros(10), state_bits=bits)], [torch.zeros(10)])
