@@ -355,11 +355,20 @@ def _shaped(t, shape, dtype, name):
     return p
 
 
+def _rows(n):
+    """A size that the C ABI takes as int32 (ctypes would drop its upper bits)."""
+    if n > 0x7FFFFFFF:
+        raise ValueError("%d rows or columns are more than 2^31 - 1" % n)
+    return n
+
+
 @functools.lru_cache(maxsize=256)
 def _norm_setup(T, d, xt, yt, gate_kind, gate_sigmoid, scale, eps, w_offset):
     """Descriptor of a call with these settings, the gate's shape and its type."""
     if gate_kind not in GATE_KINDS:
         raise ValueError("gate_kind must be one of %s" % ", ".join(GATE_KINDS))
+    _rows(T)
+    _rows(d)
     desc = MoeNormDesc(T, d, _type(xt, "x"), _type(yt, "y"), GATE_KINDS[gate_kind],
                        1 if gate_sigmoid else 0, scale, eps, w_offset)
     gshape, gtype = {"none": ((0,), None), "token": ((T,), torch.float32),
@@ -456,6 +465,7 @@ def moe_router_loss_fwd(logits, counts, k, losses, lse, pmean, ws, stream=None):
     """losses [2] = (load-balancing loss, z loss), lse [T], pmean [E] of logits
     [T,E]; counts: moe_route's (its first E entries are read)."""
     T, E = logits.shape
+    _rows(T)
     f32 = torch.float32
     _check(load().moe_router_loss_fwd(
         _f32(logits, "logits"), T, E, int(k), _counts(counts, E),
@@ -469,6 +479,7 @@ def moe_router_bwd(logits, lse, counts, ids, weights, dweights, dlogits, aux_coe
     """dlogits [T,E] through the top-k weights (dweights [T,k], or None) and
     through aux_coef losses[0] + z_coef losses[1].  k: needed without ids."""
     T, E = logits.shape
+    _rows(T)
     f32 = torch.float32
     k = int(k) if k is not None else ids.shape[1]
     _check(load().moe_router_bwd(

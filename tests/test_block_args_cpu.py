@@ -179,3 +179,19 @@ def test_state_bits_of_a_parameter(L, bits):
     from expert_routing_grouped_moe_gb300 import MoEAdamW
     with pytest.raises(ValueError, match="state_bits"):
         MoEAdamW([dict(param=torch.zeros(10), state_bits=bits)], [torch.zeros(10)])
+
+
+def test_more_rows_than_the_c_interface_counts(L):
+    """ctypes drops the upper bits of an int32: 2^32 + 2 rows would pass as 2."""
+    import torch
+    T = 2 ** 32 + 2
+    x = torch.empty(T, 1, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError, match="2\\^31"):
+        L.moe_block_norm_fwd(x, None, None, x)
+    with pytest.raises(ValueError, match="2\\^31"):
+        L.moe_block_norm_bwd(x, x, x, None, x)
+    l = torch.empty(T, 1, device="meta")
+    with pytest.raises(ValueError, match="2\\^31"):
+        L.moe_router_loss_fwd(l, None, 1, None, None, None, None)
+    with pytest.raises(ValueError, match="2\\^31"):
+        L.moe_router_bwd(l, None, None, None, None, None, l, k=1)
