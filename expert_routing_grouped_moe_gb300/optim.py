@@ -86,7 +86,9 @@ class MoEAdamW:
                 if (r[k] is None) != (s.get(k) is None) or (
                         r[k] is not None and (r[k].shape != s[k].shape or r[k].dtype != s[k].dtype)):
                     raise ValueError("%s of the state does not fit" % k)
+        step = int(state["step"])
         for r, s in zip(self.table.rows, state["tensors"]):
-            for k, t in s.items():
-                r[k].copy_(t)
-        self.step_count = int(state["step"])
+            for k in ("m", "v", "scales", "master"):
+                if r[k] is not None:
+                    r[k].copy_(s[k])
+        self.step_count = step

@@ -167,3 +167,20 @@ def test_the_optimizers_table_keeps_its_memory():
         table.refresh()
     L.moe_adamw_step(table, 1, lr=0.1)
     assert all(bool((t == 1).all()) for t in again)
+
+
+def test_a_state_that_is_refused_loads_nothing():
+    p, g = torch.randn(500, device=DEV), torch.randn(500, device=DEV)
+    a = MoEAdamW([p, p.clone()], [g, g], lr=1e-2, state_bits=8)
+    a.step()
+    held = [{k: t.clone() for k, t in s.items()} for s in a.state_dict()["tensors"]]
+    other = [{k: torch.zeros_like(t) for k, t in s.items()} for s in held]
+    with pytest.raises(KeyError):
+        a.load_state_dict({"tensors": other})                     # no step
+    with pytest.raises(ValueError, match="does not fit"):
+        a.load_state_dict({"step": 3, "tensors": [other[0], dict(other[1], m=None)]})
+    assert a.step_count == 1
+    for s, h in zip(a.state_dict()["tensors"], held):
+        assert all(torch.equal(s[k].view(torch.uint8), h[k].view(torch.uint8)) for k in h)
+    a.load_state_dict({"step": 3, "tensors": [dict(s, note="kept elsewhere") for s in other]})
+    assert a.step_count == 3 and not a.state_dict()["tensors"][1]["scales"].any()
