@@ -12,7 +12,9 @@ w_pre being the weight of the norm before the next block.  The backward takes
 gate and the router's weight; the router's load-balancing and z losses enter
 through ``aux_coef`` and ``z_coef``.  The products with W_r are plain matrix
 products (torch.matmul); everything else runs in the CUDA library, all on the
-current stream.
+current stream.  The block's gate is one value for each channel and its block side
+bf16; gates for tokens or elements, weights kept around 0 and an fp32 block side are
+arguments of ``lib.moe_block_norm_fwd`` / ``_bwd``.
 """
 from __future__ import annotations
 

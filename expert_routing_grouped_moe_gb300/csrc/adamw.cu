@@ -27,9 +27,10 @@
 // 32-bit moments are bound by memory: 52 M bf16 parameters with fp32 gradients and
 // master copies take 274 us with the clip (0.96 of the rate of a plain copy on what
 // both passes read and write, some of it in the L2; 300 us with 16-byte accesses,
-// which touch every line of fp32 values by halves).  8-bit moments are bound by what
-// an SM issues as much as by memory: the same 164 us, 5.8 TB/s; 16 M bf16 values with
-// bf16 gradients and no master copies 41 us, 4 TB/s.
+// which touch every line of fp32 values by halves).  With 8-bit moments the same take
+// 164 us, 5.8 TB/s; 16 M bf16 values with bf16 gradients and no master copies 41 us,
+// 4 TB/s (what holds them there is not shown: of 40 such tensors, 4 M values, an SM
+// issues in 40 % of its cycles).
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

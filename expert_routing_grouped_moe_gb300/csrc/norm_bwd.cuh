@@ -15,7 +15,7 @@
 // A row costs some 40 instructions for 8 columns and two waits for its sums, so
 // rows overlap: several blocks on an SM, and a ring that loads ahead.  Bound by
 // memory where the weights are frozen (32768x2880, fp32 stream, element gate:
-// 325 us with 6.3 TB/s); with column sums by what an SM issues between a row's two
+// 328 us with 6.2 TB/s); with column sums by what an SM issues between a row's two
 // barriers: channel gate, 4096x2048 29 us, 16384x2048 83 us, 4.3 ns a further row
 // (0.84 of a plain copy's rate; with frozen weights 4.0).  Of the 29 us the second
 // kernel takes 4, and loading the factors, filling the ring and writing the partial

@@ -7,8 +7,9 @@
 // row whose logits are all -inf has P = 0, adds nothing to either loss and
 // gets a zero gradient; its lse is -inf.
 // Each pass reads the logits once, as float4 where rows allow.  1,048,576 x 128:
-// losses 92 us, 5.8 TB/s (0.87 of a plain copy's rate), gradient 187 us, 0.89;
-// the loads' latency bounds them (16 logits a lane in flight).  4096 x 128: losses
+// losses 92 us, 5.9 TB/s (0.87 of a plain copy's rate), gradient 195 us, 6.0 TB/s
+// (0.89; 187 us without the second sum of a row); the loads' latency bounds them
+// (16 logits a lane in flight).  4096 x 128: losses
 // 5.8 us, of which the two launches and the last sum are 4.
 #include <algorithm>
 #include <cstdint>
@@ -483,8 +484,8 @@ cudaError_t grad(const RouterLaunch& q) {
 // of 4, or logits off a 16-byte boundary) take 8 lanes, and more of them at once, so
 // that a load covers 32 bytes of a row: from 33 experts on for the losses, from 17
 // for the gradient, which also writes so.  300,000 rows of 61, losses: 23.9 us
-// against 27.5, gradient 43.7 against 60.4; 944,811 rows of 19: 41.2 against 33.2,
-// gradient 86 against 137; 900,000 rows of 5, gradient: 30.7 against 24.3.
+// against 27.5, gradient 46 against 62; 944,811 rows of 19: 41.2 against 33.2,
+// gradient 91 against 136; 900,000 rows of 5, gradient: 79 against 17.
 // 300,000 rows of 64, by vectors, with 8 lanes: 21.8 against 19.9.
 template <bool VEC>
 cudaError_t launch_loss(const RouterLaunch& q) {
