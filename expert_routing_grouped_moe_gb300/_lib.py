@@ -29,6 +29,11 @@ MOE_PROBE_LINEAR = 0
 MOE_PROBE_TILES = 1
 MOE_F32 = 0
 MOE_BF16 = 1
+MOE_I32 = 2
+MOE_I64 = 3
+MOE_LOGPROB_MAX_TARGETS = 64
+MOE_LOGPROB_MAX_TOP = 32
+MOE_CKPT_BLOCK = 32
 MOE_NORM_MAX_D = 16384
 MOE_ADAMW_BLOCK = 256
 GATE_KINDS = {"none": 0, "token": 1, "channel": 2, "element": 3}
@@ -43,6 +48,9 @@ EXPORTED = (
     "moe_block_norm_fwd", "moe_block_norm_workspace_size", "moe_block_norm_bwd",
     "moe_router_loss_workspace_size", "moe_router_loss_fwd", "moe_router_bwd",
     "moe_adamw_workspace_size", "moe_adamw_step", "moe_selftest_ring_timeout",
+    "moe_embed_fwd", "moe_embed_workspace_size", "moe_embed_bwd", "moe_logprob_fwd",
+    "moe_logprob_bwd", "moe_logprob_step", "moe_ckpt_pack", "moe_ckpt_unpack",
+    "moe_ckpt_unpack_swiglu",
 )
 
 
@@ -79,6 +87,17 @@ _SZ = ctypes.c_size_t
 class MoeNormDesc(ctypes.Structure):
     _fields_ = [("T", _I), ("d", _I), ("x_type", _I), ("y_type", _I), ("gate", _I),
                 ("gate_sigmoid", _I), ("scale", _F), ("eps", _F), ("w_offset", _F)]
+
+
+class MoeEmbedDesc(ctypes.Structure):
+    _fields_ = [("T", _I), ("V", _I), ("d", _I), ("id_type", _I), ("table_type", _I),
+                ("row_type", _I), ("scale", _F)]
+
+
+class MoeLogprobDesc(ctypes.Structure):
+    _fields_ = [("T", _I), ("V", _I), ("m", _I), ("top", _I), ("type", _I), ("target_type", _I),
+                ("ld", ctypes.c_int64), ("dld", ctypes.c_int64), ("ignore_id", ctypes.c_int64),
+                ("inv_temp", _F)]
 
 
 class MoeAdamWTensor(ctypes.Structure):
@@ -142,6 +161,16 @@ def load(path: str = LIB_PATH):
             "moe_adamw_workspace_size": (_SZ, [ctypes.POINTER(MoeAdamWTensor), _I]),
             "moe_adamw_step": (ctypes.c_int, [ctypes.POINTER(MoeAdamWTensor), _I,
                                               ctypes.POINTER(MoeAdamWHyper), _P, _P, _SZ, _P]),
+            "moe_embed_fwd": (ctypes.c_int, [ctypes.POINTER(MoeEmbedDesc)] + [_P] * 4),
+            "moe_embed_workspace_size": (_SZ, [_I, _I, _I]),
+            "moe_embed_bwd": (ctypes.c_int, [ctypes.POINTER(MoeEmbedDesc), _P, _P, _P,
+                                             ctypes.c_int64, _I, _P, _SZ, _P]),
+            "moe_logprob_fwd": (ctypes.c_int, [ctypes.POINTER(MoeLogprobDesc)] + [_P] * 9),
+            "moe_logprob_bwd": (ctypes.c_int, [ctypes.POINTER(MoeLogprobDesc)] + [_P] * 9),
+            "moe_logprob_step": (ctypes.c_int, [ctypes.POINTER(MoeLogprobDesc)] + [_P] * 13),
+            "moe_ckpt_pack": (ctypes.c_int, [_P, _I, _I, _I, _P, _P, _P]),
+            "moe_ckpt_unpack": (ctypes.c_int, [_P, _P, _I, _I, _P, _I, _P]),
+            "moe_ckpt_unpack_swiglu": (ctypes.c_int, [_P, _P, _I, _I, _P, _P, _I, _I, _P, _P, _P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -598,6 +627,229 @@ def moe_adamw_step(table: AdamWTable, step, lr, betas=(0.9, 0.999), eps=1e-8, gr
         table.array, table.n, ctypes.byref(h), _shaped(grad_norm, (1,), torch.float32, "grad_norm"),
         _ptr(ws, name="ws"), 0 if ws is None else ws.numel() * ws.element_size(),
         _stream(stream)), "moe_adamw_step")
+
+
+# ------------------------------------- embedding, log probabilities, 8-bit checkpoints
+
+_ID_TYPES = {torch.int32: MOE_I32, torch.int64: MOE_I64}
+
+
+def _id_type(t, name):
+    code = _ID_TYPES.get(getattr(t, "dtype", None))
+    if code is None:
+        raise ValueError("%s must be a tensor of torch.int32 or torch.int64" % name)
+    return code
+
+
+def _here(*tensors):
+    """The calls run on the current device: refuses tensors of another one."""
+    dev = _device() if _raw_stream is not None else torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("a tensor is on cuda:%d, the current device is cuda:%d"
+                             % (t.get_device(), dev))
+
+
+@functools.lru_cache(maxsize=256)
+def _embed_desc(T, V, d, id_type, table, rows, scale):
+    return ctypes.byref(MoeEmbedDesc(_rows(T), _rows(V), _rows(d), id_type, _type(table, "table"),
+                                     _type(rows, "rows"), scale))
+
+
+def _embed_setup(ids, rows, table, scale, names):
+    """Descriptor of a lookup of ids [...] in a table [V,d] with rows [...,d]."""
+    code = _id_type(ids, "ids")
+    for t, name in zip((rows, table), names):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % name)
+    if table.dim() != 2:
+        raise ValueError("%s must be [V, d], got %s" % (names[1], tuple(table.shape)))
+    V, d = table.shape
+    return _embed_desc(ids.numel(), V, d, code, table.dtype, rows.dtype, float(scale))
+
+
+def moe_embed_fwd(ids, table, out, scale=1.0, stream=None):
+    """out[...,d] = scale * table[ids]; ids [...] int32 or int64, table [V,d], out of
+    ids' shape and d; both fp32 or bf16.  An id outside the table gives zeros and
+    MOE_ERR_BAD_IDS in the status word."""
+    desc = _embed_setup(ids, out, table, scale, ("out", "table"))
+    sh = ids.shape + table.shape[1:]
+    args = (_ptr(ids, name="ids"), _ptr(table, name="table"), _shaped(out, sh, out.dtype, "out"))
+    _here(ids, table, out)
+    _check(load().moe_embed_fwd(desc, *args, _stream(stream)), "moe_embed_fwd")
+
+
+def moe_embed_workspace_size(T, V, d) -> int:
+    return int(load().moe_embed_workspace_size(_rows(int(T)), _rows(int(V)), _rows(int(d))))
+
+
+def moe_embed_bwd(ids, dout, dtable, ws, scale=1.0, pad_id=None, accumulate=False, stream=None):
+    """dtable [V,d] = scale * the sum of dout's rows for each id (dense: rows without a
+    token are zeros), or += where accumulate.  Tokens with id pad_id add nothing.
+    ws: moe_embed_workspace_size(tokens, V, d) bytes."""
+    desc = _embed_setup(ids, dout, dtable, scale, ("dout", "dtable"))
+    if pad_id is not None and pad_id < 0:
+        raise ValueError("pad_id must not be negative")
+    sh = ids.shape + dtable.shape[1:]
+    args = (_ptr(ids, name="ids"), _shaped(dout, sh, dout.dtype, "dout"),
+            _ptr(dtable, name="dtable"), -1 if pad_id is None else int(pad_id),
+            1 if accumulate else 0, _ptr(ws, name="ws"),
+            0 if ws is None else ws.numel() * ws.element_size())
+    _here(ids, dout, dtable, ws)
+    _check(load().moe_embed_bwd(desc, *args, _stream(stream)), "moe_embed_bwd")
+
+
+@functools.lru_cache(maxsize=256)
+def _logprob_desc(T, V, m, top, dtype, target_type, ld, dld, ignore_id, inv_temp):
+    return ctypes.byref(MoeLogprobDesc(_rows(T), _rows(V), m, top, _type(dtype, "logits"),
+                                       target_type, ld, dld, ignore_id, inv_temp))
+
+
+def _matrix(t, shape, dtype, name):
+    """Pointer and row stride of [T,V] whose rows are dense (not always adjacent)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError("%s must be [T, V]%s, got %s" % (
+            name, "" if shape is None else " = %s" % (tuple(shape),), tuple(t.shape)))
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    T, V = t.shape
+    if (V > 1 and t.stride(1) != 1) or (T > 1 and t.stride(0) < V):
+        raise ValueError("%s must have dense rows that do not overlap" % name)
+    return t.data_ptr(), t.stride(0) if T > 1 else V
+
+
+def _logprob_rows(logits, targets, dlogits, top_ids, top_logp, inv_temp, ignore_id):
+    """Descriptor and the pointers of logits, targets, dlogits."""
+    x, ld = _matrix(logits, None, None, "logits")
+    T, V = logits.shape
+    code = _id_type(targets, "targets")
+    if targets.dim() not in (1, 2) or targets.shape[0] != T:
+        raise ValueError("targets must be [T] or [T, m] with T = %d, got %s"
+                         % (T, tuple(targets.shape)))
+    dx, dld = (None, V) if dlogits is None else _matrix(dlogits, logits.shape, logits.dtype,
+                                                        "dlogits")
+    top = 0
+    for t, name in ((top_ids, "top_ids"), (top_logp, "top_logp")):
+        if t is not None:
+            if t.dim() != 2 or t.shape[0] != T or (top and t.shape[1] != top):
+                raise ValueError("%s must be [T, top], got %s" % (name, tuple(t.shape)))
+            top = t.shape[1]
+    m = 1 if targets.dim() == 1 else targets.shape[1]
+    desc = _logprob_desc(T, V, m, top, logits.dtype, code, ld, dld, int(ignore_id),
+                         float(inv_temp))
+    return desc, x, _ptr(targets, name="targets"), dx
+
+
+def _logprob_out(logits, targets, logp, stats, lse, entropy, top_ids, top_logp):
+    T, f32 = logits.shape[0], torch.float32
+    for t, name in ((logp, "logp"), (stats, "stats")):
+        if t is None:
+            raise TypeError("%s must be a torch.Tensor" % name)
+    return (_shaped(logp, targets.shape, f32, "logp"), _shaped(stats, (T, 2), f32, "stats"),
+            _shaped(lse, (T,), f32, "lse"), _shaped(entropy, (T,), f32, "entropy"),
+            _i32(top_ids, "top_ids"), _f32(top_logp, "top_logp"))
+
+
+def moe_logprob_fwd(logits, targets, logp, stats, lse=None, entropy=None, top_ids=None,
+                    top_logp=None, inv_temp=1.0, ignore_id=-100, stream=None):
+    """Log probabilities logp of the tokens targets ([T], or [T,m] for m tokens of each
+    row) under softmax(inv_temp * logits), logits [T,V] fp32 or bf16 with any row
+    stride; optionally each row's log sum of exponentials, its entropy, and its
+    likeliest tokens (top_ids int32, top_logp [T,top]).  stats [T,2]: for the
+    backward.  A target ignore_id gets 0."""
+    desc, x, y, _ = _logprob_rows(logits, targets, None, top_ids, top_logp, inv_temp, ignore_id)
+    out = _logprob_out(logits, targets, logp, stats, lse, entropy, top_ids, top_logp)
+    _here(logits, targets, logp, stats, lse, entropy, top_ids, top_logp)
+    _check(load().moe_logprob_fwd(desc, x, y, *out, _stream(stream)), "moe_logprob_fwd")
+
+
+def moe_logprob_bwd(logits, targets, stats, dlogp, dlogits, entropy=None, dentropy=None, dlse=None,
+                    inv_temp=1.0, ignore_id=-100, stream=None):
+    """dlogits [T,V] (may be logits) from the gradients of logp, entropy and lse, each
+    of which may be None; stats and, with dentropy, entropy as the forward wrote them."""
+    if dlogits is None:
+        raise TypeError("dlogits must be a torch.Tensor")
+    desc, x, y, dx = _logprob_rows(logits, targets, dlogits, None, None, inv_temp, ignore_id)
+    T, f32 = logits.shape[0], torch.float32
+    args = (_shaped(stats, (T, 2), f32, "stats"), _shaped(entropy, (T,), f32, "entropy"),
+            _shaped(dlogp, targets.shape, f32, "dlogp"),
+            _shaped(dentropy, (T,), f32, "dentropy"), _shaped(dlse, (T,), f32, "dlse"))
+    _here(logits, targets, stats, entropy, dlogp, dentropy, dlse, dlogits)
+    _check(load().moe_logprob_bwd(desc, x, y, *args, dx, _stream(stream)), "moe_logprob_bwd")
+
+
+def moe_logprob_step(logits, targets, logp, stats, dlogp, dlogits, dentropy=None, dlse=None,
+                     lse=None, entropy=None, top_ids=None, top_logp=None, inv_temp=1.0,
+                     ignore_id=-100, stream=None):
+    """moe_logprob_fwd and moe_logprob_bwd in one call, for gradients that are known
+    ahead; reads the logits from memory once."""
+    if dlogits is None:
+        raise TypeError("dlogits must be a torch.Tensor")
+    desc, x, y, dx = _logprob_rows(logits, targets, dlogits, top_ids, top_logp, inv_temp,
+                                   ignore_id)
+    T, f32 = logits.shape[0], torch.float32
+    grads = (_shaped(dlogp, targets.shape, f32, "dlogp"),
+             _shaped(dentropy, (T,), f32, "dentropy"), _shaped(dlse, (T,), f32, "dlse"))
+    out = _logprob_out(logits, targets, logp, stats, lse, entropy, top_ids, top_logp)
+    _here(logits, targets, dlogp, dentropy, dlse, logp, stats, lse, entropy, top_ids, top_logp,
+          dlogits)
+    _check(load().moe_logprob_step(desc, x, y, *grads, *out, dx, _stream(stream)),
+           "moe_logprob_step")
+
+
+def _ckpt_rows(x, codes, scales):
+    """Type, R, C and pointers of rows x [R,C], their codes and scales."""
+    p = _ptr(x, name="x")
+    if x is None or x.dim() != 2:
+        raise ValueError("x must be [R, C]")
+    code = _type(x.dtype, "x")
+    R, C = x.shape
+    if codes is None or scales is None:
+        raise TypeError("codes and scales must be torch.Tensors")
+    q = (_shaped(codes, x.shape, torch.int8, "codes"),
+         _shaped(scales, (R, -(-C // MOE_CKPT_BLOCK)), torch.uint8, "scales"))
+    _here(x, codes, scales)
+    return p, code, _rows(R), _rows(C), q
+
+
+def moe_ckpt_pack(x, codes, scales, stream=None):
+    """x [R,C] fp32 or bf16 into 8 bits: codes [R,C] int8 and a power-of-two scale for
+    each 32 values of a row, scales [R, ceil(C/32)] uint8 (exponent bytes)."""
+    p, code, R, C, q = _ckpt_rows(x, codes, scales)
+    _check(load().moe_ckpt_pack(p, code, R, C, *q, _stream(stream)), "moe_ckpt_pack")
+
+
+def moe_ckpt_unpack(codes, scales, x, stream=None):
+    """x [R,C] fp32 or bf16 = the values that moe_ckpt_pack's codes stand for."""
+    p, code, R, C, q = _ckpt_rows(x, codes, scales)
+    _check(load().moe_ckpt_unpack(*q, R, C, p, code, _stream(stream)), "moe_ckpt_unpack")
+
+
+def moe_ckpt_unpack_swiglu(codes, scales, sorted_src, topk_w, shared_expert, h, act, stream=None):
+    """A layer's saved h [P,hs] fp32 from its 8-bit codes, and act [2,P,f] (bf16 pair) =
+    w_p silu(gate) up, w_p being topk_w's weight of sorted row p's slot."""
+    p, code, P, C, q = _ckpt_rows(h, codes, scales)
+    if code != MOE_F32:
+        raise ValueError("h must be torch.float32")
+    if act is None or act.dim() != 3 or C != 32 * ((act.shape[2] + 15) // 16):
+        raise ValueError("act must be [2, P, f] with 32 * ceil(f / 16) columns of h")
+    if topk_w is None or topk_w.dim() != 2:
+        raise ValueError("topk_w must be [T, k]")
+    T, k = topk_w.shape
+    if T * (k + (1 if shared_expert else 0)) != P:
+        raise ValueError("h has %d rows for %d tokens" % (P, T))
+    f = act.shape[2]
+    args = (_shaped(sorted_src, (P,), torch.int32, "sorted_src"), _f32(topk_w, "topk_w"), k,
+            1 if shared_expert else 0, p, _shaped(act, (2, P, f), torch.bfloat16, "act"))
+    if sorted_src is None:
+        raise TypeError("sorted_src must be a torch.Tensor")
+    _here(sorted_src, topk_w, act)
+    _check(load().moe_ckpt_unpack_swiglu(*q, P, f, *args, _stream(stream)),
+           "moe_ckpt_unpack_swiglu")
 
 
 def moe_status(stream=None) -> int:

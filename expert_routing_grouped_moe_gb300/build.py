@@ -17,8 +17,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmoe_gb300.so")
-SOURCES = ["gemm.cu", "norm_bwd_ring.cu", "norm_bwd.cu", "norm_fwd.cu", "adamw.cu", "router.cu",
-           "route.cu", "api.cu", "rows.cu", "route_noalloc.cu", "probe.cu", "ep.cu", "norm.cu"]
+SOURCES = ["gemm.cu", "norm_bwd_ring.cu", "norm_bwd.cu", "norm_fwd.cu", "adamw.cu", "logprob.cu",
+           "router.cu", "embed.cu", "ckpt.cu", "route.cu", "api.cu", "rows.cu", "route_noalloc.cu", "probe.cu", "ep.cu", "norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]

@@ -82,7 +82,8 @@ const char* const kKernelNames[] = {
     "route", "permute", "combine", "router_topk", "xa_gu", "gate_up", "xa_dn", "down",
     "u", "dgrad_dn", "v", "dgrad_gu", "dB_dn", "dA_dn", "dB_gu", "dA_gu", "dw_reduce",
     "dW_dn", "dW_gu", "ep_row_weights", "ep_segment_ids", "block_norm_fwd", "block_norm_bwd",
-    "router_loss", "router_bwd", "grad_norm", "adamw"};
+    "router_loss", "router_bwd", "grad_norm", "adamw", "embed_fwd", "embed_bwd", "logprob_fwd",
+    "logprob_bwd", "logprob_step", "ckpt_pack", "ckpt_unpack", "ckpt_unpack_swiglu"};
 constexpr int kNumKernels = sizeof(kKernelNames) / sizeof(kKernelNames[0]);
 
 struct Probe {

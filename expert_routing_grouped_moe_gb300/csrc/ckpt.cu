@@ -1,0 +1,417 @@
+// Activation checkpoints in 8 bits.  A block of 32 consecutive values of a row
+// shares the scale 2^e, e the least integer (>= -126) with max |x| <= 127 2^e:
+//   code = rint(x 2^-e)  (int8),   scale byte = e + 127,   x' = code 2^e
+// e is at most 121: above 127 2^121, within 0.8 % of the largest fp32 value, values
+// count as that (64 2^122 would be infinite).
+// 127 = 1.984375 * 2^6, so e is read off the largest value's bits: its exponent
+// less 6, one more where its mantissa exceeds 0.984375 * 2^23 (a carry does it).
+// Whole numbers and powers of two throughout: the one rounding is the code's.
+// Power-of-two scales cost up to one of the codes' 7 bits, half a bit on average,
+// against scales of any value; they make codes and results exact to state and
+// restore, where a rounded quotient would move a code now and then.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/moe_gb300.h"
+#include "internal.h"
+#include "ptx.cuh"
+#include "rowvec.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kCkptThreads = 256;
+constexpr int kSegCols = 256;  // columns of a warp's unit: 8 values, or every 32nd of 8, a lane
+constexpr int kUnits = 2;      // units whose loads are in flight at once
+
+// The bits of a block's largest |x| to its scale byte; 255 where it is not finite.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t bits) {
+  if (bits >= 0x7F800000u) return 255u;
+  const int b = static_cast<int>((bits + 0x1FFFFu) >> 23) - 6;
+  return static_cast<uint32_t>(b < 1 ? 1 : b);
+}
+// Blocks whose largest value is above 127 2^121: the scale stays and values are cut.
+constexpr uint32_t kMaxByte = 248u;
+constexpr float kMaxValue = 3.376239110640e38f;
+__device__ __forceinline__ float cut(float x) { return fminf(fmaxf(x, -kMaxValue), kMaxValue); }
+__device__ __forceinline__ f2 cut(f2 a) {
+  const float2 x = unpk(a);
+  return pk(cut(x.x), cut(x.y));
+}
+// 2^-e of a scale byte (any number for 255: the codes are set to 0 there).
+__device__ __forceinline__ float inverse_scale(uint32_t byte) {
+  return __uint_as_float((254u - (byte == 255u ? 127u : byte)) << 23);
+}
+// 2^e; infinite for 255, so that 0 * 2^e is NaN.
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// Rounding to the nearest integer by adding 1.5 * 2^23: the sum's last byte is the
+// code (|x 2^-e| <= 127; the product is exact, so the fused sum rounds once).
+constexpr float kRoundShift = 12582912.f;
+__device__ __forceinline__ uint32_t four_codes(f2 a, f2 b, f2 s) {
+  const float2 u = unpk(fma2(a, s, pk(kRoundShift))), v = unpk(fma2(b, s, pk(kRoundShift)));
+  const uint32_t lo = __byte_perm(__float_as_uint(u.x), __float_as_uint(u.y), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
+}
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+__device__ __forceinline__ uint32_t abs_bits(f2 a) {
+  const float2 x = unpk(a);
+  return max(abs_bits(x.x), abs_bits(x.y));
+}
+// Codes to values: a byte b, its sign bit flipped, as the last byte of 2^23 is
+// 2^23 + 128 + b.
+__device__ __forceinline__ void four_values(uint32_t codes, f2 scale, f2& a, f2& b) {
+  const uint32_t u = codes ^ 0x80808080u;
+  const f2 shift = pk(-8388736.f);
+  a = mul2(add2(pk(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540)),
+                   __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7541))), shift), scale);
+  b = mul2(add2(pk(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7542)),
+                   __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7543))), shift), scale);
+}
+
+// Row and first column of unit u, `segs` to a row.
+__device__ __forceinline__ void unit_place(int64_t u, int64_t segs, bool flat, int64_t& row,
+                                           int64_t& seg) {
+  if (flat) {
+    row = 0;
+  } else if ((u >> 32) == 0) {
+    row = static_cast<uint32_t>(u) / static_cast<uint32_t>(segs);
+  } else {
+    row = u / segs;
+  }
+  seg = u - row * segs;
+}
+
+__device__ __forceinline__ void load_share(const bf16_t* p, Raw8<bf16_t>& r) {
+  r.v = *reinterpret_cast<const uint4*>(p);
+}
+__device__ __forceinline__ void load_share(const float* p, Raw8<float>& r) { load8_wide(p, r); }
+__device__ __forceinline__ void store_share(bf16_t* p, const Raw8<bf16_t>& r) {
+  *reinterpret_cast<uint4*>(p) = r.v;
+}
+__device__ __forceinline__ void store_share(float* p, const Raw8<float>& r) { store8_wide(p, r); }
+__device__ __forceinline__ float widen1(bf16_t x) { return __uint_as_float(uint32_t(x.bits) << 16); }
+__device__ __forceinline__ float widen1(float x) { return x; }
+__device__ __forceinline__ void narrow1(float x, float* p) { *p = x; }
+__device__ __forceinline__ void narrow1(float x, bf16_t* p) {
+  p->bits = static_cast<uint16_t>(pack_bf16x2(x, 0.f));
+}
+
+// C columns a row, nb blocks a row; flat: the rows have no gaps between blocks (C a
+// multiple of 32) and count as one row of R C columns.
+// VEC: a lane has 8 consecutive values, four lanes a block.  Else a lane has every
+// 32nd value and a warp's 32 lanes are a block, so that loads of any alignment and
+// width cover whole sectors.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kCkptThreads) ckpt_pack_kernel(const T* __restrict__ x, int64_t R,
+                                                                int64_t C, int64_t nb,
+                                                                int8_t* __restrict__ codes,
+                                                                uint8_t* __restrict__ scales) {
+  const int lane = threadIdx.x & 31;
+  const int64_t segs = (C + kSegCols - 1) / kSegCols, units = R * segs;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kCkptThreads / 32);
+  pdl_wait();
+  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * (kCkptThreads / 32) + (threadIdx.x >> 5);
+       u0 < units; u0 += warps * kUnits) {
+    if (VEC) {
+      Raw8<T> raw[kUnits];
+      int64_t row[kUnits], col[kUnits];
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int64_t u = u0 + i * warps;
+        int64_t seg = 0;
+        raw[i] = Raw8<T>{};
+        col[i] = C;
+        if (u < units) {
+          unit_place(u, segs, R == 1, row[i], seg);
+          col[i] = seg * kSegCols + 8 * lane;
+          if (col[i] < C) load_share(x + row[i] * C + col[i], raw[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        f2 f[4];
+        widen(raw[i], f);
+        uint32_t big = max(max(abs_bits(f[0]), abs_bits(f[1])), max(abs_bits(f[2]), abs_bits(f[3])));
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        uint32_t byte = scale_byte(big);
+        if (byte == kMaxByte + 1) {
+          byte = kMaxByte;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] = cut(f[e]);
+        }
+        const f2 s = pk(inverse_scale(byte));
+        uint2 q = make_uint2(four_codes(f[0], f[1], s), four_codes(f[2], f[3], s));
+        if (byte == 255u) q = make_uint2(0u, 0u);
+        if (col[i] < C) {
+          *reinterpret_cast<uint2*>(codes + row[i] * C + col[i]) = q;
+          if ((lane & 3) == 0) scales[row[i] * nb + col[i] / MOE_CKPT_BLOCK] = static_cast<uint8_t>(byte);
+        }
+      }
+    } else {
+      for (int i = 0; i < kUnits; ++i) {
+        const int64_t u = u0 + i * warps;
+        if (u >= units) break;
+        int64_t row = 0, seg = 0;
+        unit_place(u, segs, R == 1, row, seg);
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int64_t c = seg * kSegCols + 32 * e + lane;
+          f[e] = c < C ? widen1(x[row * C + c]) : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int64_t c = seg * kSegCols + 32 * e + lane;
+          uint32_t byte = scale_byte(__reduce_max_sync(0xffffffffu, abs_bits(f[e])));
+          if (byte == kMaxByte + 1) byte = kMaxByte, f[e] = cut(f[e]);
+          const uint32_t q = __float_as_uint(fmaf(f[e], inverse_scale(byte), kRoundShift));
+          if (c < C) {
+            codes[row * C + c] = static_cast<int8_t>(byte == 255u ? 0u : q & 0xFFu);
+            if (lane == 0) scales[row * nb + c / MOE_CKPT_BLOCK] = static_cast<uint8_t>(byte);
+          }
+        }
+      }
+    }
+  }
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kCkptThreads) ckpt_unpack_kernel(const int8_t* __restrict__ codes,
+                                                                  const uint8_t* __restrict__ scales,
+                                                                  int64_t R, int64_t C, int64_t nb,
+                                                                  T* __restrict__ x) {
+  const int lane = threadIdx.x & 31;
+  const int64_t segs = (C + kSegCols - 1) / kSegCols, units = R * segs;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kCkptThreads / 32);
+  pdl_wait();
+  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * (kCkptThreads / 32) + (threadIdx.x >> 5);
+       u0 < units; u0 += warps * kUnits) {
+    if (VEC) {
+      uint2 q[kUnits];
+      uint32_t byte[kUnits];
+      int64_t at[kUnits];
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int64_t u = u0 + i * warps;
+        at[i] = -1;
+        if (u < units) {
+          int64_t row = 0, seg = 0;
+          unit_place(u, segs, R == 1, row, seg);
+          const int64_t col = seg * kSegCols + 8 * lane;
+          if (col < C) {
+            at[i] = row * C + col;
+            q[i] = *reinterpret_cast<const uint2*>(codes + at[i]);
+            byte[i] = scales[row * nb + col / MOE_CKPT_BLOCK];
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        if (at[i] < 0) continue;
+        const f2 s = pk(scale_of(byte[i]));
+        f2 f[4];
+        four_values(q[i].x, s, f[0], f[1]);
+        four_values(q[i].y, s, f[2], f[3]);
+        Raw8<T> raw;
+        narrow(f, raw);
+        store_share(x + at[i], raw);
+      }
+    } else {
+      for (int i = 0; i < kUnits; ++i) {
+        const int64_t u = u0 + i * warps;
+        if (u >= units) break;
+        int64_t row = 0, seg = 0;
+        unit_place(u, segs, R == 1, row, seg);
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int64_t c = seg * kSegCols + 32 * e + lane;
+          f[e] = c < C ? static_cast<float>(codes[row * C + c]) * scale_of(scales[row * nb + c / MOE_CKPT_BLOCK])
+                       : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int64_t c = seg * kSegCols + 32 * e + lane;
+          if (c < C) narrow1(f[e], x + row * C + c);
+        }
+      }
+    }
+  }
+}
+
+// A thread takes 8 features: half of a chunk's gates and their ups.  `per` such
+// items to a row (hs / 16), of which those past f have no act.
+constexpr int kSwigluItems = 2;  // items of a thread, their loads in flight at once
+__global__ void __launch_bounds__(kCkptThreads) ckpt_unpack_swiglu_kernel(
+    const int8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t items, int per, int f,
+    const int32_t* __restrict__ sorted_src, const float* __restrict__ topk_w, int k, int K,
+    float* __restrict__ h, uint16_t* __restrict__ act, int64_t pair) {
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * (kCkptThreads * kSwigluItems);
+  const int64_t row0 = base / per;
+  const unsigned rem0 = static_cast<unsigned>(base - row0 * per);
+  uint2 gate[kSwigluItems], up[kSwigluItems];
+  uint32_t byte[kSwigluItems];
+  float w[kSwigluItems];
+  int64_t row[kSwigluItems];
+  int half[kSwigluItems];
+  pdl_wait();
+#pragma unroll
+  for (int i = 0; i < kSwigluItems; ++i) {
+    const unsigned loc = threadIdx.x + i * kCkptThreads;
+    row[i] = -1;
+    if (base + loc >= items) continue;
+    const unsigned r = (rem0 + loc) / static_cast<unsigned>(per);
+    half[i] = static_cast<int>(rem0 + loc - r * static_cast<unsigned>(per));
+    const int64_t p = row0 + r;
+    const int src = __ldg(sorted_src + p);
+    if (src < 0) continue;
+    row[i] = p;
+    const int8_t* q = codes + p * (16 * static_cast<int64_t>(per)) + 32 * (half[i] >> 1) + 8 * (half[i] & 1);
+    gate[i] = __ldg(reinterpret_cast<const uint2*>(q));
+    up[i] = __ldg(reinterpret_cast<const uint2*>(q + 16));
+    byte[i] = __ldg(scales + p * (per >> 1) + (half[i] >> 1));
+    const int t = src / K, j = src - t * K;
+    w[i] = j < k ? __ldg(topk_w + static_cast<int64_t>(t) * k + j) : 1.f;
+  }
+#pragma unroll
+  for (int i = 0; i < kSwigluItems; ++i) {
+    if (row[i] < 0) continue;
+    const f2 s = pk(scale_of(byte[i]));
+    f2 g[4], u[4];
+    four_values(gate[i].x, s, g[0], g[1]);
+    four_values(gate[i].y, s, g[2], g[3]);
+    four_values(up[i].x, s, u[0], u[1]);
+    four_values(up[i].y, s, u[2], u[3]);
+    float* to = h + row[i] * (16 * static_cast<int64_t>(per)) + 32 * (half[i] >> 1) + 8 * (half[i] & 1);
+    Raw8<float> raw;
+    narrow(g, raw);
+    *reinterpret_cast<float4*>(to) = raw.a;
+    *reinterpret_cast<float4*>(to + 4) = raw.b;
+    narrow(u, raw);
+    *reinterpret_cast<float4*>(to + 16) = raw.a;
+    *reinterpret_cast<float4*>(to + 20) = raw.b;
+    if (8 * half[i] >= f) continue;
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 a = unpk(g[e]), b = unpk(u[e]);
+      const float x = w[i] * __fdividef(a.x, 1.f + __expf(-a.x)) * b.x;
+      const float y = w[i] * __fdividef(a.y, 1.f + __expf(-a.y)) * b.y;
+      hi[e] = pack_bf16x2(x, y);
+      lo[e] = pack_bf16x2(x - bf16lo(hi[e]), y - bf16hi(hi[e]));
+    }
+    uint4* out = reinterpret_cast<uint4*>(act + row[i] * f + 8 * half[i]);
+    out[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(act + pair + row[i] * f + 8 * half[i]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+}
+
+int bad(const char* msg) { return record_error(MOE_ERR_INVALID_ARG, msg); }
+bool misaligned(const void* p, unsigned size) { return (reinterpret_cast<uintptr_t>(p) & (size - 1)) != 0; }
+
+int check_rows(const void* x, int32_t x_type, int32_t R, int32_t C, const void* codes, const void* scales) {
+  if (R < 0 || C <= 0) return bad("R must not be negative, C must be positive");
+  if (x_type != MOE_F32 && x_type != MOE_BF16) return bad("x_type must be MOE_F32 or MOE_BF16");
+  if (R == 0) return MOE_OK;
+  if (!x || !codes || !scales) return bad("NULL pointer");
+  if (misaligned(x, x_type == MOE_BF16 ? 2 : 4)) return bad("x is misaligned");
+  return MOE_OK;
+}
+
+struct CkptShape {
+  int64_t R, C, nb;
+  unsigned blocks;
+};
+// Enough blocks for eight on each SM (all that fit), each unit's loads kUnits deep.
+CkptShape ckpt_shape(int64_t R, int64_t C) {
+  CkptShape q{R, C, (C + MOE_CKPT_BLOCK - 1) / MOE_CKPT_BLOCK, 0};
+  if (C % MOE_CKPT_BLOCK == 0) {
+    q.C = R * C;
+    q.nb = R * q.nb;
+    q.R = 1;
+  }
+  const int64_t units = q.R * ((q.C + kSegCols - 1) / kSegCols), per = kCkptThreads / 32 * kUnits;
+  q.blocks = static_cast<unsigned>(std::min<int64_t>((units + per - 1) / per, 8 * kSMs * 16));
+  return q;
+}
+
+template <typename T>
+cudaError_t pack(const CkptShape& q, bool vec, const void* x, int8_t* codes, uint8_t* scales, cudaStream_t s) {
+  return launch_pdl(vec ? ckpt_pack_kernel<T, true> : ckpt_pack_kernel<T, false>, dim3(q.blocks),
+                    dim3(kCkptThreads), 0, s, static_cast<const T*>(x), q.R, q.C, q.nb, codes, scales);
+}
+template <typename T>
+cudaError_t unpack(const CkptShape& q, bool vec, const int8_t* codes, const uint8_t* scales, void* x,
+                   cudaStream_t s) {
+  return launch_pdl(vec ? ckpt_unpack_kernel<T, true> : ckpt_unpack_kernel<T, false>, dim3(q.blocks),
+                    dim3(kCkptThreads), 0, s, codes, scales, q.R, q.C, q.nb, static_cast<T*>(x));
+}
+bool by_vectors(const void* x, int32_t x_type, int32_t C, const void* codes) {
+  return C % 8 == 0 && !misaligned(x, x_type == MOE_BF16 ? 16 : 32) && !misaligned(codes, 8);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_ckpt_pack(const void* x, int32_t x_type, int32_t R, int32_t C, int8_t* codes, uint8_t* scales,
+                  moe_stream_t stream) {
+  NvtxScope nvtx("moe_ckpt_pack");
+  const int rc = check_rows(x, x_type, R, C, codes, scales);
+  if (rc) return rc;
+  if (R == 0) return record_error(MOE_OK, "");
+  const CkptShape q = ckpt_shape(R, C);
+  const bool vec = by_vectors(x, x_type, C, codes);
+  ProbeScope probe("ckpt_pack", stream);
+  const cudaError_t e = x_type == MOE_BF16 ? pack<bf16_t>(q, vec, x, codes, scales, stream)
+                                           : pack<float>(q, vec, x, codes, scales, stream);
+  if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
+  return record_error(MOE_OK, "");
+}
+
+int moe_ckpt_unpack(const int8_t* codes, const uint8_t* scales, int32_t R, int32_t C, void* x,
+                    int32_t x_type, moe_stream_t stream) {
+  NvtxScope nvtx("moe_ckpt_unpack");
+  const int rc = check_rows(x, x_type, R, C, codes, scales);
+  if (rc) return rc;
+  if (R == 0) return record_error(MOE_OK, "");
+  const CkptShape q = ckpt_shape(R, C);
+  const bool vec = by_vectors(x, x_type, C, codes);
+  ProbeScope probe("ckpt_unpack", stream);
+  const cudaError_t e = x_type == MOE_BF16 ? unpack<bf16_t>(q, vec, codes, scales, x, stream)
+                                           : unpack<float>(q, vec, codes, scales, x, stream);
+  if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
+  return record_error(MOE_OK, "");
+}
+
+int moe_ckpt_unpack_swiglu(const int8_t* codes, const uint8_t* scales, int32_t P, int32_t f,
+                           const int32_t* sorted_src, const float* topk_w, int32_t k,
+                           int32_t shared_expert, float* h, moe_bf16* act, moe_stream_t stream) {
+  NvtxScope nvtx("moe_ckpt_unpack_swiglu");
+  if (P < 0 || f <= 0 || f % 8 != 0) return bad("P must not be negative, f a positive multiple of 8");
+  if (k <= 0 || k > 32 || (shared_expert != 0 && shared_expert != 1)) return bad("bad k or shared_expert");
+  if (P == 0) return record_error(MOE_OK, "");
+  if (!codes || !scales || !sorted_src || !topk_w || !h || !act) return bad("NULL pointer");
+  if (misaligned(codes, 8) || misaligned(sorted_src, 4) || misaligned(topk_w, 4) || misaligned(h, 16) ||
+      misaligned(act, 16))
+    return bad("misaligned pointer");
+  const int per = 2 * static_cast<int>((static_cast<int64_t>(f) + 15) / 16);
+  const int64_t items = static_cast<int64_t>(P) * per;
+  const int64_t blocks = (items + kCkptThreads * kSwigluItems - 1) / (kCkptThreads * kSwigluItems);
+  if (blocks > 0x7FFFFFFF) return record_error(MOE_ERR_UNSUPPORTED, "P x f is too large");
+  ProbeScope probe("ckpt_unpack_swiglu", stream);
+  const cudaError_t e = launch_pdl(ckpt_unpack_swiglu_kernel, dim3(static_cast<unsigned>(blocks)),
+                                   dim3(kCkptThreads), 0, stream, codes, scales, items, per, f, sorted_src,
+                                   topk_w, k, k + shared_expert, h, act, static_cast<int64_t>(P) * f);
+  if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
+  return record_error(MOE_OK, "");
+}
+
+}  // extern "C"

@@ -475,6 +475,137 @@ MOE_API int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t n,
                            size_t ws_bytes, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* At the ends of a stack of blocks: embedding and log probabilities          */
+/* ------------------------------------------------------------------------ */
+/* Rows may have any width and alignment (of their element), as above. */
+
+/* Element types of ids and targets passed as void*. */
+enum { MOE_I32 = 2, MOE_I64 = 3 };
+
+typedef struct moe_embed_desc {
+  int32_t T, V, d;       /* tokens, rows of the table, columns */
+  int32_t id_type;       /* MOE_I32 or MOE_I64 */
+  int32_t table_type;    /* the table, or its gradient: MOE_F32 or MOE_BF16 */
+  int32_t row_type;      /* out or dout: likewise */
+  float scale;
+} moe_embed_desc;
+
+/* out[t] = scale * table[ids[t]], rounded once.  ids [T], table [V,d], out
+ * [T,d].  An id outside [0,V) sets MOE_ERR_BAD_IDS in the status word and its
+ * row becomes zeros.  out must not overlap the table.  T = 0 does nothing. */
+MOE_API int moe_embed_fwd(const moe_embed_desc* desc, const void* ids, const void* table, void* out,
+                          moe_stream_t stream);
+
+/* Bytes of scratch moe_embed_bwd needs. */
+MOE_API size_t moe_embed_workspace_size(int32_t T, int32_t V, int32_t d);
+
+/* dtable[v] = scale * sum over the tokens t with ids[t] = v of dout[t], fp32 sums
+ * in an order that depends on the ids alone: the tokens are sorted by id (stable)
+ * and each id's rows added in their order, long runs in parts.
+ *   accumulate = 0: rows without a token become zeros, so that all of dtable
+ *                   [V,d] is written;
+ *   accumulate = 1: the sum is added to what dtable holds; other rows are left
+ *                   as they are (a tied head's gradient, or micro-batches).
+ * Tokens with ids[t] = pad_id add nothing (pad_id < 0: no such id); an id
+ * outside [0,V) that is not pad_id adds nothing either and sets MOE_ERR_BAD_IDS.
+ * ws: moe_embed_workspace_size bytes, 16-byte aligned, its contents need no
+ * initialisation.  T = 0 writes zeros, or nothing where it accumulates. */
+MOE_API int moe_embed_bwd(const moe_embed_desc* desc, const void* ids, const void* dout, void* dtable,
+                          int64_t pad_id, int32_t accumulate, void* ws, size_t ws_bytes,
+                          moe_stream_t stream);
+
+#define MOE_LOGPROB_MAX_TARGETS 64
+#define MOE_LOGPROB_MAX_TOP 32
+
+typedef struct moe_logprob_desc {
+  int32_t T, V;          /* rows; columns of a row that count */
+  int32_t m;             /* given tokens of a row, 1 .. MOE_LOGPROB_MAX_TARGETS */
+  int32_t top;           /* alternatives listed, 0 .. MOE_LOGPROB_MAX_TOP */
+  int32_t type;          /* logits and dlogits: MOE_F32 or MOE_BF16 */
+  int32_t target_type;   /* MOE_I32 or MOE_I64 */
+  int64_t ld, dld;       /* elements from one row of logits (dlogits) to the next, >= V */
+  int64_t ignore_id;     /* a target that asks for nothing */
+  float inv_temp;        /* > 0: z = inv_temp * logits */
+} moe_logprob_desc;
+
+/* Log probabilities of given tokens, entropy and likeliest tokens of each row:
+ *   lse = log sum_e exp z_e,  logp[t,j] = z[y_tj] - lse,  p = exp(z - lse)
+ *   entropy = - sum_e p_e log p_e
+ *   top_ids, top_logp [T,top]: the tokens with the largest logits, larger first,
+ *   of equal ones the lower id first; a logit of -inf (or NaN) is never listed,
+ *   places that remain get id -1 and -inf
+ * targets [T,m]; logp [T,m]; stats [T,2]: what the backward needs (the shift of a
+ * row's exponents and their sum); lse, entropy [T], top_ids and top_logp may be
+ * NULL; outputs fp32, top_ids int32.  A target equal to ignore_id gets logp 0; one
+ * outside [0,V) otherwise too, and sets MOE_ERR_BAD_IDS in the status word.
+ * A row whose logits are all -inf has lse = logp = -inf and entropy 0.  A NaN or
+ * +inf among a row's logits makes its values NaN.  No workspace.  T = 0 does
+ * nothing. */
+MOE_API int moe_logprob_fwd(const moe_logprob_desc* desc, const void* logits, const void* targets,
+                            float* logp, float* stats, float* lse, float* entropy, int32_t* top_ids,
+                            float* top_logp, moe_stream_t stream);
+
+/* Gradient of the logits, given dlogp [T,m], dentropy [T] and dlse [T] (each may
+ * be NULL: zero):
+ *   dlogits_e = inv_temp (sum_j dlogp_j (1[e = y_j] - p_e)
+ *                         - dentropy p_e (log p_e + entropy) + dlse p_e)
+ * logits, targets, stats as given to or written by the forward; entropy as
+ * written (needed with dentropy).  Targets that were ignored or out of range
+ * add nothing; a target named twice adds twice.  A row to which all three give
+ * nothing but zeros gets zeros and is not read, a row whose logits are all -inf
+ * gets zeros.  dlogits may be logits (then in place, dld = ld); other overlaps
+ * are not allowed.  desc->top is not looked at.  T = 0 does nothing. */
+MOE_API int moe_logprob_bwd(const moe_logprob_desc* desc, const void* logits, const void* targets,
+                            const float* stats, const float* entropy, const float* dlogp,
+                            const float* dentropy, const float* dlse, void* dlogits,
+                            moe_stream_t stream);
+
+/* Forward and backward in one call, for losses whose weights are known ahead
+ * (dlogp = -1 / tokens, say): same arguments and results as the two in turn
+ * (entropy may be NULL here even with dentropy), but each row is read from
+ * memory once and its gradient written while the row is still in the L2. */
+MOE_API int moe_logprob_step(const moe_logprob_desc* desc, const void* logits, const void* targets,
+                             const float* dlogp, const float* dentropy, const float* dlse,
+                             float* logp, float* stats, float* lse, float* entropy,
+                             int32_t* top_ids, float* top_logp, void* dlogits, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Activation checkpoints in 8 bits                                          */
+/* ------------------------------------------------------------------------ */
+
+/* Values of a row that share a scale. */
+#define MOE_CKPT_BLOCK 32
+
+/* x [R,C] fp32 or bf16 (x_type) as codes [R,C] int8 and scales [R, ceil(C / 32)]
+ * bytes: for each block of 32 values of a row (the last may be shorter), with e
+ * the least integer >= -126 for which max |x| <= 127 2^e,
+ *   code = x / 2^e to the nearest integer (ties to even),  scale byte = e + 127
+ * so that |x - code 2^e| <= 2^e / 2 <= max |x| / 127 (where max |x| >= 2^-119).
+ * e is at most 121: values above 127 2^121, 0.99 of the largest, count as that.
+ * A block with a value that is not finite has scale byte 255 and codes 0.
+ * R = 0 does nothing. */
+MOE_API int moe_ckpt_pack(const void* x, int32_t x_type, int32_t R, int32_t C, int8_t* codes,
+                          uint8_t* scales, moe_stream_t stream);
+
+/* x = code 2^(byte - 127), exact in both types; NaN where the byte is 255. */
+MOE_API int moe_ckpt_unpack(const int8_t* codes, const uint8_t* scales, int32_t R, int32_t C,
+                            void* x, int32_t x_type, moe_stream_t stream);
+
+/* A layer's saved pre-activations back from 8 bits, for moe_lora_grouped_mlp_bwd:
+ * codes [P,hs] and scales [P, hs / 32] of h (hs = 32 ceil(f / 16): a block is one
+ * chunk, 16 gates and their 16 ups) give
+ *   h   [P,hs]   fp32, code 2^(byte - 127)
+ *   act [2,P,f]  bf16 pair of w_p silu(gate) up
+ * with w_p the weight of the row's slot: topk_w[t,j] where sorted_src[p] = t K + j
+ * and j < k, 1 for the shared slot (K = k + shared_expert).  Rows with
+ * sorted_src[p] < 0 are left as they are.  f is a multiple of 8; h, act 16-byte
+ * aligned, codes 8-byte aligned.  P = 0 does nothing. */
+MOE_API int moe_ckpt_unpack_swiglu(const int8_t* codes, const uint8_t* scales, int32_t P, int32_t f,
+                                   const int32_t* sorted_src, const float* topk_w, int32_t k,
+                                   int32_t shared_expert, float* h, moe_bf16* act,
+                                   moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Status                                                                    */
 /* ------------------------------------------------------------------------ */
 
@@ -534,9 +665,11 @@ MOE_API int moe_probe_read_stream(const void* src, size_t bytes, int32_t pattern
  * xa_dn, down, u, dgrad_dn, v, dgrad_gu, the weight-gradient GEMMs dB_dn,
  * dA_dn, dB_gu, dA_gu, dw_reduce, the full weight-gradient GEMMs dW_dn and
  * dW_gu, ep_row_weights, ep_segment_ids, block_norm_fwd, block_norm_bwd,
- * router_loss, router_bwd, grad_norm and adamw.  (A name covers all kernels of
- * its call: "route" moe_route_kernel_count, "router_loss" one or two, "block_norm_bwd"
- * two with sums over tokens, "adamw" one for each kind of tensor.) */
+ * router_loss, router_bwd, grad_norm, adamw, embed_fwd, embed_bwd, logprob_fwd,
+ * logprob_bwd, logprob_step, ckpt_pack, ckpt_unpack and ckpt_unpack_swiglu.  (A name
+ * covers all kernels of its call: "route" moe_route_kernel_count, "router_loss" one or
+ * two, "block_norm_bwd" two with sums over tokens, "adamw" one for each kind of tensor,
+ * "embed_bwd" its sort, zeros, sums and joins.) */
 MOE_API const char* moe_kernel_name(int32_t i);
 
 /* Arms the probe of one kernel: its next n launches record start_events[i]
