@@ -5,22 +5,23 @@
 //   H = ln S - ln 2 (sum 2^t t) / S
 //   dx_e = inv_temp (sum_j g_j (1[e=y_j] - p_e) - gH p_e (ln p_e + H) + gl p_e),  p = 2^t / S
 //        = 2^t (A + B t) + inv_temp sum_j g_j 1[e=y_j]
-// One pass over a row: a thread keeps the sums relative to a maximum of its own and
-// moves them when a logit exceeds it by 2^4 (each logit's t is then off by 4 * 2^-24
-// at most, and most words move nothing).  Differences are taken before the factor:
-// a row of the type's lowest values, whose product with c would overflow, is then
-// uniform as the formula says.
+// One pass over a row: a thread keeps the sums relative to a shift of its own, t = x c -
+// shift in one fused operation, and moves them when a logit exceeds it by 2^4 (each t
+// is then off by 4 * 2^-24 at most, and most words move nothing).  The row's shift is
+// its largest logit times c, rounded, the same for every use.  Rows whose largest logit
+// is so large or small that products with c overflow (all of them the type's lowest
+// value, say) are summed once more with t = (x - M) c.
 //
-// The likeliest n tokens cost the pass over the row one comparison for each word of
-// 16 bytes: a thread remembers the largest logit of its words and the word it is
-// in.  The n best of a row lie in the words of the n threads whose best is largest
-// (were one in another thread, n threads' bests would be above it), so those
-// threads' words alone, 1/16 of a long row or less, are read again, and of them
-// what reaches the n-th thread's best is sorted.
+// The likeliest n tokens cost the pass over the row next to nothing: a thread has the
+// largest logit of its words at hand, and notes it for each quarter of them.  The n best
+// of a row lie in the n such parts with the largest best (were one in another part, n
+// parts' bests would be above it), so those parts' words alone, 1/50 of a long row for
+// 20 tokens, are read again, and of them what reaches the n-th part's best is sorted.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "../../include/moe_gb300.h"
 #include "internal.h"
@@ -33,10 +34,13 @@ namespace {
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kSlack = 4.f;      // how far t may exceed 0 before a thread's sums move
 constexpr float kLeast = -1000.f;  // t of a logit of -inf, whose 2^t is 0
+// |M c| from which a row is extreme; the shift before any logit was seen, below every
+// other one; and what t c of a logit of -inf counts as where t is needed, lower still.
+constexpr float kExtreme = 1e37f, kUnset = -1.5e37f, kFloor = -2e37f;
 constexpr int kMaxTargets = MOE_LOGPROB_MAX_TARGETS, kMaxTop = MOE_LOGPROB_MAX_TOP;
 constexpr int kMaxCluster = 8;
-constexpr int kCandidates = 1024;  // that are sorted at once
-constexpr int kWinners = 64;       // threads whose words are read again
+constexpr int kCandidates = 512;   // that are sorted at once
+constexpr int kWinners = 64;       // parts whose words are read again
 
 struct Args {
   const void* x;
@@ -47,6 +51,7 @@ struct Args {
   int same;              // rows of x and dx have the same alignment
   int64_t ignore;
   float inv_temp, c;
+  uint32_t floor;        // kFloor / c: as fp32, or twice as bf16
   const void* targets;
   const float *dlogp, *dent, *dlse, *entropy_in;
   const float* stats_in;
@@ -121,6 +126,22 @@ __device__ __forceinline__ float word_max(const uint4& q, float) {
   return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)),
                fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
 }
+// The word with values of at least `low` (NaN stays).
+__device__ __forceinline__ uint4 at_least(uint4 q, uint32_t low, bf16_t) {
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(q.x) : "r"(low));
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(q.y) : "r"(low));
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(q.z) : "r"(low));
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(q.w) : "r"(low));
+  return q;
+}
+__device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+  return __float_as_uint(r);
+}
+__device__ __forceinline__ uint4 at_least(const uint4& q, uint32_t low, float) {
+  return make_uint4(max_nan(q.x, low), max_nan(q.y, low), max_nan(q.z, low), max_nan(q.w, low));
+}
 template <typename T>
 __device__ __forceinline__ float word_value(const uint4& q, int e) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -141,47 +162,61 @@ __device__ __forceinline__ f2 ex2(f2 a) {
   const float2 x = unpk(a);
   return pk(ex2(x.x), ex2(x.y));
 }
-__device__ __forceinline__ f2 at_least(f2 a, float low) {
-  const float2 x = unpk(a);
-  return pk(fmaxf(x.x, low), fmaxf(x.y, low));
-}
 
 // ---- a thread's sums ------------------------------------------------------------
-// S = sum 2^((x - m) c), U = sum 2^t t of the logits seen, relative to m; mx is the
-// largest of them.
+// S = sum 2^t and U = sum 2^t t of the logits seen, t = x c - at; mx: the largest logit.
 template <bool ENT>
 struct Sums {
-  float m = -FLT_MAX, mx = -INFINITY;
+  float at = kUnset, mx = -INFINITY;
   f2 S = pk(0.f), U = pk(0.f);
 
   template <typename T>
-  __device__ __forceinline__ float add(const uint4& q, float c) {
+  __device__ __forceinline__ void add(uint4 q, float c, uint32_t floor) {
     const float big = word_max(q, T{});
     mx = fmaxf(mx, big);
-    if ((big - m) * c > kSlack) move(big, c);
+    if (fmaf(big, c, -at) > kSlack) move(big * c);
+    if (ENT) q = at_least(q, floor, T{});
     f2 f[kPairs<T>];
     pairs(q, T{}, f);
-    const f2 minus = pk(-m), c2 = pk(c);
+    const f2 minus = pk(-at), c2 = pk(c);
 #pragma unroll
     for (int i = 0; i < kPairs<T>; ++i) {
-      const f2 t = mul2(add2(f[i], minus), c2), e = ex2(t);
+      const f2 t = fma2(f[i], c2, minus), e = ex2(t);
       S = add2(S, e);
-      if (ENT) U = fma2(e, at_least(t, kLeast), U);
+      if (ENT) U = fma2(e, t, U);
     }
-    return big;
   }
-  __device__ __forceinline__ void move(float to, float c) {
-    const float by = (m - to) * c, f = ex2(by);
+  __device__ __forceinline__ void move(float to) {
+    const float by = at - to, f = ex2(by);
     if (ENT) U = f == 0.f ? pk(0.f) : mul2(fma2(S, pk(by), U), pk(f));
     S = mul2(S, pk(f));
-    m = to;
+    at = to;
   }
 };
-// Sums relative to `from` made relative to `to` >= from (both > -inf).
-__device__ __forceinline__ void relate(float from, float to, float c, float& S, float& U) {
-  const float by = (from - to) * c, f = ex2(by);
+// Sums relative to `from` made relative to `to` >= from.
+__device__ __forceinline__ void relate(float from, float to, float& S, float& U) {
+  const float by = from - to, f = ex2(by);
   U = f == 0.f ? 0.f : (U + by * S) * f;
   S *= f;
+}
+// What a row's exponents are taken relative to.
+struct Shift {
+  float M, at, c;
+  bool extreme;
+  __device__ __forceinline__ Shift(float M_, float c_) : M(M_), at(M_ * c_), c(c_) {
+    extreme = !(fabsf(at) < kExtreme);
+  }
+  __device__ __forceinline__ float t(float x) const { return extreme ? (x - M) * c : fmaf(x, c, -at); }
+};
+// An extreme row's sums, its largest logit known.
+template <typename T>
+__device__ __forceinline__ void add_extreme(const uint4& q, const Shift& h, float& S, float& U) {
+#pragma unroll
+  for (int e = 0; e < 16 / static_cast<int>(sizeof(T)); ++e) {
+    const float t = (word_value<T>(q, e) - h.M) * h.c, p = ex2(t);
+    S += p;
+    U += p * fmaxf(t, kLeast);
+  }
 }
 
 // ---- order of tokens --------------------------------------------------------------
@@ -204,8 +239,9 @@ struct TopShared {
   uint64_t cand[kCandidates];
   uint64_t out[kMaxTop];    // the block's n best, in order; 0: none
   uint64_t red[32];
-  int win[kWinners];
-  int nwin, count;
+  int win[kWinners];        // first word, from the block's first on, of a part that is read again
+  int nwin, count, above;
+  uint32_t least;
 };
 
 // The n largest of cand[0 .. count), in order, into out (0 past them).
@@ -223,59 +259,138 @@ __device__ __forceinline__ void rank_candidates(TopShared& s, int count, int n) 
   __syncthreads();
 }
 
-// The n best of words [a, b) of a row, which the block's threads read NT apart, and
-// of the partial words edge0 and edge1 (-1: none).  best, best_word: this thread's
-// largest logit and the first word that has it.
+// A thread's words are seen in P parts, each a run of `step` words of the block's (a
+// multiple of NT; the last may be shorter): the largest logit of a part stands for it.
+// Four in blocks of 256 threads, whose threads have up to 75 words of a row of 151936
+// logits; one in smaller blocks, where all threads find the n-th best together sooner
+// than a warp does (one row of 151936, 20 tokens: 14.9 us against 20.5).
+template <int NT>
+constexpr int kParts = NT == 256 ? 4 : 1;
+
+// The n best of words [a, b) of a row, which the block's threads read NT apart, and of
+// the partial words edge0 and edge1 (-1: none).  s.best: the largest logit of each part
+// of each thread.
 template <typename T, int NT>
-__device__ __forceinline__ void block_top(TopShared& s, const Row<T>& row, int a, int b, int edge0, int edge1,
-                                          float best, int best_word, int n) {
-  const uint32_t o = best > -INFINITY ? ordered(best) : 0u;
+__device__ __forceinline__ void block_top(TopShared& s, uint32_t (&s_best)[kParts<NT> * NT], const Row<T>& row, int a,
+                                          int b, int step, int edge0, int edge1, int n) {
+  constexpr int P = kParts<NT>;
+  const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) s.nwin = s.count = 0;
-  uint32_t least = 1;      // the value, and among equal ones the word, of the last thread let in
-  int last = 0x7FFFFFFF;
-  if (__syncthreads_count(o != 0) > n) {
-    uint32_t v = 0;
-    int above = NT;
-    for (int bit = 31; bit >= 0 && above != n; --bit) {
-      const uint32_t trial = v | (1u << bit);
-      const int k = __syncthreads_count(o >= trial);
-      if (k >= n) v = trial, above = k;
-    }
-    least = v;
-    if (above > kWinners) {  // too many equal ones: those with the first words
-      int w = 0;             // the most words that let in fewer than n
-      for (int bit = 30; bit >= 0; --bit) {
-        const int trial = w | (1 << bit);
-        if (__syncthreads_count(o > v || (o == v && best_word < trial)) < n) w = trial;
+  __syncthreads();
+  // the n-th largest of the parts' orders: the largest v that n of them reach, bit by bit
+  constexpr int kLastBit = sizeof(T) == 2 ? 16 : 0;  // bf16 has 16 bits
+  constexpr int kFew = P * NT / 32;                  // parts that a lane of the first warp looks at
+  uint32_t v = 1;
+  if (P == 1) {
+    const uint32_t o = s_best[threadIdx.x];
+    int above = __syncthreads_count(o != 0);
+    if (above > n) {
+      v = 0;
+      for (int bit = 31; bit >= kLastBit && above != n; --bit) {
+        const int k = __syncthreads_count(o >= (v | (1u << bit)));
+        if (k >= n) v |= 1u << bit, above = k;
       }
-      last = w;
+    }
+    if (threadIdx.x == 0) s.above = above;
+  } else if (threadIdx.x < 32) {
+    uint32_t o[kFew];
+    int above = 0;
+#pragma unroll
+    for (int i = 0; i < kFew; ++i) {
+      o[i] = s_best[32 * i + lane];
+      above += o[i] != 0;
+    }
+    above = __reduce_add_sync(0xffffffffu, above);
+    if (above > n) {
+      v = 0;
+      for (int bit = 31; bit >= kLastBit && above != n; --bit) {
+        int k = 0;
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) k += o[i] >= (v | (1u << bit));
+        k = __reduce_add_sync(0xffffffffu, k);
+        if (k >= n) v |= 1u << bit, above = k;
+      }
+    }
+    if (lane == 0) s.above = above;
+  }
+  // the last 16 bits of a bf16's order are its sign's: ones where it is negative
+  if (sizeof(T) == 2 && v != 1 && !(v & 0x80000000u)) v |= 0xFFFFu;
+  if (threadIdx.x == 0) s.least = v;
+  __syncthreads();
+  const uint32_t least = s.least;
+  int last = 0x7FFFFFFF;
+  int best_word[P];
+  if (s.above > kWinners) {  // too many equal ones: those whose first such word comes first
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      best_word[i] = 0;
+      if (s_best[i * NT + threadIdx.x] == least) {
+        const int to = min(b, a + (i + 1) * step);
+        for (best_word[i] = a + i * step + static_cast<int>(threadIdx.x); best_word[i] < to; best_word[i] += NT)
+          if (ordered(word_max(row.word(best_word[i]), T{})) == least) break;
+      }
+    }
+    int w = 0;  // the most words that let in fewer than n
+    for (int bit = 30; bit >= 0; --bit) {
+      const int trial = w | (1 << bit);
+      int k = 0;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const uint32_t o = s_best[i * NT + threadIdx.x];
+        k += o > least || (o == least && best_word[i] < trial);
+      }
+      k = __reduce_add_sync(0xffffffffu, k);
+      if (lane == 0) s.red[threadIdx.x >> 5] = k;
+      __syncthreads();
+      int all = 0;
+      for (int i = 0; i < NT / 32; ++i) all += static_cast<int>(s.red[i]);
+      if (all < n) w = trial;
+      __syncthreads();
+    }
+    last = w;
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const uint32_t o = s_best[i * NT + threadIdx.x];
+    if (o != 0 && (o > least || (o == least && (last == 0x7FFFFFFF || best_word[i] <= last)))) {
+      const int at = atomicAdd(&s.nwin, 1);  // n at most, or kWinners
+      if (at < kWinners) s.win[at] = i * step + threadIdx.x;
     }
   }
-  if (o != 0 && (o > least || (o == least && best_word <= last))) s.win[atomicAdd(&s.nwin, 1)] = threadIdx.x;
   __syncthreads();
-  const int per = (b - a + NT - 1) / NT, items = s.nwin * (per > 0 ? per : 0);
-  // every value of these words that may be among the n best, to `take`
+  const int per = step / NT, items = min(s.nwin, kWinners) * per;
+  // every value of these words that may be among the n best, to `take`; a few words' loads
+  // at once (a long row's words may have left the L2)
   auto scan = [&](auto&& take) {
-    for (int it = threadIdx.x; it < items + 2; it += NT) {
-      int i;
-      uint4 q;
-      bool whole = it < items;
-      if (whole) {
-        const int w = it / per;
-        i = a + s.win[w] + (it - w * per) * NT;
-        if (i >= b) continue;
-        q = row.word(i);
-      } else {
-        i = it == items ? edge0 : edge1;
-        if (i < 0) continue;
-        q = row.partial(i);
-      }
+    auto values = [&](const uint4& q, int i, int to) {
+      if (ordered(word_max(q, T{})) < least) return;
 #pragma unroll
       for (int e = 0; e < Row<T>::E; ++e) {
         const uint32_t v = ordered(word_value<T>(q, e));
-        if (v > kOrderedInf && (v > least || (v == least && (!whole || i <= last))))
+        if (v > kOrderedInf && (v > least || (v == least && i <= to)))
           take(token_key(v, static_cast<uint32_t>(row.col(i) + e)));
       }
+    };
+    constexpr int B = 3;
+    for (int it = threadIdx.x; it < items; it += B * NT) {
+      uint4 q[B];
+      int at[B];
+#pragma unroll
+      for (int u = 0; u < B; ++u) {
+        at[u] = b;
+        if (it + u * NT < items) {
+          const int w = (it + u * NT) / per, first = s.win[w];
+          at[u] = a + first + (it + u * NT - w * per) * NT;
+        }
+        if (at[u] < b) q[u] = row.word(at[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < B; ++u)
+        if (at[u] < b) values(q[u], at[u], last);
+    }
+    if (threadIdx.x < 2) {
+      const int i = threadIdx.x == 0 ? edge0 : edge1;
+      if (i >= 0) values(row.partial(i), i, 0x7FFFFFFF);
     }
   };
   scan([&](uint64_t key) {
@@ -300,7 +415,7 @@ __device__ __forceinline__ void block_top(TopShared& s, const Row<T>& row, int a
       const uint64_t other = __shfl_xor_sync(0xffffffffu, top, i);
       top = other > top ? other : top;
     }
-    if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5] = top;
+    if (lane == 0) s.red[threadIdx.x >> 5] = top;
     __syncthreads();
     for (int i = 0; i < NT / 32; ++i) top = s.red[i] > top ? s.red[i] : top;
     if (threadIdx.x == 0) s.out[r] = top;
@@ -310,16 +425,24 @@ __device__ __forceinline__ void block_top(TopShared& s, const Row<T>& row, int a
 }
 
 // ---- gradient ----------------------------------------------------------------------
-// dx = 2^t (A + B t) of a word, at the word's place in dx.
-template <typename T, bool ENT>
-__device__ __forceinline__ void gradient_pairs(const uint4& q, float M, float c, float A, float B,
+// dx = 2^t (A + B t) of a word.
+template <typename T, bool ENT, bool EXTREME>
+__device__ __forceinline__ void gradient_pairs(uint4 q, const Shift& h, uint32_t floor, float A, float B,
                                                f2 (&f)[kPairs<T>]) {
+  if (ENT && !EXTREME) q = at_least(q, floor, T{});
   pairs(q, T{}, f);
-  const f2 minus = pk(-M), c2 = pk(c), a2 = pk(A), b2 = pk(B);
+  const f2 minus = pk(EXTREME ? -h.M : -h.at), c2 = pk(h.c), a2 = pk(A), b2 = pk(B);
 #pragma unroll
   for (int i = 0; i < kPairs<T>; ++i) {
-    const f2 t = mul2(add2(f[i], minus), c2), e = ex2(t);
-    f[i] = ENT ? mul2(e, fma2(at_least(t, kLeast), b2, a2)) : mul2(e, a2);
+    f2 t;
+    if (EXTREME) {
+      const float2 x = unpk(mul2(add2(f[i], minus), c2));
+      t = pk(fmaxf(x.x, kLeast), fmaxf(x.y, kLeast));
+    } else {
+      t = fma2(f[i], c2, minus);
+    }
+    const f2 e = ex2(t);
+    f[i] = ENT ? mul2(e, fma2(t, b2, a2)) : mul2(e, a2);
   }
 }
 __device__ __forceinline__ uint4 narrowed(const f2 (&f)[4], bf16_t) {
@@ -335,46 +458,60 @@ __device__ __forceinline__ uint4 narrowed(const f2 (&f)[2], float) {
   const float2 x = unpk(f[0]), y = unpk(f[1]);
   return make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
 }
-// A whole word, or (whole = false, or rows of other alignment) value by value.
 template <typename T>
-__device__ __forceinline__ void put_word(T* drow, const Row<T>& row, int i, const uint4& w, bool whole) {
+__device__ __forceinline__ void put_values(T* drow, const Row<T>& row, int i, const uint4& w) {
   const int64_t at = static_cast<int64_t>(i) * Row<T>::E - row.h;
-  if (whole) {
-    __stcs(reinterpret_cast<uint4*>(drow + at), w);
-    return;
-  }
 #pragma unroll
   for (int e = 0; e < Row<T>::E; ++e)
     if (at + e >= 0 && at + e < row.V) put(drow + at + e, word_value<T>(w, e));
 }
-// The gradient of words [a, b), NT apart, and of the partial words edge0 and edge1.
-// zero: nothing is read and zeros are written.
-template <typename T, int NT, int U, bool ENT>
-__device__ __forceinline__ void gradient_words(const Row<T>& row, T* drow, int a, int b, int edge0, int edge1,
-                                               bool same, bool zero, float M, float c, float A, float B) {
+// The gradient of words [a, b), NT apart from thread `id` on, and of the partial words
+// edge0 and edge1; words come from word(i).  zero: nothing is read, zeros are written.
+// same: rows of dx have the alignment of x's, so that whole words are written.
+template <typename T, int NT, int U, bool ENT, typename Word>
+__device__ __forceinline__ void gradient_words(const Row<T>& row, T* drow, int id, int a, int b, int edge0,
+                                               int edge1, bool same, bool zero, const Shift& h, uint32_t floor,
+                                               float A, float B, Word&& word) {
   const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-  for (int i0 = a + static_cast<int>(threadIdx.x); i0 < b; i0 += NT * U) {
-    uint4 q[U];
+  auto slow = [&](const uint4& q) {
+    f2 f[kPairs<T>];
+    if (h.extreme) gradient_pairs<T, ENT, true>(q, h, floor, A, B, f);
+    else gradient_pairs<T, ENT, false>(q, h, floor, A, B, f);
+    return narrowed(f, T{});
+  };
+  uint4* to = reinterpret_cast<uint4*>(drow - row.h);
+  if (zero && same) {
+    for (int i = a + id; i < b; i += NT) __stcs(to + i, none);
+  } else if (same && !h.extreme) {
+    int i = a + id;
+    for (; i + (U - 1) * NT < b; i += NT * U) {
+      uint4 q[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      q[u] = none;
-      if (!zero && i0 + u * NT < b) q[u] = row.word(i0 + u * NT);
+      for (int u = 0; u < U; ++u) q[u] = word(i + u * NT);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        f2 f[kPairs<T>];
+        gradient_pairs<T, ENT, false>(q[u], h, floor, A, B, f);
+        __stcs(to + i + u * NT, narrowed(f, T{}));
+      }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (i0 + u * NT >= b) break;
+#pragma unroll 1
+    for (; i < b; i += NT) {
       f2 f[kPairs<T>];
-      gradient_pairs<T, ENT>(q[u], M, c, A, B, f);
-      put_word<T>(drow, row, i0 + u * NT, zero ? none : narrowed(f, T{}), same);
+      gradient_pairs<T, ENT, false>(word(i), h, floor, A, B, f);
+      __stcs(to + i, narrowed(f, T{}));
+    }
+  } else {
+#pragma unroll 1
+    for (int i = a + id; i < b; i += NT) {
+      const uint4 w = zero ? none : slow(word(i));
+      if (same) __stcs(to + i, w);
+      else put_values(drow, row, i, w);
     }
   }
-  if (threadIdx.x < 2) {
-    const int i = threadIdx.x == 0 ? edge0 : edge1;
-    if (i >= 0) {
-      f2 f[kPairs<T>];
-      gradient_pairs<T, ENT>(zero ? none : row.partial(i), M, c, A, B, f);
-      put_word<T>(drow, row, i, zero ? none : narrowed(f, T{}), false);
-    }
+  if (id < 2) {
+    const int i = id == 0 ? edge0 : edge1;
+    if (i >= 0) put_values(drow, row, i, zero ? none : slow(row.partial(i)));
   }
 }
 
@@ -404,9 +541,9 @@ __device__ __forceinline__ int target(const Args& a, int64_t t, int j, bool tell
   }
   return static_cast<int>(y);
 }
-// The gradient of target j's logit, where it is the first that names it.
+// The gradient of target j's logit: the first that names a token adds up what all get.
 template <typename T>
-__device__ __forceinline__ void put_target(const Targets& s, int j, int m, T* drow, float M, float c, float A,
+__device__ __forceinline__ void put_target(const Targets& s, int j, int m, T* drow, const Shift& h, float A,
                                            float B, float inv_temp) {
   const int y = s.y[j];
   float g = 0.f;
@@ -415,19 +552,27 @@ __device__ __forceinline__ void put_target(const Targets& s, int j, int m, T* dr
       if (i < j) return;
       g += s.g[i];
     }
-  const float t = (s.x[j] - M) * c;
+  const float t = h.t(s.x[j]);
   put(drow + y, fmaf(inv_temp, g, ex2(t) * fmaf(fmaxf(t, kLeast), B, A)));
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ---- kernels --------------------------------------------------------------------------
 // A cluster of 1 to 8 blocks takes a row, each block a run of its words.  GRAD: the
-// gradient follows, from the L2.
-template <typename T, int NT, int U, bool TOP, bool ENT, bool GRAD>
-__global__ void __launch_bounds__(NT) logprob_kernel(const Args a) {
-  __shared__ float s_m[NT / 32], s_S[NT / 32], s_U[NT / 32];
+// gradient follows, from a second reading that the L2 serves.
+template <typename T, int NT, int MINB, int U, bool TOP, bool ENT, bool GRAD>
+__global__ void __launch_bounds__(NT, MINB) logprob_kernel(const Args a) {
+  constexpr int W = NT / 32;
+  __shared__ float s_m[W], s_S[W], s_U[W];
   __shared__ float4 s_part;
   __shared__ Targets s_y;
   __shared__ TopShared s_top;
+  __shared__ uint32_t s_best[kParts<NT> * NT];
   const unsigned rank = cluster_ctarank();
   unsigned nc;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(nc));
@@ -436,83 +581,107 @@ __global__ void __launch_bounds__(NT) logprob_kernel(const Args a) {
   pdl_wait();
   const T* x = static_cast<const T*>(a.x) + t * a.ld;
   const Row<T> row(x, a.V);
-  if (static_cast<int>(threadIdx.x) < a.m) {
-    const int y = target(a, t, threadIdx.x, rank == 0);
-    s_y.y[threadIdx.x] = y;
-    s_y.x[threadIdx.x] = y >= 0 ? value(x + y) : 0.f;
-    s_y.g[threadIdx.x] = GRAD && y >= 0 && a.dlogp != nullptr ? a.dlogp[t * a.m + threadIdx.x] : 0.f;
-  }
   // this block's whole words, and the partial ones that are its
   const int per = (row.nw + static_cast<int>(nc) - 1) / static_cast<int>(nc);
   const int w0 = min(row.nw, static_cast<int>(rank) * per), w1 = min(row.nw, w0 + per);
   const int first = max(w0, row.head ? 1 : 0), end = min(w1, row.nw - (row.tail ? 1 : 0));
   const int edge0 = row.head && w0 == 0 ? 0 : -1;
   const int edge1 = row.tail && w0 < row.nw && w1 == row.nw ? row.nw - 1 : -1;
+  for (int j = threadIdx.x; j < a.m; j += NT) {
+    const int y = target(a, t, j, rank == 0);
+    s_y.y[j] = y;
+    s_y.x[j] = y >= 0 ? value(x + y) : 0.f;
+    s_y.g[j] = GRAD && y >= 0 && a.dlogp != nullptr ? a.dlogp[t * a.m + j] : 0.f;
+  }
 
   Sums<ENT> sums;
-  float best = -INFINITY;
-  int best_word = 0;
-  for (int i0 = first + static_cast<int>(threadIdx.x); i0 < end; i0 += NT * U) {
-    uint4 q[U];
+  // words from i0 up to `to`, NT apart
+  auto add_words = [&](int i0, int to) {
+    for (; i0 + (U - 1) * NT < to; i0 += NT * U) {
+      uint4 q[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i0 + u * NT < end) q[u] = row.word(i0 + u * NT);
+      for (int u = 0; u < U; ++u) q[u] = row.word(i0 + u * NT);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (i0 + u * NT >= end) break;
-      const float big = sums.template add<T>(q[u], a.c);
-      if (TOP && big > best) best = big, best_word = i0 + u * NT;
+      for (int u = 0; u < U; ++u) sums.template add<T>(q[u], a.c, a.floor);
     }
+    if (i0 < to) {
+      uint4 q[U - 1];
+#pragma unroll
+      for (int u = 0; u < U - 1; ++u)
+        if (i0 + u * NT < to) q[u] = row.word(i0 + u * NT);
+#pragma unroll
+      for (int u = 0; u < U - 1; ++u)
+        if (i0 + u * NT < to) sums.template add<T>(q[u], a.c, a.floor);
+    }
+  };
+  // words of a part: whole groups of loads, so that the parts cost the loop nothing
+  const int step = (max(end - first, 0) + kParts<NT> * NT * U - 1) / (kParts<NT> * NT * U) * (NT * U);
+  if (TOP) {
+    float all = -INFINITY;
+#pragma unroll 1
+    for (int i = 0; i < kParts<NT>; ++i) {
+      sums.mx = -INFINITY;
+      add_words(first + i * step + static_cast<int>(threadIdx.x), min(end, first + (i + 1) * step));
+      s_best[i * NT + threadIdx.x] = sums.mx > -INFINITY ? ordered(sums.mx) : 0u;
+      all = fmaxf(all, sums.mx);
+    }
+    sums.mx = all;
+  } else {
+    add_words(first + static_cast<int>(threadIdx.x), end);
   }
   if (threadIdx.x < 2) {
     const int i = threadIdx.x == 0 ? edge0 : edge1;
-    if (i >= 0) sums.template add<T>(row.partial(i), a.c);
+    if (i >= 0) sums.template add<T>(row.partial(i), a.c, a.floor);
   }
 
-  // over the block
+  // sums of the threads' S and U over the block, in every thread
+  auto block_sums = [&](float& S, float& Us) {
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) {
+      S += __shfl_xor_sync(0xffffffffu, S, i);
+      if (ENT) Us += __shfl_xor_sync(0xffffffffu, Us, i);
+    }
+    if (W == 1) return;
+    if (lane == 0) s_S[warp] = S, s_U[warp] = Us;
+    __syncthreads();
+    S = Us = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) S += s_S[i], Us += ENT ? s_U[i] : 0.f;
+  };
   float M = sums.mx;
 #pragma unroll
   for (int i = 16; i > 0; i >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
   if (lane == 0) s_m[warp] = M;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < NT / 32; ++i) M = fmaxf(M, s_m[i]);
-  M = fmaxf(M, -FLT_MAX);  // nothing but -inf: S stays 0
+  for (int i = 0; i < W; ++i) M = fmaxf(M, s_m[i]);
   float S = sum2(sums.S), Us = ENT ? sum2(sums.U) : 0.f;
-  relate(sums.m, M, a.c, S, Us);
-#pragma unroll
-  for (int i = 16; i > 0; i >>= 1) {
-    S += __shfl_xor_sync(0xffffffffu, S, i);
-    if (ENT) Us += __shfl_xor_sync(0xffffffffu, Us, i);
-  }
-  if (lane == 0) s_S[warp] = S, s_U[warp] = Us;
-  __syncthreads();
-  S = Us = 0.f;
-#pragma unroll
-  for (int i = 0; i < NT / 32; ++i) S += s_S[i], Us += s_U[i];
-  if (TOP) block_top<T, NT>(s_top, row, first, end, edge0, edge1, best, best_word, a.top);
+  const float block_at = M > -INFINITY ? M * a.c : kUnset;
+  relate(sums.at, block_at, S, Us);
+  block_sums(S, Us);
+  if (TOP) block_top<T, NT>(s_top, s_best, row, first, end, step, edge0, edge1, a.top);
 
   // over the cluster
   if (nc > 1) {
-    if (threadIdx.x == 0) s_part = make_float4(M, S, Us, 0.f);
+    if (threadIdx.x == 0) s_part = make_float4(M, S, Us, block_at);
     cluster_sync();
-    float pm[kMaxCluster], ps[kMaxCluster], pu[kMaxCluster];
-    const float own = M;
+    float pm[kMaxCluster], ps[kMaxCluster], pu[kMaxCluster], pa[kMaxCluster];
 #pragma unroll
     for (unsigned r = 0; r < kMaxCluster; ++r) {
-      pm[r] = own, ps[r] = pu[r] = 0.f;
+      pm[r] = -INFINITY, ps[r] = pu[r] = 0.f, pa[r] = kUnset;
       if (r < nc) {
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, _}, [%3];"
-                     : "=f"(pm[r]), "=f"(ps[r]), "=f"(pu[r])
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(pm[r]), "=f"(ps[r]), "=f"(pu[r]), "=f"(pa[r])
                      : "r"(mapa_shared(smem_u32(&s_part), r))
                      : "memory");
       }
       M = fmaxf(M, pm[r]);
     }
     S = Us = 0.f;
+    const float at = M > -INFINITY ? M * a.c : kUnset;
 #pragma unroll
     for (unsigned r = 0; r < kMaxCluster; ++r) {
-      relate(pm[r], M, a.c, ps[r], pu[r]);
+      relate(pa[r], at, ps[r], pu[r]);
       S += ps[r];
       Us += pu[r];
     }
@@ -528,31 +697,55 @@ __global__ void __launch_bounds__(NT) logprob_kernel(const Args a) {
         s_top.cand[i] = key;
       }
       __syncthreads();  // s_top.out of this block was read above, before it is written
-      // empty places (0) of several blocks are equal: they rank past every token
-      const uint64_t key = static_cast<int>(threadIdx.x) < total ? s_top.cand[threadIdx.x] : 0;
-      static_assert(kMaxCluster * kMaxTop <= 256, "a thread for each key, or two");
       for (int i = threadIdx.x; i < a.top; i += NT) s_top.out[i] = 0;
       __syncthreads();
+      // empty places (0) of several blocks are equal: they are left out
       for (int i = threadIdx.x; i < total; i += NT) {
-        const uint64_t k = i == static_cast<int>(threadIdx.x) ? key : s_top.cand[i];
+        const uint64_t key = s_top.cand[i];
         int place = 0;
-        for (int j = 0; j < total; ++j) place += s_top.cand[j] > k;
-        if (k != 0 && place < a.top) s_top.out[place] = k;
+        for (int j = 0; j < total; ++j) place += s_top.cand[j] > key;
+        if (key != 0 && place < a.top) s_top.out[place] = key;
       }
       __syncthreads();
     }
   }
+  const Shift shift(M > -INFINITY ? M : 0.f, a.c);
+  if (shift.extreme) {  // the same for the whole cluster
+    S = Us = 0.f;
+    for (int i = first + static_cast<int>(threadIdx.x); i < end; i += NT) add_extreme<T>(row.word(i), shift, S, Us);
+    if (threadIdx.x < 2) {
+      const int i = threadIdx.x == 0 ? edge0 : edge1;
+      if (i >= 0) add_extreme<T>(row.partial(i), shift, S, Us);
+    }
+    __syncthreads();  // s_S was read above
+    block_sums(S, Us);
+    if (nc > 1) {
+      cluster_sync();  // s_part was read by every block
+      if (threadIdx.x == 0) s_part = make_float4(M, S, Us, 0.f);
+      cluster_sync();
+      S = Us = 0.f;
+      for (unsigned r = 0; r < nc; ++r) {
+        float4 p;
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(p.x), "=f"(p.y), "=f"(p.z), "=f"(p.w)
+                     : "r"(mapa_shared(smem_u32(&s_part), r))
+                     : "memory");
+        S += p.y;
+        Us += p.z;
+      }
+    }
+  }
 
+  if (nc > 1) cluster_arrive();  // has read the others' shared memory
   const bool empty = S == 0.f;
   const float log_S = logf(S);
   if (rank == 0) {
-    if (static_cast<int>(threadIdx.x) < a.m)
-      a.logp[t * a.m + threadIdx.x] =
-          s_y.y[threadIdx.x] < 0 ? 0.f : empty ? -INFINITY : (s_y.x[threadIdx.x] - M) * a.inv_temp - log_S;
+    for (int j = threadIdx.x; j < a.m; j += NT)
+      a.logp[t * a.m + j] = s_y.y[j] < 0 ? 0.f : empty ? -INFINITY : fmaf(kLn2, shift.t(s_y.x[j]), -log_S);
     if (threadIdx.x == 0) {
-      a.stats[2 * t] = M;
+      a.stats[2 * t] = shift.M;
       a.stats[2 * t + 1] = S;
-      if (a.lse != nullptr) a.lse[t] = empty ? -INFINITY : fmaf(M, a.inv_temp, log_S);
+      if (a.lse != nullptr) a.lse[t] = empty ? -INFINITY : fmaf(shift.M, a.inv_temp, log_S);
       if (ENT && a.entropy != nullptr) a.entropy[t] = empty ? 0.f : log_S - kLn2 * Us / S;
     }
     if (TOP && static_cast<int>(threadIdx.x) < a.top) {
@@ -560,7 +753,7 @@ __global__ void __launch_bounds__(NT) logprob_kernel(const Args a) {
       const int64_t at = t * a.top + threadIdx.x;
       if (a.top_ids != nullptr) a.top_ids[at] = key != 0 ? static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key)) : -1;
       if (a.top_logp != nullptr)
-        a.top_logp[at] = key != 0 ? (from_ordered(static_cast<uint32_t>(key >> 32)) - M) * a.inv_temp - log_S : -INFINITY;
+        a.top_logp[at] = key != 0 ? fmaf(kLn2, shift.t(from_ordered(static_cast<uint32_t>(key >> 32))), -log_S) : -INFINITY;
     }
   }
   if (GRAD) {
@@ -574,119 +767,129 @@ __global__ void __launch_bounds__(NT) logprob_kernel(const Args a) {
     const bool zero = empty || !(some || dent != 0.f || dlse != 0.f);
     const Coefs k = coefs(sum_g, dent, dlse, S, ENT ? kLn2 * Us / S : 0.f, a.inv_temp);
     T* drow = static_cast<T*>(a.dx) + t * a.dld;
-    gradient_words<T, NT, U, ENT>(row, drow, first, end, edge0, edge1, a.same != 0, zero, M, a.c, k.A, k.B);
+    gradient_words<T, NT, U, ENT>(row, drow, threadIdx.x, first, end, edge0, edge1, a.same != 0, zero, shift,
+                                  a.floor, k.A, k.B, [&](int i) { return row.word(i); });
     __syncthreads();
-    if (!zero && static_cast<int>(threadIdx.x) < a.m && s_y.y[threadIdx.x] >= 0) {
-      const int w = (s_y.y[threadIdx.x] + row.h) / Row<T>::E;
-      if (w >= w0 && w < w1) put_target<T>(s_y, threadIdx.x, a.m, drow, M, a.c, k.A, k.B, a.inv_temp);
-    }
+    if (!zero)
+      for (int j = threadIdx.x; j < a.m; j += NT) {
+        const int y = s_y.y[j], w = (y + row.h) / Row<T>::E;
+        if (y >= 0 && w >= w0 && w < w1) put_target(s_y, j, a.m, drow, shift, k.A, k.B, a.inv_temp);
+      }
   }
-  if (nc > 1) cluster_sync();  // no block leaves while its shared memory is read
+  if (nc > 1) cluster_wait();  // no block leaves while its shared memory is read
 }
 
-// The gradient alone: units of kBwdThreads * kBwdWords words of a row.
-constexpr int kBwdThreads = 256, kBwdWords = 4, kBwdUnit = kBwdThreads * kBwdWords;
+// The gradient alone: a warp takes a unit of kBwdWords * `turns` words a lane.
+constexpr int kBwdThreads = 256, kBwdWarps = kBwdThreads / 32, kBwdWords = 4;
 template <typename T, bool ENT>
-__global__ void __launch_bounds__(kBwdThreads) logprob_bwd_kernel(const Args a, int chunks, int64_t units) {
-  __shared__ Targets s_y;
+__global__ void __launch_bounds__(kBwdThreads, 5) logprob_bwd_kernel(const Args a, int turns, int chunks,
+                                                                    int64_t units) {
+  __shared__ Targets s_targets[kBwdWarps];
   const int lane = threadIdx.x & 31;
+  Targets& s_y = s_targets[threadIdx.x >> 5];
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kBwdWarps;
   pdl_wait();
-  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int64_t t = unit / chunks;
+  for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kBwdWarps + (threadIdx.x >> 5); unit < units;
+       unit += warps) {
+    const int64_t t = (unit >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(unit) / static_cast<uint32_t>(chunks))
+                                        : unit / chunks;
     const int chunk = static_cast<int>(unit - t * chunks);
     const T* x = static_cast<const T*>(a.x) + t * a.ld;
     const Row<T> row(x, a.V);
-    const int w0 = chunk * kBwdUnit, w1 = min(row.nw, w0 + kBwdUnit);
+    const int w0 = chunk * 32 * kBwdWords * turns, w1 = min(row.nw, w0 + 32 * kBwdWords * turns);
     if (w0 >= w1) continue;
     const int first = max(w0, row.head ? 1 : 0), end = min(w1, row.nw - (row.tail ? 1 : 0));
     const int edge0 = row.head && w0 == 0 ? 0 : -1, edge1 = row.tail && w1 == row.nw ? row.nw - 1 : -1;
-    float sum_g = 0.f;
-    bool some = false, here = false;
-    for (int j0 = 0; j0 < a.m; j0 += 32) {
-      int y = -1;
-      float g = 0.f;
-      if (j0 + lane < a.m) {
-        y = target(a, t, j0 + lane, false);
-        if (y >= 0 && a.dlogp != nullptr) g = a.dlogp[t * a.m + j0 + lane];
-      }
-      some |= __any_sync(0xffffffffu, g != 0.f);
-      const int w = (y + row.h) / Row<T>::E;
-      here |= __any_sync(0xffffffffu, y >= 0 && w >= w0 && w < w1);
-#pragma unroll
-      for (int i = 16; i > 0; i >>= 1) g += __shfl_xor_sync(0xffffffffu, g, i);
-      sum_g += g;
-    }
     const float M = a.stats_in[2 * t], S = a.stats_in[2 * t + 1];
     const float dent = ENT ? a.dent[t] : 0.f, dlse = a.dlse != nullptr ? a.dlse[t] : 0.f;
-    const bool zero = S == 0.f || !(some || dent != 0.f || dlse != 0.f);
-    const Coefs k = coefs(sum_g, dent, dlse, S, ENT ? logf(S) - a.entropy_in[t] : 0.f, a.inv_temp);
-    here &= !zero;  // the same for every warp
-    int mine = -1;
-    if (here) {
-      // targets' logits are read before any word of theirs is overwritten
-      if (static_cast<int>(threadIdx.x) < a.m) {
-        const int y = target(a, t, threadIdx.x, false);
-        s_y.y[threadIdx.x] = y;
-        s_y.g[threadIdx.x] = y >= 0 && a.dlogp != nullptr ? a.dlogp[t * a.m + threadIdx.x] : 0.f;
-        const int w = (y + row.h) / Row<T>::E;
-        if (y >= 0 && w >= w0 && w < w1) mine = y;
-        s_y.x[threadIdx.x] = mine >= 0 ? value(x + y) : 0.f;
+    const float less = ENT ? logf(S) - a.entropy_in[t] : 0.f;
+    auto mine = [&](int y) {
+      const int w = (y + row.h) / Row<T>::E;
+      return y >= 0 && w >= w0 && w < w1;
+    };
+    float sum_g = 0.f;
+    bool some = false, here = false;  // a gradient that is not zero; a target in this unit
+    for (int j = lane; j < (a.m + 31 & ~31); j += 32) {
+      const int y = j < a.m ? target(a, t, j, false) : -1;
+      float g = y >= 0 && a.dlogp != nullptr ? a.dlogp[t * a.m + j] : 0.f;
+      some |= __any_sync(0xffffffffu, g != 0.f);
+      here |= __any_sync(0xffffffffu, mine(y));
+      if (a.m > 1) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) g += __shfl_xor_sync(0xffffffffu, g, o);
       }
-      __syncthreads();
+      sum_g += __shfl_sync(0xffffffffu, g, 0);
+    }
+    const bool zero = S == 0.f || !(some || dent != 0.f || dlse != 0.f);
+    const Coefs k = coefs(sum_g, dent, dlse, S, less, a.inv_temp);
+    const Shift shift(M, a.c);
+    here &= !zero;
+    if (here) {
+      // logits of targets are read before their words are overwritten (dlogits may be logits)
+      __syncwarp();
+      for (int j = lane; j < a.m; j += 32) {
+        const int y = target(a, t, j, false);
+        s_y.y[j] = mine(y) ? y : -1;
+        s_y.g[j] = y >= 0 && a.dlogp != nullptr ? a.dlogp[t * a.m + j] : 0.f;
+        s_y.x[j] = mine(y) ? value(x + y) : 0.f;
+      }
+      __syncwarp();
     }
     T* drow = static_cast<T*>(a.dx) + t * a.dld;
-    gradient_words<T, kBwdThreads, kBwdWords, ENT>(row, drow, first, end, edge0, edge1, a.same != 0, zero, M,
-                                                   a.c, k.A, k.B);
+    gradient_words<T, 32, kBwdWords, ENT>(row, drow, lane, first, end, edge0, edge1, a.same != 0, zero, shift,
+                                          a.floor, k.A, k.B, [&](int i) { return row.word(i); });
     if (here) {
-      __syncthreads();
-      if (mine >= 0) put_target<T>(s_y, threadIdx.x, a.m, drow, M, a.c, k.A, k.B, a.inv_temp);
-      __syncthreads();  // before s_y is written again
+      __syncwarp();
+      for (int j = lane; j < a.m; j += 32)
+        if (s_y.y[j] >= 0) put_target(s_y, j, a.m, drow, shift, k.A, k.B, a.inv_temp);
     }
   }
 }
 
 // ---- launches -----------------------------------------------------------------------------
-// Threads of a block: 128 for rows of up to 2048 words, else 512.  Blocks of a row:
-// one where there are two rows for each SM, more where there are fewer; always eight
-// for the step, so that the rows in flight (about 80) stay in the L2 until their
-// second reading.
-constexpr int kShortWords = 2048;
+// Threads of a block: about 8 words each, 256 where a row is longer.  Blocks of a row:
+// one where that gives four for each SM, more, up to eight, where there are fewer rows.
+// With the gradient also as many as it takes for the rows in flight, five blocks to an
+// SM, to stay in the L2 until their second reading.
+constexpr int kLane = 256, kSmall = 2048;       // words of a block up to which it has 32, 128 threads
+constexpr int64_t kInFlight = int64_t(80) << 20;
 
-template <typename T, int NT, bool TOP, bool ENT, bool GRAD>
-cudaError_t row_kernel(const Args& a, unsigned cluster, cudaStream_t s) {
-  return launch_pdl_cluster(logprob_kernel<T, NT, 4, TOP, ENT, GRAD>,
-                            dim3(static_cast<unsigned>(a.T) * cluster), dim3(NT), 0, s, cluster, a);
-}
-template <typename T, int NT>
-cudaError_t rows(const Args& a, bool grad, unsigned cluster, cudaStream_t s) {
-  const bool ent = a.entropy != nullptr || a.dent != nullptr, top = a.top > 0;
-  if (grad)
-    return top ? (ent ? row_kernel<T, NT, true, true, true>(a, cluster, s)
-                      : row_kernel<T, NT, true, false, true>(a, cluster, s))
-               : (ent ? row_kernel<T, NT, false, true, true>(a, cluster, s)
-                      : row_kernel<T, NT, false, false, true>(a, cluster, s));
-  return top ? (ent ? row_kernel<T, NT, true, true, false>(a, cluster, s)
-                    : row_kernel<T, NT, true, false, false>(a, cluster, s))
-             : (ent ? row_kernel<T, NT, false, true, false>(a, cluster, s)
-                    : row_kernel<T, NT, false, false, false>(a, cluster, s));
+template <typename T, int NT, int MINB, bool GRAD>
+cudaError_t rows(const Args& a, unsigned cluster, cudaStream_t s) {
+  const bool ent = a.entropy != nullptr || a.dent != nullptr;
+  auto kernel = a.top > 0 ? (ent ? logprob_kernel<T, NT, MINB, 4, true, true, GRAD>
+                                 : logprob_kernel<T, NT, MINB, 4, true, false, GRAD>)
+                          : (ent ? logprob_kernel<T, NT, MINB, 4, false, true, GRAD>
+                                 : logprob_kernel<T, NT, MINB, 4, false, false, GRAD>);
+  return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(a.T) * cluster), dim3(NT), 0, s, cluster, a);
 }
 template <typename T>
-cudaError_t launch_rows(const Args& a, bool grad, cudaStream_t s) {
-  const int words = static_cast<int>((static_cast<int64_t>(a.V) * sizeof(T) + 15) / 16);
-  if (words <= kShortWords) return rows<T, 128>(a, grad, 1, s);
-  unsigned cluster = kMaxCluster;
-  if (!grad)
-    while (cluster > 1 && static_cast<int64_t>(a.T) * cluster >= 4 * kSMs) cluster /= 2;
-  return rows<T, 512>(a, grad, cluster, s);
+int64_t row_words(const Args& a) {  // a row's most
+  return (static_cast<int64_t>(a.V) + 2 * Row<T>::E - 2) / Row<T>::E;
+}
+template <typename T, bool GRAD>
+cudaError_t launch_rows(const Args& a, cudaStream_t s) {
+  const int64_t words = row_words<T>(a);
+  unsigned cluster = 1;
+  while (cluster < kMaxCluster &&
+         ((static_cast<int64_t>(a.T) * cluster < 4 * kSMs && words > kSmall / 2 * static_cast<int64_t>(cluster)) ||
+          (GRAD && words > kSmall && words * 16 * (5 * kSMs / cluster) > kInFlight)))
+    cluster *= 2;
+  const int64_t each = (words + cluster - 1) / cluster;
+  return each <= kLane    ? rows<T, 32, 20, GRAD>(a, cluster, s)
+         : each <= kSmall ? rows<T, 128, 8, GRAD>(a, cluster, s)
+         : a.top > 0     ? rows<T, 256, 4, GRAD>(a, cluster, s)
+                          : rows<T, 256, 5, GRAD>(a, cluster, s);
 }
 template <typename T>
 cudaError_t launch_bwd(const Args& a, cudaStream_t s) {
-  constexpr int E = Row<T>::E;
-  const int64_t words = (static_cast<int64_t>(a.V) + 2 * E - 2) / E;
-  const int64_t chunks = (words + kBwdUnit - 1) / kBwdUnit, units = chunks * a.T;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, 0x7FFFFFFF));
+  const int64_t words = row_words<T>(a);
+  const int turns = words >= 4096 ? 4 : 1;
+  const int64_t unit = 32 * kBwdWords * turns, chunks = (words + unit - 1) / unit, units = chunks * a.T;
+  const int64_t blocks = (units + kBwdWarps - 1) / kBwdWarps;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(blocks, 0x7FFFFFFF));
   return launch_pdl(a.dent != nullptr ? logprob_bwd_kernel<T, true> : logprob_bwd_kernel<T, false>, dim3(grid),
-                    dim3(kBwdThreads), 0, s, a, static_cast<int>(chunks), units);
+                    dim3(kBwdThreads), 0, s, a, turns, static_cast<int>(chunks), units);
 }
 
 int bad(const char* msg) { return record_error(MOE_ERR_INVALID_ARG, msg); }
@@ -701,7 +904,7 @@ int check_desc(const moe_logprob_desc* q, bool grad) {
   if (q->m < 1 || q->m > kMaxTargets) return bad("m must be in 1 .. MOE_LOGPROB_MAX_TARGETS");
   if (q->top < 0 || q->top > kMaxTop) return bad("top must be in 0 .. MOE_LOGPROB_MAX_TOP");
   if (q->T > 1 && (q->ld < q->V || (grad && q->dld < q->V))) return bad("a row stride is below V");
-  if (!(q->inv_temp > 0.f) || !std::isfinite(q->inv_temp)) return bad("inv_temp must be positive");
+  if (!(q->inv_temp >= 1e-30f && q->inv_temp <= 1e30f)) return bad("inv_temp must be in 1e-30 .. 1e30");
   if (static_cast<int64_t>(q->T) * kMaxCluster > 0x7FFFFFFF) return record_error(MOE_ERR_UNSUPPORTED, "T is too large");
   return MOE_OK;
 }
@@ -716,6 +919,9 @@ int fill(const moe_logprob_desc* q, const void* logits, const void* targets, Arg
   a.t64 = q->target_type == MOE_I64; a.ignore = q->ignore_id;
   a.inv_temp = q->inv_temp;
   a.c = static_cast<float>(static_cast<double>(q->inv_temp) * 1.4426950408889634074);
+  const float low = std::fmax(kFloor / a.c, -3e38f);
+  std::memcpy(&a.floor, &low, 4);
+  if (q->type == MOE_BF16) a.floor = (a.floor >> 16) | (a.floor & 0xFFFF0000u);
   return MOE_OK;
 }
 int fill_grad(const moe_logprob_desc* q, const float* dlogp, const float* dent, const float* dlse,
@@ -760,8 +966,8 @@ int moe_logprob_fwd(const moe_logprob_desc* desc, const void* logits, const void
   if ((rc = fill(desc, logits, targets, a)) || (rc = fill_out(desc, logp, stats, lse, entropy, top_ids, top_logp, a)) || (rc = device_status_word(&a.status)))
     return rc;
   ProbeScope probe("logprob_fwd", stream);
-  const cudaError_t e = desc->type == MOE_BF16 ? launch_rows<bf16_t>(a, false, stream)
-                                               : launch_rows<float>(a, false, stream);
+  const cudaError_t e = desc->type == MOE_BF16 ? launch_rows<bf16_t, false>(a, stream)
+                                               : launch_rows<float, false>(a, stream);
   if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
   return record_error(MOE_OK, "");
 }
@@ -797,8 +1003,8 @@ int moe_logprob_step(const moe_logprob_desc* desc, const void* logits, const voi
       (rc = fill_out(desc, logp, stats, lse, entropy, top_ids, top_logp, a)) || (rc = device_status_word(&a.status)))
     return rc;
   ProbeScope probe("logprob_step", stream);
-  const cudaError_t e = desc->type == MOE_BF16 ? launch_rows<bf16_t>(a, true, stream)
-                                               : launch_rows<float>(a, true, stream);
+  const cudaError_t e = desc->type == MOE_BF16 ? launch_rows<bf16_t, true>(a, stream)
+                                               : launch_rows<float, true>(a, stream);
   if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
   return record_error(MOE_OK, "");
 }

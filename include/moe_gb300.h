@@ -525,7 +525,7 @@ typedef struct moe_logprob_desc {
   int32_t target_type;   /* MOE_I32 or MOE_I64 */
   int64_t ld, dld;       /* elements from one row of logits (dlogits) to the next, >= V */
   int64_t ignore_id;     /* a target that asks for nothing */
-  float inv_temp;        /* > 0: z = inv_temp * logits */
+  float inv_temp;        /* 1e-30 .. 1e30: z = inv_temp * logits */
 } moe_logprob_desc;
 
 /* Log probabilities of given tokens, entropy and likeliest tokens of each row:
@@ -561,9 +561,10 @@ MOE_API int moe_logprob_bwd(const moe_logprob_desc* desc, const void* logits, co
                             moe_stream_t stream);
 
 /* Forward and backward in one call, for losses whose weights are known ahead
- * (dlogp = -1 / tokens, say): same arguments and results as the two in turn
- * (entropy may be NULL here even with dentropy), but each row is read from
- * memory once and its gradient written while the row is still in the L2. */
+ * (dlogp = -1 / tokens, say): same arguments and results as the two in turn, but
+ * for the order in which a row's sums are taken (entropy may be NULL here even with
+ * dentropy); each row is read from memory once and held on the chip until its
+ * gradient is written. */
 MOE_API int moe_logprob_step(const moe_logprob_desc* desc, const void* logits, const void* targets,
                              const float* dlogp, const float* dentropy, const float* dlse,
                              float* logp, float* stats, float* lse, float* entropy,

@@ -148,15 +148,11 @@ def test_values_and_gradient(T, V, dtype, m, top, off, pad):
     c.check_fwd(r)
     c.bwd()
     c.check_bwd(r)
-    first = [t.clone() for t in (c.logp, c.stats, c.lse, c.entropy)]
     c.clear()
     c.dwhole.fill_(11)
     c.step()
     c.check_fwd(r)
     c.check_bwd(r)
-    if T >= 8 * 4 * 152 // 8 or V < 4096:   # as many blocks to a row: the same sums
-        for a, b in zip(first, (c.logp, c.stats, c.lse, c.entropy)):
-            assert torch.equal(a, b) or V >= 16384
     assert L.moe_status() == L.MOE_OK
 
 
@@ -374,9 +370,13 @@ def test_offsets_past_2_to_31_values():
     dlogp[-2:], dh[-2:], dl[-2:] = c.dlogp, c.dh, c.dl
     dlogp[0] = 1
     ids, lp, ent = torch.empty(T, 3, dtype=torch.int32, device=DEV), torch.empty(T, 3, device=DEV), torch.empty(T, device=DEV)
-    L.moe_logprob_step(x, y, big["logp"], big["stats"], dlogp, x, dentropy=dh, dlse=dl, entropy=ent, top_ids=ids,
-                       top_logp=lp)
-    assert torch.equal(x[-2:], c.dlogits) and torch.equal(big["logp"][-2:], c.logp)
+    lse = torch.empty(T, device=DEV)
+    L.moe_logprob_step(x, y, big["logp"], big["stats"], dlogp, x, dentropy=dh, dlse=dl, lse=lse, entropy=ent,
+                       top_ids=ids, top_logp=lp)
+    for to, got in ((c.logp, big["logp"]), (c.lse, lse), (c.entropy, ent), (c.top_ids, ids), (c.top_logp, lp)):
+        to.copy_(got[-2:])
+    c.check_fwd()
+    c.check_bwd(got=x[-2:])
     assert torch.equal(ids[-2:], c.top_ids) and (ids[:-2] == torch.arange(3, device=DEV)).all()
     assert x[0, 0] > 0.9 and not x[1:-2].any()
 
