@@ -4,7 +4,9 @@
 // Forward: a copy of rows, bound by memory.
 //
 // Gradient.  The tokens are sorted by id: a stable radix sort, least digit first,
-// of up to 9 bits a pass, so two passes for a table of up to 2^18 rows.  Sorted
+// of up to 9 bits a pass, so two passes for a table of up to 2^18 rows; up to
+// 65536 tokens in one launch of one cluster, which keeps them in its shared
+// memory between passes, while a second kernel writes the zeros.  Sorted
 // tokens are cut into chunks of equal length, and a group of threads walks one
 // chunk with 8 columns a thread: it adds up rows while the id stays the same and
 // writes a run that lies in its chunk straight to the table.  A run that reaches
@@ -12,7 +14,9 @@
 // a second kernel adds them in order.  So the work is even whatever the ids'
 // frequencies, nothing is atomic, and the order of every sum depends on the ids
 // alone.  What bounds it: T d reads of gradient rows and, dense, V d writes of
-// which most are zeros.
+// which most are zeros.  4096 x 2048 into 151936 rows, dense: 214 us (floor 186, the
+// zeros alone 186; the sort runs beside them), 32768 x 2048: 255.  Added to a table
+// instead, 4096 x 2048: 39 us, three launches that wait for one another.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -25,36 +29,60 @@
 namespace moe {
 namespace {
 
-// ---- forward -----------------------------------------------------------------
-// A warp moves up to 512 columns of a row, two shares of 8 a lane.
-constexpr int kFwdThreads = 256, kFwdShares = 64;
+// Lets the next kernel of the stream start while this one runs.
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-template <typename T, typename O, bool VEC>
+// ---- forward -----------------------------------------------------------------
+// A warp moves up to 256 SH columns of a row, SH shares of 8 a lane: four where that
+// leaves every SM its 64 warps, else two.
+constexpr int kFwdThreads = 256, kFwdWarps = kFwdThreads / 32;
+
+__device__ __forceinline__ void put_share(bf16_t* row, int v, const f2 (&f)[4], bool) {
+  Raw8<bf16_t> r;
+  narrow(f, r);
+  *(reinterpret_cast<uint4*>(row) + v) = r.v;
+}
+// wide: rows are 32-byte aligned, and a share is one access (see store8_wide).
+__device__ __forceinline__ void put_share(float* row, int v, const f2 (&f)[4], bool wide) {
+  Raw8<float> r;
+  narrow(f, r);
+  if (wide) {
+    store8_wide(row + 8 * v, r);
+  } else {
+    *(reinterpret_cast<float4*>(row) + 2 * v) = r.a;
+    *(reinterpret_cast<float4*>(row) + 2 * v + 1) = r.b;
+  }
+}
+
+template <typename T, typename O, bool VEC, int SH>
 __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const void* __restrict__ ids, int id64,
                                                                const T* __restrict__ table, int64_t T_, int V,
-                                                               int d, float scale, O* __restrict__ out,
+                                                               int d, float scale, O* __restrict__ out, bool wide,
                                                                int* status) {
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int segs = (d + 8 * kFwdShares - 1) / (8 * kFwdShares);
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kFwdThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = unit / segs;
+  const unsigned segs = (d + 256 * SH - 1) / (256 * SH);
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kFwdWarps + (threadIdx.x >> 5);
+  const int64_t t = (unit >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(unit) / segs) : unit / segs;
   if (t >= T_) return;
-  const int v0 = static_cast<int>(unit - t * segs) * kFwdShares + lane;
+  const int v0 = static_cast<int>(unit - t * segs) * 32 * SH + lane;
   const int64_t id = id64 ? static_cast<const int64_t*>(ids)[t] : static_cast<const int32_t*>(ids)[t];
   const bool ok = id >= 0 && id < V;
   if (!ok && lane == 0) atomicCAS(status, 0, kErrBadIds);
   const T* from = table + (ok ? id : 0) * static_cast<int64_t>(d);
   O* to = out + t * d;
-  f2 f[2][4];
+  Raw8<T> raw[SH];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) get8<T, VEC>(from, v0 + 32 * i, d, f[i]);
+  for (int i = 0; i < SH; ++i) load8<VEC>(from, v0 + 32 * i, d, raw[i]);
   const f2 s = pk(scale);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < SH; ++i) {
+    f2 f[4];
+    widen(raw[i], f);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) f[i][e] = ok ? mul2(f[i][e], s) : pk(0.f);
-    put8<O, VEC>(to, v0 + 32 * i, d, f[i]);
+    for (int e = 0; e < 4; ++e) f[e] = ok ? mul2(f[e], s) : pk(0.f);
+    if (!VEC) put8<O, VEC>(to, v0 + 32 * i, d, f);
+    else if (8 * (v0 + 32 * i) < d) put_share(to, v0 + 32 * i, f, wide);
   }
 }
 
@@ -92,6 +120,21 @@ struct Source {
 };
 __device__ __forceinline__ uint32_t source_key(const Source& s, int64_t i, int* status) {
   return s.ids != nullptr ? key_of(s.ids, s.id64, i, s.V, s.pad, status) : s.keys[i];
+}
+
+// The lanes of `live` with this lane's digit, by a vote on each of its bits (matching the
+// digits by one instruction takes longer where most of them differ: the sort of 65536
+// tokens 33 us against 29).
+__device__ __forceinline__ unsigned lanes_with(uint32_t digit, int bits, unsigned live) {
+  unsigned same = live;
+#pragma unroll
+  for (int b = 0; b < kMaxDigit; ++b) {
+    if (b >= bits) break;
+    const bool one = (digit >> b) & 1u;
+    const unsigned vote = __ballot_sync(0xffffffffu, one);
+    same &= one ? vote : ~vote;
+  }
+  return same;
 }
 
 // counts[bin][chunk] of this pass's digit.
@@ -160,12 +203,12 @@ __global__ void __launch_bounds__(kScanThreads) sort_scan_kernel(uint32_t* __res
 // Tokens to their places.  Each warp takes a run of its block's tokens; lanes with the
 // same digit find each other, so that a token's rank in its bin is what the warps
 // before, the rounds before and the lanes before hold.
-__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const Source src, int64_t n, int shift, int bins,
+__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const Source src, int64_t n, int shift, int bits,
                                                                  int chunks, const uint32_t* __restrict__ starts,
                                                                  uint32_t* __restrict__ keys,
                                                                  uint32_t* __restrict__ tokens) {
   __shared__ uint32_t s_count[kSortWarps][kMaxBins];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = 1 << bits;
   for (int b = lane; b < bins; b += 32) s_count[warp][b] = 0;
   pdl_wait();
   __syncwarp();
@@ -178,7 +221,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const Source s
     const bool ok = base + 32 * r < n;
     const uint32_t digit = (key[r] >> shift) & (bins - 1);
     const unsigned live = __ballot_sync(0xffffffffu, ok);
-    const unsigned same = __match_any_sync(0xffffffffu, digit) & live;
+    const unsigned same = lanes_with(digit, bits, live);
     rank[r] = s_count[warp][digit] + __popc(same & ((1u << lane) - 1));
     __syncwarp();
     if (ok && (same >> lane) == 1u) s_count[warp][digit] += __popc(same);  // the last lane with it
@@ -205,9 +248,147 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const Source s
   }
 }
 
-// ---- sums --------------------------------------------------------------------
-__global__ void __launch_bounds__(256) embed_zero_kernel(uint8_t* __restrict__ p, int64_t bytes, int head) {
+// The whole sort by one cluster of up to 8 blocks, each with 1024 R tokens.  A pass ranks
+// the tokens as above, adds up the blocks' counts out of their shared memory, and puts
+// its tokens in order in shared memory first, so that neighbours then travel together to
+// their places in the blocks' shared memory, in the last pass to global memory.
+constexpr int kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32, kMaxCluster = 8, kMaxRounds = 8;
+constexpr int64_t kClusterMost = int64_t(kMaxCluster) * kClusterThreads * kMaxRounds;
+
+__device__ __forceinline__ uint32_t cluster_load(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_store(uint32_t a, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+constexpr size_t cluster_sort_smem(int R) {
+  return static_cast<size_t>(2 * R * kClusterThreads) * 8 + 2 * kMaxBins * 4 + kClusterWarps * kMaxBins * 2;
+}
+
+template <int R>
+__global__ void __launch_bounds__(kClusterThreads) sort_cluster_kernel(const Source src, int n, int passes, int bits,
+                                                                      uint32_t* __restrict__ keys,
+                                                                      uint32_t* __restrict__ tokens, int* status) {
+  constexpr int kLen = R * kClusterThreads;
+  extern __shared__ uint64_t s_sort[];
+  uint64_t* s_place = s_sort;          // [kLen] this block's places: key and token
+  uint64_t* s_local = s_place + kLen;  // [kLen] this block's tokens in the pass's order
+  uint32_t* s_total = reinterpret_cast<uint32_t*>(s_local + kLen);  // [bins] tokens of a bin in this block
+  uint32_t* s_delta = s_total + kMaxBins;  // [bins] from a token's place in s_local to its place in all
+  uint16_t* s_count = reinterpret_cast<uint16_t*>(s_delta + kMaxBins);  // [warps][bins]
+  __shared__ uint32_t s_all[kMaxBins / 32], s_own[kMaxBins / 32], s_first[kMaxBins];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = 1 << bits;
+  const int me = static_cast<int>(cluster_ctarank()), blocks = static_cast<int>(gridDim.x);
+  const int have = min(kLen, max(0, n - me * kLen));
+  const int first = warp * 32 * R + lane;  // of this thread's places in the block, 32 apart
+  uint16_t* mine = s_count + warp * bins;
   pdl_wait();
+  pdl_launch();
+  uint32_t key[R], token[R], rank[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    token[r] = me * kLen + first + 32 * r;
+    key[r] = first + 32 * r < have ? key_of(src.ids, src.id64, token[r], src.V, src.pad, status) : 0u;
+  }
+  for (int p = 0; p < passes; ++p) {
+    const int shift = p * bits;
+    if (p > 0) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint64_t q = s_place[first + 32 * r];
+        key[r] = static_cast<uint32_t>(q >> 32);
+        token[r] = static_cast<uint32_t>(q);
+      }
+    }
+    for (int b = lane; b < bins; b += 32) mine[b] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool ok = first + 32 * r < have;
+      const uint32_t digit = (key[r] >> shift) & (bins - 1);
+      const unsigned live = __ballot_sync(0xffffffffu, ok);
+      const unsigned same = lanes_with(digit, bits, live);
+      rank[r] = mine[digit] + __popc(same & ((1u << lane) - 1));
+      __syncwarp();
+      if (ok && (same >> lane) == 1u) mine[digit] = static_cast<uint16_t>(mine[digit] + __popc(same));
+      __syncwarp();
+    }
+    __syncthreads();
+    uint32_t own = 0;  // tokens of bin threadIdx.x in this block
+    if (static_cast<int>(threadIdx.x) < bins) {
+#pragma unroll 16
+      for (int w = 0; w < kClusterWarps; ++w) {
+        const uint32_t q = s_count[w * bins + threadIdx.x];
+        s_count[w * bins + threadIdx.x] = static_cast<uint16_t>(own);
+        own += q;
+      }
+      s_total[threadIdx.x] = own;
+    }
+    if (blocks > 1) cluster_sync();
+    uint32_t before = 0, all = own, all_incl = 0, own_incl = 0;
+    if (static_cast<int>(threadIdx.x) < kMaxBins) {  // whole warps
+      if (blocks > 1 && static_cast<int>(threadIdx.x) < bins) {
+        all = 0;
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q) {
+          const uint32_t v = q < blocks ? cluster_load(mapa_shared(smem_u32(s_total + threadIdx.x), q)) : 0u;
+          before += q < me ? v : 0u;
+          all += v;
+        }
+      }
+      all_incl = all;
+      own_incl = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, all_incl, o), v = __shfl_up_sync(0xffffffffu, own_incl, o);
+        if (lane >= o) all_incl += u, own_incl += v;
+      }
+      if (lane == 31) s_all[warp] = all_incl, s_own[warp] = own_incl;
+    }
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < bins) {
+      for (int w = 0; w < warp; ++w) all_incl += s_all[w], own_incl += s_own[w];
+      const uint32_t local = own_incl - own;  // first place of the bin in s_local
+      s_delta[threadIdx.x] = all_incl - all + before - local;
+      s_first[threadIdx.x] = local;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (first + 32 * r >= have) continue;
+      const uint32_t digit = (key[r] >> shift) & (bins - 1);
+      s_local[s_first[digit] + mine[digit] + rank[r]] = (static_cast<uint64_t>(key[r]) << 32) | token[r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = threadIdx.x + r * kClusterThreads;
+      if (i >= have) continue;
+      const uint64_t q = s_local[i];
+      const uint32_t at = i + s_delta[(static_cast<uint32_t>(q >> 32) >> shift) & (bins - 1)];
+      if (p == passes - 1) {
+        keys[at] = static_cast<uint32_t>(q >> 32);
+        tokens[at] = static_cast<uint32_t>(q);
+      } else if (blocks > 1) {
+        cluster_store(mapa_shared(smem_u32(s_place + at % kLen), at / kLen), q);
+      } else {
+        s_place[at] = q;
+      }
+    }
+    // every place is filled, and every block has read the counts
+    if (blocks > 1) cluster_sync();
+    else __syncthreads();
+  }
+}
+
+// ---- sums --------------------------------------------------------------------
+// `beside`: launched while the sort runs, whose results it does not touch; it waits for
+// the sort at its end, so that what waits for this kernel has waited for both.
+__global__ void __launch_bounds__(256) embed_zero_kernel(uint8_t* __restrict__ p, int64_t bytes, int head,
+                                                        bool beside) {
+  if (!beside) pdl_wait();
   // p + head is 16-byte aligned; bytes counts from p
   const int64_t words = (bytes - head) / 16;
   const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
@@ -219,6 +400,7 @@ __global__ void __launch_bounds__(256) embed_zero_kernel(uint8_t* __restrict__ p
     const int64_t rest = head + words * 16 + threadIdx.x;
     if (threadIdx.x < 16 && rest < bytes) p[rest] = 0;
   }
+  if (beside) pdl_wait();
 }
 
 struct SumArgs {
@@ -234,19 +416,105 @@ struct SumArgs {
   int add;
 };
 
-// Adds scale * f (or writes it) to row `key`, share v.
+// Columns 8 v .. 8 v + 7 of a row that begins anywhere: the two or three aligned words
+// that hold them, shifted into place.  Words that reach past the whole tensor
+// [begin, end) are read value by value; columns past d are 0.
+__device__ __forceinline__ uint4 word_within(uintptr_t w, uintptr_t begin, uintptr_t end, bf16_t) {
+  if (w >= begin && w + 16 <= end) return *reinterpret_cast<const uint4*>(w);
+  uint32_t q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uintptr_t p = w + 2 * e;
+    q[e] = p >= begin && p < end ? *reinterpret_cast<const uint16_t*>(p) : 0u;
+  }
+  return make_uint4(q[0] | q[1] << 16, q[2] | q[3] << 16, q[4] | q[5] << 16, q[6] | q[7] << 16);
+}
+__device__ __forceinline__ float4 word_within(uintptr_t w, uintptr_t begin, uintptr_t end, float) {
+  if (w >= begin && w + 16 <= end) return *reinterpret_cast<const float4*>(w);
+  float q[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uintptr_t p = w + 4 * e;
+    q[e] = p >= begin && p < end ? *reinterpret_cast<const float*>(p) : 0.f;
+  }
+  return make_float4(q[0], q[1], q[2], q[3]);
+}
+__device__ __forceinline__ void load8_any(const bf16_t* row, int v, int d, uintptr_t begin, uintptr_t end,
+                                          Raw8<bf16_t>& r) {
+  r.v = make_uint4(0u, 0u, 0u, 0u);
+  if (8 * v >= d) return;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row + 8 * v), word = at & ~uintptr_t(15);
+  const unsigned shift = static_cast<unsigned>(at - word) / 2;  // values
+  const uint4 a = word_within(word, begin, end, bf16_t{});
+  uint4 b = make_uint4(0u, 0u, 0u, 0u);
+  if (shift != 0 && word + 16 < end) b = word_within(word + 16, begin, end, bf16_t{});
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (shift & 4)
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  if (shift & 2)
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  if (shift & 1)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  const int left = d - 8 * v;  // columns that are the row's
+  if (left < 8)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] &= left >= 2 * i + 2 ? 0xFFFFFFFFu : left == 2 * i + 1 ? 0xFFFFu : 0u;
+  r.v = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void load8_any(const float* row, int v, int d, uintptr_t begin, uintptr_t end,
+                                          Raw8<float>& r) {
+  r.a = r.b = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (8 * v >= d) return;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row + 8 * v), word = at & ~uintptr_t(15);
+  const unsigned shift = static_cast<unsigned>(at - word) / 4;
+  const float4 a = word_within(word, begin, end, 0.f);
+  float4 b = make_float4(0.f, 0.f, 0.f, 0.f), c = b;
+  if (word + 16 < end) b = word_within(word + 16, begin, end, 0.f);
+  if (shift != 0 && word + 32 < end) c = word_within(word + 32, begin, end, 0.f);
+  float w[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+  if (shift & 2)
+#pragma unroll
+    for (int i = 0; i < 10; ++i) w[i] = w[i + 2];
+  if (shift & 1)
+#pragma unroll
+    for (int i = 0; i < 9; ++i) w[i] = w[i + 1];
+  const int left = d - 8 * v;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = i < left ? w[i] : 0.f;
+  r.a = make_float4(w[0], w[1], w[2], w[3]);
+  r.b = make_float4(w[4], w[5], w[6], w[7]);
+}
+
+// Adds scale * f (or writes it) to columns 8 v .. 8 v + 7 of row `key`.  Not VEC: whole
+// warps call this, 32 shares in a row each, and pass the 256 columns through shared
+// memory (turn: 256 floats of the warp), so that neighbouring lanes write neighbouring
+// values.
 template <typename G, bool VEC>
-__device__ __forceinline__ void put_row(const SumArgs& a, uint32_t key, int v, const f2 (&f)[4]) {
+__device__ __forceinline__ void put_row(const SumArgs& a, uint32_t key, int v, const f2 (&f)[4], float* turn) {
   G* row = static_cast<G*>(a.dtable) + static_cast<int64_t>(key) * a.d;
   const f2 s = pk(a.scale);
-  f2 r[4];
+  f2 r[4], g[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) g[e] = f[e];
+  if (!VEC) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) *reinterpret_cast<float2*>(turn + 8 * lane + 2 * e) = unpk(f[e]);
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) g[e] = pk(turn[lane + 64 * e], turn[lane + 64 * e + 32]);
+  }
   if (a.add) {
     get8<G, VEC>(row, v, a.d, r);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = fma2(f[e], s, r[e]);
+    for (int e = 0; e < 4; ++e) r[e] = fma2(g[e], s, r[e]);
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = mul2(f[e], s);
+    for (int e = 0; e < 4; ++e) r[e] = mul2(g[e], s);
   }
   put8<G, VEC>(row, v, a.d, r);
 }
@@ -254,44 +522,56 @@ __device__ __forceinline__ float* part_row(const SumArgs& a, int64_t chunk, int 
   return a.part + (2 * chunk + last) * a.ld;
 }
 
-constexpr int kAhead = 4;  // rows whose loads are in flight
+// Rows whose loads are in flight: 128 bytes a thread.
+template <typename T>
+constexpr int kAhead = 16 / sizeof(T);
+constexpr int kMaxLen = 64, kMaxGroups = 32;
 template <typename T, typename G, bool VEC>
 __global__ void __launch_bounds__(256) embed_sum_kernel(const SumArgs a) {
+  __shared__ uint32_t s_key[kMaxGroups * kMaxLen], s_token[kMaxGroups * kMaxLen];
+  __shared__ float s_turn[VEC ? 1 : 8 * 256];
   const int group = threadIdx.x / a.width;
-  if (group >= a.groups) return;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * a.groups + group;
-  const int64_t chunk = item / a.tiles;
-  if (chunk >= a.chunks) return;
-  const int v = static_cast<int>(item - chunk * a.tiles) * a.width + threadIdx.x - group * a.width;
-  if (VEC && 8 * v >= a.d) return;
-  pdl_wait();
-  const int64_t i0 = chunk * a.len, i1 = min(a.T, i0 + a.len);
   const uint32_t none = static_cast<uint32_t>(a.V);
-  uint32_t key = a.keys[i0];
+  float* turn = s_turn + (VEC ? 0 : (threadIdx.x >> 5) * 256);
+  pdl_wait();
+  // the chunks' ids and tokens, all at once
+  for (int i = threadIdx.x; i < a.groups * a.len; i += blockDim.x) {
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * a.groups + i / a.len) / a.tiles * a.len + i % a.len;
+    s_key[i] = at < a.T ? a.keys[at] : none;
+    s_token[i] = at < a.T ? a.tokens[at] : 0u;
+  }
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * a.groups + group, chunk = item / a.tiles;
+  const int v = static_cast<int>(item - chunk * a.tiles) * a.width + threadIdx.x - group * a.width;
+  const int64_t i0 = chunk * a.len;
+  const bool live = i0 < a.T && (!VEC || 8 * v < a.d);
+  const uint32_t prev = live && i0 > 0 ? a.keys[i0 - 1] : none, next = live && i0 + a.len < a.T ? a.keys[i0 + a.len] : none;
+  __syncthreads();
+  if (!live) return;
+  const uint32_t *keys = s_key + group * a.len, *tokens = s_token + group * a.len;
+  uint32_t key = keys[0];
   if (key == none) return;
-  // the run that this chunk begins with began before it
-  bool open = i0 > 0 && a.keys[i0 - 1] == key;
+  bool open = prev == key;  // the run that this chunk begins with began before it
   f2 sum[4] = {pk(0.f), pk(0.f), pk(0.f), pk(0.f)};
   const T* dout = static_cast<const T*>(a.dout);
-  for (int64_t i = i0; i < i1; i += kAhead) {
-    Raw8<T> raw[kAhead];
-    uint32_t k[kAhead];
+  const uintptr_t begin = reinterpret_cast<uintptr_t>(dout), end = reinterpret_cast<uintptr_t>(dout + a.T * a.d);
+  constexpr int A = kAhead<T>;
+  for (int i = 0; i < a.len; i += A) {
+    Raw8<T> raw[A];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      k[u] = i + u < i1 ? a.keys[i + u] : none;
-      if (k[u] != none) load8<VEC>(dout + static_cast<int64_t>(a.tokens[i + u]) * a.d, v, a.d, raw[u]);
-    }
+    for (int u = 0; u < A; ++u)
+      if (keys[i + u] != none) {
+        const T* row = dout + static_cast<int64_t>(tokens[i + u]) * a.d;
+        if (VEC) load8<true>(row, v, a.d, raw[u]);
+        else load8_any(row, v, a.d, begin, end, raw[u]);
+      }
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (i + u >= i1) break;
-      if (k[u] != key) {
-        if (open) {
-          put8<float, VEC>(part_row(a, chunk, 0), v, a.ld, sum);
-        } else {
-          put_row<G, VEC>(a, key, v, sum);
-        }
+    for (int u = 0; u < A; ++u) {
+      const uint32_t k = keys[i + u];
+      if (k != key) {
+        if (open) put8<float, true>(part_row(a, chunk, 0), v, a.ld, sum);
+        else put_row<G, VEC>(a, key, v, sum, turn);
         open = false;
-        key = k[u];
+        key = k;
         if (key == none) return;
         sum[0] = sum[1] = sum[2] = sum[3] = pk(0.f);
       }
@@ -301,64 +581,110 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const SumArgs a) {
       for (int e = 0; e < 4; ++e) sum[e] = add2(sum[e], f[e]);
     }
   }
-  if (open) {
-    put8<float, VEC>(part_row(a, chunk, 0), v, a.ld, sum);
-  } else if (i1 < a.T && a.keys[i1] == key) {
-    put8<float, VEC>(part_row(a, chunk, 1), v, a.ld, sum);
-  } else {
-    put_row<G, VEC>(a, key, v, sum);
-  }
+  if (open) put8<float, true>(part_row(a, chunk, 0), v, a.ld, sum);
+  else if (next == key) put8<float, true>(part_row(a, chunk, 1), v, a.ld, sum);
+  else put_row<G, VEC>(a, key, v, sum, turn);
 }
 
 // Runs that reach over chunk borders.  The chunk that a run begins in adds its own part
-// and the first parts of the chunks that follow, up to the one the run ends in.  A warp
-// has 256 columns, a block's eight warps every eighth part; then warp 0 adds the eight.
+// and the first parts of the chunks that follow, up to the one the run ends in.  A block
+// looks at 32 chunks, a lane each; a warp takes 256 columns of a short run by itself, the
+// eight warps every eighth part of a long one, whose sums warp 0 then adds.
+constexpr int kJoinChunks = 32, kLongRun = 32;
 template <typename G, bool VEC>
 __global__ void __launch_bounds__(256) embed_join_kernel(const SumArgs a) {
   __shared__ float s_sum[8][256];
+  __shared__ uint32_t s_key[kJoinChunks], s_first[256];
+  __shared__ int64_t s_parts[kJoinChunks];  // parts of the run that begins in a chunk, 0: none to add
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
-  const int64_t chunk = blockIdx.x;
-  const int64_t i0 = chunk * a.len, i1 = i0 + a.len;  // not the last chunk: i1 < T
-  const uint32_t key = a.keys[i1 - 1];
-  if (key == static_cast<uint32_t>(a.V) || a.keys[i1] != key) return;
-  if (i0 > 0 && a.keys[i0] == key && a.keys[i0 - 1] == key) return;  // it began before
-  // the last chunk with a part of the run, by bisection over the chunks' first ids
-  int64_t lo = chunk + 1, hi = a.chunks - 1;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi + 1) / 2;
-    if (a.keys[mid * a.len] == key) lo = mid;
-    else hi = mid - 1;
-  }
-  const int v = blockIdx.y * 32 + lane;
-  f2 sum[4] = {pk(0.f), pk(0.f), pk(0.f), pk(0.f)};
-  const int64_t parts = lo - chunk + 1;
-  for (int64_t q = warp; q < parts; q += 8) {
-    f2 f[4];
-    get8<float, VEC>(q == 0 ? part_row(a, chunk, 1) : part_row(a, chunk + q, 0), v, a.ld, f);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] = add2(sum[e], f[e]);
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 x = unpk(sum[e]);
-    s_sum[warp][64 * e + lane] = x.x;
-    s_sum[warp][64 * e + 32 + lane] = x.y;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kJoinChunks;
+  const uint32_t none = static_cast<uint32_t>(a.V);
+  // the first ids of this block's chunks and of those that follow, all at once
+  s_first[threadIdx.x] = c0 + threadIdx.x < a.chunks ? a.keys[(c0 + threadIdx.x) * a.len] : none;
+  uint32_t key = none, prev = none;
+  const int64_t chunk = c0 + lane, i0 = chunk * a.len;
+  if (warp == 0 && chunk < a.chunks - 1) {
+    key = a.keys[i0 + a.len - 1];
+    if (i0 > 0) prev = a.keys[i0 - 1];
   }
   __syncthreads();
-  if (warp != 0) return;
-  const int n = parts < 8 ? static_cast<int>(parts) : 8;
-  for (int w = 1; w < n; ++w)
+  if (warp == 0) {
+    int64_t parts = 0;
+    if (key != none && s_first[lane + 1] == key && !(s_first[lane] == key && prev == key)) {
+      // the last chunk with a part of the run: within reach, or by bisection over first ids
+      int near = lane + 1;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] = add2(sum[e], pk(s_sum[w][64 * e + lane], s_sum[w][64 * e + 32 + lane]));
-  put_row<G, VEC>(a, key, v, sum);
+      for (int step = 128; step > 0; step >>= 1)
+        if (near + step < 256 && s_first[near + step] == key) near += step;
+      int64_t lo = c0 + near, hi = near < 255 ? lo : a.chunks - 1;
+      while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) / 2;
+        if (a.keys[mid * a.len] == key) lo = mid;
+        else hi = mid - 1;
+      }
+      parts = lo - chunk + 1;
+    }
+    s_key[lane] = key;
+    s_parts[lane] = parts;
+  }
+  __syncthreads();
+  const int v = blockIdx.y * 32 + lane;
+  auto add_parts = [&](int64_t chunk, int64_t parts, int64_t from, int64_t step, f2 (&sum)[4]) {
+    sum[0] = sum[1] = sum[2] = sum[3] = pk(0.f);
+    for (int64_t q = from; q < parts; q += 4 * step) {
+      Raw8<float> raw[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t p = q + u * step;
+        if (p < parts) load8<true>(part_row(a, chunk + p, p == 0 ? 1 : 0), v, a.ld, raw[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (q + u * step >= parts) break;
+        f2 f[4];
+        widen(raw[u], f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] = add2(sum[e], f[e]);
+      }
+    }
+  };
+  f2 sum[4];
+  for (int i = warp; i < kJoinChunks; i += 8) {
+    const int64_t parts = s_parts[i];
+    if (parts == 0 || parts > kLongRun) continue;
+    add_parts(c0 + i, parts, 0, 1, sum);
+    put_row<G, VEC>(a, s_key[i], v, sum, s_sum[warp]);
+  }
+  for (int i = 0; i < kJoinChunks; ++i) {
+    const int64_t parts = s_parts[i];
+    if (parts <= kLongRun) continue;
+    add_parts(c0 + i, parts, warp, 8, sum);
+    __syncthreads();  // s_sum was read
+#pragma unroll
+    for (int e = 0; e < 4; ++e) *reinterpret_cast<float2*>(&s_sum[warp][64 * e + 2 * lane]) = unpk(sum[e]);
+    __syncthreads();
+    if (warp != 0) continue;
+    for (int w = 1; w < 8; ++w)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = *reinterpret_cast<const float2*>(&s_sum[w][64 * e + 2 * lane]);
+        sum[e] = add2(sum[e], pk(x.x, x.y));
+      }
+    put_row<G, VEC>(a, s_key[i], v, sum, s_sum[0]);
+  }
 }
 
 // ---- sizes -------------------------------------------------------------------
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-// Tokens of a chunk: from 8, up to 64 as the batch grows.
-int chunk_len(int64_t T) { return T <= 8192 ? 8 : T <= 32768 ? 16 : T <= 131072 ? 32 : 64; }
+// Tokens of a chunk, a multiple of 8: 8 or 16 where the chunks then run at once, three
+// blocks of 256 threads with 8 columns each on an SM; else up to 64 (kMaxLen) as the
+// batch grows, for fewer parts.
+int chunk_len(int64_t T, int64_t d) {
+  const int64_t at_once = 3 * kSMs * 2048;
+  return T * d <= 8 * at_once ? 8 : T * d <= 16 * at_once || T <= 32768 ? 16 : T <= 131072 ? 32 : 64;
+}
 
 struct Workspace {
   uint32_t *keys[2], *tokens[2], *counts;
@@ -380,31 +706,49 @@ Workspace workspace(void* ws, int64_t T, int V, int d) {
     q.tokens[i] = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(T) * 4));
   }
   q.counts = reinterpret_cast<uint32_t*>(take((static_cast<size_t>(sort_chunks) << digits(V).bits) * 4));
-  const int64_t len = chunk_len(T), chunks = (T + len - 1) / len;
+  const int64_t len = chunk_len(T, d), chunks = (T + len - 1) / len;
   q.part = reinterpret_cast<float*>(take(static_cast<size_t>(chunks) * 2 * static_cast<size_t>(round_up(d, 8)) * 4));
   q.bytes = at;
   return q;
 }
 
 // ---- launches ----------------------------------------------------------------
+template <typename T, typename O, int SH>
+cudaError_t forward(const moe_embed_desc* q, bool vec, const void* ids, const void* table, void* out, int* status,
+                    cudaStream_t s) {
+  const int64_t segs = (static_cast<int64_t>(q->d) + 256 * SH - 1) / (256 * SH);
+  const int64_t blocks = (q->T * segs + kFwdWarps - 1) / kFwdWarps;
+  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  return launch_pdl(vec ? embed_fwd_kernel<T, O, true, SH> : embed_fwd_kernel<T, O, false, SH>,
+                    dim3(static_cast<unsigned>(blocks)), dim3(kFwdThreads), 0, s, ids,
+                    q->id_type == MOE_I64 ? 1 : 0, static_cast<const T*>(table), static_cast<int64_t>(q->T), q->V,
+                    q->d, q->scale, static_cast<O*>(out), (reinterpret_cast<uintptr_t>(out) & 31u) == 0, status);
+}
 template <typename T, typename O>
 cudaError_t forward(const moe_embed_desc* q, bool vec, const void* ids, const void* table, void* out, int* status,
                     cudaStream_t s) {
-  const int64_t segs = (static_cast<int64_t>(q->d) + 8 * kFwdShares - 1) / (8 * kFwdShares);
-  const int64_t blocks = (q->T * segs + kFwdThreads / 32 - 1) / (kFwdThreads / 32);
-  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  return launch_pdl(vec ? embed_fwd_kernel<T, O, true> : embed_fwd_kernel<T, O, false>,
-                    dim3(static_cast<unsigned>(blocks)), dim3(kFwdThreads), 0, s, ids,
-                    q->id_type == MOE_I64 ? 1 : 0, static_cast<const T*>(table), static_cast<int64_t>(q->T), q->V,
-                    q->d, q->scale, static_cast<O*>(out), status);
+  return static_cast<int64_t>(q->T) * ((q->d + 1023) / 1024) >= 64 * kSMs
+             ? forward<T, O, 4>(q, vec, ids, table, out, status, s)
+             : forward<T, O, 2>(q, vec, ids, table, out, status, s);
 }
 
-cudaError_t zeros(void* p, int64_t bytes, cudaStream_t s) {
+cudaError_t zeros(void* p, int64_t bytes, bool beside, cudaStream_t s) {
   const int64_t to = static_cast<int64_t>(-reinterpret_cast<intptr_t>(p) & 15);
   const int head = static_cast<int>(std::min<int64_t>(to, bytes));
   const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((bytes / 16 + 1023) / 1024, 8 * kSMs));
   return launch_pdl(embed_zero_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s,
-                    static_cast<uint8_t*>(p), bytes, head);
+                    static_cast<uint8_t*>(p), bytes, head, beside);
+}
+
+template <int R>
+cudaError_t sort_cluster(const Source& src, const moe_embed_desc* q, const Workspace& w, unsigned blocks, int* status,
+                         cudaStream_t s) {
+  const Digits g = digits(q->V);
+  const cudaError_t e = cudaFuncSetAttribute(sort_cluster_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(cluster_sort_smem(R)));
+  if (e != cudaSuccess) return e;
+  return launch_pdl_cluster(sort_cluster_kernel<R>, dim3(blocks), dim3(kClusterThreads), cluster_sort_smem(R), s, blocks,
+                            src, q->T, g.passes, g.bits, w.keys[0], w.tokens[0], status);
 }
 
 // Sorts the tokens by id; the result is in keys[*out], tokens[*out].
@@ -414,6 +758,17 @@ cudaError_t sort_tokens(const moe_embed_desc* q, const void* ids, int64_t pad, c
   const int bins = 1 << g.bits;
   const int64_t n = q->T, chunks = (n + kSortChunk - 1) / kSortChunk;
   Source src = {ids, nullptr, nullptr, q->id_type == MOE_I64 ? 1 : 0, q->V, pad};
+  if (n <= kClusterMost) {
+    // as many blocks as have 1024 tokens each, then more tokens to a block
+    unsigned blocks = 1;
+    while (blocks < kMaxCluster && static_cast<int64_t>(blocks) * kClusterThreads < n) blocks *= 2;
+    const int64_t rounds = (n + static_cast<int64_t>(blocks) * kClusterThreads - 1) / (static_cast<int64_t>(blocks) * kClusterThreads);
+    *out = 0;
+    return rounds <= 1   ? sort_cluster<1>(src, q, w, blocks, status, s)
+           : rounds <= 2 ? sort_cluster<2>(src, q, w, blocks, status, s)
+           : rounds <= 4 ? sort_cluster<4>(src, q, w, blocks, status, s)
+                         : sort_cluster<8>(src, q, w, blocks, status, s);
+  }
   cudaError_t e = cudaSuccess;
   for (int p = 0; p < g.passes && e == cudaSuccess; ++p) {
     const int shift = p * g.bits, to = p & 1;
@@ -423,7 +778,7 @@ cudaError_t sort_tokens(const moe_embed_desc* q, const void* ids, int64_t pad, c
     e = launch_pdl(sort_scan_kernel, dim3(1), dim3(kScanThreads), 0, s, w.counts, chunks * bins);
     if (e != cudaSuccess) break;
     e = launch_pdl(sort_place_kernel, dim3(static_cast<unsigned>(chunks)), dim3(kSortThreads), 0, s, src, n, shift,
-                   bins, static_cast<int>(chunks), static_cast<const uint32_t*>(w.counts), w.keys[to], w.tokens[to]);
+                   g.bits, static_cast<int>(chunks), static_cast<const uint32_t*>(w.counts), w.keys[to], w.tokens[to]);
     src.ids = nullptr;
     src.keys = w.keys[to];
     src.tokens = w.tokens[to];
@@ -439,12 +794,14 @@ cudaError_t sums(SumArgs a, cudaStream_t s) {
   a.tiles = (shares + 255) / 256;
   a.width = (shares + a.tiles - 1) / a.tiles;
   if (!VEC) a.width = (a.width + 31) / 32 * 32;
-  a.groups = 256 / a.width;
+  a.groups = std::min(kMaxGroups, 256 / a.width);
   const int64_t items = a.chunks * a.tiles, blocks = (items + a.groups - 1) / a.groups;
-  cudaError_t e = launch_pdl(embed_sum_kernel<T, G, VEC>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a);
+  cudaError_t e = launch_pdl(embed_sum_kernel<T, G, VEC>, dim3(static_cast<unsigned>(blocks)),
+                             dim3(static_cast<unsigned>(a.width * a.groups)), 0, s, a);
   if (e != cudaSuccess || a.chunks < 2) return e;
   return launch_pdl(embed_join_kernel<G, VEC>,
-                    dim3(static_cast<unsigned>(a.chunks - 1), static_cast<unsigned>((static_cast<int64_t>(a.d) + 255) / 256)),
+                    dim3(static_cast<unsigned>((a.chunks - 1 + kJoinChunks - 1) / kJoinChunks),
+                         static_cast<unsigned>((static_cast<int64_t>(a.d) + 255) / 256)),
                     dim3(256), 0, s, a);
 }
 template <typename T, typename G>
@@ -527,26 +884,26 @@ int moe_embed_bwd(const moe_embed_desc* desc, const void* ids, const void* dout,
   if (rc != MOE_OK) return rc;
   ProbeScope probe("embed_bwd", stream);
   cudaError_t e = cudaSuccess;
-  if (!accumulate) {
-    const int64_t bytes = static_cast<int64_t>(desc->V) * desc->d * size_of(desc->table_type);
-    e = zeros(dtable, bytes, stream);
-  }
-  if (any && e == cudaSuccess) {
-    const Workspace w = workspace(ws, desc->T, desc->V, desc->d);
-    int at = 0;
+  Workspace w = {};
+  int at = 0;
+  if (any) {
+    w = workspace(ws, desc->T, desc->V, desc->d);
     e = sort_tokens(desc, ids, pad_id, w, status, &at, stream);
-    if (e == cudaSuccess) {
-      SumArgs a = {};
-      a.dout = dout; a.dtable = dtable; a.keys = w.keys[at]; a.tokens = w.tokens[at]; a.part = w.part;
-      a.T = desc->T; a.len = chunk_len(desc->T); a.chunks = (a.T + a.len - 1) / a.len;
-      a.V = desc->V; a.d = desc->d; a.ld = static_cast<int>(round_up(desc->d, 8));
-      a.scale = desc->scale; a.add = accumulate;
-      const bool vec = desc->d % 8 == 0 && !misaligned(dout, 16) && !misaligned(dtable, 16);
-      if (desc->row_type == MOE_BF16)
-        e = desc->table_type == MOE_BF16 ? sums<bf16_t, bf16_t>(a, vec, stream) : sums<bf16_t, float>(a, vec, stream);
-      else
-        e = desc->table_type == MOE_BF16 ? sums<float, bf16_t>(a, vec, stream) : sums<float, float>(a, vec, stream);
-    }
+  }
+  if (!accumulate && e == cudaSuccess)
+    e = zeros(dtable, static_cast<int64_t>(desc->V) * desc->d * size_of(desc->table_type),
+              any && desc->T <= kClusterMost, stream);
+  if (any && e == cudaSuccess) {
+    SumArgs a = {};
+    a.dout = dout; a.dtable = dtable; a.keys = w.keys[at]; a.tokens = w.tokens[at]; a.part = w.part;
+    a.T = desc->T; a.len = chunk_len(desc->T, desc->d); a.chunks = (a.T + a.len - 1) / a.len;
+    a.V = desc->V; a.d = desc->d; a.ld = static_cast<int>(round_up(desc->d, 8));
+    a.scale = desc->scale; a.add = accumulate;
+    const bool vec = desc->d % 8 == 0 && !misaligned(dout, 16) && !misaligned(dtable, 16);
+    if (desc->row_type == MOE_BF16)
+      e = desc->table_type == MOE_BF16 ? sums<bf16_t, bf16_t>(a, vec, stream) : sums<bf16_t, float>(a, vec, stream);
+    else
+      e = desc->table_type == MOE_BF16 ? sums<float, bf16_t>(a, vec, stream) : sums<float, float>(a, vec, stream);
   }
   if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
   return record_error(MOE_OK, "");

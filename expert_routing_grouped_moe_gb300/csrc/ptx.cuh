@@ -24,7 +24,7 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // the previous kernel of its stream is finishing.  pdl_wait() blocks until
 // that kernel has completed and its memory is visible; everything before it
 // must not read what earlier kernels write.  A no-op for a normal launch.
-// (No kernel here signals its dependents early: waiting CTAs of the next
+// (No kernel of the layer signals its dependents early: waiting CTAs of the next
 // kernel would then hold SMs that the second stream's kernels can use.)
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
