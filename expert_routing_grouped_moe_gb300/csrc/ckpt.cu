@@ -23,7 +23,11 @@ namespace {
 
 constexpr int kCkptThreads = 256;
 constexpr int kSegCols = 256;  // columns of a warp's unit: 8 values, or every 32nd of 8, a lane
-constexpr int kUnits = 2;      // units whose loads are in flight at once
+// Units whose loads are in flight at once: two when packing, and 16 bytes of codes a lane
+// when unpacking fp32 and 32 bf16 (unpacking 16384 x 2880 into bf16: 27 us, 29 with two).
+constexpr int kPackUnits = 2;
+template <typename T>
+constexpr int kUnpackUnits = 8 / sizeof(T);
 
 // The bits of a block's largest |x| to its scale byte; 255 where it is not finite.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t bits) {
@@ -114,12 +118,12 @@ __global__ void __launch_bounds__(kCkptThreads) ckpt_pack_kernel(const T* __rest
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kCkptThreads / 32);
   pdl_wait();
   for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * (kCkptThreads / 32) + (threadIdx.x >> 5);
-       u0 < units; u0 += warps * kUnits) {
+       u0 < units; u0 += warps * kPackUnits) {
     if (VEC) {
-      Raw8<T> raw[kUnits];
-      int64_t row[kUnits], col[kUnits];
+      Raw8<T> raw[kPackUnits];
+      int64_t row[kPackUnits], col[kPackUnits];
 #pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
+      for (int i = 0; i < kPackUnits; ++i) {
         const int64_t u = u0 + i * warps;
         int64_t seg = 0;
         raw[i] = Raw8<T>{};
@@ -131,7 +135,7 @@ __global__ void __launch_bounds__(kCkptThreads) ckpt_pack_kernel(const T* __rest
         }
       }
 #pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
+      for (int i = 0; i < kPackUnits; ++i) {
         f2 f[4];
         widen(raw[i], f);
         uint32_t big = max(max(abs_bits(f[0]), abs_bits(f[1])), max(abs_bits(f[2]), abs_bits(f[3])));
@@ -152,7 +156,7 @@ __global__ void __launch_bounds__(kCkptThreads) ckpt_pack_kernel(const T* __rest
         }
       }
     } else {
-      for (int i = 0; i < kUnits; ++i) {
+      for (int i = 0; i < kPackUnits; ++i) {
         const int64_t u = u0 + i * warps;
         if (u >= units) break;
         int64_t row = 0, seg = 0;
@@ -184,6 +188,7 @@ __global__ void __launch_bounds__(kCkptThreads) ckpt_unpack_kernel(const int8_t*
                                                                   const uint8_t* __restrict__ scales,
                                                                   int64_t R, int64_t C, int64_t nb,
                                                                   T* __restrict__ x) {
+  constexpr int kUnits = kUnpackUnits<T>;
   const int lane = threadIdx.x & 31;
   const int64_t segs = (C + kSegCols - 1) / kSegCols, units = R * segs;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kCkptThreads / 32);
@@ -244,70 +249,60 @@ __global__ void __launch_bounds__(kCkptThreads) ckpt_unpack_kernel(const int8_t*
 }
 
 // A thread takes 8 features: half of a chunk's gates and their ups.  `per` such
-// items to a row (hs / 16), of which those past f have no act.
-constexpr int kSwigluItems = 2;  // items of a thread, their loads in flight at once
+// items to a row (hs / 16), of which those past f have no act.  The writes bound it, and
+// one item a thread, so more blocks, is faster than two or four (32768 rows of 768
+// features 60, 64, 70 us).  wide: h is 32-byte aligned.
 __global__ void __launch_bounds__(kCkptThreads) ckpt_unpack_swiglu_kernel(
-    const int8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t items, int per, int f,
+    const int8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t items, unsigned per, int f,
     const int32_t* __restrict__ sorted_src, const float* __restrict__ topk_w, int k, int K,
-    float* __restrict__ h, uint16_t* __restrict__ act, int64_t pair) {
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * (kCkptThreads * kSwigluItems);
+    float* __restrict__ h, bool wide, uint16_t* __restrict__ act, int64_t pair) {
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * kCkptThreads;
   const int64_t row0 = base / per;
-  const unsigned rem0 = static_cast<unsigned>(base - row0 * per);
-  uint2 gate[kSwigluItems], up[kSwigluItems];
-  uint32_t byte[kSwigluItems];
-  float w[kSwigluItems];
-  int64_t row[kSwigluItems];
-  int half[kSwigluItems];
+  const unsigned at = static_cast<unsigned>(base - row0 * per) + threadIdx.x;
+  const unsigned r = at / per;
+  const int half = static_cast<int>(at - r * per);
+  const int64_t p = row0 + r;
   pdl_wait();
+  if (base + threadIdx.x >= items) return;
+  const int src = __ldg(sorted_src + p);
+  if (src < 0) return;
+  const int64_t first = p * (16 * static_cast<int64_t>(per)) + 32 * (half >> 1) + 8 * (half & 1);
+  const uint2 gate = __ldg(reinterpret_cast<const uint2*>(codes + first));
+  const uint2 up = __ldg(reinterpret_cast<const uint2*>(codes + first + 16));
+  const f2 s = pk(scale_of(__ldg(scales + p * (per >> 1) + (half >> 1))));
+  const int t = src / K, j = src - t * K;
+  const float w = j < k ? __ldg(topk_w + static_cast<int64_t>(t) * k + j) : 1.f;
+  f2 g[4], u[4];
+  four_values(gate.x, s, g[0], g[1]);
+  four_values(gate.y, s, g[2], g[3]);
+  four_values(up.x, s, u[0], u[1]);
+  four_values(up.y, s, u[2], u[3]);
+  Raw8<float> raw[2];
+  narrow(g, raw[0]);
+  narrow(u, raw[1]);
 #pragma unroll
-  for (int i = 0; i < kSwigluItems; ++i) {
-    const unsigned loc = threadIdx.x + i * kCkptThreads;
-    row[i] = -1;
-    if (base + loc >= items) continue;
-    const unsigned r = (rem0 + loc) / static_cast<unsigned>(per);
-    half[i] = static_cast<int>(rem0 + loc - r * static_cast<unsigned>(per));
-    const int64_t p = row0 + r;
-    const int src = __ldg(sorted_src + p);
-    if (src < 0) continue;
-    row[i] = p;
-    const int8_t* q = codes + p * (16 * static_cast<int64_t>(per)) + 32 * (half[i] >> 1) + 8 * (half[i] & 1);
-    gate[i] = __ldg(reinterpret_cast<const uint2*>(q));
-    up[i] = __ldg(reinterpret_cast<const uint2*>(q + 16));
-    byte[i] = __ldg(scales + p * (per >> 1) + (half[i] >> 1));
-    const int t = src / K, j = src - t * K;
-    w[i] = j < k ? __ldg(topk_w + static_cast<int64_t>(t) * k + j) : 1.f;
-  }
-#pragma unroll
-  for (int i = 0; i < kSwigluItems; ++i) {
-    if (row[i] < 0) continue;
-    const f2 s = pk(scale_of(byte[i]));
-    f2 g[4], u[4];
-    four_values(gate[i].x, s, g[0], g[1]);
-    four_values(gate[i].y, s, g[2], g[3]);
-    four_values(up[i].x, s, u[0], u[1]);
-    four_values(up[i].y, s, u[2], u[3]);
-    float* to = h + row[i] * (16 * static_cast<int64_t>(per)) + 32 * (half[i] >> 1) + 8 * (half[i] & 1);
-    Raw8<float> raw;
-    narrow(g, raw);
-    *reinterpret_cast<float4*>(to) = raw.a;
-    *reinterpret_cast<float4*>(to + 4) = raw.b;
-    narrow(u, raw);
-    *reinterpret_cast<float4*>(to + 16) = raw.a;
-    *reinterpret_cast<float4*>(to + 20) = raw.b;
-    if (8 * half[i] >= f) continue;
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 a = unpk(g[e]), b = unpk(u[e]);
-      const float x = w[i] * __fdividef(a.x, 1.f + __expf(-a.x)) * b.x;
-      const float y = w[i] * __fdividef(a.y, 1.f + __expf(-a.y)) * b.y;
-      hi[e] = pack_bf16x2(x, y);
-      lo[e] = pack_bf16x2(x - bf16lo(hi[e]), y - bf16hi(hi[e]));
+  for (int i = 0; i < 2; ++i) {
+    float* to = h + first + 16 * i;
+    if (wide) {
+      store8_wide(to, raw[i]);
+    } else {
+      *reinterpret_cast<float4*>(to) = raw[i].a;
+      *reinterpret_cast<float4*>(to + 4) = raw[i].b;
     }
-    uint4* out = reinterpret_cast<uint4*>(act + row[i] * f + 8 * half[i]);
-    out[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(act + pair + row[i] * f + 8 * half[i]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
+  if (8 * half >= f) return;
+  uint32_t hi[4], lo[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 a = unpk(g[e]), b = unpk(u[e]);
+    const float x = w * (a.x / (1.f + expf(-a.x))) * b.x;
+    const float y = w * (a.y / (1.f + expf(-a.y))) * b.y;
+    hi[e] = pack_bf16x2(x, y);
+    lo[e] = pack_bf16x2(x - bf16lo(hi[e]), y - bf16hi(hi[e]));
+  }
+  uint16_t* out = act + p * f + 8 * half;
+  *reinterpret_cast<uint4*>(out) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  *reinterpret_cast<uint4*>(out + pair) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
 int bad(const char* msg) { return record_error(MOE_ERR_INVALID_ARG, msg); }
@@ -326,15 +321,15 @@ struct CkptShape {
   int64_t R, C, nb;
   unsigned blocks;
 };
-// Enough blocks for eight on each SM (all that fit), each unit's loads kUnits deep.
-CkptShape ckpt_shape(int64_t R, int64_t C) {
+// At most 16 blocks for each place on the SMs; more units are taken in turn.
+CkptShape ckpt_shape(int64_t R, int64_t C, int at_once) {
   CkptShape q{R, C, (C + MOE_CKPT_BLOCK - 1) / MOE_CKPT_BLOCK, 0};
   if (C % MOE_CKPT_BLOCK == 0) {
     q.C = R * C;
     q.nb = R * q.nb;
     q.R = 1;
   }
-  const int64_t units = q.R * ((q.C + kSegCols - 1) / kSegCols), per = kCkptThreads / 32 * kUnits;
+  const int64_t units = q.R * ((q.C + kSegCols - 1) / kSegCols), per = kCkptThreads / 32 * at_once;
   q.blocks = static_cast<unsigned>(std::min<int64_t>((units + per - 1) / per, 8 * kSMs * 16));
   return q;
 }
@@ -367,7 +362,7 @@ int moe_ckpt_pack(const void* x, int32_t x_type, int32_t R, int32_t C, int8_t* c
   const int rc = check_rows(x, x_type, R, C, codes, scales);
   if (rc) return rc;
   if (R == 0) return record_error(MOE_OK, "");
-  const CkptShape q = ckpt_shape(R, C);
+  const CkptShape q = ckpt_shape(R, C, kPackUnits);
   const bool vec = by_vectors(x, x_type, C, codes);
   ProbeScope probe("ckpt_pack", stream);
   const cudaError_t e = x_type == MOE_BF16 ? pack<bf16_t>(q, vec, x, codes, scales, stream)
@@ -382,7 +377,7 @@ int moe_ckpt_unpack(const int8_t* codes, const uint8_t* scales, int32_t R, int32
   const int rc = check_rows(x, x_type, R, C, codes, scales);
   if (rc) return rc;
   if (R == 0) return record_error(MOE_OK, "");
-  const CkptShape q = ckpt_shape(R, C);
+  const CkptShape q = ckpt_shape(R, C, x_type == MOE_BF16 ? kUnpackUnits<bf16_t> : kUnpackUnits<float>);
   const bool vec = by_vectors(x, x_type, C, codes);
   ProbeScope probe("ckpt_unpack", stream);
   const cudaError_t e = x_type == MOE_BF16 ? unpack<bf16_t>(q, vec, codes, scales, x, stream)
@@ -402,14 +397,14 @@ int moe_ckpt_unpack_swiglu(const int8_t* codes, const uint8_t* scales, int32_t P
   if (misaligned(codes, 8) || misaligned(sorted_src, 4) || misaligned(topk_w, 4) || misaligned(h, 16) ||
       misaligned(act, 16))
     return bad("misaligned pointer");
-  const int per = 2 * static_cast<int>((static_cast<int64_t>(f) + 15) / 16);
-  const int64_t items = static_cast<int64_t>(P) * per;
-  const int64_t blocks = (items + kCkptThreads * kSwigluItems - 1) / (kCkptThreads * kSwigluItems);
+  const unsigned per = 2 * static_cast<unsigned>((static_cast<int64_t>(f) + 15) / 16);
+  const int64_t items = static_cast<int64_t>(P) * per, blocks = (items + kCkptThreads - 1) / kCkptThreads;
   if (blocks > 0x7FFFFFFF) return record_error(MOE_ERR_UNSUPPORTED, "P x f is too large");
   ProbeScope probe("ckpt_unpack_swiglu", stream);
   const cudaError_t e = launch_pdl(ckpt_unpack_swiglu_kernel, dim3(static_cast<unsigned>(blocks)),
                                    dim3(kCkptThreads), 0, stream, codes, scales, items, per, f, sorted_src,
-                                   topk_w, k, k + shared_expert, h, act, static_cast<int64_t>(P) * f);
+                                   topk_w, k, k + shared_expert, h, !misaligned(h, 32), act,
+                                   static_cast<int64_t>(P) * f);
   if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
   return record_error(MOE_OK, "");
 }
