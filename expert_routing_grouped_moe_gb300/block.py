@@ -21,6 +21,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib as L
+from .ckpt import Packed8
 from .layer import MoELoRALayer
 
 
@@ -28,13 +29,22 @@ class MoEBlock:
     """w: the layer's weights (W_gu, A_gu, B_gu, W_dn, A_dn, B_dn) and W_r [E,d]
     bf16; optionally w_post [d], w_pre [d] and gate [d] fp32 (left out: no such
     norm or gate).  residual: type of the residual stream (torch.bfloat16 or
-    torch.float32); the block side is bf16."""
+    torch.float32); the block side is bf16.  checkpoint: a LayerScratch; the layer's
+    pre-activations and output are then kept in 8 bits from forward to backward,
+    and what lives within a call is shared by the blocks with the same scratch:
+    the dr that backward returns holds until the next such call."""
 
     def __init__(self, T, d, f, E, k, r, alpha, w: dict, scale=1.0, gate_sigmoid=False, eps=1e-6,
                  aux_coef=0.0, z_coef=0.0, residual=torch.bfloat16, shared_expert=False,
-                 train_norms=True, train_router=False, device="cuda"):
+                 train_norms=True, train_router=False, device="cuda", checkpoint=None):
         self.layer = MoELoRALayer(T, d, f, E, k, r, alpha, w, shared_expert=shared_expert,
-                                  device=device)
+                                  device=device, checkpoint=checkpoint)
+        self.y8 = None if checkpoint is None else Packed8(T, d, device)
+
+        def buf(name, *shape, dtype):
+            if checkpoint is None:
+                return torch.empty(*shape, dtype=dtype, device=device)
+            return checkpoint.take(name, shape, dtype)
         self.T, self.E, self.k = T, E, k
         self.scale, self.sigmoid, self.eps = float(scale), bool(gate_sigmoid), float(eps)
         self.aux_coef, self.z_coef = float(aux_coef), float(z_coef)
@@ -47,15 +57,13 @@ class MoEBlock:
         self.topk_w = torch.empty(T, k, **f32)
         self.losses, self.lse, self.pmean = torch.empty(2, **f32), torch.empty(T, **f32), torch.empty(
             E, **f32)
-        self.loss_ws = torch.empty(max(16, L.moe_router_loss_workspace_size(T, E)),
-                                   dtype=torch.uint8, device=device)
-        self.dlogits = torch.empty(T, E, **f32)
+        self.loss_ws = buf("loss_ws", max(16, L.moe_router_loss_workspace_size(T, E)), dtype=torch.uint8)
+        self.dlogits = buf("dlogits", T, E, dtype=torch.float32)
         self.r, self.n = torch.empty(T, d, **res), None if self.w_pre is None else torch.empty(T, d, **bf)
         self.rstd_y = None if self.w_post is None else torch.empty(T, **f32)
         self.rstd_r = None if self.w_pre is None else torch.empty(T, **f32)
-        self.dr, self.dy = torch.empty(T, d, **res), torch.empty(T, d, **bf)
-        self.norm_ws = torch.empty(max(16, L.moe_block_norm_workspace_size(T, d)), dtype=torch.uint8,
-                                   device=device)
+        self.dr, self.dy = buf("dr", T, d, dtype=residual), buf("dy", T, d, dtype=torch.bfloat16)
+        self.norm_ws = buf("norm_ws", max(16, L.moe_block_norm_workspace_size(T, d)), dtype=torch.uint8)
         self.norm_grads = {"dw_post": like(self.w_post), "dw_pre": like(self.w_pre),
                            "dgate": like(self.gate)}
         self.dW_r = torch.empty_like(self.W_r, dtype=torch.float32) if train_router else None
@@ -76,12 +84,16 @@ class MoEBlock:
                               self.pmean, self.loss_ws)
         L.moe_block_norm_fwd(r, y, self.r, self.n, w_post=self.w_post, w_pre=self.w_pre,
                              rstd_y=self.rstd_y, rstd_r=self.rstd_r, **self._gate())
+        if self.y8 is not None:
+            self.y8.pack(y)
         return self.r, self.n
 
     def backward(self, dr, dn=None):
         """(dr, dn, grads) for the gradients of r' (None: zero) and n'.  dn is a
         new bf16 tensor, the rest are the block's own buffers."""
         g = self.norm_grads
+        if self.y8 is not None:
+            self.y8.unpack(self.layer.Y)
         L.moe_block_norm_bwd(dr, dn, self.r, self.layer.Y, self.dr, self.dy, w_post=self.w_post,
                              w_pre=self.w_pre, rstd_y=self.rstd_y, rstd_r=self.rstd_r,
                              dgate=g["dgate"], dw_post=g["dw_post"], dw_pre=g["dw_pre"],

@@ -1,0 +1,60 @@
+"""Buffers that a stack of layers shares when each keeps its activations in 8 bits.
+
+A layer needs most of its device memory only while one of its calls runs: the
+permuted rows, the pre-activations in fp32, the activations as pairs, the
+gradients' rows.  With a ``LayerScratch`` those belong to all layers together,
+and a layer keeps from its forward to its backward what 8 bits hold: the
+pre-activations (``lib.moe_ckpt_pack``), from which the backward gets them and
+the activations back (``lib.moe_ckpt_unpack_swiglu``).  At T = 4096, d = 2048,
+f = 768, top-8, r = 64 a layer then keeps 0.1 GB instead of 1.2.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _lib as L
+
+
+class LayerScratch:
+    """Device buffers by name, each as large as its largest user asked for; users get
+    views.  What one call leaves there the next call of any layer overwrites."""
+
+    def __init__(self, device="cuda"):
+        self.device = torch.device(device)
+        self._buf = {}
+
+    def take(self, name, shape, dtype):
+        """A tensor of this shape over the buffer of that name (made, or made larger,
+        on first use; layers take theirs when they are built)."""
+        n = 1
+        for s in shape:
+            n *= int(s)
+        size = n * torch.empty(0, dtype=dtype).element_size()
+        buf = self._buf.get(name)
+        if buf is None or buf.numel() < size:
+            # a larger buffer replaces the smaller one for later users; earlier ones keep theirs
+            buf = self._buf[name] = torch.empty(max(16, size), dtype=torch.uint8,
+                                                device=self.device)
+        return buf[:size].view(dtype).view(*shape)
+
+    def bytes(self):
+        return sum(b.numel() for b in self._buf.values())
+
+
+class Packed8:
+    """Rows [R, C] kept in 8 bits: codes and scales, and the calls that fill and read them."""
+
+    def __init__(self, R, C, device="cuda"):
+        self.codes = torch.empty(R, C, dtype=torch.int8, device=device)
+        self.scales = torch.empty(R, -(-C // L.MOE_CKPT_BLOCK), dtype=torch.uint8, device=device)
+
+    def pack(self, x, stream=None):
+        L.moe_ckpt_pack(x, self.codes, self.scales, stream=stream)
+
+    def unpack(self, x, stream=None):
+        L.moe_ckpt_unpack(self.codes, self.scales, x, stream=stream)
+        return x
+
+    def unpack_swiglu(self, sorted_src, topk_w, shared_expert, h, act, stream=None):
+        L.moe_ckpt_unpack_swiglu(self.codes, self.scales, sorted_src, topk_w, shared_expert, h, act,
+                                 stream=stream)

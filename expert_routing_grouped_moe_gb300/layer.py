@@ -8,14 +8,17 @@ routing-weight gradient.  With ``gather=False`` (default) the token rows are
 first permuted into Xp / dYp by moe_permute and the GEMMs read them with TMA;
 with ``gather=True`` the GEMMs copy token rows straight from X and dY
 (sorted_src picks them), which saves the two [N, d] permuted buffers but is
-slower on GB300.  All arithmetic happens in the CUDA library; this module
-only sequences calls and owns memory.
+slower on GB300.  With ``checkpoint`` (a ``LayerScratch``) the layer keeps its
+pre-activations in 8 bits between forward and backward and shares the other
+buffers with the layers that have the same scratch.  All arithmetic happens in
+the CUDA library; this module only sequences calls and owns memory.
 """
 from __future__ import annotations
 
 import torch
 
 from . import _lib as L
+from .ckpt import Packed8
 
 # Kernel launches issued by one forward / one backward in the default
 # (permuted) mode: route 2 or 3 (L.moe_route_kernel_count), permute 1,
@@ -27,12 +30,18 @@ LAUNCHES_BWD = 11
 
 class MoELoRALayer:
     def __init__(self, T, d, f, E, k, r, alpha, weights: dict, shared_expert=False,
-                 device="cuda", gather=False, full_grads=False, rank_r_tokens=False):
+                 device="cuda", gather=False, full_grads=False, rank_r_tokens=False,
+                 checkpoint=None):
         """full_grads: the backward also returns dW_gu [G,2f,d] and dW_dn
         [G,d,f] (fp32 gradients of the expert weights, for full fine-tuning;
         needs the permuted-row mode).  rank_r_tokens (permuted-row mode):
         the LoRA-A products xa_gu and u read the token rows of X / dY (small
-        enough to stay in L2) instead of the permuted copies."""
+        enough to stay in L2) instead of the permuted copies.  checkpoint: a
+        LayerScratch; the forward then leaves h in 8 bits and the backward works on
+        what these stand for (each h off by at most 1/254 of the largest of its
+        chunk of 32); X is read again in the backward and must not change until
+        then, and dX, dw and Y are the scratch's: they hold until the next call of
+        a layer with the same scratch."""
         if full_grads and gather:
             raise ValueError("full weight gradients need the permuted-row mode (gather=False)")
         self.gather = bool(gather)
@@ -51,6 +60,12 @@ class MoELoRALayer:
         bf = dict(dtype=torch.bfloat16, device=dev)
         f32 = dict(dtype=torch.float32, device=dev)
         P, G = self.N, self.G
+        self.scratch = checkpoint
+
+        def buf(name, *shape, dtype):   # lives within a call: the scratch's, if there is one
+            if checkpoint is None:
+                return torch.empty(*shape, dtype=dtype, device=dev)
+            return checkpoint.take(name, shape, dtype)
         self.counts = torch.zeros(G, **i32)
         self.offsets = torch.zeros(G + 1, **i32)
         self.tile_off = torch.zeros(G + 1, **i32)
@@ -58,19 +73,22 @@ class MoELoRALayer:
         self.dest_pos = torch.zeros(self.N, **i32)
         self.route_ws = torch.empty(max(16, L.moe_route_workspace_size(T, self.K, G)),
                                     dtype=torch.uint8, device=dev)
-        self.Xp = None if self.gather else torch.empty(P, d, **bf)
-        self.Yp = torch.empty(P, d, **bf)
+        b16, b32 = torch.bfloat16, torch.float32
+        self.Xp = None if self.gather else buf("Xp", P, d, dtype=b16)
+        self.Yp = buf("Yp", P, d, dtype=b16)
         # saved intermediates: h in fp32; act / xa_gu / xa_dn as hi+lo bf16 pairs
-        self.h = torch.empty(P, 32 * ((f + 15) // 16), **f32)  # [gate 16 | up 16] chunks
-        self.act = torch.empty(2, P, f, **bf)
+        hs = 32 * ((f + 15) // 16)
+        self.h = buf("h", P, hs, dtype=b32)  # [gate 16 | up 16] chunks
+        self.act = buf("act", 2, P, f, dtype=b16)
+        self.h8 = None if checkpoint is None else Packed8(P, hs, dev)
         self.xa_gu = torch.empty(2, P, r, **bf)
         self.xa_dn = torch.empty(2, P, r, **bf)
-        self.Y = torch.empty(T, d, **bf)
-        self.dYp = None if self.gather else torch.empty(P, d, **bf)
-        self.dXp = torch.empty(P, d, **bf)
-        self.dw_rows = torch.empty(P, **f32)
-        self.dX = torch.empty(T, d, **bf)
-        self.dw = torch.empty(T, k, **f32)
+        self.Y = buf("Y", T, d, dtype=b16)
+        self.dYp = None if self.gather else buf("dYp", P, d, dtype=b16)
+        self.dXp = buf("dXp", P, d, dtype=b16)
+        self.dw_rows = buf("dw_rows", P, dtype=b32)
+        self.dX = buf("dX", T, d, dtype=b16)
+        self.dw = buf("dw", T, k, dtype=b32)
         self.grads = {
             "dA_gu": torch.empty(G, r, d, **f32), "dB_gu": torch.empty(G, 2 * f, r, **f32),
             "dA_dn": torch.empty(G, r, f, **f32), "dB_dn": torch.empty(G, d, r, **f32),
@@ -78,15 +96,15 @@ class MoELoRALayer:
         if self.full_grads:
             self.grads["dW_gu"] = torch.empty(G, 2 * f, d, **f32)
             self.grads["dW_dn"] = torch.empty(G, d, f, **f32)
-        self.bwd_ws = torch.empty(L.moe_mlp_bwd_workspace_size(self.dims), dtype=torch.uint8,
-                                  device=dev)
+        self.bwd_ws = buf("bwd_ws", L.moe_mlp_bwd_workspace_size(self.dims), dtype=torch.uint8)
         self._ids = None
         self._topk_w = None
 
     def launches_per_step(self):
         """Kernel launches of one forward + backward in this layer's mode."""
+        ckpt = 0 if self.h8 is None else 2 if self.gather else 3   # pack, unpack, X permuted again
         return (L.moe_route_kernel_count(self.T, self.K, self.G) + LAUNCHES_FWD + LAUNCHES_BWD
-                - (2 if self.gather else 0) + (2 if self.full_grads else 0))
+                - (2 if self.gather else 0) + (2 if self.full_grads else 0) + ckpt)
 
     # ------------------------------------------------------------------ steps
     def route(self, ids, stream=None):
@@ -108,12 +126,18 @@ class MoELoRALayer:
                                    self.xa_gu, self.xa_dn, stream)
         L.moe_unpermute_combine(self.Yp, self.dest_pos, self.k, self.shared, self.Y,
                                 stream=stream)
+        if self.h8 is not None:
+            self.h8.pack(self.h, stream)
         return self.Y
 
     def backward(self, dY, stream=None):
         """dX [T,d] bf16, dw [T,k] fp32 and the four fp32 LoRA gradients."""
         if self._ids is None:
             raise RuntimeError("backward before forward")
+        if self.h8 is not None:   # other layers have used the buffers since
+            self.h8.unpack_swiglu(self.sorted_src, self._topk_w, self.shared, self.h, self.act, stream)
+            if not self.gather:
+                L.moe_permute(self._X, self.K, self.dest_pos, self.Xp, stream)
         if not self.gather:
             L.moe_permute(dY, self.K, self.dest_pos, self.dYp, stream)
         w, g = self.w, self.grads
