@@ -21,10 +21,11 @@
 namespace moe {
 namespace {
 
-constexpr int kCkptThreads = 256;
+constexpr int kCkptThreads = 256, kCkptWarps = kCkptThreads / 32;
 constexpr int kSegCols = 256;  // columns of a warp's unit: 8 values, or every 32nd of 8, a lane
-// Units whose loads are in flight at once: two when packing, and 16 bytes of codes a lane
-// when unpacking fp32 and 32 bf16 (unpacking 16384 x 2880 into bf16: 27 us, 29 with two).
+// Units whose loads are in flight at once: two when packing (four: 32768 x 1536 fp32 41 us
+// against 39), and 16 bytes of codes a lane
+// when unpacking fp32 and 32 bf16 (unpacking 16384 x 2880 into bf16: 23 us).
 constexpr int kPackUnits = 2;
 template <typename T>
 constexpr int kUnpackUnits = 8 / sizeof(T);
@@ -60,9 +61,15 @@ __device__ __forceinline__ uint32_t four_codes(f2 a, f2 b, f2 s) {
   return __byte_perm(lo, hi, 0x5410);
 }
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-__device__ __forceinline__ uint32_t abs_bits(f2 a) {
-  const float2 x = unpk(a);
-  return max(abs_bits(x.x), abs_bits(x.y));
+// The bits of a share's largest |x|, as an fp32 value has them.
+__device__ __forceinline__ uint32_t share_max(const Raw8<bf16_t>& r) {
+  const uint32_t m = __vmaxu2(__vmaxu2(r.v.x & 0x7FFF7FFFu, r.v.y & 0x7FFF7FFFu),
+                              __vmaxu2(r.v.z & 0x7FFF7FFFu, r.v.w & 0x7FFF7FFFu));
+  return max(m & 0xFFFF0000u, m << 16);
+}
+__device__ __forceinline__ uint32_t share_max(const Raw8<float>& r) {
+  return max(max(max(abs_bits(r.a.x), abs_bits(r.a.y)), max(abs_bits(r.a.z), abs_bits(r.a.w))),
+             max(max(abs_bits(r.b.x), abs_bits(r.b.y)), max(abs_bits(r.b.z), abs_bits(r.b.w))));
 }
 // Codes to values: a byte b, its sign bit flipped, as the last byte of 2^23 is
 // 2^23 + 128 + b.
@@ -75,17 +82,14 @@ __device__ __forceinline__ void four_values(uint32_t codes, f2 scale, f2& a, f2&
                    __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7543))), shift), scale);
 }
 
-// Row and first column of unit u, `segs` to a row.
-__device__ __forceinline__ void unit_place(int64_t u, int64_t segs, bool flat, int64_t& row,
-                                           int64_t& seg) {
-  if (flat) {
-    row = 0;
-  } else if ((u >> 32) == 0) {
-    row = static_cast<uint32_t>(u) / static_cast<uint32_t>(segs);
-  } else {
-    row = u / segs;
-  }
-  seg = u - row * segs;
+// Where unit u's columns lie: of row `row` from column `col` on, `segs` units to a row.
+// FLAT: one row, without a division.
+template <bool FLAT>
+__device__ __forceinline__ void unit_place(int64_t u, int64_t segs, int64_t& row, int64_t& col) {
+  if (FLAT) row = 0;
+  else if ((u >> 32) == 0) row = static_cast<uint32_t>(u) / static_cast<uint32_t>(segs);
+  else row = u / segs;
+  col = (FLAT ? u : u - row * segs) * kSegCols;
 }
 
 __device__ __forceinline__ void load_share(const bf16_t* p, Raw8<bf16_t>& r) {
@@ -103,146 +107,144 @@ __device__ __forceinline__ void narrow1(float x, bf16_t* p) {
   p->bits = static_cast<uint16_t>(pack_bf16x2(x, 0.f));
 }
 
-// C columns a row, nb blocks a row; flat: the rows have no gaps between blocks (C a
-// multiple of 32) and count as one row of R C columns.
-// VEC: a lane has 8 consecutive values, four lanes a block.  Else a lane has every
-// 32nd value and a warp's 32 lanes are a block, so that loads of any alignment and
-// width cover whole sectors.
-template <typename T, bool VEC>
+// How the values are reached.  kFlat: the rows have no gaps between blocks (C a multiple
+// of 32) and count as one row of R C columns, kRows: they do not; in both a lane has 8
+// consecutive values, four lanes a block.  kSingle: a lane has every 32nd value and a
+// warp's 32 lanes are a block, so that loads of any alignment and width cover whole
+// sectors.
+enum { kFlat = 0, kRows = 1, kSingle = 2 };
+
+// C columns a row, nb blocks a row.  A block's warps have neighbouring units.
+template <typename T, int HOW>
 __global__ void __launch_bounds__(kCkptThreads) ckpt_pack_kernel(const T* __restrict__ x, int64_t R,
                                                                 int64_t C, int64_t nb,
                                                                 int8_t* __restrict__ codes,
                                                                 uint8_t* __restrict__ scales) {
+  constexpr bool FLAT = HOW == kFlat;
   const int lane = threadIdx.x & 31;
   const int64_t segs = (C + kSegCols - 1) / kSegCols, units = R * segs;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kCkptThreads / 32);
   pdl_wait();
-  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * (kCkptThreads / 32) + (threadIdx.x >> 5);
-       u0 < units; u0 += warps * kPackUnits) {
-    if (VEC) {
-      Raw8<T> raw[kPackUnits];
-      int64_t row[kPackUnits], col[kPackUnits];
+  const int64_t u0 = static_cast<int64_t>(blockIdx.x) * kCkptWarps * kPackUnits + (threadIdx.x >> 5);
+  if (HOW != kSingle) {
+    Raw8<T> raw[kPackUnits];
+    int64_t at[kPackUnits];  // of the lane's values, -1: none
+    int64_t block[kPackUnits];
 #pragma unroll
-      for (int i = 0; i < kPackUnits; ++i) {
-        const int64_t u = u0 + i * warps;
-        int64_t seg = 0;
-        raw[i] = Raw8<T>{};
-        col[i] = C;
-        if (u < units) {
-          unit_place(u, segs, R == 1, row[i], seg);
-          col[i] = seg * kSegCols + 8 * lane;
-          if (col[i] < C) load_share(x + row[i] * C + col[i], raw[i]);
-        }
+    for (int i = 0; i < kPackUnits; ++i) {
+      // lanes past the end load the first values, so that no load waits for a branch
+      const int64_t u = u0 + i * kCkptWarps;
+      int64_t row, col;
+      unit_place<FLAT>(u, segs, row, col);
+      col += 8 * lane;
+      const bool ok = u < units && col < C;
+      at[i] = ok ? row * C + col : -1;
+      block[i] = row * nb + col / MOE_CKPT_BLOCK;
+      load_share(x + (ok ? at[i] : 0), raw[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kPackUnits; ++i) {
+      if (u0 + i * kCkptWarps >= units) break;
+      uint32_t big = at[i] >= 0 ? share_max(raw[i]) : 0u;
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      f2 f[4];
+      widen(raw[i], f);
+      uint32_t byte = scale_byte(big);
+      if (byte == kMaxByte + 1) {
+        byte = kMaxByte;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = cut(f[e]);
+      }
+      const f2 s = pk(inverse_scale(byte));
+      uint2 q = make_uint2(four_codes(f[0], f[1], s), four_codes(f[2], f[3], s));
+      if (byte == 255u) q = make_uint2(0u, 0u);
+      if (at[i] >= 0) {
+        *reinterpret_cast<uint2*>(codes + at[i]) = q;
+        if ((lane & 3) == 0) scales[block[i]] = static_cast<uint8_t>(byte);
+      }
+    }
+  } else {
+    for (int i = 0; i < kPackUnits; ++i) {
+      const int64_t u = u0 + i * kCkptWarps;
+      if (u >= units) break;
+      int64_t row, col;
+      unit_place<false>(u, segs, row, col);
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int64_t c = col + 32 * e + lane;
+        f[e] = c < C ? widen1(x[row * C + c]) : 0.f;
       }
 #pragma unroll
-      for (int i = 0; i < kPackUnits; ++i) {
-        f2 f[4];
-        widen(raw[i], f);
-        uint32_t big = max(max(abs_bits(f[0]), abs_bits(f[1])), max(abs_bits(f[2]), abs_bits(f[3])));
-        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        uint32_t byte = scale_byte(big);
-        if (byte == kMaxByte + 1) {
-          byte = kMaxByte;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) f[e] = cut(f[e]);
-        }
-        const f2 s = pk(inverse_scale(byte));
-        uint2 q = make_uint2(four_codes(f[0], f[1], s), four_codes(f[2], f[3], s));
-        if (byte == 255u) q = make_uint2(0u, 0u);
-        if (col[i] < C) {
-          *reinterpret_cast<uint2*>(codes + row[i] * C + col[i]) = q;
-          if ((lane & 3) == 0) scales[row[i] * nb + col[i] / MOE_CKPT_BLOCK] = static_cast<uint8_t>(byte);
-        }
-      }
-    } else {
-      for (int i = 0; i < kPackUnits; ++i) {
-        const int64_t u = u0 + i * warps;
-        if (u >= units) break;
-        int64_t row = 0, seg = 0;
-        unit_place(u, segs, R == 1, row, seg);
-        float f[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int64_t c = seg * kSegCols + 32 * e + lane;
-          f[e] = c < C ? widen1(x[row * C + c]) : 0.f;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int64_t c = seg * kSegCols + 32 * e + lane;
-          uint32_t byte = scale_byte(__reduce_max_sync(0xffffffffu, abs_bits(f[e])));
-          if (byte == kMaxByte + 1) byte = kMaxByte, f[e] = cut(f[e]);
-          const uint32_t q = __float_as_uint(fmaf(f[e], inverse_scale(byte), kRoundShift));
-          if (c < C) {
-            codes[row * C + c] = static_cast<int8_t>(byte == 255u ? 0u : q & 0xFFu);
-            if (lane == 0) scales[row * nb + c / MOE_CKPT_BLOCK] = static_cast<uint8_t>(byte);
-          }
+      for (int e = 0; e < 8; ++e) {
+        const int64_t c = col + 32 * e + lane;
+        uint32_t byte = scale_byte(__reduce_max_sync(0xffffffffu, abs_bits(f[e])));
+        if (byte == kMaxByte + 1) byte = kMaxByte, f[e] = cut(f[e]);
+        const uint32_t q = __float_as_uint(fmaf(f[e], inverse_scale(byte), kRoundShift));
+        if (c < C) {
+          codes[row * C + c] = static_cast<int8_t>(byte == 255u ? 0u : q & 0xFFu);
+          if (lane == 0) scales[row * nb + c / MOE_CKPT_BLOCK] = static_cast<uint8_t>(byte);
         }
       }
     }
   }
 }
 
-template <typename T, bool VEC>
+template <typename T, int HOW>
 __global__ void __launch_bounds__(kCkptThreads) ckpt_unpack_kernel(const int8_t* __restrict__ codes,
                                                                   const uint8_t* __restrict__ scales,
                                                                   int64_t R, int64_t C, int64_t nb,
                                                                   T* __restrict__ x) {
   constexpr int kUnits = kUnpackUnits<T>;
+  constexpr bool FLAT = HOW == kFlat;
   const int lane = threadIdx.x & 31;
   const int64_t segs = (C + kSegCols - 1) / kSegCols, units = R * segs;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kCkptThreads / 32);
   pdl_wait();
-  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * (kCkptThreads / 32) + (threadIdx.x >> 5);
-       u0 < units; u0 += warps * kUnits) {
-    if (VEC) {
-      uint2 q[kUnits];
-      uint32_t byte[kUnits];
-      int64_t at[kUnits];
+  const int64_t u0 = static_cast<int64_t>(blockIdx.x) * kCkptWarps * kUnits + (threadIdx.x >> 5);
+  if (HOW != kSingle) {
+    uint2 q[kUnits];
+    uint32_t byte[kUnits];
+    int64_t at[kUnits];
 #pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const int64_t u = u0 + i * warps;
-        at[i] = -1;
-        if (u < units) {
-          int64_t row = 0, seg = 0;
-          unit_place(u, segs, R == 1, row, seg);
-          const int64_t col = seg * kSegCols + 8 * lane;
-          if (col < C) {
-            at[i] = row * C + col;
-            q[i] = *reinterpret_cast<const uint2*>(codes + at[i]);
-            byte[i] = scales[row * nb + col / MOE_CKPT_BLOCK];
-          }
-        }
+    for (int i = 0; i < kUnits; ++i) {
+      // lanes past the end load the first values, so that no load waits for a branch
+      const int64_t u = u0 + i * kCkptWarps;
+      int64_t row, col;
+      unit_place<FLAT>(u, segs, row, col);
+      col += 8 * lane;
+      const bool ok = u < units && col < C;
+      at[i] = ok ? row * C + col : -1;
+      q[i] = __ldg(reinterpret_cast<const uint2*>(codes + (ok ? at[i] : 0)));
+      byte[i] = __ldg(scales + (ok ? row * nb + col / MOE_CKPT_BLOCK : 0));
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      if (at[i] < 0) continue;
+      const f2 s = pk(scale_of(byte[i]));
+      f2 f[4];
+      four_values(q[i].x, s, f[0], f[1]);
+      four_values(q[i].y, s, f[2], f[3]);
+      Raw8<T> raw;
+      narrow(f, raw);
+      store_share(x + at[i], raw);
+    }
+  } else {
+    for (int i = 0; i < kUnits; ++i) {
+      const int64_t u = u0 + i * kCkptWarps;
+      if (u >= units) break;
+      int64_t row, col;
+      unit_place<false>(u, segs, row, col);
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int64_t c = col + 32 * e + lane;
+        f[e] = c < C ? static_cast<float>(codes[row * C + c]) * scale_of(scales[row * nb + c / MOE_CKPT_BLOCK])
+                     : 0.f;
       }
 #pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        if (at[i] < 0) continue;
-        const f2 s = pk(scale_of(byte[i]));
-        f2 f[4];
-        four_values(q[i].x, s, f[0], f[1]);
-        four_values(q[i].y, s, f[2], f[3]);
-        Raw8<T> raw;
-        narrow(f, raw);
-        store_share(x + at[i], raw);
-      }
-    } else {
-      for (int i = 0; i < kUnits; ++i) {
-        const int64_t u = u0 + i * warps;
-        if (u >= units) break;
-        int64_t row = 0, seg = 0;
-        unit_place(u, segs, R == 1, row, seg);
-        float f[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int64_t c = seg * kSegCols + 32 * e + lane;
-          f[e] = c < C ? static_cast<float>(codes[row * C + c]) * scale_of(scales[row * nb + c / MOE_CKPT_BLOCK])
-                       : 0.f;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int64_t c = seg * kSegCols + 32 * e + lane;
-          if (c < C) narrow1(f[e], x + row * C + c);
-        }
+      for (int e = 0; e < 8; ++e) {
+        const int64_t c = col + 32 * e + lane;
+        if (c < C) narrow1(f[e], x + row * C + c);
       }
     }
   }
@@ -318,35 +320,38 @@ int check_rows(const void* x, int32_t x_type, int32_t R, int32_t C, const void* 
 }
 
 struct CkptShape {
-  int64_t R, C, nb;
-  unsigned blocks;
+  int64_t R, C, nb, blocks;
+  int how;
 };
-// At most 16 blocks for each place on the SMs; more units are taken in turn.
-CkptShape ckpt_shape(int64_t R, int64_t C, int at_once) {
-  CkptShape q{R, C, (C + MOE_CKPT_BLOCK - 1) / MOE_CKPT_BLOCK, 0};
-  if (C % MOE_CKPT_BLOCK == 0) {
-    q.C = R * C;
-    q.nb = R * q.nb;
-    q.R = 1;
-  }
-  const int64_t units = q.R * ((q.C + kSegCols - 1) / kSegCols), per = kCkptThreads / 32 * at_once;
-  q.blocks = static_cast<unsigned>(std::min<int64_t>((units + per - 1) / per, 8 * kSMs * 16));
+CkptShape ckpt_shape(const void* x, int32_t x_type, int64_t R, int64_t C, const void* codes, int at_once) {
+  CkptShape q{R, C, (C + MOE_CKPT_BLOCK - 1) / MOE_CKPT_BLOCK, 0, kRows};
+  if (C % 8 != 0 || misaligned(x, x_type == MOE_BF16 ? 16 : 32) || misaligned(codes, 8)) q.how = kSingle;
+  else if (C % MOE_CKPT_BLOCK == 0) q = CkptShape{1, R * C, R * q.nb, 0, kFlat};
+  const int64_t units = q.R * ((q.C + kSegCols - 1) / kSegCols), per = kCkptWarps * at_once;
+  q.blocks = (units + per - 1) / per;
   return q;
 }
 
 template <typename T>
-cudaError_t pack(const CkptShape& q, bool vec, const void* x, int8_t* codes, uint8_t* scales, cudaStream_t s) {
-  return launch_pdl(vec ? ckpt_pack_kernel<T, true> : ckpt_pack_kernel<T, false>, dim3(q.blocks),
-                    dim3(kCkptThreads), 0, s, static_cast<const T*>(x), q.R, q.C, q.nb, codes, scales);
+cudaError_t pack(const void* x, int type, int64_t R, int64_t C, int8_t* codes, uint8_t* scales, cudaStream_t s) {
+  const CkptShape q = ckpt_shape(x, type, R, C, codes, kPackUnits);
+  if (q.blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  return launch_pdl(q.how == kFlat   ? ckpt_pack_kernel<T, kFlat>
+                    : q.how == kRows ? ckpt_pack_kernel<T, kRows>
+                                     : ckpt_pack_kernel<T, kSingle>,
+                    dim3(static_cast<unsigned>(q.blocks)), dim3(kCkptThreads), 0, s, static_cast<const T*>(x), q.R,
+                    q.C, q.nb, codes, scales);
 }
 template <typename T>
-cudaError_t unpack(const CkptShape& q, bool vec, const int8_t* codes, const uint8_t* scales, void* x,
+cudaError_t unpack(const int8_t* codes, const uint8_t* scales, int64_t R, int64_t C, void* x, int type,
                    cudaStream_t s) {
-  return launch_pdl(vec ? ckpt_unpack_kernel<T, true> : ckpt_unpack_kernel<T, false>, dim3(q.blocks),
-                    dim3(kCkptThreads), 0, s, codes, scales, q.R, q.C, q.nb, static_cast<T*>(x));
-}
-bool by_vectors(const void* x, int32_t x_type, int32_t C, const void* codes) {
-  return C % 8 == 0 && !misaligned(x, x_type == MOE_BF16 ? 16 : 32) && !misaligned(codes, 8);
+  const CkptShape q = ckpt_shape(x, type, R, C, codes, kUnpackUnits<T>);
+  if (q.blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  return launch_pdl(q.how == kFlat   ? ckpt_unpack_kernel<T, kFlat>
+                    : q.how == kRows ? ckpt_unpack_kernel<T, kRows>
+                                     : ckpt_unpack_kernel<T, kSingle>,
+                    dim3(static_cast<unsigned>(q.blocks)), dim3(kCkptThreads), 0, s, codes, scales, q.R, q.C, q.nb,
+                    static_cast<T*>(x));
 }
 
 }  // namespace
@@ -362,11 +367,9 @@ int moe_ckpt_pack(const void* x, int32_t x_type, int32_t R, int32_t C, int8_t* c
   const int rc = check_rows(x, x_type, R, C, codes, scales);
   if (rc) return rc;
   if (R == 0) return record_error(MOE_OK, "");
-  const CkptShape q = ckpt_shape(R, C, kPackUnits);
-  const bool vec = by_vectors(x, x_type, C, codes);
   ProbeScope probe("ckpt_pack", stream);
-  const cudaError_t e = x_type == MOE_BF16 ? pack<bf16_t>(q, vec, x, codes, scales, stream)
-                                           : pack<float>(q, vec, x, codes, scales, stream);
+  const cudaError_t e = x_type == MOE_BF16 ? pack<bf16_t>(x, x_type, R, C, codes, scales, stream)
+                                           : pack<float>(x, x_type, R, C, codes, scales, stream);
   if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
   return record_error(MOE_OK, "");
 }
@@ -377,11 +380,9 @@ int moe_ckpt_unpack(const int8_t* codes, const uint8_t* scales, int32_t R, int32
   const int rc = check_rows(x, x_type, R, C, codes, scales);
   if (rc) return rc;
   if (R == 0) return record_error(MOE_OK, "");
-  const CkptShape q = ckpt_shape(R, C, x_type == MOE_BF16 ? kUnpackUnits<bf16_t> : kUnpackUnits<float>);
-  const bool vec = by_vectors(x, x_type, C, codes);
   ProbeScope probe("ckpt_unpack", stream);
-  const cudaError_t e = x_type == MOE_BF16 ? unpack<bf16_t>(q, vec, codes, scales, x, stream)
-                                           : unpack<float>(q, vec, codes, scales, x, stream);
+  const cudaError_t e = x_type == MOE_BF16 ? unpack<bf16_t>(codes, scales, R, C, x, x_type, stream)
+                                           : unpack<float>(codes, scales, R, C, x, x_type, stream);
   if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
   return record_error(MOE_OK, "");
 }
