@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kCkptThreads) ckpt_unpack_kernel(const int8_t*
 // features 60, 64, 70 us).  wide: h is 32-byte aligned.
 __global__ void __launch_bounds__(kCkptThreads) ckpt_unpack_swiglu_kernel(
     const int8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t items, unsigned per, int f,
-    const int32_t* __restrict__ sorted_src, const float* __restrict__ topk_w, int k, int K,
+    const int32_t* __restrict__ sorted_src, const float* __restrict__ topk_w, int P, int k, int K,
     float* __restrict__ h, bool wide, uint16_t* __restrict__ act, int64_t pair) {
   const int64_t base = static_cast<int64_t>(blockIdx.x) * kCkptThreads;
   const int64_t row0 = base / per;
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kCkptThreads) ckpt_unpack_swiglu_kernel(
   pdl_wait();
   if (base + threadIdx.x >= items) return;
   const int src = __ldg(sorted_src + p);
-  if (src < 0) return;
+  if (src < 0 || src >= P) return;  // P = T K
   const int64_t first = p * (16 * static_cast<int64_t>(per)) + 32 * (half >> 1) + 8 * (half & 1);
   const uint2 gate = __ldg(reinterpret_cast<const uint2*>(codes + first));
   const uint2 up = __ldg(reinterpret_cast<const uint2*>(codes + first + 16));
@@ -404,7 +404,7 @@ int moe_ckpt_unpack_swiglu(const int8_t* codes, const uint8_t* scales, int32_t P
   ProbeScope probe("ckpt_unpack_swiglu", stream);
   const cudaError_t e = launch_pdl(ckpt_unpack_swiglu_kernel, dim3(static_cast<unsigned>(blocks)),
                                    dim3(kCkptThreads), 0, stream, codes, scales, items, per, f, sorted_src,
-                                   topk_w, k, k + shared_expert, h, !misaligned(h, 32), act,
+                                   topk_w, P, k, k + shared_expert, h, !misaligned(h, 32), act,
                                    static_cast<int64_t>(P) * f);
   if (e != cudaSuccess) return record_error(MOE_ERR_CUDA, cudaGetErrorString(e));
   return record_error(MOE_OK, "");

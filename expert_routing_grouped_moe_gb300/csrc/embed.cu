@@ -14,9 +14,9 @@
 // a second kernel adds them in order.  So the work is even whatever the ids'
 // frequencies, nothing is atomic, and the order of every sum depends on the ids
 // alone.  What bounds it: T d reads of gradient rows and, dense, V d writes of
-// which most are zeros.  4096 x 2048 into 151936 rows, dense: 214 us (floor 186, the
-// zeros alone 186; the sort runs beside them), 32768 x 2048: 255.  Added to a table
-// instead, 4096 x 2048: 39 us, three launches that wait for one another.
+// which most are zeros.  4096 x 2048 into 151936 rows, dense: 195 us (floor 186, the
+// zeros alone 162; all else runs beside them), 32768 x 2048: 225.  Added to a table
+// instead, 4096 x 2048: 34 us, three launches that wait for one another.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -580,7 +580,8 @@ __device__ __forceinline__ float* part_row(const SumArgs& a, int64_t chunk, int 
   return a.part + (2 * chunk + last) * a.ld;
 }
 
-// Rows whose loads are in flight: 128 bytes a thread.
+// Rows whose loads are in flight: 128 bytes a thread, four rows where each takes two or
+// three aligned words (30011 x 1001 added: 72 us, with eight rows 87).
 template <typename T>
 constexpr int kAhead = 16 / sizeof(T);
 constexpr int kMaxLen = 64, kMaxGroups = 32;
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const SumArgs a) {
   f2 sum[4] = {pk(0.f), pk(0.f), pk(0.f), pk(0.f)};
   const T* dout = static_cast<const T*>(a.dout);
   const uintptr_t begin = reinterpret_cast<uintptr_t>(dout), end = reinterpret_cast<uintptr_t>(dout + a.T * a.d);
-  constexpr int A = kAhead<T>;
+  constexpr int A = VEC ? kAhead<T> : 4;
   for (int i = 0; i < a.len; i += A) {
     Raw8<T> raw[A];
 #pragma unroll
@@ -647,9 +648,10 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const SumArgs a) {
 
 // Runs that reach over chunk borders.  The chunk that a run begins in adds its own part
 // and the first parts of the chunks that follow, up to the one the run ends in.  A block
-// looks at 32 chunks, a lane each; a warp takes 256 columns of a short run by itself, the
-// eight warps every eighth part of a long one, whose sums warp 0 then adds.
-constexpr int kJoinChunks = 32, kLongRun = 32;
+// looks at 16 chunks, a lane each (4096 x 2048 added: 34 us, with 32 chunks 36); a warp
+// takes 256 columns of a short run by itself, the eight warps every eighth part of a long
+// one, whose sums warp 0 then adds.
+constexpr int kJoinChunks = 16, kLongRun = 32;
 template <typename G, bool VEC>
 __global__ void __launch_bounds__(256) embed_join_kernel(const SumArgs a) {
   __shared__ float s_sum[8][256];
@@ -664,12 +666,12 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const SumArgs a) {
   s_first[threadIdx.x] = c0 + threadIdx.x < a.chunks ? a.keys[(c0 + threadIdx.x) * a.len] : none;
   uint32_t key = none, prev = none;
   const int64_t chunk = c0 + lane, i0 = chunk * a.len;
-  if (warp == 0 && chunk < a.chunks - 1) {
+  if (warp == 0 && lane < kJoinChunks && chunk < a.chunks - 1) {
     key = a.keys[i0 + a.len - 1];
     if (i0 > 0) prev = a.keys[i0 - 1];
   }
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 0 && lane < kJoinChunks) {
     int64_t parts = 0;
     if (key != none && s_first[lane + 1] == key && !(s_first[lane] == key && prev == key)) {
       // the last chunk with a part of the run: within reach, or by bisection over first ids

@@ -76,9 +76,10 @@ struct Row {
     tail = (h + V) % E != 0 && !(nw == 1 && head);
   }
   __device__ __forceinline__ int col(int i) const { return i * E - h; }
-  __device__ __forceinline__ uint4 word(int i) const {
-    return *reinterpret_cast<const uint4*>(p + static_cast<int64_t>(i) * E - h);
+  __device__ __forceinline__ const uint4* at(int i) const {
+    return reinterpret_cast<const uint4*>(p + static_cast<int64_t>(i) * E - h);
   }
+  __device__ __forceinline__ uint4 word(int i) const { return *at(i); }
   __device__ __forceinline__ uint4 partial(int i) const;
 };
 template <>
@@ -767,8 +768,13 @@ __global__ void __launch_bounds__(NT, MINB) logprob_kernel(const Args a) {
     const bool zero = empty || !(some || dent != 0.f || dlse != 0.f);
     const Coefs k = coefs(sum_g, dent, dlse, S, ENT ? kLn2 * Us / S : 0.f, a.inv_temp);
     T* drow = static_cast<T*>(a.dx) + t * a.dld;
+    // where a row takes a cluster, the rows in flight fill the L2: what is read for the second
+    // time may leave it first (4096 x 151936: 438 us, 446 otherwise; 16384 x 32000, a block
+    // each: 334, 322)
     gradient_words<T, NT, U, ENT>(row, drow, threadIdx.x, first, end, edge0, edge1, a.same != 0, zero, shift,
-                                  a.floor, k.A, k.B, [&](int i) { return row.word(i); });
+                                  a.floor, k.A, k.B, [&](int i) {
+                                    return nc > 1 ? __ldcs(row.at(i)) : *row.at(i);
+                                  });
     __syncthreads();
     if (!zero)
       for (int j = threadIdx.x; j < a.m; j += NT) {

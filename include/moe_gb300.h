@@ -508,8 +508,9 @@ MOE_API size_t moe_embed_workspace_size(int32_t T, int32_t V, int32_t d);
  *                   as they are (a tied head's gradient, or micro-batches).
  * Tokens with ids[t] = pad_id add nothing (pad_id < 0: no such id); an id
  * outside [0,V) that is not pad_id adds nothing either and sets MOE_ERR_BAD_IDS.
- * ws: moe_embed_workspace_size bytes, 16-byte aligned, its contents need no
- * initialisation.  T = 0 writes zeros, or nothing where it accumulates. */
+ * dtable must not overlap the inputs.  ws: moe_embed_workspace_size bytes, 16-byte
+ * aligned, its contents need no initialisation; calls that may run at the same time
+ * need one each.  T = 0 writes zeros, or nothing where it accumulates. */
 MOE_API int moe_embed_bwd(const moe_embed_desc* desc, const void* ids, const void* dout, void* dtable,
                           int64_t pad_id, int32_t accumulate, void* ws, size_t ws_bytes,
                           moe_stream_t stream);
@@ -598,9 +599,9 @@ MOE_API int moe_ckpt_unpack(const int8_t* codes, const uint8_t* scales, int32_t 
  *   h   [P,hs]   fp32, code 2^(byte - 127)
  *   act [2,P,f]  bf16 pair of w_p silu(gate) up
  * with w_p the weight of the row's slot: topk_w[t,j] where sorted_src[p] = t K + j
- * and j < k, 1 for the shared slot (K = k + shared_expert).  Rows with
- * sorted_src[p] < 0 are left as they are.  f is a multiple of 8; h, act 16-byte
- * aligned, codes 8-byte aligned.  P = 0 does nothing. */
+ * and j < k, 1 for the shared slot (K = k + shared_expert, P = T K).  Rows with
+ * sorted_src[p] outside [0,P) are left as they are.  f is a multiple of 8; h, act
+ * 16-byte aligned, codes 8-byte aligned.  P = 0 does nothing. */
 MOE_API int moe_ckpt_unpack_swiglu(const int8_t* codes, const uint8_t* scales, int32_t P, int32_t f,
                                    const int32_t* sorted_src, const float* topk_w, int32_t k,
                                    int32_t shared_expert, float* h, moe_bf16* act,
