@@ -641,13 +641,50 @@ def _id_type(t, name):
     return code
 
 
-def _here(*tensors):
-    """The calls run on the current device: refuses tensors of another one."""
-    dev = _device() if _raw_stream is not None else torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("a tensor is on cuda:%d, the current device is cuda:%d"
-                             % (t.get_device(), dev))
+def _home(t, name):
+    """Device index of a CUDA tensor, which has to be the current device's: the calls
+    run there."""
+    try:
+        dev = t.get_device()
+    except AttributeError:
+        raise TypeError("%s must be a torch.Tensor" % name) from None
+    if dev < 0:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    current = _device() if _raw_stream is not None else torch.cuda.current_device()
+    if dev != current:
+        raise ValueError("%s is on cuda:%d, the current device is cuda:%d" % (name, dev, current))
+    return dev
+
+
+def _at(t, shape, dtype, dev, name):
+    """_shaped for a tensor that also has to be on device dev (None stays None)."""
+    if t is None:
+        return None
+    try:
+        if (t.dtype is dtype and t.get_device() == dev and t.shape == shape
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    p = _shaped(t, shape, dtype, name)   # says what is wrong
+    if t.get_device() != dev:
+        raise ValueError("%s must be on cuda:%d" % (name, dev))
+    return p
+
+
+def _needed(t, name):
+    if t is None:
+        raise TypeError("%s must be a torch.Tensor" % name)
+
+
+def _bytes(ws, dev):
+    """Pointer and size of a workspace (None: none)."""
+    if ws is None:
+        return None, 0
+    p = _ptr(ws, name="ws")
+    if ws.get_device() != dev:
+        raise ValueError("ws must be on cuda:%d" % dev)
+    return p, ws.numel() * ws.element_size()
 
 
 @functools.lru_cache(maxsize=256)
@@ -657,26 +694,27 @@ def _embed_desc(T, V, d, id_type, table, rows, scale):
 
 
 def _embed_setup(ids, rows, table, scale, names):
-    """Descriptor of a lookup of ids [...] in a table [V,d] with rows [...,d]."""
+    """Descriptor of a lookup of ids [...] in a table [V,d] with rows [...,d], and the
+    pointers of ids, rows, table."""
     code = _id_type(ids, "ids")
-    for t, name in zip((rows, table), names):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("%s must be a torch.Tensor" % name)
+    _needed(rows, names[0])
+    dev = _home(table, names[1])
     if table.dim() != 2:
         raise ValueError("%s must be [V, d], got %s" % (names[1], tuple(table.shape)))
     V, d = table.shape
-    return _embed_desc(ids.numel(), V, d, code, table.dtype, rows.dtype, float(scale))
+    sh = ids.shape
+    p = (_at(ids, sh, ids.dtype, dev, "ids"), _at(rows, (*sh, d), rows.dtype, dev, names[0]),
+         _at(table, (V, d), table.dtype, dev, names[1]))
+    desc = _embed_desc(ids.numel(), V, d, code, table.dtype, rows.dtype, float(scale))
+    return desc, p, dev
 
 
 def moe_embed_fwd(ids, table, out, scale=1.0, stream=None):
     """out[...,d] = scale * table[ids]; ids [...] int32 or int64, table [V,d], out of
     ids' shape and d; both fp32 or bf16.  An id outside the table gives zeros and
     MOE_ERR_BAD_IDS in the status word."""
-    desc = _embed_setup(ids, out, table, scale, ("out", "table"))
-    sh = ids.shape + table.shape[1:]
-    args = (_ptr(ids, name="ids"), _ptr(table, name="table"), _shaped(out, sh, out.dtype, "out"))
-    _here(ids, table, out)
-    _check(load().moe_embed_fwd(desc, *args, _stream(stream)), "moe_embed_fwd")
+    desc, (i, o, w), _ = _embed_setup(ids, out, table, scale, ("out", "table"))
+    _check(load().moe_embed_fwd(desc, i, w, o, _stream(stream)), "moe_embed_fwd")
 
 
 def moe_embed_workspace_size(T, V, d) -> int:
@@ -687,16 +725,12 @@ def moe_embed_bwd(ids, dout, dtable, ws, scale=1.0, pad_id=None, accumulate=Fals
     """dtable [V,d] = scale * the sum of dout's rows for each id (dense: rows without a
     token are zeros), or += where accumulate.  Tokens with id pad_id add nothing.
     ws: moe_embed_workspace_size(tokens, V, d) bytes."""
-    desc = _embed_setup(ids, dout, dtable, scale, ("dout", "dtable"))
+    desc, (i, o, w), dev = _embed_setup(ids, dout, dtable, scale, ("dout", "dtable"))
     if pad_id is not None and pad_id < 0:
         raise ValueError("pad_id must not be negative")
-    sh = ids.shape + dtable.shape[1:]
-    args = (_ptr(ids, name="ids"), _shaped(dout, sh, dout.dtype, "dout"),
-            _ptr(dtable, name="dtable"), -1 if pad_id is None else int(pad_id),
-            1 if accumulate else 0, _ptr(ws, name="ws"),
-            0 if ws is None else ws.numel() * ws.element_size())
-    _here(ids, dout, dtable, ws)
-    _check(load().moe_embed_bwd(desc, *args, _stream(stream)), "moe_embed_bwd")
+    _check(load().moe_embed_bwd(desc, i, o, w, -1 if pad_id is None else int(pad_id),
+                                1 if accumulate else 0, *_bytes(ws, dev), _stream(stream)),
+           "moe_embed_bwd")
 
 
 @functools.lru_cache(maxsize=256)
@@ -705,53 +739,44 @@ def _logprob_desc(T, V, m, top, dtype, target_type, ld, dld, ignore_id, inv_temp
                                        target_type, ld, dld, ignore_id, inv_temp))
 
 
-def _matrix(t, shape, dtype, name):
-    """Pointer and row stride of [T,V] whose rows are dense (not always adjacent)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
-        raise ValueError("%s must be [T, V]%s, got %s" % (
-            name, "" if shape is None else " = %s" % (tuple(shape),), tuple(t.shape)))
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    T, V = t.shape
-    if (V > 1 and t.stride(1) != 1) or (T > 1 and t.stride(0) < V):
+def _matrix(t, name):
+    """Pointer, T, V and row stride of [T,V] whose rows are dense (not always adjacent)."""
+    if t.dim() != 2:
+        raise ValueError("%s must be [T, V], got %s" % (name, tuple(t.shape)))
+    (T, V), (ld, step) = t.shape, t.stride()
+    if (V > 1 and step != 1) or (T > 1 and ld < V):
         raise ValueError("%s must have dense rows that do not overlap" % name)
-    return t.data_ptr(), t.stride(0) if T > 1 else V
+    return t.data_ptr(), T, V, ld if T > 1 else V
 
 
-def _logprob_rows(logits, targets, dlogits, top_ids, top_logp, inv_temp, ignore_id):
-    """Descriptor and the pointers of logits, targets, dlogits."""
-    x, ld = _matrix(logits, None, None, "logits")
-    T, V = logits.shape
+def _logprob_setup(logits, targets, dlogits, top_ids, top_logp, inv_temp, ignore_id):
+    """Descriptor, the pointers of logits, targets, dlogits, top_ids and top_logp, the
+    shape of targets, the device."""
+    dev = _home(logits, "logits")
+    x, T, V, ld = _matrix(logits, "logits")
     code = _id_type(targets, "targets")
-    if targets.dim() not in (1, 2) or targets.shape[0] != T:
-        raise ValueError("targets must be [T] or [T, m] with T = %d, got %s"
-                         % (T, tuple(targets.shape)))
-    dx, dld = (None, V) if dlogits is None else _matrix(dlogits, logits.shape, logits.dtype,
-                                                        "dlogits")
-    top = 0
-    for t, name in ((top_ids, "top_ids"), (top_logp, "top_logp")):
-        if t is not None:
-            if t.dim() != 2 or t.shape[0] != T or (top and t.shape[1] != top):
+    ysh = targets.shape
+    if len(ysh) not in (1, 2) or ysh[0] != T:
+        raise ValueError("targets must be [T] or [T, m] with T = %d, got %s" % (T, tuple(ysh)))
+    y = _at(targets, ysh, targets.dtype, dev, "targets")
+    dx, dld = None, V
+    if dlogits is not None:
+        if _home(dlogits, "dlogits") != dev or dlogits.dtype is not logits.dtype or (
+                dlogits.shape != (T, V)):
+            raise ValueError("dlogits must be like logits: %s %s, got %s %s" % (
+                logits.dtype, (T, V), dlogits.dtype, tuple(dlogits.shape)))
+        dx, _, _, dld = _matrix(dlogits, "dlogits")
+    top, ids, lp = 0, None, None
+    if top_ids is not None or top_logp is not None:
+        for t, name in ((top_ids, "top_ids"), (top_logp, "top_logp")):
+            if t is not None and (t.dim() != 2 or t.shape[0] != T):
                 raise ValueError("%s must be [T, top], got %s" % (name, tuple(t.shape)))
-            top = t.shape[1]
-    m = 1 if targets.dim() == 1 else targets.shape[1]
-    desc = _logprob_desc(T, V, m, top, logits.dtype, code, ld, dld, int(ignore_id),
-                         float(inv_temp))
-    return desc, x, _ptr(targets, name="targets"), dx
-
-
-def _logprob_out(logits, targets, logp, stats, lse, entropy, top_ids, top_logp):
-    T, f32 = logits.shape[0], torch.float32
-    for t, name in ((logp, "logp"), (stats, "stats")):
-        if t is None:
-            raise TypeError("%s must be a torch.Tensor" % name)
-    return (_shaped(logp, targets.shape, f32, "logp"), _shaped(stats, (T, 2), f32, "stats"),
-            _shaped(lse, (T,), f32, "lse"), _shaped(entropy, (T,), f32, "entropy"),
-            _i32(top_ids, "top_ids"), _f32(top_logp, "top_logp"))
+        top = (top_ids if top_ids is not None else top_logp).shape[1]
+        ids = _at(top_ids, (T, top), torch.int32, dev, "top_ids")
+        lp = _at(top_logp, (T, top), torch.float32, dev, "top_logp")
+    desc = _logprob_desc(T, V, 1 if len(ysh) == 1 else ysh[1], top, logits.dtype, code, ld, dld,
+                         int(ignore_id), float(inv_temp))
+    return desc, x, y, dx, ids, lp, T, ysh, dev
 
 
 def moe_logprob_fwd(logits, targets, logp, stats, lse=None, entropy=None, top_ids=None,
@@ -761,25 +786,29 @@ def moe_logprob_fwd(logits, targets, logp, stats, lse=None, entropy=None, top_id
     stride; optionally each row's log sum of exponentials, its entropy, and its
     likeliest tokens (top_ids int32, top_logp [T,top]).  stats [T,2]: for the
     backward.  A target ignore_id gets 0."""
-    desc, x, y, _ = _logprob_rows(logits, targets, None, top_ids, top_logp, inv_temp, ignore_id)
-    out = _logprob_out(logits, targets, logp, stats, lse, entropy, top_ids, top_logp)
-    _here(logits, targets, logp, stats, lse, entropy, top_ids, top_logp)
-    _check(load().moe_logprob_fwd(desc, x, y, *out, _stream(stream)), "moe_logprob_fwd")
+    _needed(logp, "logp")
+    _needed(stats, "stats")
+    desc, x, y, _, ids, lp, T, ysh, dev = _logprob_setup(logits, targets, None, top_ids, top_logp,
+                                                         inv_temp, ignore_id)
+    f32 = torch.float32
+    _check(load().moe_logprob_fwd(
+        desc, x, y, _at(logp, ysh, f32, dev, "logp"), _at(stats, (T, 2), f32, dev, "stats"),
+        _at(lse, (T,), f32, dev, "lse"), _at(entropy, (T,), f32, dev, "entropy"), ids, lp,
+        _stream(stream)), "moe_logprob_fwd")
 
 
 def moe_logprob_bwd(logits, targets, stats, dlogp, dlogits, entropy=None, dentropy=None, dlse=None,
                     inv_temp=1.0, ignore_id=-100, stream=None):
     """dlogits [T,V] (may be logits) from the gradients of logp, entropy and lse, each
     of which may be None; stats and, with dentropy, entropy as the forward wrote them."""
-    if dlogits is None:
-        raise TypeError("dlogits must be a torch.Tensor")
-    desc, x, y, dx = _logprob_rows(logits, targets, dlogits, None, None, inv_temp, ignore_id)
-    T, f32 = logits.shape[0], torch.float32
-    args = (_shaped(stats, (T, 2), f32, "stats"), _shaped(entropy, (T,), f32, "entropy"),
-            _shaped(dlogp, targets.shape, f32, "dlogp"),
-            _shaped(dentropy, (T,), f32, "dentropy"), _shaped(dlse, (T,), f32, "dlse"))
-    _here(logits, targets, stats, entropy, dlogp, dentropy, dlse, dlogits)
-    _check(load().moe_logprob_bwd(desc, x, y, *args, dx, _stream(stream)), "moe_logprob_bwd")
+    _needed(dlogits, "dlogits")
+    desc, x, y, dx, _, _, T, ysh, dev = _logprob_setup(logits, targets, dlogits, None, None, inv_temp,
+                                                       ignore_id)
+    f32 = torch.float32
+    _check(load().moe_logprob_bwd(
+        desc, x, y, _at(stats, (T, 2), f32, dev, "stats"), _at(entropy, (T,), f32, dev, "entropy"),
+        _at(dlogp, ysh, f32, dev, "dlogp"), _at(dentropy, (T,), f32, dev, "dentropy"),
+        _at(dlse, (T,), f32, dev, "dlse"), dx, _stream(stream)), "moe_logprob_bwd")
 
 
 def moe_logprob_step(logits, targets, logp, stats, dlogp, dlogits, dentropy=None, dlse=None,
@@ -787,69 +816,63 @@ def moe_logprob_step(logits, targets, logp, stats, dlogp, dlogits, dentropy=None
                      ignore_id=-100, stream=None):
     """moe_logprob_fwd and moe_logprob_bwd in one call, for gradients that are known
     ahead; reads the logits from memory once."""
-    if dlogits is None:
-        raise TypeError("dlogits must be a torch.Tensor")
-    desc, x, y, dx = _logprob_rows(logits, targets, dlogits, top_ids, top_logp, inv_temp,
-                                   ignore_id)
-    T, f32 = logits.shape[0], torch.float32
-    grads = (_shaped(dlogp, targets.shape, f32, "dlogp"),
-             _shaped(dentropy, (T,), f32, "dentropy"), _shaped(dlse, (T,), f32, "dlse"))
-    out = _logprob_out(logits, targets, logp, stats, lse, entropy, top_ids, top_logp)
-    _here(logits, targets, dlogp, dentropy, dlse, logp, stats, lse, entropy, top_ids, top_logp,
-          dlogits)
-    _check(load().moe_logprob_step(desc, x, y, *grads, *out, dx, _stream(stream)),
-           "moe_logprob_step")
+    for t, name in ((logp, "logp"), (stats, "stats"), (dlogits, "dlogits")):
+        _needed(t, name)
+    desc, x, y, dx, ids, lp, T, ysh, dev = _logprob_setup(logits, targets, dlogits, top_ids, top_logp,
+                                                          inv_temp, ignore_id)
+    f32 = torch.float32
+    _check(load().moe_logprob_step(
+        desc, x, y, _at(dlogp, ysh, f32, dev, "dlogp"), _at(dentropy, (T,), f32, dev, "dentropy"),
+        _at(dlse, (T,), f32, dev, "dlse"), _at(logp, ysh, f32, dev, "logp"),
+        _at(stats, (T, 2), f32, dev, "stats"), _at(lse, (T,), f32, dev, "lse"),
+        _at(entropy, (T,), f32, dev, "entropy"), ids, lp, dx, _stream(stream)), "moe_logprob_step")
 
 
 def _ckpt_rows(x, codes, scales):
-    """Type, R, C and pointers of rows x [R,C], their codes and scales."""
-    p = _ptr(x, name="x")
-    if x is None or x.dim() != 2:
-        raise ValueError("x must be [R, C]")
-    code = _type(x.dtype, "x")
-    R, C = x.shape
-    if codes is None or scales is None:
-        raise TypeError("codes and scales must be torch.Tensors")
-    q = (_shaped(codes, x.shape, torch.int8, "codes"),
-         _shaped(scales, (R, -(-C // MOE_CKPT_BLOCK)), torch.uint8, "scales"))
-    _here(x, codes, scales)
-    return p, code, _rows(R), _rows(C), q
+    """Pointer, type, R, C of rows x [R,C], pointers of their codes and scales, device."""
+    dev = _home(x, "x")
+    _needed(codes, "codes")
+    _needed(scales, "scales")
+    sh = x.shape
+    if len(sh) != 2:
+        raise ValueError("x must be [R, C], got %s" % (tuple(sh),))
+    R, C = sh
+    return (_at(x, sh, x.dtype, dev, "x"), _type(x.dtype, "x"), _rows(R), _rows(C),
+            _at(codes, sh, torch.int8, dev, "codes"),
+            _at(scales, (R, -(-C // MOE_CKPT_BLOCK)), torch.uint8, dev, "scales"), dev)
 
 
 def moe_ckpt_pack(x, codes, scales, stream=None):
     """x [R,C] fp32 or bf16 into 8 bits: codes [R,C] int8 and a power-of-two scale for
     each 32 values of a row, scales [R, ceil(C/32)] uint8 (exponent bytes)."""
-    p, code, R, C, q = _ckpt_rows(x, codes, scales)
-    _check(load().moe_ckpt_pack(p, code, R, C, *q, _stream(stream)), "moe_ckpt_pack")
+    p, code, R, C, q, s, _ = _ckpt_rows(x, codes, scales)
+    _check(load().moe_ckpt_pack(p, code, R, C, q, s, _stream(stream)), "moe_ckpt_pack")
 
 
 def moe_ckpt_unpack(codes, scales, x, stream=None):
     """x [R,C] fp32 or bf16 = the values that moe_ckpt_pack's codes stand for."""
-    p, code, R, C, q = _ckpt_rows(x, codes, scales)
-    _check(load().moe_ckpt_unpack(*q, R, C, p, code, _stream(stream)), "moe_ckpt_unpack")
+    p, code, R, C, q, s, _ = _ckpt_rows(x, codes, scales)
+    _check(load().moe_ckpt_unpack(q, s, R, C, p, code, _stream(stream)), "moe_ckpt_unpack")
 
 
 def moe_ckpt_unpack_swiglu(codes, scales, sorted_src, topk_w, shared_expert, h, act, stream=None):
     """A layer's saved h [P,hs] fp32 from its 8-bit codes, and act [2,P,f] (bf16 pair) =
     w_p silu(gate) up, w_p being topk_w's weight of sorted row p's slot."""
-    p, code, P, C, q = _ckpt_rows(h, codes, scales)
+    for t, name in ((sorted_src, "sorted_src"), (topk_w, "topk_w"), (act, "act")):
+        _needed(t, name)
+    p, code, P, C, q, s, dev = _ckpt_rows(h, codes, scales)
     if code != MOE_F32:
         raise ValueError("h must be torch.float32")
-    if act is None or act.dim() != 3 or C != 32 * ((act.shape[2] + 15) // 16):
+    ash, wsh, shared = act.shape, topk_w.shape, 1 if shared_expert else 0
+    if len(ash) != 3 or C != 32 * ((ash[2] + 15) // 16):
         raise ValueError("act must be [2, P, f] with 32 * ceil(f / 16) columns of h")
-    if topk_w is None or topk_w.dim() != 2:
-        raise ValueError("topk_w must be [T, k]")
-    T, k = topk_w.shape
-    if T * (k + (1 if shared_expert else 0)) != P:
-        raise ValueError("h has %d rows for %d tokens" % (P, T))
-    f = act.shape[2]
-    args = (_shaped(sorted_src, (P,), torch.int32, "sorted_src"), _f32(topk_w, "topk_w"), k,
-            1 if shared_expert else 0, p, _shaped(act, (2, P, f), torch.bfloat16, "act"))
-    if sorted_src is None:
-        raise TypeError("sorted_src must be a torch.Tensor")
-    _here(sorted_src, topk_w, act)
-    _check(load().moe_ckpt_unpack_swiglu(*q, P, f, *args, _stream(stream)),
-           "moe_ckpt_unpack_swiglu")
+    if len(wsh) != 2 or wsh[0] * (wsh[1] + shared) != P:
+        raise ValueError("topk_w must be [T, k] with T (k + shared) = %d, got %s" % (P, tuple(wsh)))
+    _check(load().moe_ckpt_unpack_swiglu(
+        q, s, P, ash[2], _at(sorted_src, (P,), torch.int32, dev, "sorted_src"),
+        _at(topk_w, wsh, torch.float32, dev, "topk_w"), wsh[1], shared, p,
+        _at(act, (2, P, ash[2]), torch.bfloat16, dev, "act"), _stream(stream)),
+        "moe_ckpt_unpack_swiglu")
 
 
 def moe_status(stream=None) -> int:
