@@ -236,7 +236,9 @@ __device__ __forceinline__ uint64_t token_key(uint32_t o, uint32_t col) {
   return (static_cast<uint64_t>(o) << 32) | (0xFFFFFFFFu - col);
 }
 
+constexpr int kBuckets = 64;
 struct TopShared {
+  int bucket[kBuckets];
   uint64_t cand[kCandidates];
   uint64_t out[kMaxTop];    // the block's n best, in order; 0: none
   uint64_t red[32];
@@ -263,60 +265,75 @@ __device__ __forceinline__ void rank_candidates(TopShared& s, int count, int n) 
 // A thread's words are seen in P parts, each a run of `step` words of the block's (a
 // multiple of NT; the last may be shorter): the largest logit of a part stands for it.
 // Four in blocks of 256 threads, whose threads have up to 75 words of a row of 151936
-// logits; one in smaller blocks, where all threads find the n-th best together sooner
-// than a warp does (one row of 151936, 20 tokens: 14.9 us against 20.5).
+// logits, one in others.
 template <int NT>
 constexpr int kParts = NT == 256 ? 4 : 1;
 
 // The n best of words [a, b) of a row, which the block's threads read NT apart, and of
-// the partial words edge0 and edge1 (-1: none).  s.best: the largest logit of each part
-// of each thread.
+// the partial words edge0 and edge1 (-1: none).  s_best: the order of the largest
+// logit of each part of each thread; largest: of all of them, or above.
 template <typename T, int NT>
 __device__ __forceinline__ void block_top(TopShared& s, uint32_t (&s_best)[kParts<NT> * NT], const Row<T>& row, int a,
-                                          int b, int step, int edge0, int edge1, int n) {
+                                          int b, int step, int edge0, int edge1, uint32_t largest, int n) {
   constexpr int P = kParts<NT>;
   const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) s.nwin = s.count = 0;
+  for (int i = threadIdx.x; i < kBuckets; i += NT) s.bucket[i] = 0;
   __syncthreads();
-  // the n-th largest of the parts' orders: the largest v that n of them reach, bit by bit
-  constexpr int kLastBit = sizeof(T) == 2 ? 16 : 0;  // bf16 has 16 bits
-  constexpr int kFew = P * NT / 32;                  // parts that a lane of the first warp looks at
-  uint32_t v = 1;
-  if (P == 1) {
-    const uint32_t o = s_best[threadIdx.x];
-    int above = __syncthreads_count(o != 0);
-    if (above > n) {
-      v = 0;
-      for (int bit = 31; bit >= kLastBit && above != n; --bit) {
-        const int k = __syncthreads_count(o >= (v | (1u << bit)));
-        if (k >= n) v |= 1u << bit, above = k;
-      }
-    }
-    if (threadIdx.x == 0) s.above = above;
-  } else if (threadIdx.x < 32) {
-    uint32_t o[kFew];
-    int above = 0;
+  // What the parts' orders have to reach: first from counts of them in buckets of four steps
+  // of a bf16 below the largest, which let in a few more than n.
 #pragma unroll
-    for (int i = 0; i < kFew; ++i) {
-      o[i] = s_best[32 * i + lane];
-      above += o[i] != 0;
-    }
-    above = __reduce_add_sync(0xffffffffu, above);
-    if (above > n) {
-      v = 0;
-      for (int bit = 31; bit >= kLastBit && above != n; --bit) {
-        int k = 0;
-#pragma unroll
-        for (int i = 0; i < kFew; ++i) k += o[i] >= (v | (1u << bit));
-        k = __reduce_add_sync(0xffffffffu, k);
-        if (k >= n) v |= 1u << bit, above = k;
-      }
-    }
-    if (lane == 0) s.above = above;
+  for (int i = 0; i < P; ++i) {
+    const uint32_t o = s_best[i * NT + threadIdx.x], below = (largest >> 16) - (o >> 16);
+    if (o != 0 && below / 4 < kBuckets) atomicAdd(&s.bucket[below / 4], 1);
   }
-  // the last 16 bits of a bf16's order are its sign's: ones where it is negative
-  if (sizeof(T) == 2 && v != 1 && !(v & 0x80000000u)) v |= 0xFFFFu;
-  if (threadIdx.x == 0) s.least = v;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int b0 = s.bucket[2 * lane], b1 = s.bucket[2 * lane + 1];
+    int upto = b0 + b1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int q = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += q;
+    }
+    const unsigned enough = __ballot_sync(0xffffffffu, upto >= n);
+    uint32_t v = 1;
+    int above = -1;
+    if (enough != 0) {
+      const int l = __ffs(enough) - 1;
+      const int all = __shfl_sync(0xffffffffu, upto, l), less = __shfl_sync(0xffffffffu, upto - b1, l);
+      above = less >= n ? less : all;
+      const uint32_t reach = 4 * (2 * l + (less >= n ? 0 : 1)) + 3, top = largest >> 16;
+      v = max(1u, (top > reach ? top - reach : 0u) << 16);
+    }
+    // where the n are further down, or too many that near: the largest v that n of them
+    // reach, bit by bit
+    if (above < 0 || above > kWinners) {
+      constexpr int kFew = P * NT / 32;  // parts that a lane looks at
+      uint32_t o[kFew];
+      above = 0;
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) {
+        o[i] = s_best[32 * i + lane];
+        above += o[i] != 0;
+      }
+      above = __reduce_add_sync(0xffffffffu, above);
+      v = 1;
+      if (above > n) {
+        v = 0;
+        for (int bit = 31; bit >= (sizeof(T) == 2 ? 16 : 0) && above != n; --bit) {  // bf16: 16 bits
+          int k = 0;
+#pragma unroll
+          for (int i = 0; i < kFew; ++i) k += o[i] >= (v | (1u << bit));
+          k = __reduce_add_sync(0xffffffffu, k);
+          if (k >= n) v |= 1u << bit, above = k;
+        }
+        // the last 16 bits of a bf16's order are its sign's: ones where it is negative
+        if (sizeof(T) == 2 && !(v & 0x80000000u)) v |= 0xFFFFu;
+      }
+    }
+    if (lane == 0) s.least = v, s.above = above;
+  }
   __syncthreads();
   const uint32_t least = s.least;
   int last = 0x7FFFFFFF;
@@ -660,7 +677,7 @@ __global__ void __launch_bounds__(NT, MINB) logprob_kernel(const Args a) {
   const float block_at = M > -INFINITY ? M * a.c : kUnset;
   relate(sums.at, block_at, S, Us);
   block_sums(S, Us);
-  if (TOP) block_top<T, NT>(s_top, s_best, row, first, end, step, edge0, edge1, a.top);
+  if (TOP) block_top<T, NT>(s_top, s_best, row, first, end, step, edge0, edge1, ordered(M), a.top);
 
   // over the cluster
   if (nc > 1) {
@@ -853,20 +870,21 @@ __global__ void __launch_bounds__(kBwdThreads, 5) logprob_bwd_kernel(const Args 
 }
 
 // ---- launches -----------------------------------------------------------------------------
-// Threads of a block: about 8 words each, 256 where a row is longer.  Blocks of a row:
+// Threads of a block: about 8 words each, 256 where a row is longer, 512 where there are
+// few rows (one of 151936 logits, its 20 likeliest: 8.2 us, with 256 threads 9.9).  Blocks of a row:
 // one where that gives four for each SM, more, up to eight, where there are fewer rows.
 // With the gradient also as many as it takes for the rows in flight, five blocks to an
 // SM, to stay in the L2 until their second reading.
 constexpr int kLane = 256, kSmall = 2048;       // words of a block up to which it has 32, 128 threads
 constexpr int64_t kInFlight = int64_t(80) << 20;
 
-template <typename T, int NT, int MINB, bool GRAD>
+template <typename T, int NT, int MINB, bool GRAD, int U = 4>
 cudaError_t rows(const Args& a, unsigned cluster, cudaStream_t s) {
   const bool ent = a.entropy != nullptr || a.dent != nullptr;
-  auto kernel = a.top > 0 ? (ent ? logprob_kernel<T, NT, MINB, 4, true, true, GRAD>
-                                 : logprob_kernel<T, NT, MINB, 4, true, false, GRAD>)
-                          : (ent ? logprob_kernel<T, NT, MINB, 4, false, true, GRAD>
-                                 : logprob_kernel<T, NT, MINB, 4, false, false, GRAD>);
+  auto kernel = a.top > 0 ? (ent ? logprob_kernel<T, NT, MINB, U, true, true, GRAD>
+                                 : logprob_kernel<T, NT, MINB, U, true, false, GRAD>)
+                          : (ent ? logprob_kernel<T, NT, MINB, U, false, true, GRAD>
+                                 : logprob_kernel<T, NT, MINB, U, false, false, GRAD>);
   return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(a.T) * cluster), dim3(NT), 0, s, cluster, a);
 }
 template <typename T>
@@ -882,6 +900,11 @@ cudaError_t launch_rows(const Args& a, cudaStream_t s) {
           (GRAD && words > kSmall && words * 16 * (5 * kSMs / cluster) > kInFlight)))
     cluster *= 2;
   const int64_t each = (words + cluster - 1) / cluster;
+  // so few rows that every block has half an SM: all of a thread's loads at once.  (256, as not
+  // every SM has a place in a cluster of eight: 38 rows in 304 blocks take two turns, 14.6 us
+  // against 11.4 with 256 threads.)
+  if (each > kSmall / 2 && static_cast<int64_t>(a.T) * cluster <= 256)
+    return rows<T, 512, 2, GRAD, 8>(a, cluster, s);
   return each <= kLane    ? rows<T, 32, 20, GRAD>(a, cluster, s)
          : each <= kSmall ? rows<T, 128, 8, GRAD>(a, cluster, s)
          : a.top > 0     ? rows<T, 256, 4, GRAD>(a, cluster, s)
