@@ -14,7 +14,7 @@
 // a second kernel adds them in order.  So the work is even whatever the ids'
 // frequencies, nothing is atomic, and the order of every sum depends on the ids
 // alone.  What bounds it: T d reads of gradient rows and, dense, V d writes of
-// which most are zeros.  4096 x 2048 into 151936 rows, dense: 195 us (floor 186, the
+// which most are zeros.  4096 x 2048 into 151936 rows, dense: 179 us (floor 186 at the rate of a copy; the
 // zeros alone 162; all else runs beside them), 32768 x 2048: 225.  Added to a table
 // instead, 4096 x 2048: 34 us, three launches that wait for one another.
 #include <algorithm>
@@ -428,6 +428,29 @@ __global__ void __launch_bounds__(1024) embed_mark_kernel(const Source src, int 
 // Zeros for the rows without a token (`named`, complete before the sort began), beside
 // the sort, the sums and the joins of a small batch, which write the others.  It is
 // launched last, while those wait for one another, and a block waits for them at its end.
+// Rows of whole words on 16-byte boundaries: a block takes `each` rows, about 16 KB, and
+// mostly finds none of them named.
+__global__ void __launch_bounds__(kZeroThreads) embed_zero_whole_rows_kernel(const uint32_t* __restrict__ named,
+                                                                            uint4* __restrict__ p, int64_t V,
+                                                                            int each, int row_words) {
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * each;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(each), V - row0));
+  auto is_named = [&](int64_t r) { return named[r >> 5] >> (r & 31) & 1u; };
+  bool any = false;
+  for (int r = threadIdx.x; r < rows; r += kZeroThreads) any |= is_named(row0 + r) != 0;
+  uint4* w = p + row0 * row_words;
+  const int words = rows * row_words;
+  if (!__syncthreads_or(any)) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < words; i += kZeroThreads) w[i] = make_uint4(0u, 0u, 0u, 0u);
+  } else {
+    for (int i = threadIdx.x; i < words; i += kZeroThreads)
+      if (!is_named(row0 + i / row_words)) w[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (blockIdx.x == 0) pdl_wait();
+}
+
+// The same for rows that begin anywhere, by the words of the whole table.
 __global__ void __launch_bounds__(kZeroThreads) embed_zero_rows_kernel(const uint32_t* __restrict__ named,
                                                                       uint8_t* __restrict__ p, int64_t bytes,
                                                                       int head, unsigned row_bytes, int size) {
@@ -815,7 +838,12 @@ cudaError_t mark_rows(const Source& src, int n, uint32_t* named, cudaStream_t s)
                     dim3(1024), 0, s, src, n, named);
 }
 cudaError_t zero_rows(const uint32_t* named, void* p, int64_t V, int64_t d, unsigned size, cudaStream_t s) {
-  const int64_t bytes = V * d * size;
+  const int64_t bytes = V * d * size, row_bytes = d * size;
+  if (row_bytes % 16 == 0 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+    const int64_t each = std::max<int64_t>(1, 16 * kZeroBlock / row_bytes), blocks = (V + each - 1) / each;
+    return launch_pdl(embed_zero_whole_rows_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kZeroThreads), 0, s,
+                      named, static_cast<uint4*>(p), V, static_cast<int>(each), static_cast<int>(row_bytes / 16));
+  }
   if (zero_blocks(bytes) > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   return launch_pdl(embed_zero_rows_kernel, dim3(static_cast<unsigned>(zero_blocks(bytes))), dim3(kZeroThreads), 0, s,
                     named, static_cast<uint8_t*>(p), bytes, head_of(p, bytes), static_cast<unsigned>(d * size),
