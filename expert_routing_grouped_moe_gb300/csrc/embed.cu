@@ -14,9 +14,9 @@
 // a second kernel adds them in order.  So the work is even whatever the ids'
 // frequencies, nothing is atomic, and the order of every sum depends on the ids
 // alone.  What bounds it: T d reads of gradient rows and, dense, V d writes of
-// which most are zeros.  4096 x 2048 into 151936 rows, dense: 179 us (floor 186 at the rate of a copy; the
-// zeros alone 162; all else runs beside them), 32768 x 2048: 225.  Added to a table
-// instead, 4096 x 2048: 34 us, three launches that wait for one another.
+// which most are zeros.  4096 x 2048 into 151936 rows, dense: 179 us (186 at a copy's
+// rate; the zeros alone 162, all else runs beside them), 32768 x 2048: 225.  Added to a
+// table instead, 4096 x 2048: 34 us, three launches that wait for one another.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
