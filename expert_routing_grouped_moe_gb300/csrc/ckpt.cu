@@ -393,6 +393,7 @@ int moe_ckpt_unpack_swiglu(const int8_t* codes, const uint8_t* scales, int32_t P
   NvtxScope nvtx("moe_ckpt_unpack_swiglu");
   if (P < 0 || f <= 0 || f % 8 != 0) return bad("P must not be negative, f a positive multiple of 8");
   if (k <= 0 || k > 32 || (shared_expert != 0 && shared_expert != 1)) return bad("bad k or shared_expert");
+  if (P % (k + shared_expert) != 0) return bad("P must be a multiple of k + shared_expert");
   if (P == 0) return record_error(MOE_OK, "");
   if (!codes || !scales || !sorted_src || !topk_w || !h || !act) return bad("NULL pointer");
   if (misaligned(codes, 8) || misaligned(sorted_src, 4) || misaligned(topk_w, 4) || misaligned(h, 16) ||

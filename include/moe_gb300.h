@@ -564,8 +564,7 @@ MOE_API int moe_logprob_bwd(const moe_logprob_desc* desc, const void* logits, co
 /* Forward and backward in one call, for losses whose weights are known ahead
  * (dlogp = -1 / tokens, say): same arguments and results as the two in turn, but
  * for the order in which a row's sums are taken (entropy may be NULL here even with
- * dentropy); each row is read from memory once and held on the chip until its
- * gradient is written. */
+ * dentropy); a row's second reading comes from the L2. */
 MOE_API int moe_logprob_step(const moe_logprob_desc* desc, const void* logits, const void* targets,
                              const float* dlogp, const float* dentropy, const float* dlse,
                              float* logp, float* stats, float* lse, float* entropy,
@@ -601,7 +600,8 @@ MOE_API int moe_ckpt_unpack(const int8_t* codes, const uint8_t* scales, int32_t 
  * with w_p the weight of the row's slot: topk_w[t,j] where sorted_src[p] = t K + j
  * and j < k, 1 for the shared slot (K = k + shared_expert, P = T K).  Rows with
  * sorted_src[p] outside [0,P) are left as they are.  f is a multiple of 8; h, act
- * 16-byte aligned, codes 8-byte aligned.  P = 0 does nothing. */
+ * 16-byte aligned, codes 8-byte aligned; a P that no T gives is refused.  P = 0
+ * does nothing. */
 MOE_API int moe_ckpt_unpack_swiglu(const int8_t* codes, const uint8_t* scales, int32_t P, int32_t f,
                                    const int32_t* sorted_src, const float* topk_w, int32_t k,
                                    int32_t shared_expert, float* h, moe_bf16* act,

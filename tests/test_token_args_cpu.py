@@ -132,6 +132,12 @@ def test_ckpt(L):
                                               args[5], None) == bad
 
 
+@pytest.mark.parametrize("P,k,shared", [(5, 2, 0), (8, 2, 1), (1, 1, 1)])
+def test_rows_that_are_not_whole_tokens(L, P, k, shared):
+    """P rows are T tokens' k slots (and shared one): the last weight read is topk_w[T - 1]."""
+    assert L.load().moe_ckpt_unpack_swiglu(A, A, P, 64, A, A, k, shared, A, A, None) == L.MOE_ERR_INVALID_ARG
+
+
 def test_nothing_to_do_is_no_error(L):
     lib = L.load()
     assert lib.moe_embed_fwd(embed(L, T=0), None, None, None, None) == L.MOE_OK
