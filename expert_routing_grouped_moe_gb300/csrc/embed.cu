@@ -428,6 +428,7 @@ __global__ void __launch_bounds__(1024) embed_mark_kernel(const Source src, int 
 // Zeros for the rows without a token (`named`, complete before the sort began), beside
 // the sort, the sums and the joins of a small batch, which write the others.  It is
 // launched last, while those wait for one another, and a block waits for them at its end.
+// As it has not waited for the marks' launch itself, it reads them from the L2.
 // Rows of whole words on 16-byte boundaries: a block takes `each` rows, about 16 KB, and
 // mostly finds none of them named.
 __global__ void __launch_bounds__(kZeroThreads) embed_zero_whole_rows_kernel(const uint32_t* __restrict__ named,
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(kZeroThreads) embed_zero_whole_rows_kernel(con
                                                                             int each, int row_words) {
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * each;
   const int rows = static_cast<int>(min(static_cast<int64_t>(each), V - row0));
-  auto is_named = [&](int64_t r) { return named[r >> 5] >> (r & 31) & 1u; };
+  auto is_named = [&](int64_t r) { return __ldcg(named + (r >> 5)) >> (r & 31) & 1u; };
   bool any = false;
   for (int r = threadIdx.x; r < rows; r += kZeroThreads) any |= is_named(row0 + r) != 0;
   uint4* w = p + row0 * row_words;
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(kZeroThreads) embed_zero_rows_kernel(const uin
   const int64_t from = static_cast<int64_t>(blockIdx.x) * kZeroBlock * 16 + head;
   const int64_t row0 = from / row_bytes;
   const unsigned off0 = static_cast<unsigned>(from - row0 * row_bytes);
-  auto is_named = [&](int64_t r) { return named[r >> 5] >> (r & 31) & 1u; };
+  auto is_named = [&](int64_t r) { return __ldcg(named + (r >> 5)) >> (r & 31) & 1u; };
 #pragma unroll
   for (int u = 0; u < kZeroWords; ++u) {
     const unsigned at = 16u * (threadIdx.x + u * kZeroThreads);
