@@ -18,7 +18,8 @@ from . import _lib as L
 
 class LayerScratch:
     """Device buffers by name, each as large as its largest user asked for; users get
-    views.  What one call leaves there the next call of any layer overwrites."""
+    views.  What one call leaves there the next call of any layer overwrites, so the
+    layers of one scratch take turns: on one stream, or ordered by their caller."""
 
     def __init__(self, device="cuda"):
         self.device = torch.device(device)

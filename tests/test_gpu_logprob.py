@@ -156,6 +156,15 @@ def test_values_and_gradient(T, V, dtype, m, top, off, pad):
     assert L.moe_status() == L.MOE_OK
 
 
+@pytest.mark.parametrize("T,V,dtype,top,off", [(761, 17000, BF, 0, 0), (1216, 9001, F32, 0, 1),
+                                               (609, 16501, F32, 4, 3), (900, 20001, BF, 32, 5)])
+def test_rows_just_above_the_places_for_blocks(T, V, dtype, top, off):
+    c = Case(T, V, dtype, 1, top, off, 0)
+    c.fwd()
+    c.check_fwd()
+    assert L.moe_status() == L.MOE_OK
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("inv", [0.25, 1.0, 1.7])
 def test_temperature_in_place_and_without_entropy(dtype, inv):
