@@ -168,28 +168,32 @@ __global__ void __launch_bounds__(kCkptThreads) ckpt_pack_kernel(const T* __rest
       }
     }
   } else {
+    float f[kPackUnits][8];
+    int64_t at[kPackUnits], block[kPackUnits];  // of the lane's first value, of the unit's first block
+    int left[kPackUnits];                       // columns from the lane's first value to the row's end
+#pragma unroll
     for (int i = 0; i < kPackUnits; ++i) {
-      const int64_t u = u0 + i * kCkptWarps;
-      if (u >= units) break;
       int64_t row, col;
-      unit_place<false>(u, segs, row, col);
-      float f[8];
+      unit_place<false>(u0 + i * kCkptWarps, segs, row, col);
+      at[i] = row * C + col + lane;
+      block[i] = row * nb + col / MOE_CKPT_BLOCK;
+      left[i] = u0 + i * kCkptWarps < units ? static_cast<int>(C - col) - lane : 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[i][e] = 32 * e < left[i] ? widen1(x[at[i] + 32 * e]) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kPackUnits; ++i) {
+      uint32_t mine = 0;  // the scale of block `lane`
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int64_t c = col + 32 * e + lane;
-        f[e] = c < C ? widen1(x[row * C + c]) : 0.f;
+        uint32_t byte = scale_byte(__reduce_max_sync(0xffffffffu, abs_bits(f[i][e])));
+        if (byte == kMaxByte + 1) byte = kMaxByte, f[i][e] = cut(f[i][e]);
+        const uint32_t q = __float_as_uint(fmaf(f[i][e], inverse_scale(byte), kRoundShift));
+        if (32 * e < left[i]) codes[at[i] + 32 * e] = static_cast<int8_t>(byte == 255u ? 0u : q & 0xFFu);
+        if (lane == e) mine = byte;
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int64_t c = col + 32 * e + lane;
-        uint32_t byte = scale_byte(__reduce_max_sync(0xffffffffu, abs_bits(f[e])));
-        if (byte == kMaxByte + 1) byte = kMaxByte, f[e] = cut(f[e]);
-        const uint32_t q = __float_as_uint(fmaf(f[e], inverse_scale(byte), kRoundShift));
-        if (c < C) {
-          codes[row * C + c] = static_cast<int8_t>(byte == 255u ? 0u : q & 0xFFu);
-          if (lane == 0) scales[row * nb + c / MOE_CKPT_BLOCK] = static_cast<uint8_t>(byte);
-        }
-      }
+      // lane e is e columns from the unit's first; block e begins 31 e further on
+      if (lane < 8 && 31 * lane < left[i]) scales[block[i] + lane] = static_cast<uint8_t>(mine);
     }
   }
 }
@@ -233,24 +237,27 @@ __global__ void __launch_bounds__(kCkptThreads) ckpt_unpack_kernel(const int8_t*
       store_share(x + at[i], raw);
     }
   } else {
+    int q[kUnits][8];
+    uint32_t byte[kUnits];  // the scale of block `lane`
+    int64_t at[kUnits];
+    int left[kUnits];
+#pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const int64_t u = u0 + i * kCkptWarps;
-      if (u >= units) break;
       int64_t row, col;
-      unit_place<false>(u, segs, row, col);
-      float f[8];
+      unit_place<false>(u0 + i * kCkptWarps, segs, row, col);
+      at[i] = row * C + col + lane;
+      left[i] = u0 + i * kCkptWarps < units ? static_cast<int>(C - col) - lane : 0;
+      byte[i] = lane < 8 && 31 * lane < left[i] ? __ldg(scales + row * nb + col / MOE_CKPT_BLOCK + lane) : 0u;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int64_t c = col + 32 * e + lane;
-        f[e] = c < C ? static_cast<float>(codes[row * C + c]) * scale_of(scales[row * nb + c / MOE_CKPT_BLOCK])
-                     : 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int64_t c = col + 32 * e + lane;
-        if (c < C) narrow1(f[e], x + row * C + c);
-      }
+      for (int e = 0; e < 8; ++e) q[i][e] = 32 * e < left[i] ? __ldg(codes + at[i] + 32 * e) : 0;
     }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float scale = scale_of(__shfl_sync(0xffffffffu, byte[i], e));
+        if (32 * e < left[i]) narrow1(static_cast<float>(q[i][e]) * scale, x + at[i] + 32 * e);
+      }
   }
 }
 
