@@ -183,17 +183,33 @@ __global__ void __launch_bounds__(kCkptThreads) ckpt_pack_kernel(const T* __rest
     }
 #pragma unroll
     for (int i = 0; i < kPackUnits; ++i) {
-      uint32_t mine = 0;  // the scale of block `lane`
+      // the 8 blocks' largest, that of block lane / 4 in each lane: in each exchange a lane
+      // hands half of its blocks to another.  (32768 x 1001: 41 us, with a reduction over
+      // the warp for each block, and its scale in every lane, 52.)
+      uint32_t big[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) big[e] = abs_bits(f[i][e]);
+#pragma unroll
+      for (int n = 4; n > 0; n >>= 1) {
+        const bool upper = (lane & 4 * n) != 0;
+#pragma unroll
+        for (int e = 0; e < n; ++e) {
+          const uint32_t give = upper ? big[e] : big[e + n], keep = upper ? big[e + n] : big[e];
+          big[e] = max(keep, __shfl_xor_sync(0xffffffffu, give, 4 * n));
+        }
+      }
+      big[0] = max(big[0], __shfl_xor_sync(0xffffffffu, big[0], 2));
+      big[0] = max(big[0], __shfl_xor_sync(0xffffffffu, big[0], 1));
+      uint32_t byte = scale_byte(big[0]);
+      if (byte == kMaxByte + 1) byte = kMaxByte;
+      const float inverse = byte == 255u ? 0.f : inverse_scale(byte);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        uint32_t byte = scale_byte(__reduce_max_sync(0xffffffffu, abs_bits(f[i][e])));
-        if (byte == kMaxByte + 1) byte = kMaxByte, f[i][e] = cut(f[i][e]);
-        const uint32_t q = __float_as_uint(fmaf(f[i][e], inverse_scale(byte), kRoundShift));
-        if (32 * e < left[i]) codes[at[i] + 32 * e] = static_cast<int8_t>(byte == 255u ? 0u : q & 0xFFu);
-        if (lane == e) mine = byte;
+        const float s = __shfl_sync(0xffffffffu, inverse, 4 * e);
+        const uint32_t q = __float_as_uint(fmaf(cut(f[i][e]), s, kRoundShift));
+        if (32 * e < left[i]) codes[at[i] + 32 * e] = static_cast<int8_t>(s == 0.f ? 0u : q & 0xFFu);
       }
-      // lane e is e columns from the unit's first; block e begins 31 e further on
-      if (lane < 8 && 31 * lane < left[i]) scales[block[i] + lane] = static_cast<uint8_t>(mine);
+      if ((lane & 3) == 0 && 7 * lane < left[i]) scales[block[i] + lane / 4] = static_cast<uint8_t>(byte);
     }
   }
 }
