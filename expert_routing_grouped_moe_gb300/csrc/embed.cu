@@ -451,7 +451,9 @@ __global__ void __launch_bounds__(kZeroThreads) embed_zero_whole_rows_kernel(con
   if (blockIdx.x == 0) pdl_wait();
 }
 
-// The same for rows that begin anywhere, by the words of the whole table.
+// The same for rows that begin anywhere, by the words of the whole table.  A word holds
+// values of two rows at most where a row has its 16 bytes; narrower rows are looked up
+// value by value.
 __global__ void __launch_bounds__(kZeroThreads) embed_zero_rows_kernel(const uint32_t* __restrict__ named,
                                                                       uint8_t* __restrict__ p, int64_t bytes,
                                                                       int head, unsigned row_bytes, int size) {
@@ -459,6 +461,7 @@ __global__ void __launch_bounds__(kZeroThreads) embed_zero_rows_kernel(const uin
   const int64_t from = static_cast<int64_t>(blockIdx.x) * kZeroBlock * 16 + head;
   const int64_t row0 = from / row_bytes;
   const unsigned off0 = static_cast<unsigned>(from - row0 * row_bytes);
+  const bool wide = row_bytes >= 16;
   auto is_named = [&](int64_t r) { return __ldcg(named + (r >> 5)) >> (r & 31) & 1u; };
 #pragma unroll
   for (int u = 0; u < kZeroWords; ++u) {
@@ -466,9 +469,9 @@ __global__ void __launch_bounds__(kZeroThreads) embed_zero_rows_kernel(const uin
     if (from + at + 16 > bytes) continue;
     const int64_t r = row0 + (off0 + at) / row_bytes, q = row0 + (off0 + at + 15) / row_bytes;
     const bool a = is_named(r), b = q != r && is_named(q);
-    if (!a && !b) {
+    if (wide && !a && !b) {
       *reinterpret_cast<uint4*>(p + from + at) = make_uint4(0u, 0u, 0u, 0u);
-    } else if (q != r && !(a && b)) {  // two rows' values
+    } else if (!wide || (q != r && !(a && b))) {
       for (unsigned e = 0; e < 16; e += size)
         if (!is_named(row0 + (off0 + at + e) / row_bytes)) {
           if (size == 2) *reinterpret_cast<uint16_t*>(p + from + at + e) = 0;

@@ -117,6 +117,31 @@ def test_gradient(T, V, d, rows, table, kind, scale, add, off):
     assert torch.equal(again, dw)
 
 
+@pytest.mark.parametrize("T", [40, 9000])
+@pytest.mark.parametrize("table", [BF, F32])
+@pytest.mark.parametrize("d", [1, 2, 3, 4, 5, 6, 7, 8, 9, 17])
+def test_dense_gradient_of_narrow_tables(d, table, T):
+    """Rows of which several fit a 16-byte word, from every place within one, over garbage: rows
+    with and without a token in turn, alone and in pairs; a small batch (rows without a token
+    are found one by one) and a larger one (all are zeroed ahead of the sums)."""
+    g = gen(100 * d + T)
+    V = 301
+    rows = torch.arange(V, device=DEV)
+    some = torch.cat([rows[:100:2], rows[100:200:4], rows[101:200:4], rows[200::7], rows[-1:]])
+    ids = some[torch.randint(0, some.numel(), (T,), generator=g, device=DEV)]
+    ids[:some.numel()] = some[:T]
+    dout = torch.randn(T, d, generator=g, device=DEV)
+    ref, mag, n = to.embed_grad(ids.cpu().numpy(), np64(dout), V)
+    ws = workspace(T, V, d)
+    for off in range(16 // (2 if table == BF else 4)):
+        dw, untouched = place((V, d), table, off)
+        dw.fill_(float("nan"))
+        L.moe_embed_bwd(ids, dout, dw, ws)
+        close(dw, ref, (n[:, None] + 4) * U * mag + HALF[table] * np.abs(ref))
+        assert not np64(dw)[n == 0].any() and untouched(), off
+    assert L.moe_status() == L.MOE_OK
+
+
 @pytest.mark.parametrize("ids", [torch.int32, torch.int64])
 @pytest.mark.parametrize("add", [False, True])
 def test_gradient_with_padding_and_bad_ids(ids, add):
