@@ -214,6 +214,11 @@ struct Shift {
     extreme = !(fabsf(at) < kExtreme);
   }
   __device__ __forceinline__ float t(float x) const { return extreme ? (x - M) * c : fmaf(x, c, -at); }
+  // ln of x's share of a sum.  Where t overflows, its factor log2 e may be all that did.
+  __device__ __forceinline__ float log_share(float x, float log_S, float inv_temp) const {
+    const float e = t(x);
+    return e == -INFINITY ? (x - M) * inv_temp - log_S : fmaf(kLn2, e, -log_S);
+  }
 };
 // An extreme row's sums, its largest logit known.
 template <typename T>
@@ -765,7 +770,9 @@ __global__ void __launch_bounds__(NT, MINB) logprob_kernel(const Args a) {
   const float log_S = logf(S);
   if (rank == 0) {
     for (int j = threadIdx.x; j < a.m; j += NT)
-      a.logp[t * a.m + j] = s_y.y[j] < 0 ? 0.f : empty ? -INFINITY : fmaf(kLn2, shift.t(s_y.x[j]), -log_S);
+      a.logp[t * a.m + j] = s_y.y[j] < 0 ? 0.f
+                            : empty      ? -INFINITY
+                                         : shift.log_share(s_y.x[j], log_S, a.inv_temp);
     if (threadIdx.x == 0) {
       a.stats[2 * t] = shift.M;
       a.stats[2 * t + 1] = S;
@@ -777,7 +784,8 @@ __global__ void __launch_bounds__(NT, MINB) logprob_kernel(const Args a) {
       const int64_t at = t * a.top + threadIdx.x;
       if (a.top_ids != nullptr) a.top_ids[at] = key != 0 ? static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key)) : -1;
       if (a.top_logp != nullptr)
-        a.top_logp[at] = key != 0 ? fmaf(kLn2, shift.t(from_ordered(static_cast<uint32_t>(key >> 32))), -log_S) : -INFINITY;
+        a.top_logp[at] = key == 0 ? -INFINITY
+                                  : shift.log_share(from_ordered(static_cast<uint32_t>(key >> 32)), log_S, a.inv_temp);
     }
   }
   if (GRAD) {

@@ -246,6 +246,23 @@ def test_a_target_that_is_masked():
     c.check_bwd(r)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_target_of_the_lowest_value(dtype):
+    """Its log probability is the type's lowest value too, and finite; listed last."""
+    low = torch.finfo(dtype).min
+    x = torch.full((2, 64), low, device=DEV)
+    x[0, 3], x[1, :60] = 1.0, 0.5
+    c = Case(2, 64, dtype, 2, 4, x=x, y=torch.tensor([[5, 3], [63, 0]], device=DEV))
+    r = c.ref()
+    c.fwd()
+    c.check_fwd(r)
+    assert torch.isfinite(c.logp).all() and torch.isfinite(c.top_logp).all()
+    c.bwd()
+    c.check_bwd(r)
+    c.step()
+    c.check_fwd(r)
+
+
 @pytest.mark.parametrize("V", [90, 30000])
 @pytest.mark.parametrize("what", [float("nan"), INF])
 def test_rows_that_are_not_finite_spoil_themselves_only(V, what):
