@@ -8,9 +8,10 @@
 // One pass over a row: a thread keeps the sums relative to a shift of its own, t = x c -
 // shift in one fused operation, and moves them when a logit exceeds it by 2^4 (each t
 // is then off by 4 * 2^-24 at most, and most words move nothing).  The row's shift is
-// its largest logit times c, rounded, the same for every use.  Rows whose largest logit
-// is so large or small that products with c overflow (all of them the type's lowest
-// value, say) are summed once more with t = (x - M) c.
+// its largest logit times c, rounded, the same for every use.  That rounding is half a
+// step of M c, so it takes rows with |M c| below 2^22; the others (all of a row masked
+// by some low value, say) are summed once more with t = (x - M) c.  Lower logits than
+// that are no shift of a thread's either: next to such a row's largest they are nothing.
 //
 // The likeliest n tokens cost the pass over the row next to nothing: a thread has the
 // largest logit of its words at hand, and notes it for each quarter of them.  The n best
@@ -40,9 +41,11 @@ namespace {
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kSlack = 4.f;      // how far t may exceed 0 before a thread's sums move
 constexpr float kLeast = -1000.f;  // t of a logit of -inf, whose 2^t is 0
-// |M c| from which a row is extreme; the shift before any logit was seen, below every
-// other one; and what t c of a logit of -inf counts as where t is needed, lower still.
-constexpr float kExtreme = 1e37f, kUnset = -1.5e37f, kFloor = -2e37f;
+// |M c| from which a row is extreme (the rounding of M c is 2^-3 at most below it); a
+// thread's shift before it saw a logit above that, below every other row's; and what x c
+// counts as where t is needed and x c is lower still.  Apart by 2^21 each, so that 2^t is 0
+// from one to the next, and small enough for t times any gradient to stay finite.
+constexpr float kExtreme = 0x1p22f, kUnset = -0x1.8p22f, kFloor = -0x1p23f;
 constexpr int kMaxTargets = MOE_LOGPROB_MAX_TARGETS, kMaxTop = MOE_LOGPROB_MAX_TOP;
 constexpr int kMaxCluster = 8;
 constexpr int kCandidates = 512;   // that are sorted at once
@@ -685,7 +688,7 @@ __global__ void __launch_bounds__(NT, MINB) logprob_kernel(const Args a) {
 #pragma unroll
   for (int i = 0; i < W; ++i) M = fmaxf(M, s_m[i]);
   float S = sum2(sums.S), Us = ENT ? sum2(sums.U) : 0.f;
-  const float block_at = M > -INFINITY ? M * a.c : kUnset;
+  const float block_at = fmaxf(M * a.c, kUnset);
   relate(sums.at, block_at, S, Us);
   block_sums(S, Us);
   if (TOP) block_top<T, NT>(s_top, s_best, row, first, end, step, edge0, edge1, ordered(M), a.top);
@@ -707,7 +710,7 @@ __global__ void __launch_bounds__(NT, MINB) logprob_kernel(const Args a) {
       M = fmaxf(M, pm[r]);
     }
     S = Us = 0.f;
-    const float at = M > -INFINITY ? M * a.c : kUnset;
+    const float at = fmaxf(M * a.c, kUnset);
 #pragma unroll
     for (unsigned r = 0; r < kMaxCluster; ++r) {
       relate(pa[r], at, ps[r], pu[r]);
@@ -969,7 +972,7 @@ int fill(const moe_logprob_desc* q, const void* logits, const void* targets, Arg
   a.t64 = q->target_type == MOE_I64; a.ignore = q->ignore_id;
   a.inv_temp = q->inv_temp;
   a.c = static_cast<float>(static_cast<double>(q->inv_temp) * 1.4426950408889634074);
-  const float low = std::fmax(kFloor / a.c, -3e38f);
+  const float low = kFloor / a.c;  // inv_temp >= 1e-30: above the types' lowest value
   std::memcpy(&a.floor, &low, 4);
   if (q->type == MOE_BF16) a.floor = (a.floor >> 16) | (a.floor & 0xFFFF0000u);
   return MOE_OK;

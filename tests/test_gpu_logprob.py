@@ -234,6 +234,92 @@ def test_masked_rows(V, dtype):
     c.check_bwd(r)
 
 
+def masked_rows(V, value, g):
+    """Rows with `value` in whole words and threads' shares, scattered, everywhere, and all but
+    one place; one more row is as large as the value is low."""
+    x = torch.randn(8, V, generator=g, device=DEV)
+    x[0, :3 * V // 4] = value
+    x[1, V // 3:] = value
+    x[2], x[2, V // 2] = value, 1.5
+    x[3] = value
+    x[4, torch.rand(V, generator=g, device=DEV) < 0.5] = value
+    x[5], x[5, V // 3] = value, -INF
+    x[6, V - 2] = 1e30
+    x[7, :V // 2] = -INF
+    y = torch.tensor([[V - 1], [0], [V // 2], [4], [1], [0], [V - 2], [V - 1]], device=DEV)
+    x[4, 1] = 0.25
+    return x, y
+
+
+@pytest.mark.parametrize("V", [300, 40001])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("value", [-1e4, -1e7, -1e10, -1e30, "lowest", -INF])
+@pytest.mark.parametrize("inv", [1.0, 0.7])
+def test_masks_of_any_value(V, dtype, value, inv):
+    """Logits of any size count as far below the rest, in the words of a thread that sees
+    nothing else too; a row of nothing else is uniform."""
+    x, y = masked_rows(V, torch.finfo(dtype).min if value == "lowest" else value, gen(V))
+    c = Case(8, V, dtype, 1, 6, x=x.to(dtype).float(), y=y, inv=inv)
+    r = c.ref()
+    c.fwd()
+    c.check_fwd(r)
+    c.bwd()
+    c.check_bwd(r)
+    c.clear()
+    c.dwhole.fill_(11)
+    c.step()
+    c.check_fwd(r)
+    c.check_bwd(r)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("value", [-1e30, "lowest", -INF])
+@pytest.mark.parametrize("inv", [1e-30, 1e-3, 0.01, 0.03, 0.045])
+def test_masks_at_any_temperature(dtype, value, inv):
+    x, y = masked_rows(5000, torch.finfo(dtype).min if value == "lowest" else value, gen(8))
+    c = Case(8, 5000, dtype, 1, 6, x=x.to(dtype).float(), y=y, inv=inv)
+    r = c.ref()
+    c.fwd()
+    c.check_fwd(r)
+    c.bwd()
+    c.check_bwd(r)
+    c.clear()
+    c.dwhole.fill_(11)
+    c.step()
+    c.check_fwd(r)
+    c.check_bwd(r)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_the_lowest_temperature(dtype):
+    """All of a row's probability on its best tokens, two of them in one row."""
+    x, y = masked_rows(700, -INF, gen(9))
+    x[6, 698], x[5] = 30.0, 2.0
+    x[4, 9], x[4, 500] = 20.0, 20.0
+    c = Case(8, 700, dtype, 1, 6, x=x.to(dtype).float(), y=y, inv=1e30)
+    r = c.ref()
+    c.fwd()
+    c.check_fwd(r)
+    c.bwd()
+    c.check_bwd(r)
+
+
+@pytest.mark.parametrize("V", [300, 40001])
+@pytest.mark.parametrize("value", [-1e30, "lowest", -INF])
+def test_large_gradients_of_the_entropy(V, value):
+    """p = 0 has no gradient, however large its logarithm times the entropy's gradient is."""
+    x, y = masked_rows(V, torch.finfo(BF).min if value == "lowest" else value, gen(V))
+    c = Case(8, V, BF, 1, x=x.to(BF).float(), y=y)
+    c.dh.mul_(1e6)
+    r = c.ref()
+    c.fwd()
+    c.bwd()
+    c.check_bwd(r)
+    c.dwhole.fill_(11)
+    c.step()
+    c.check_bwd(r)
+
+
 def test_a_target_that_is_masked():
     x = torch.zeros(2, 64, device=DEV)
     x[:, 5] = -INF
