@@ -283,12 +283,12 @@ bool make_map_mn4d(CUtensorMap* m, const void* base, uint64_t G, uint64_t rows, 
 }
 
 bool make_map_split4d(CUtensorMap* m, const void* base, uint64_t G, uint64_t half,
-                      uint64_t cols, uint32_t box_rows, uint32_t box_cols) {
+                      uint64_t cols, uint32_t box_rows, uint32_t box_cols, uint32_t halves) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[4] = {cols, half, 2, G};
   const cuuint64_t strides[3] = {cols * 2, half * cols * 2, 2 * half * cols * 2};
-  const cuuint32_t box[4] = {box_cols, box_rows, 2, 1};
+  const cuuint32_t box[4] = {box_cols, box_rows, halves, 1};
   const cuuint32_t es[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -388,6 +388,13 @@ int run_gemm(const GemmShape& sh, GemmParams& p, int64_t row_tiles, int num_sms,
 #define MAP3(dst, ptr, g, rows, cols, br, bc)                                      \
   do {                                                                             \
     if (!make_map_3d(&(dst), (ptr), (g), (rows), (cols), (br), (bc)))              \
+      return fail(MOE_ERR_CUDA, "tensor map encode failed (%s)", #ptr);            \
+  } while (0)
+
+// Gate and up rows of [G, 2 half, cols] as halves of 128-row boxes; rows past a half read 0.
+#define MAP_SPLIT(dst, ptr, half, cols, halves)                                    \
+  do {                                                                             \
+    if (!make_map_split4d(&(dst), (ptr), G, (half), (cols), 128, 64, (halves)))    \
       return fail(MOE_ERR_CUDA, "tensor map encode failed (%s)", #ptr);            \
   } while (0)
 
@@ -662,22 +669,15 @@ int moe_lora_grouped_mlp_fwd(const moe_dims* dims, const moe_bf16* Xp, const moe
   const bool pair_rows = pair_tiles(dims, kPairDown, true);
   const int64_t R2 = max_pair_tiles(dims->T, dims->k + dims->shared_expert, G);
   {  // h = Xp W_gu^T + (s xa) B_gu^T (fp32) ; act pair = w * silu(gate) * up
-    // (B boxes of 128 rows: one gate or up half; a CTA pair stages one each)
+    // (B boxes of 128 rows of a half, so that h past f is 0: both halves' at once, or one
+    // each for the CTAs of a pair)
     GemmParams p = base;
-    SLICE_ROWS(p, 0, Xp, X, d, MAP3(p.sl[0].b, W_gu, G, 2 * f, d, 128, 64), d);
-    SLICE(p, 1, xa_gu, N, r, MAP3(p.sl[1].b, B_gu, G, 2 * f, r, 128, 64), r);
-    SLICE(p, 2, xa_gu + Nr, N, r, MAP3(p.sl[2].b, B_gu, G, 2 * f, r, 128, 64), r);
-    p.nslices = 3; p.N = f; p.n_ntiles = (f + 127) / 128; p.b_split = f;
+    const uint32_t halves = pair_x ? 1 : 2;
+    SLICE_ROWS(p, 0, Xp, X, d, MAP_SPLIT(p.sl[0].b, W_gu, f, d, halves), d);
+    SLICE(p, 1, xa_gu, N, r, MAP_SPLIT(p.sl[1].b, B_gu, f, r, halves), r);
+    SLICE(p, 2, xa_gu + Nr, N, r, MAP_SPLIT(p.sl[2].b, B_gu, f, r, halves), r);
+    p.nslices = 3; p.N = f; p.n_ntiles = (f + 127) / 128; p.b4d = 1;
     p.fout = h; p.ldf = 32 * ((f + 15) / 16); p.ld0 = 2 * f; p.out0 = act; p.pair = Nf;
-    if (!pair_x) {  // one 4-D box per K block for both halves (the 3-D maps stay as fallback)
-      GemmSlice q[3] = {p.sl[0], p.sl[1], p.sl[2]};
-      if (make_map_split4d(&q[0].b, W_gu, G, f, d, 128, 64) &&
-          make_map_split4d(&q[1].b, B_gu, G, f, r, 128, 64) &&
-          make_map_split4d(&q[2].b, B_gu, G, f, r, 128, 64)) {
-        for (int i = 0; i < 3; ++i) p.sl[i] = q[i];
-        p.b4d = 1;
-      }
-    }
     if ((rc = run_gemm({256, false, false, Epi::kSwiGLU, pair_x}, p, pair_x ? R2 : R, st->num_sms,
                        s, "gate_up")))
       return rc;

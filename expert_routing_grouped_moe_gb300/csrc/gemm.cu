@@ -565,8 +565,9 @@ __device__ __forceinline__ void epi_dgrad_dn(const GemmParams& p, const TileInfo
     }
     // Columns past f in a partial last chunk need no mask: this tile's
     // accumulator is exactly 0 there (W_dn and A_dn columns TMA zero-fills) and
-    // the h the forward stored there is finite, so they add 0 to dot, and
-    // their dh is not stored.
+    // the h the forward stored there is 0 (restored from 8 bits, NaN where its
+    // features are), so they add nothing to dot that those do not, and their dh
+    // is not stored.
     float dg[16], du[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -1010,10 +1011,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<BN, EPI, PAIR, B_MN>::kCtasPerSm
                     tma_load_3d_pair(sb + c * kChunkBytes, mb, fbl, ti.nt * BN + half + c * 64, kc,
                                      ti.g);
                 }
-              } else if (p.b_split) {
+              } else if (p.b4d) {
                 // gate_up: the even CTA stages the gate rows, the odd one the up rows
-                tma_load_3d_pair(sb, mb, fbl, kc,
-                                 ti.nt * (BN / 2) + static_cast<int>(crank) * p.b_split, ti.g);
+                tma_load_4d_pair(sb, mb, fbl, kc, ti.nt * (BN / 2), static_cast<int>(crank), ti.g);
               } else {
                 tma_load_3d_pair(sb, mb, fbl, kc, ti.nt * BN + half, ti.g);
               }
@@ -1034,13 +1034,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BN, EPI, PAIR, B_MN>::kCtasPerSm
                   if (!B_MN) tma_load_4d(sb, mb, fb, kc, ti.nt * (BN / 2), 0, ti.g);
                   else tma_load_4d(sb, mb, fb, 0, kc, ti.nt * (BN / 64), ti.g);
                 } else if (!B_MN) {
-                  if (p.b_split) {
-                    const int n0 = ti.nt * (BN / 2);
-                    tma_load_3d(sb, mb, fb, kc, n0, ti.g);
-                    tma_load_3d(sb + (BN / 2) * 128, mb, fb, kc, n0 + p.b_split, ti.g);
-                  } else {
-                    tma_load_3d(sb, mb, fb, kc, ti.nt * BN, ti.g);
-                  }
+                  tma_load_3d(sb, mb, fb, kc, ti.nt * BN, ti.g);
                 } else {
 #pragma unroll
                   for (int c = 0; c < BN / 64; ++c)

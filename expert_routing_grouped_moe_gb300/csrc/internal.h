@@ -193,9 +193,8 @@ struct GemmParams {
   int M;              // wgrad: rows of the weight gradient (d, f or 2f)
   int n_ntiles;       // N tiles per M tile (rows mode) / M tiles per group (wgrad)
   int n_btiles;       // wgrad: N tiles over the B matrix's columns (1 for the LoRA gradients)
-  int b_split;        // rows offset of the second B half (gate/up pairing), 0 = none
   int b4d;            // every slice's B map is 4-D: one box per K block (MN-major
-                      // 64-column chunks, or the two gate/up halves)
+                      // 64-column chunks, or the gate/up halves: both, or a pair's one each)
   int G, k, K;        // groups, top-k, slots per token
   float scale;        // LoRA scale s
   const int32_t* tile_off;
@@ -263,10 +262,11 @@ bool make_map_3d(CUtensorMap* m, const void* base, uint64_t G, uint64_t rows, ui
 // mn: (64 columns, rows, cols / 64 chunks, G), box (64, box_rows, chunks, 1),
 //     landing as `chunks` consecutive [box_rows][64] blocks; cols % 64 == 0.
 // split: rows = two halves of `half` rows: (cols, half, 2, G), box
-//     (box_cols, box_rows, 2, 1), landing as the two halves' blocks.
+//     (box_cols, box_rows, halves, 1), landing as the halves' blocks; rows past a
+//     half read 0.
 bool make_map_mn4d(CUtensorMap* m, const void* base, uint64_t G, uint64_t rows, uint64_t cols,
                    uint32_t box_rows, uint32_t chunks);
 bool make_map_split4d(CUtensorMap* m, const void* base, uint64_t G, uint64_t half,
-                      uint64_t cols, uint32_t box_rows, uint32_t box_cols);
+                      uint64_t cols, uint32_t box_rows, uint32_t box_cols, uint32_t halves);
 
 }  // namespace moe

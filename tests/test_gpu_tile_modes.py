@@ -29,3 +29,15 @@ def test_random_shapes_in_tile_mode(mode):
                        timeout=900)
     assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-2000:]
     assert " passed" in r.stdout
+
+
+@pytest.mark.parametrize("mode", ["1", "0"])
+def test_no_features_past_the_last_in_tile_mode(mode):
+    env = dict(os.environ, MOE_PAIR_TILES=mode)
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-p",
+                        "no:cacheprovider", os.path.join(HERE, "test_gpu_tokens.py"),
+                        "-k", "no_feature or own_features"],
+                       env=env, cwd=os.path.dirname(HERE), capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-2000:]
+    assert "7 passed" in r.stdout

@@ -72,6 +72,45 @@ def test_checkpointed_gradients_are_near_the_exact_ones(cfg):
         assert off < 0.03, (n, float(off))
 
 
+def wide_ups(cfg, seed, times=1000.0, **kw):
+    """A layer whose first eight up features are large, and its inputs."""
+    w = synth.layer_weights(cfg, seed, device=DEV)
+    w["W_gu"][:, cfg.f:cfg.f + 8] *= times
+    a = synth.layer_activations(cfg, seed, device=DEV)
+    ids = torch.empty(cfg.T, cfg.k, dtype=torch.int32, device=DEV)
+    tw = torch.empty(cfg.T, cfg.k, device=DEV)
+    L.moe_router_topk(a["logits"], cfg.k, ids, tw)
+    make = lambda **k2: MoELoRALayer(cfg.T, cfg.d, cfg.f, cfg.E, cfg.k, cfg.r, cfg.alpha, w,  # noqa: E731
+                                     shared_expert=cfg.shared, **kw, **k2)
+    return make, a["X"], ids, tw, a["dY"]
+
+
+@pytest.mark.parametrize("f", [8, 72, 136])
+@pytest.mark.parametrize("gather", [False, True])
+def test_h_holds_zeros_where_there_is_no_feature(f, gather):
+    """f = 8 mod 16: the last chunk has 8 gates and 8 ups, whichever tiles the product takes."""
+    cfg = synth.scaled(CFGS[0], f=f)
+    make, X, ids, tw, _ = wide_ups(cfg, 3, gather=gather)
+    p = make()
+    p.h.fill_(9)
+    p.forward(X, ids, tw)
+    last = p.h.view(p.N, -1, 2, 16)[:, -1]
+    assert not last[:, :, 8:].any() and last[:, :, :8].any()
+
+
+def test_the_last_chunk_is_scaled_by_its_own_features():
+    """Codes and scales as those of h with zeros past f: eight large up features of another
+    chunk do not cost the last one its bits."""
+    make, X, ids, tw, _ = wide_ups(CFGS[1], 4)
+    p, c = make(), make(checkpoint=LayerScratch(DEV))
+    p.forward(X, ids, tw)
+    c.forward(X, ids, tw)
+    h = p.h.clone()
+    h.view(p.N, -1, 2, 16)[:, -1, :, 8:] = 0
+    codes, scales = to.ckpt_pack(h.cpu().numpy())
+    assert np.array_equal(c.h8.codes.cpu().numpy(), codes) and np.array_equal(c.h8.scales.cpu().numpy(), scales)
+
+
 def test_layers_that_share_a_scratch():
     """Forward one, forward the other, backward in reverse: the same as each alone."""
     s = LayerScratch(DEV)
