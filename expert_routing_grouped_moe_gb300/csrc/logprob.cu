@@ -925,10 +925,13 @@ cudaError_t launch_rows(const Args& a, cudaStream_t s) {
     return rows<T, 512, 2, GRAD, 8>(a, cluster, s);
   // Rows that blocks of 128 threads have places for at once, and those of 256 do not: one
   // turn instead of two (900 rows of 151936: 50 us, 59; 620, which 256 threads have places
-  // for: 44, 37).  With a list, whose second reading is by as many threads, while that is short
-  // (900 rows of 32000, 5 tokens: 21 us, 27; of 151936, 20 tokens: 80, 64).
+  // for: 44, 37).  With a list, whose second reading is by half as many threads, while rows,
+  // words and tokens listed are few.  Of 175 points (1 to 32 tokens, 620 to 1200 rows of
+  // 20000 to 151936) the rule takes the faster form or one within 2 % but for five (3 to 9 %):
+  // 900x32000, 5 tokens 21 us, 27; 1024x100352, 5 tokens 47.6, 48.0; 1200x128000, 5 tokens
+  // 66, 60; 900x50257, 20 tokens 32, 34, 32 tokens 37, 35.
   const bool one_turn = !GRAD && cluster == 1 && a.T <= 8 * kSMs && a.T > (a.top > 0 ? 4 : 5) * kSMs &&
-                        words * a.top <= 80 << 10;
+                        (a.top == 0 || a.T * words * (a.top + 6) <= 145 << 20);
   return each <= kLane                 ? rows<T, 32, 20, GRAD>(a, cluster, s)
          : each <= kSmall || one_turn ? rows<T, 128, 8, GRAD>(a, cluster, s)
          : a.top > 0                  ? rows<T, 256, 4, GRAD>(a, cluster, s)
