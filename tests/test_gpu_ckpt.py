@@ -68,6 +68,26 @@ def test_every_code_and_scale():
         assert np.array_equal(np64(y), want)
 
 
+@pytest.mark.parametrize("C", [256, 250])
+def test_the_outermost_scale_bytes(C):
+    """Byte 0 is 2^-127, byte 255 is NaN whatever the codes are."""
+    codes = torch.arange(-128, 128, device=DEV).to(torch.int8)[:C].repeat(2, 1)
+    scales = torch.tensor([0, 255], dtype=torch.uint8, device=DEV)[:, None].repeat(1, 8).contiguous()
+    for out in (BF, F32):
+        y = torch.empty(2, C, dtype=out, device=DEV)
+        L.moe_ckpt_unpack(codes, scales, y)
+        assert np.array_equal(np64(y), to.ckpt_value(codes.cpu().numpy(), scales.cpu().numpy()), equal_nan=True)
+
+
+def test_the_outermost_scale_bytes_of_a_layer():
+    codes = torch.full((2, 32), 3, dtype=torch.int8, device=DEV)
+    scales = torch.tensor([[0], [255]], dtype=torch.uint8, device=DEV)
+    h, act = torch.empty(2, 32, device=DEV), torch.empty(2, 2, 16, dtype=BF, device=DEV)
+    L.moe_ckpt_unpack_swiglu(codes, scales, torch.arange(2, dtype=torch.int32, device=DEV),
+                             torch.ones(2, 1, device=DEV), False, h, act)
+    assert (h[0] == 3 * 2.0 ** -127).all() and torch.isnan(h[1]).all() and torch.isnan(act[0, 1]).all()
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("C", [64, 33])
 def test_the_largest_values_stay_finite(C, dtype):
