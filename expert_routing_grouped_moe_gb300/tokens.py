@@ -77,21 +77,21 @@ class MoEHead:
                     top_logp=self.top_logp, inv_temp=self.inv_temp, ignore_id=self.ignore_id)
 
     def _logits(self, n):
-        self._n = n
+        self._n = None     # of the call before; this one's once its logits have their values
         torch.mm(n, self.W.t(), out=self.logits)
 
     def forward(self, n, targets):
         """logp of targets [tokens] or [tokens, m] (int32 or int64)."""
         self._logits(n)
-        self._targets = targets
         L.moe_logprob_fwd(self.logits, targets, self.logp, self.stats, **self._wanted())
+        self._n, self._targets = n, targets
         return self.logp
 
-    def _back(self):
+    def _back(self, n):
+        self._n = None     # the logits are gone
         torch.mm(self.logits, self.W, out=self.dn)
         if self.dW is not None:
-            torch.mm(self.logits.t(), self._n, out_dtype=torch.float32, out=self.dW)
-        self._n = None
+            torch.mm(self.logits.t(), n, out_dtype=torch.float32, out=self.dW)
         return self.dn, self.dW
 
     def backward(self, dlogp, dentropy=None, dlse=None):
@@ -101,7 +101,7 @@ class MoEHead:
         L.moe_logprob_bwd(self.logits, self._targets, self.stats, dlogp, self.logits,
                           entropy=self.entropy, dentropy=dentropy, dlse=dlse,
                           inv_temp=self.inv_temp, ignore_id=self.ignore_id)
-        return self._back()
+        return self._back(self._n)
 
     def step(self, n, targets, dlogp, dentropy=None, dlse=None):
         """forward and backward together, for gradients that are known ahead:
@@ -109,7 +109,7 @@ class MoEHead:
         self._logits(n)
         L.moe_logprob_step(self.logits, targets, self.logp, self.stats, dlogp, self.logits,
                            dentropy=dentropy, dlse=dlse, **self._wanted())
-        return self._back()
+        return self._back(n)
 
 
 class MoEStack:

@@ -166,6 +166,23 @@ def test_head(m):
     assert (dW2 - dW).norm() <= 0.01 * dW.norm()
 
 
+def test_a_head_that_was_refused_has_nothing_to_go_back_from():
+    g = gen(5)
+    W = torch.randn(40, 16, generator=g, device=DEV).to(BF)
+    n, y = torch.randn(6, 16, generator=g, device=DEV).to(BF), torch.zeros(6, dtype=torch.int64, device=DEV)
+    dlogp = torch.ones(6, device=DEV)
+    h = MoEHead(W, 6, train=True)
+    h.forward(n, y)
+    for call in (lambda: h.step(n, y, dlogp[:5]), lambda: h.forward(n, y[:5])):
+        h.forward(n, y)
+        with pytest.raises(ValueError):
+            call()
+        with pytest.raises(RuntimeError):
+            h.backward(dlogp)
+    h.forward(n, y)
+    h.backward(dlogp)
+
+
 def stack(cfg, V, blocks, checkpoint, tied, residual=BF, **kw):
     import finetune_block as ex
     g = gen(11)
