@@ -161,9 +161,11 @@ class MoELoRALayer:
 
     def h_gate_up(self):
         """The saved pre-activations as a plain [N, 2f] (gate | up) fp32 tensor
-        (un-interleaves the 16-feature chunks of the stored layout)."""
+        (un-interleaves the 16-feature chunks of the stored layout); of a
+        checkpointed layer what its 8 bits stand for."""
         n, f = self.N, self.f
-        hc = self.h.view(n, -1, 2, 16)
+        h = self.h if self.h8 is None else self.h8.unpack(torch.empty_like(self.h))
+        hc = h.view(n, -1, 2, 16)
         gate = hc[:, :, 0, :].reshape(n, -1)[:, :f]
         up = hc[:, :, 1, :].reshape(n, -1)[:, :f]
         return torch.cat([gate, up], dim=1)

@@ -132,6 +132,19 @@ def test_layers_that_share_a_scratch():
     assert shared[1][0].h.untyped_storage().nbytes() >= shared[1][0].h.numel() * 4
 
 
+def test_h_gate_up_of_a_checkpointed_layer_is_its_own():
+    """What its codes stand for, also after another layer of the same scratch ran."""
+    s = LayerScratch(DEV)
+    a, pa, *xa = layer_pair(CFGS[1], s, 5)
+    b, _, *xb = layer_pair(CFGS[1], s, 6)
+    a.forward(*xa[:3])
+    pa.forward(*xa[:3])
+    b.forward(*xb[:3])
+    L.moe_ckpt_unpack(a.h8.codes, a.h8.scales, pa.h)
+    assert torch.equal(a.h_gate_up(), pa.h_gate_up())
+    assert not torch.equal(a.h_gate_up(), b.h_gate_up())
+
+
 @pytest.mark.parametrize("m", [1, 3])
 def test_head(m):
     """Its gradients against 64 bits from the logits as they were rounded: dn and dW are
