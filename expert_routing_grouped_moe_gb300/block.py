@@ -44,7 +44,7 @@ class MoEBlock:
         def buf(name, *shape, dtype):
             if checkpoint is None:
                 return torch.empty(*shape, dtype=dtype, device=device)
-            return checkpoint.take(name, shape, dtype)
+            return checkpoint.take(name, shape, dtype, device)
         self.T, self.E, self.k = T, E, k
         self.scale, self.sigmoid, self.eps = float(scale), bool(gate_sigmoid), float(eps)
         self.aux_coef, self.z_coef = float(aux_coef), float(z_coef)

@@ -19,15 +19,18 @@ from . import _lib as L
 class LayerScratch:
     """Device buffers by name, each as large as its largest user asked for; users get
     views.  What one call leaves there the next call of any layer overwrites, so the
-    layers of one scratch take turns: on one stream, or ordered by their caller."""
+    layers of one scratch take turns: on one stream, or ordered by their caller.  A
+    buffer stays where it is for the scratch's life: a layer larger than those before it
+    gets another, which later layers share, so build the largest first."""
 
     def __init__(self, device="cuda"):
         self.device = torch.device(device)
-        self._buf = {}
+        self._buf, self._made = {}, []
 
-    def take(self, name, shape, dtype):
+    def take(self, name, shape, dtype, device=None):
         """A tensor of this shape over the buffer of that name (made, or made larger,
-        on first use; layers take theirs when they are built)."""
+        on first use; layers take theirs when they are built).  device: the user's, which
+        has to be the scratch's."""
         n = 1
         for s in shape:
             n *= int(s)
@@ -35,12 +38,17 @@ class LayerScratch:
         buf = self._buf.get(name)
         if buf is None or buf.numel() < size:
             # a larger buffer replaces the smaller one for later users; earlier ones keep theirs
-            buf = self._buf[name] = torch.empty(max(16, size), dtype=torch.uint8,
-                                                device=self.device)
+            buf = torch.empty(max(16, size), dtype=torch.uint8, device=self.device)
+        if device is not None and torch.empty(0, device=device).device != buf.device:
+            raise ValueError("the scratch is on %s, its user on %s" % (buf.device, device))
+        if self._buf.get(name) is not buf:
+            self._buf[name] = buf
+            self._made.append(buf)
         return buf[:size].view(dtype).view(*shape)
 
     def bytes(self):
-        return sum(b.numel() for b in self._buf.values())
+        """Of all buffers, replaced ones among them."""
+        return sum(b.numel() for b in self._made)
 
 
 class Packed8:

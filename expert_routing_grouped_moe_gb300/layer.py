@@ -65,7 +65,7 @@ class MoELoRALayer:
         def buf(name, *shape, dtype):   # lives within a call: the scratch's, if there is one
             if checkpoint is None:
                 return torch.empty(*shape, dtype=dtype, device=dev)
-            return checkpoint.take(name, shape, dtype)
+            return checkpoint.take(name, shape, dtype, dev)
         self.counts = torch.zeros(G, **i32)
         self.offsets = torch.zeros(G + 1, **i32)
         self.tile_off = torch.zeros(G + 1, **i32)

@@ -177,3 +177,21 @@ def test_bindings_refuse_before_the_library(L):
             L.moe_ckpt_pack(*args)
         with pytest.raises((ValueError, TypeError)):
             L.moe_ckpt_unpack(args[1], args[2], args[0])
+
+
+def test_scratch():
+    """Views of one buffer a name; a larger user's replaces it, and both count; a user of another
+    device is refused before anything is kept."""
+    from expert_routing_grouped_moe_gb300 import LayerScratch
+    s = LayerScratch("cpu")
+    a, b = s.take("h", (3, 8), torch.float32, "cpu"), s.take("h", (5, 4), torch.bfloat16)
+    assert a.shape == (3, 8) and b.shape == (5, 4) and a.data_ptr() == b.data_ptr() and s.bytes() == 96
+    c, d = s.take("h", (100,), torch.float32), s.take("h", (2, 8), torch.float32)
+    assert d.data_ptr() == c.data_ptr() != a.data_ptr() and s.bytes() == 96 + 400
+    a.fill_(1)
+    c.fill_(2)
+    assert (a == 1).all()
+    for name, n in (("h", 4), ("h", 1000), ("new", 4)):
+        with pytest.raises(ValueError):
+            s.take(name, (n,), torch.float32, "meta")
+    assert s.bytes() == 96 + 400 and s.take("h", (100,), torch.float32).data_ptr() == c.data_ptr()
