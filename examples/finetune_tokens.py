@@ -46,7 +46,7 @@ def train(cfg, vocab=1000, blocks=4, steps=40, tied=False, lr=2e-3, seed=1, devi
     weights = [block_weights(cfg, seed + i, device) for i in range(blocks)]
     model = MoEStack(cfg.T, cfg, table, weights, torch.ones(cfg.d, device=device), head=head,
                      residual=torch.float32, scale=0.1 if tied else 1.0, inv_temp=cfg.d ** -0.5 if tied else 1.0,
-                     train_head=True, gate_sigmoid=True, aux_coef=0.01, z_coef=0.001)
+                     checkpoint=True, train_head=True, gate_sigmoid=True, aux_coef=0.01, z_coef=0.001)
     data = batches(cfg.T, vocab, seed, device)
     losses, opt = [], None
     for step in range(steps):

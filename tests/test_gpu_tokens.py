@@ -279,6 +279,23 @@ def test_checkpointed_stack():
     assert L.moe_status() == L.MOE_OK
 
 
+def test_a_stack_is_exact_unless_told_otherwise():
+    cfg, V = CFGS[0], 517
+    import finetune_block as ex
+    g = gen(11)
+    table = torch.randn(V, cfg.d, generator=g, device=DEV).to(BF)
+    w = lambda: [ex.block_weights(cfg, 5 + i, DEV) for i in range(2)]  # noqa: E731
+    args = (cfg.T, cfg, table)
+    first = torch.ones(cfg.d, device=DEV)
+    a, b = MoEStack(*args, w(), first), MoEStack(*args, w(), first, checkpoint=False)
+    ids, y, dlogp = batch(cfg, V, 2)
+    for m in (a, b):
+        m.forward(ids, y)
+    ga, gb = flat(a.backward(dlogp)), flat(b.backward(dlogp))
+    for n in gb:
+        assert torch.equal(ga[n], gb[n]), n
+
+
 def test_gradient_of_a_token_that_is_not_there():
     """The loss asked of one position moves only the rows of the batch's tokens."""
     cfg, V = CFGS[0], 517
