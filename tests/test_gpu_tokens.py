@@ -58,6 +58,22 @@ def test_checkpointed_layer_works_on_what_its_codes_stand_for(cfg, gather):
     assert L.moe_status() == L.MOE_OK
 
 
+@pytest.mark.parametrize("kw", [dict(full_grads=True), dict(rank_r_tokens=True),
+                                dict(full_grads=True, rank_r_tokens=True)])
+def test_checkpointed_layer_with_the_layers_other_options(kw):
+    """Full weight gradients read the activations and rows that came back; rank-r products
+    read token rows."""
+    c, p, X, ids, tw, dY = layer_pair(CFGS[1], LayerScratch(DEV), 7, **kw)
+    assert torch.equal(c.forward(X, ids, tw), p.forward(X, ids, tw))
+    for b in (c.Yp, c.act, c.h, c.dXp, c.Xp):
+        b.view(torch.uint8).fill_(0x7F)
+    L.moe_ckpt_unpack_swiglu(c.h8.codes, c.h8.scales, p.sorted_src, tw, True, p.h, p.act)
+    got, want = c.backward(dY), p.backward(dY)
+    assert sorted(got) == sorted(want)
+    for n in got:
+        assert torch.equal(got[n], want[n]), n
+
+
 @pytest.mark.parametrize("cfg", CFGS)
 def test_checkpointed_gradients_are_near_the_exact_ones(cfg):
     """Each h is off by at most 1/254 of the largest of its 32, some 3 of their spread: 1.2 %
