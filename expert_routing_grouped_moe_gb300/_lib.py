@@ -391,6 +391,13 @@ def _rows(n):
     return n
 
 
+def _word(n, name):
+    """A whole number that the C ABI takes as int64, likewise."""
+    if not -2 ** 63 <= n < 2 ** 63:
+        raise ValueError("%s = %d does not fit 64 bits" % (name, n))
+    return n
+
+
 @functools.lru_cache(maxsize=256)
 def _norm_setup(T, d, xt, yt, gate_kind, gate_sigmoid, scale, eps, w_offset):
     """Descriptor of a call with these settings, the gate's shape and its type."""
@@ -728,7 +735,7 @@ def moe_embed_bwd(ids, dout, dtable, ws, scale=1.0, pad_id=None, accumulate=Fals
     desc, (i, o, w), dev = _embed_setup(ids, dout, dtable, scale, ("dout", "dtable"))
     if pad_id is not None and pad_id < 0:
         raise ValueError("pad_id must not be negative")
-    _check(load().moe_embed_bwd(desc, i, o, w, -1 if pad_id is None else int(pad_id),
+    _check(load().moe_embed_bwd(desc, i, o, w, -1 if pad_id is None else _word(int(pad_id), "pad_id"),
                                 1 if accumulate else 0, *_bytes(ws, dev), _stream(stream)),
            "moe_embed_bwd")
 
@@ -736,7 +743,8 @@ def moe_embed_bwd(ids, dout, dtable, ws, scale=1.0, pad_id=None, accumulate=Fals
 @functools.lru_cache(maxsize=256)
 def _logprob_desc(T, V, m, top, dtype, target_type, ld, dld, ignore_id, inv_temp):
     return ctypes.byref(MoeLogprobDesc(_rows(T), _rows(V), m, top, _type(dtype, "logits"),
-                                       target_type, ld, dld, ignore_id, inv_temp))
+                                       target_type, ld, dld, _word(ignore_id, "ignore_id"),
+                                       inv_temp))
 
 
 def _matrix(t, name):

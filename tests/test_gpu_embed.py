@@ -168,6 +168,15 @@ def test_gradient_with_padding_and_bad_ids(ids, add):
     assert L.moe_status() == L.MOE_OK
 
 
+def test_padding_ids_past_64_bits_are_refused():
+    ids, dout = torch.full((100,), 4, device=DEV), torch.randn(100, 24, device=DEV)
+    dw, ws = torch.full((9, 24), 5.0, device=DEV), workspace(100, 9, 24)
+    for bad in (2 ** 63, 2 ** 64 + 4):
+        with pytest.raises(ValueError):
+            L.moe_embed_bwd(ids, dout, dw, ws, pad_id=bad)
+    assert (dw == 5.0).all()
+
+
 def test_nothing_but_padding():
     dw = torch.full((9, 24), 5.0, device=DEV)
     ids, dout = torch.full((100,), 4, device=DEV), torch.randn(100, 24, device=DEV)

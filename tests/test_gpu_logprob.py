@@ -452,6 +452,17 @@ def test_ignored_and_bad_targets(V, ids):
     assert not c.dlogits[0].any() and not c.dlogits[2].any() and c.dlogits[1].any()
 
 
+def test_ids_past_64_bits_are_refused():
+    """Their lower bits are tokens' ids."""
+    c = Case(2, 50, F32, entropy=False, grads=False)
+    for bad in (2 ** 63, 2 ** 64 + 3, -2 ** 63 - 1):
+        for call in (c.fwd, c.bwd, c.step):
+            with pytest.raises(ValueError):
+                call(ignore_id=bad)
+    c.fwd(ignore_id=2 ** 63 - 1)
+    c.check_fwd()
+
+
 def test_rows_that_get_no_gradient_are_not_read():
     """Zeros, whatever the logits hold; a NaN gradient is not nothing."""
     c = Case(3, 9000, F32, 2, entropy=False, grads=False)
