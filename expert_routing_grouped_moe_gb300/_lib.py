@@ -823,7 +823,7 @@ def moe_logprob_step(logits, targets, logp, stats, dlogp, dlogits, dentropy=None
                      lse=None, entropy=None, top_ids=None, top_logp=None, inv_temp=1.0,
                      ignore_id=-100, stream=None):
     """moe_logprob_fwd and moe_logprob_bwd in one call, for gradients that are known
-    ahead; reads the logits from memory once."""
+    ahead; the logits' second reading mostly comes from the L2."""
     for t, name in ((logp, "logp"), (stats, "stats"), (dlogits, "dlogits")):
         _needed(t, name)
     desc, x, y, dx, ids, lp, T, ysh, dev = _logprob_setup(logits, targets, dlogits, top_ids, top_logp,

@@ -231,6 +231,7 @@ MOE_API int moe_unpermute_combine(const moe_bf16* rows, const int32_t* dest_pos,
  *   h     [P,hs]   fp32  saved gate and up pre-activations, hs = 32*ceil(f/16):
  *                        features in chunks of 16, row layout
  *                        [gate c*16..c*16+15 | up c*16..c*16+15] for chunk c
+ *                        (features past f: zeros)
  *   act   [2,P,f]  bf16 pair  saved w_p * silu(gate) * up (scaled by the row's
  *                              routing weight w_p; 1 for shared-expert rows)
  *   xa_gu [2,P,r]  bf16 pair  saved s * Xp A_gu^T
@@ -500,8 +501,9 @@ MOE_API int moe_embed_fwd(const moe_embed_desc* desc, const void* ids, const voi
 MOE_API size_t moe_embed_workspace_size(int32_t T, int32_t V, int32_t d);
 
 /* dtable[v] = scale * sum over the tokens t with ids[t] = v of dout[t], fp32 sums
- * in an order that depends on the ids alone: the tokens are sorted by id (stable)
- * and each id's rows added in their order, long runs in parts.
+ * in an order that depends on the ids and on d alone: the tokens are sorted by id
+ * (stable) and each id's rows added in their order, long runs in parts (whose lengths
+ * go by T and d).
  *   accumulate = 0: rows without a token become zeros, so that all of dtable
  *                   [V,d] is written;
  *   accumulate = 1: the sum is added to what dtable holds; other rows are left
@@ -539,7 +541,8 @@ typedef struct moe_logprob_desc {
  * row's exponents and their sum); lse, entropy [T], top_ids and top_logp may be
  * NULL; outputs fp32, top_ids int32.  A target equal to ignore_id gets logp 0; one
  * outside [0,V) otherwise too, and sets MOE_ERR_BAD_IDS in the status word.
- * A row whose logits are all -inf has lse = logp = -inf and entropy 0.  A NaN or
+ * A row whose logits are all -inf has lse = logp = -inf and entropy 0.  Finite
+ * logits count as they are, whatever their size (those of a mask, say).  A NaN or
  * +inf among a row's logits makes its values NaN.  No workspace.  T = 0 does
  * nothing. */
 MOE_API int moe_logprob_fwd(const moe_logprob_desc* desc, const void* logits, const void* targets,
@@ -555,7 +558,7 @@ MOE_API int moe_logprob_fwd(const moe_logprob_desc* desc, const void* logits, co
  * add nothing; a target named twice adds twice.  A row to which all three give
  * nothing but zeros gets zeros and is not read, a row whose logits are all -inf
  * gets zeros.  dlogits may be logits (then in place, dld = ld); other overlaps
- * are not allowed.  desc->top is not looked at.  T = 0 does nothing. */
+ * are not allowed.  desc->top has no effect.  T = 0 does nothing. */
 MOE_API int moe_logprob_bwd(const moe_logprob_desc* desc, const void* logits, const void* targets,
                             const float* stats, const float* entropy, const float* dlogp,
                             const float* dentropy, const float* dlse, void* dlogits,
@@ -564,7 +567,7 @@ MOE_API int moe_logprob_bwd(const moe_logprob_desc* desc, const void* logits, co
 /* Forward and backward in one call, for losses whose weights are known ahead
  * (dlogp = -1 / tokens, say): same arguments and results as the two in turn, but
  * for the order in which a row's sums are taken (entropy may be NULL here even with
- * dentropy); a row's second reading comes from the L2. */
+ * dentropy); a row's second reading mostly comes from the L2. */
 MOE_API int moe_logprob_step(const moe_logprob_desc* desc, const void* logits, const void* targets,
                              const float* dlogp, const float* dentropy, const float* dlse,
                              float* logp, float* stats, float* lse, float* entropy,
@@ -588,7 +591,8 @@ MOE_API int moe_logprob_step(const moe_logprob_desc* desc, const void* logits, c
 MOE_API int moe_ckpt_pack(const void* x, int32_t x_type, int32_t R, int32_t C, int8_t* codes,
                           uint8_t* scales, moe_stream_t stream);
 
-/* x = code 2^(byte - 127), exact in both types; NaN where the byte is 255. */
+/* x = code 2^(byte - 127), exact in both types unless it is past their range; NaN
+ * where the byte is 255. */
 MOE_API int moe_ckpt_unpack(const int8_t* codes, const uint8_t* scales, int32_t R, int32_t C,
                             void* x, int32_t x_type, moe_stream_t stream);
 
